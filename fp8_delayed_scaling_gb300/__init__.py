@@ -66,6 +66,15 @@ _SIGS = {
     "mxfp8_scale_bytes": (_sz, [_i64, _i64]),
     "mxfp8_quantize": (_i32, [_vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "mxfp8_gemm": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _i32, _vp, _i32, _vp, _vp]),
+    "fp8_block_padded_rows": (_i64, [_i64, _i32]),
+    "fp8_block_quantize": (_i32, [_vp, _i32, _i64, _i64, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "fp8_block_quantize_weight": (_i32, [_vp, _i32, _i32, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp]),
+    "fp8_block_gemm": (_i32, [_vp, _i32, _vp, _vp, _i32, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp, _i32, _vp,
+                              _vp]),
+    "fp8_block_gemm_grouped": (_i32, [_vp, _i32, _vp, _vp, _i32, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp,
+                                      _vp]),
+    "fp8_block_gemm_grouped_wgrad": (_i32, [_vp, _i32, _vp, _vp, _i32, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _i32,
+                                            _vp, _vp]),
     "fp8_layernorm_cast": (_i32, [_vp, _i64, _i64, _vp, _vp, ctypes.c_float, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
                                   _vp, _vp]),
     "fp8_gelu_cast": (_i32, [_vp, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _vp]),
@@ -363,6 +372,126 @@ def mxfp8_gemm(A, A_s, B, B_s, D: torch.Tensor, bias: torch.Tensor | None = None
     _check(_lib.mxfp8_gemm(_p(A), _p(A_s), _p(B), _p(B_s), M, N, K, _p(bias),
                            _hp(bias) if bias is not None else BF16, _p(D), _hp(D), _p(dev_status), _stream(stream)),
            "mxfp8_gemm")
+
+
+# --------------------------------------------------------------------------
+# block-scaled FP8: one fp32 scale per 128 values (include/fp8dl.h has the layouts)
+# --------------------------------------------------------------------------
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _tensor(t, dtype, shape, name: str):
+    """t (or None) is a contiguous tensor of this dtype and shape; returns its device."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s, got %s %s%s" % (
+            name, dtype, shape, t.dtype, tuple(t.shape), "" if t.is_contiguous() else " (strided)"))
+    return t.device
+
+
+def _one_device(devices) -> None:
+    """All tensors live on the current CUDA device (the one the kernels launch on)."""
+    have = {d for d in devices if d is not None}
+    if len(have) != 1 or next(iter(have)) != torch.device("cuda", torch.cuda.current_device() if torch.cuda.is_available() else 0):
+        raise ValueError("all tensors must be on the current CUDA device, got %s" % sorted(map(str, have)))
+
+
+def _offsets(offsets, name="offsets"):
+    _need(offsets.dim() == 1 and offsets.numel() >= 2, "%s must hold n_groups + 1 entries" % name)
+    return _tensor(offsets, torch.int32, (offsets.numel(),), name)
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def fp8_block_padded_rows(rows: int, n_groups: int = 0) -> int:
+    """Columns of the transposed codes of fp8_block_quantize (every group padded to a multiple of 128)."""
+    return _lib.fp8_block_padded_rows(int(rows), int(n_groups))
+
+
+def fp8_block_quantize(x: torch.Tensor, out_dtype: int, row_q=None, row_s=None, col_q=None, col_s=None, offsets=None,
+                       dbias=None, workspace=None, stream=None) -> None:
+    """Codes and factors of x [R x C] in blocks of 128: along the rows (row_q [R x C], row_s [C/128 x R]) and
+    transposed, along the columns (col_q [C x T], col_s [T/128 x C], T = fp8_block_padded_rows(R, groups)).
+    offsets (int32 [groups + 1]): ragged groups of rows, each padded to a multiple of 128 in col_q; dbias (fp32 [C],
+    without offsets): column sums of x (workspace: fp8_cast_workspace_size bytes)."""
+    _need(x.dim() == 2 and x.is_contiguous(), "x must be a contiguous matrix")
+    rows, cols = x.shape
+    groups = 0 if offsets is None else offsets.numel() - 1
+    T = fp8_block_padded_rows(rows, groups)
+    _one_device((x.device, _tensor(row_q, torch.uint8, (rows, cols), "row_q"),
+                 _tensor(row_s, torch.float32, (_blocks(cols), rows), "row_s"),
+                 _tensor(col_q, torch.uint8, (cols, T), "col_q"),
+                 _tensor(col_s, torch.float32, (T // 128, cols), "col_s"),
+                 None if offsets is None else _offsets(offsets), _tensor(dbias, torch.float32, (cols,), "dbias")))
+    _check(_lib.fp8_block_quantize(_p(x), _hp(x), rows, cols, _p(offsets), groups, out_dtype, _p(row_q), _p(row_s),
+                                   _p(col_q), _p(col_s), _p(dbias), _p(workspace), _nbytes(workspace),
+                                   _stream(stream)), "fp8_block_quantize")
+
+
+def fp8_block_quantize_weight(w: torch.Tensor, out_dtype: int, q=None, s=None, q_t=None, s_t=None,
+                              stream=None) -> None:
+    """Codes and factors of weights w [R x C] or [E x R x C] in 128 x 128 blocks: q like w with s [(E x) C/128 x R/128]
+    (the B operand of the forward product), and transposed, q_t [(E x) C x R] with s_t [(E x) R/128 x C/128] (dgrad)."""
+    _need(w.dim() in (2, 3) and w.is_contiguous(), "w must be a contiguous [R x C] or [E x R x C] tensor")
+    lead, (rows, cols) = tuple(w.shape[:-2]), w.shape[-2:]
+    _one_device((w.device, _tensor(q, torch.uint8, lead + (rows, cols), "q"),
+                 _tensor(s, torch.float32, lead + (_blocks(cols), _blocks(rows)), "s"),
+                 _tensor(q_t, torch.uint8, lead + (cols, rows), "q_t"),
+                 _tensor(s_t, torch.float32, lead + (_blocks(rows), _blocks(cols)), "s_t")))
+    _check(_lib.fp8_block_quantize_weight(_p(w), _hp(w), lead[0] if lead else 1, rows, cols, out_dtype, _p(q), _p(s),
+                                          _p(q_t), _p(s_t), _stream(stream)), "fp8_block_quantize_weight")
+
+
+def fp8_block_gemm(A: torch.Tensor, a_dtype: int, a_s: torch.Tensor, B: torch.Tensor, b_dtype: int, b_s: torch.Tensor,
+                   D: torch.Tensor, bias: torch.Tensor | None = None, dev_status=None, stream=None) -> None:
+    """D[M,N] = sum over blocks of 128 of (A_blk * B_blk^T) * a_s * b_s, + bias.  A [M x K], a_s [K/128 x M];
+    B [N x K], b_s [K/128 x N/128] (a weight) or [K/128 x N] (an activation or gradient)."""
+    _need(A.dim() == 2 and B.dim() == 2 and A.shape[1] == B.shape[1], "A [M x K] and B [N x K] must share K")
+    (M, K), N = A.shape, B.shape[0]
+    b_rows = 1 if b_s.shape[-1] == N else 128
+    _one_device((_tensor(A, torch.uint8, (M, K), "A"), _tensor(a_s, torch.float32, (_blocks(K), M), "a_s"),
+                 _tensor(B, torch.uint8, (N, K), "B"),
+                 _tensor(b_s, torch.float32, (_blocks(K), N if b_rows == 1 else _blocks(N)), "b_s"),
+                 _tensor(D, D.dtype, (M, N), "D"), None if bias is None else _tensor(bias, bias.dtype, (N,), "bias")))
+    _check(_lib.fp8_block_gemm(_p(A), a_dtype, _p(a_s), _p(B), b_dtype, _p(b_s), b_rows, M, N, K, _p(bias),
+                               _hp(bias) if bias is not None else BF16, _p(D), _hp(D), _p(dev_status),
+                               _stream(stream)), "fp8_block_gemm")
+
+
+def fp8_block_gemm_grouped(A: torch.Tensor, a_dtype: int, a_s: torch.Tensor, B: torch.Tensor, b_dtype: int,
+                           b_s: torch.Tensor, offsets: torch.Tensor, D: torch.Tensor, dev_status=None,
+                           stream=None) -> None:
+    """D[m] = A[m] * B[g]^T for the rows m of group g: A [M x K], a_s [K/128 x M]; B [G x N x K],
+    b_s [G x K/128 x N/128]; offsets int32 [G + 1]; D [M x N].  Rows outside the groups keep their values."""
+    _need(A.dim() == 2 and B.dim() == 3 and A.shape[1] == B.shape[2], "A [M x K] and B [G x N x K] must share K")
+    (M, K), (G, N) = A.shape, B.shape[:2]
+    _need(offsets.numel() == G + 1, "offsets must hold %d entries, one more than B has matrices" % (G + 1))
+    _one_device((_tensor(A, torch.uint8, (M, K), "A"), _tensor(a_s, torch.float32, (_blocks(K), M), "a_s"),
+                 _tensor(B, torch.uint8, (G, N, K), "B"),
+                 _tensor(b_s, torch.float32, (G, _blocks(K), _blocks(N)), "b_s"), _offsets(offsets),
+                 _tensor(D, D.dtype, (M, N), "D")))
+    _check(_lib.fp8_block_gemm_grouped(_p(A), a_dtype, _p(a_s), _p(B), b_dtype, _p(b_s), _p(offsets), G, M, N, K,
+                                       _p(D), _hp(D), _p(dev_status), _stream(stream)), "fp8_block_gemm_grouped")
+
+
+def fp8_block_gemm_grouped_wgrad(A: torch.Tensor, a_dtype: int, a_s: torch.Tensor, B: torch.Tensor, b_dtype: int,
+                                 b_s: torch.Tensor, offsets: torch.Tensor, D: torch.Tensor, dev_status=None,
+                                 stream=None) -> None:
+    """D[g] = A_g * B_g^T over group g's tokens: A [M x T], a_s [T/128 x M] and B [N x T], b_s [T/128 x N] are col_q and
+    col_s of fp8_block_quantize with these offsets (int32 [G + 1]); D [G x M x N], zeros for a group without rows."""
+    _need(A.dim() == 2 and B.dim() == 2 and A.shape[1] == B.shape[1], "A [M x T] and B [N x T] must share T")
+    (M, T), N, G = A.shape, B.shape[0], offsets.numel() - 1
+    _one_device((_tensor(A, torch.uint8, (M, T), "A"), _tensor(a_s, torch.float32, (_blocks(T), M), "a_s"),
+                 _tensor(B, torch.uint8, (N, T), "B"), _tensor(b_s, torch.float32, (_blocks(T), N), "b_s"),
+                 _offsets(offsets), _tensor(D, D.dtype, (G, M, N), "D")))
+    _check(_lib.fp8_block_gemm_grouped_wgrad(_p(A), a_dtype, _p(a_s), _p(B), b_dtype, _p(b_s), _p(offsets), G, M, N,
+                                             T, _p(D), _hp(D), _p(dev_status), _stream(stream)),
+           "fp8_block_gemm_grouped_wgrad")
 
 
 # --------------------------------------------------------------------------

@@ -1,0 +1,349 @@
+// blockquant.cu — block-scaled FP8 quantisation: one fp32 scale per 128 values
+// (activations and gradients) or per 128 x 128 block (weights).
+//
+// The scale is the per-tensor scale FP8_MAX / amax of "FP8 低精度训练：Transformer
+// Engine 简析" §三.1, taken over a block instead of a tensor and from the block's
+// own values instead of a history, so it needs no state.
+#include <cuda_bf16.h>
+
+#include "block.cuh"
+
+namespace fp8dl {
+
+namespace bq {
+constexpr int THREADS = 256, TILE = 128;
+}
+
+struct BlockQuantArgs {
+    const void *x;
+    int64_t rows, cols;      // of one matrix
+    int64_t tiles_c;         // 128-column tiles
+    int64_t row_blocks;      // 128-row tiles of one matrix (of all groups together: the padded capacity / 128)
+    const int32_t *offsets;  // ragged groups, or NULL
+    int n_groups;
+    uint8_t *row_q, *col_q;  // row-major and transposed codes, either may be NULL
+    float *row_s, *col_s;
+    int64_t col_ld;          // columns of the transposed codes
+    float *ws;               // column sums per 128-row tile, or NULL
+};
+
+// (scale, stored factor) of a block whose largest finite magnitude is amax: both are
+// correctly rounded divisions.  A maximum below 2^-100 counts as 2^-100, so that the scale
+// stays finite; an all-zero block has scale 1.
+template <int FMT>
+__device__ __forceinline__ float2 block_scale(float amax) {
+    constexpr float FMAX = FMT == FP8DL_E4M3 ? 448.0f : 57344.0f;
+    const float sc = amax > 0.0f ? __fdiv_rn(FMAX, fmaxf(amax, 7.888609052210118e-31f)) : 1.0f;
+    return make_float2(sc, __frcp_rn(sc));
+}
+
+// |v|, or 0 if v is not finite (blocks that hold infinities or NaN only).
+__device__ __forceinline__ float finite_abs(float v) {
+    const float a = fabsf(v);
+    return a <= 3.402823466e38f ? a : 0.0f;
+}
+
+// One CTA converts one 128 x 128 tile: x is read once, both copies of the codes are written.
+//   Threads  16 x 16, thread (rr, cc) holds rows 8rr .. 8rr+7 and columns 8cc .. 8cc+7: its
+//            eight loads are 16 (bf16) or 32 (fp32) bytes and a warp covers whole 128-byte
+//            lines; all eight are in flight at once.
+//   Row      maxima over the 16 lanes of a half-warp by a halving exchange (8 shuffles for
+//   blocks   8 rows instead of 32), after which each lane owns one row's maximum, takes its
+//            scale once and the others fetch it by shuffle.
+//   Column   maxima over 8 rows in the thread, two row groups by shuffle, eight warps through
+//   blocks   shared memory.
+//   Codes    row-wise leave as 8-byte pieces (16 lanes: one 128-byte line).  Transposed codes
+//            are packed straight along the rows (the conversion takes two values from any two
+//            registers, so no byte transpose is needed), staged in shared memory with the
+//            8-byte chunks XOR-swizzled by column group (conflict-free both ways), and leave
+//            as whole 128-byte lines.
+// WEIGHT: one scale for the tile instead, for both copies.
+// Bound: HBM (read esz, write 2 bytes per value).
+template <int XKIND, int FMT, bool WEIGHT>
+__global__ void __launch_bounds__(bq::THREADS) block_quantize_kernel(const BlockQuantArgs args) {
+    using namespace bq;
+    pdl_wait();
+    pdl_trigger();
+    constexpr int ESZ = XKIND == FP8DL_BF16 ? 2 : 4;
+    __shared__ __align__(16) uint8_t tcode[TILE * TILE];
+    __shared__ __align__(16) float part[8][TILE];   // column maxima (or sums) per warp
+    __shared__ __align__(16) float cscale[TILE];
+    __shared__ int64_t where[2];                    // ragged groups: first row and row count of the tile
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cc = tid & 15, rr = tid >> 4;
+    const int64_t tile_r = blockIdx.x / args.tiles_c, tile_c = blockIdx.x % args.tiles_c;
+    const int64_t mat = blockIdx.y;
+    int64_t r0 = tile_r * TILE, nrows = min((int64_t)TILE, args.rows - r0);
+    if (!WEIGHT && args.offsets) {
+        if (warp == 0) {
+            int64_t first, n;
+            group_of_block(args.offsets, args.n_groups, args.rows, tile_r, first, n);
+            if (lane == 0) where[0] = first, where[1] = n;
+        }
+        __syncthreads();
+        r0 = where[0];
+        nrows = where[1];
+        if (nrows <= 0) return;  // behind the last group
+    }
+    const int64_t c0 = tile_c * TILE + 8 * cc;
+    const bool col_ok = c0 < args.cols;  // columns come in sixteens
+    const char *px = static_cast<const char *>(args.x) + ((mat * args.rows + r0 + 8 * rr) * args.cols + c0) * ESZ;
+    float v[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const bool ok = col_ok && 8 * rr + i < nrows;
+        if (ESZ == 2) {
+            const uint4 u = ok ? ldg_stream(px + i * args.cols * ESZ) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int q = 0; q < 4; q++) v[i][2 * q] = bf16_lo(w[q]), v[i][2 * q + 1] = bf16_hi(w[q]);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const uint4 u = ok ? ldg_stream(px + i * args.cols * ESZ + 16 * h) : make_uint4(0u, 0u, 0u, 0u);
+                v[i][4 * h] = __uint_as_float(u.x), v[i][4 * h + 1] = __uint_as_float(u.y);
+                v[i][4 * h + 2] = __uint_as_float(u.z), v[i][4 * h + 3] = __uint_as_float(u.w);
+            }
+        }
+    }
+    float rmax[8], cmax[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) rmax[i] = cmax[i] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const float a = finite_abs(v[i][j]);
+            rmax[i] = fmaxf(rmax[i], a);
+            cmax[j] = fmaxf(cmax[j], a);
+        }
+    if (WEIGHT) {
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; i++) m = fmaxf(m, rmax[i]);
+        m = warp_max(m);
+        if (lane == 0) cscale[warp] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < 8; w++) m = fmaxf(m, cscale[w]);
+        const float2 sc = block_scale<FMT>(m);
+        if (tid == 0) {
+            const int64_t e = mat * args.row_blocks * args.tiles_c;
+            if (args.row_s) args.row_s[e + tile_c * args.row_blocks + tile_r] = sc.y;
+            if (args.col_s) args.col_s[e + tile_r * args.tiles_c + tile_c] = sc.y;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+#pragma unroll
+            for (int j = 0; j < 8; j++) v[i][j] = __fmul_rn(v[i][j], sc.x);
+    }
+    if (args.row_q) {
+        float s8[8];
+        if (!WEIGHT) {
+            // halving exchange: after steps 8, 4, 2 lane cc holds row (cc >> 1) of its eight
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const bool up = cc & 8;
+                const float send = up ? rmax[i] : rmax[i + 4], keep = up ? rmax[i + 4] : rmax[i];
+                rmax[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, 8));
+            }
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                const bool up = cc & 4;
+                const float send = up ? rmax[i] : rmax[i + 2], keep = up ? rmax[i + 2] : rmax[i];
+                rmax[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, 4));
+            }
+            {
+                const bool up = cc & 2;
+                const float send = up ? rmax[0] : rmax[1], keep = up ? rmax[1] : rmax[0];
+                rmax[0] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, 2));
+            }
+            const float2 sc = block_scale<FMT>(fmaxf(rmax[0], __shfl_xor_sync(0xffffffffu, rmax[0], 1)));
+            const int row = 8 * rr + (cc >> 1);
+            if (!(cc & 1) && row < nrows) args.row_s[tile_c * args.rows + r0 + row] = sc.y;
+#pragma unroll
+            for (int i = 0; i < 8; i++) s8[i] = __shfl_sync(0xffffffffu, sc.x, (lane & 16) + 2 * i);
+        }
+        uint8_t *qrow = args.row_q + (mat * args.rows + r0 + 8 * rr) * args.cols + c0;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            if (!col_ok || 8 * rr + i >= nrows) continue;
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; j++) y[j] = WEIGHT ? v[i][j] : __fmul_rn(v[i][j], s8[i]);
+            *reinterpret_cast<uint2 *>(qrow + i * args.cols) =
+                make_uint2(pack4<FMT>(y[0], y[1], y[2], y[3]), pack4<FMT>(y[4], y[5], y[6], y[7]));
+        }
+    }
+    if (!WEIGHT && args.ws) {  // column sums of the tile, rows in a fixed order
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            float s = v[0][j];
+#pragma unroll
+            for (int i = 1; i < 8; i++) s += v[i][j];
+            s += __shfl_xor_sync(0xffffffffu, s, 16);
+            if (lane < 16) part[warp][8 * cc + j] = s;
+        }
+        __syncthreads();
+        if (tid < TILE && tile_c * TILE + tid < args.cols) {
+            float s = part[0][tid];
+#pragma unroll
+            for (int w = 1; w < 8; w++) s += part[w][tid];
+            args.ws[tile_r * args.cols + tile_c * TILE + tid] = s;
+        }
+        __syncthreads();
+    }
+    if (!args.col_q) return;
+    if (!WEIGHT) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            cmax[j] = fmaxf(cmax[j], __shfl_xor_sync(0xffffffffu, cmax[j], 16));
+            if (lane < 16) part[warp][8 * cc + j] = cmax[j];
+        }
+        __syncthreads();
+        if (tid < TILE) {
+            float m = part[0][tid];
+#pragma unroll
+            for (int w = 1; w < 8; w++) m = fmaxf(m, part[w][tid]);
+            const float2 sc = block_scale<FMT>(m);
+            cscale[tid] = sc.x;
+            if (tile_c * TILE + tid < args.cols) args.col_s[tile_r * args.cols + tile_c * TILE + tid] = sc.y;
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        const float s = WEIGHT ? 1.0f : cscale[8 * cc + j];
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) y[i] = WEIGHT ? v[i][j] : __fmul_rn(v[i][j], s);
+        *reinterpret_cast<uint2 *>(tcode + (8 * cc + j) * TILE + ((rr ^ cc) << 3)) =
+            make_uint2(pack4<FMT>(y[0], y[1], y[2], y[3]), pack4<FMT>(y[4], y[5], y[6], y[7]));
+    }
+    __syncthreads();
+    // weights: r0 .. r0+127 of q_t's rows (sixteens); groups: the tile's 128 padded columns
+    const int64_t out0 = tile_r * TILE;
+    uint8_t *qcol = args.col_q + (mat * args.cols + tile_c * TILE) * args.col_ld + out0;
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const int col = 32 * k + (tid >> 3), ch = tid & 7, g = col >> 3;
+        uint4 u = *reinterpret_cast<const uint4 *>(tcode + col * TILE + ((ch ^ (g >> 1)) << 4));
+        if (g & 1) u = make_uint4(u.z, u.w, u.x, u.y);
+        if (tile_c * TILE + col < args.cols && out0 + 16 * ch < args.col_ld)
+            *reinterpret_cast<uint4 *>(qcol + col * args.col_ld + 16 * ch) = u;
+    }
+}
+
+template <bool WEIGHT>
+static void launch_block_quantize(int32_t x_dtype, int32_t out_dtype, dim3 grid, cudaStream_t st, bool pdl,
+                                  const BlockQuantArgs &a) {
+    const bool e4 = out_dtype == FP8DL_E4M3;
+    if (x_dtype == FP8DL_BF16 && e4)
+        (void)launch_kernel(block_quantize_kernel<FP8DL_BF16, FP8DL_E4M3, WEIGHT>, grid, bq::THREADS, 0, st, 0, pdl, a);
+    else if (x_dtype == FP8DL_BF16)
+        (void)launch_kernel(block_quantize_kernel<FP8DL_BF16, FP8DL_E5M2, WEIGHT>, grid, bq::THREADS, 0, st, 0, pdl, a);
+    else if (e4)
+        (void)launch_kernel(block_quantize_kernel<FP8DL_F32, FP8DL_E4M3, WEIGHT>, grid, bq::THREADS, 0, st, 0, pdl, a);
+    else
+        (void)launch_kernel(block_quantize_kernel<FP8DL_F32, FP8DL_E5M2, WEIGHT>, grid, bq::THREADS, 0, st, 0, pdl, a);
+    note_launch();
+}
+
+}  // namespace fp8dl
+
+using namespace fp8dl;
+
+extern "C" int64_t fp8_block_padded_rows(int64_t rows, int32_t n_groups) {
+    if (rows <= 0) return 0;
+    const int64_t g = n_groups < 1 ? 1 : n_groups;
+    return (rows + 127 * (g < rows ? g : rows)) / 128 * 128;
+}
+
+extern "C" fp8dl_status fp8_block_quantize(const void *x, int32_t x_dtype, int64_t rows, int64_t cols,
+                                           const int32_t *offsets, int32_t n_groups, int32_t out_dtype,
+                                           uint8_t *row_q, float *row_s, uint8_t *col_q, float *col_s, float *dbias,
+                                           void *workspace, size_t workspace_bytes, fp8dl_stream_t stream) {
+    FP8DL_NVTX("fp8_block_quantize");
+    FP8DL_CHECK_ARG(x_dtype == FP8DL_F32 || x_dtype == FP8DL_BF16, "x_dtype must be FP8DL_F32 or FP8DL_BF16");
+    FP8DL_CHECK_ARG(out_dtype == FP8DL_E4M3 || out_dtype == FP8DL_E5M2, "out_dtype must be E4M3 or E5M2");
+    if (!block_tokens_ok(rows) || !dim_ok(cols, 16))
+        return fail(FP8DL_ERR_SHAPE, "rows (%lld) must be in [0, 2^31) and cols (%lld) a positive multiple of 16",
+                    (long long)rows, (long long)cols);
+    FP8DL_TRY(check_block_groups(offsets, n_groups, true));
+    FP8DL_CHECK_ARG(!offsets || !dbias, "dbias is the sum over all rows: not with offsets");
+    FP8DL_CHECK_ARG(rows == 0 || x, "x is NULL");
+    FP8DL_CHECK_ARG(rows == 0 || row_q || col_q, "row_q and col_q are both NULL");
+    FP8DL_CHECK_ARG(rows == 0 || (!row_q == !row_s && !col_q == !col_s), "row_q/row_s and col_q/col_s come in pairs");
+    if (!aligned16(x) || !aligned16(row_q) || !aligned16(row_s) || !aligned16(col_q) || !aligned16(col_s) || !aligned16(dbias))
+        return fail(FP8DL_ERR_ALIGN, "x, row_q, row_s, col_q, col_s and dbias must be 16-byte aligned");
+    if (dbias && rows > 0) {
+        if (!workspace || workspace_bytes < fp8_cast_workspace_size(rows, cols))
+            return fail(FP8DL_ERR_WORKSPACE, "dbias needs a workspace of %zu bytes (got %zu)",
+                        fp8_cast_workspace_size(rows, cols), workspace ? workspace_bytes : (size_t)0);
+        if (!aligned16(workspace)) return fail(FP8DL_ERR_ALIGN, "workspace must be 16-byte aligned");
+    }
+    FP8DL_TRY(current_device(nullptr, nullptr));
+    cudaStream_t st = (cudaStream_t)stream;
+    if (rows == 0) {
+        if (dbias && cudaMemsetAsync(dbias, 0, (size_t)cols * sizeof(float), st) != cudaSuccess)
+            return check_launch("fp8_block_quantize(empty)");
+        return FP8DL_OK;
+    }
+    BlockQuantArgs a = {};
+    a.x = x;
+    a.rows = rows;
+    a.cols = cols;
+    a.tiles_c = (cols + 127) / 128;
+    a.row_blocks = fp8_block_padded_rows(rows, n_groups) / 128;
+    a.offsets = offsets;
+    a.n_groups = n_groups;
+    a.row_q = row_q;
+    a.row_s = row_s;
+    a.col_q = col_q;
+    a.col_s = col_s;
+    a.col_ld = a.row_blocks * 128;
+    a.ws = dbias ? static_cast<float *>(workspace) : nullptr;
+    if (a.tiles_c * a.row_blocks > 0x7fffffffll)
+        return fail(FP8DL_ERR_SHAPE, "%lld x %lld is more than 2^31 - 1 tiles", (long long)rows, (long long)cols);
+    const bool pdl = short_call_bytes((double)rows * (double)cols * (x_dtype == FP8DL_BF16 ? 4.0 : 6.0));
+    launch_block_quantize<false>(x_dtype, out_dtype, dim3((unsigned)(a.tiles_c * a.row_blocks)), st, pdl, a);
+    FP8DL_TRY(check_launch("fp8_block_quantize"));
+    if (dbias) {
+        colsum_reduce(a.ws, (rows + 127) / 128, cols, dbias, st, pdl);
+        return check_launch("fp8_block_quantize(dbias reduce)");
+    }
+    return FP8DL_OK;
+}
+
+extern "C" fp8dl_status fp8_block_quantize_weight(const void *w, int32_t w_dtype, int32_t n_mats, int64_t rows,
+                                                  int64_t cols, int32_t out_dtype, uint8_t *q, float *s, uint8_t *q_t,
+                                                  float *s_t, fp8dl_stream_t stream) {
+    FP8DL_NVTX("fp8_block_quantize_weight");
+    FP8DL_CHECK_ARG(w_dtype == FP8DL_F32 || w_dtype == FP8DL_BF16, "w_dtype must be FP8DL_F32 or FP8DL_BF16");
+    FP8DL_CHECK_ARG(out_dtype == FP8DL_E4M3 || out_dtype == FP8DL_E5M2, "out_dtype must be E4M3 or E5M2");
+    FP8DL_CHECK_ARG(n_mats >= 1 && n_mats <= 65535, "n_mats must be in [1, 65535]");
+    FP8DL_CHECK_ARG(w && (q || q_t), "w and one of q and q_t must be non-NULL");
+    FP8DL_CHECK_ARG(!q == !s && !q_t == !s_t, "q/s and q_t/s_t come in pairs");
+    if (!dim_ok(rows, 16) || !dim_ok(cols, 16))
+        return fail(FP8DL_ERR_SHAPE, "rows (%lld) and cols (%lld) must be positive multiples of 16", (long long)rows,
+                    (long long)cols);
+    if (!aligned16(w) || !aligned16(q) || !aligned16(s) || !aligned16(q_t) || !aligned16(s_t))
+        return fail(FP8DL_ERR_ALIGN, "w, q, s, q_t and s_t must be 16-byte aligned");
+    BlockQuantArgs a = {};
+    a.x = w;
+    a.rows = rows;
+    a.cols = cols;
+    a.tiles_c = (cols + 127) / 128;
+    a.row_blocks = (rows + 127) / 128;
+    a.row_q = q;
+    a.row_s = s;
+    a.col_q = q_t;
+    a.col_s = s_t;
+    a.col_ld = rows;
+    if (a.tiles_c * a.row_blocks > 0x7fffffffll)
+        return fail(FP8DL_ERR_SHAPE, "%lld x %lld is more than 2^31 - 1 tiles", (long long)rows, (long long)cols);
+    FP8DL_TRY(current_device(nullptr, nullptr));
+    const bool pdl = short_call_bytes((double)n_mats * (double)rows * (double)cols * (w_dtype == FP8DL_BF16 ? 4.0 : 6.0));
+    launch_block_quantize<true>(w_dtype, out_dtype, dim3((unsigned)(a.tiles_c * a.row_blocks), (unsigned)n_mats),
+                                (cudaStream_t)stream, pdl, a);
+    return check_launch("fp8_block_quantize_weight");
+}

@@ -322,6 +322,108 @@ fp8dl_status mxfp8_gemm(const uint8_t *A, const uint8_t *A_s, const uint8_t *B, 
                         void *D, int32_t d_dtype, int32_t *dev_status, fp8dl_stream_t stream);
 
 /* ----------------------------------------------------------------------------
+ * Block-scaled FP8: one fp32 scale per 128 values, for a linear layer and for
+ * the linear layers of experts (ragged groups of tokens, one weight each).
+ * The scale of a block is the just-in-time form of the per-tensor scale
+ * FP8_MAX / amax of "FP8 低精度训练：Transformer Engine 简析" §三.1, taken over
+ *   1 x 128 blocks of activations and gradients, along the reduction axis of
+ *           the product that reads them, and
+ *   128 x 128 blocks of weights (one scale serves both of their copies).
+ * Per block:  amax = the largest finite |x|;
+ *             scale = fl32(FP8_MAX / max(amax, 2^-100)), or 1 if amax = 0;
+ *             q = enc(fl32(x * scale)); the stored factor is fl32(1 / scale).
+ * Encoding as for the cast (infinities saturate, NaN gives a NaN code).  The
+ * last block of a row or column may be short.
+ *
+ * Scale layouts are block-major: s[b][r] holds the factor of block b of row r,
+ * with rows contiguous (a warp of 32 rows reads 128 consecutive bytes).
+ *
+ * Token dimensions may have any length, also 0 (nothing is written, except
+ * sums over no tokens, which are zeros; the tensors may then be NULL).
+ * Feature dimensions are positive multiples of 16.
+ *
+ * Groups: offsets is a DEVICE array of n_groups + 1 non-decreasing int32 with
+ * offsets[0] >= 0 and offsets[n_groups] <= rows; group g owns rows
+ * offsets[g] .. offsets[g+1]-1, possibly none; 1 <= n_groups <= 1024.  Rows
+ * outside every group are neither read nor written.  The host does not see
+ * the values: the kernels clamp them to the tensor, so wrong offsets give
+ * wrong results but no access out of bounds. */
+
+/* Columns of the transposed codes of fp8_block_quantize: every group is padded
+ * to a multiple of 128, at most floor128(rows + 127 * min(n_groups, rows)) in
+ * all; for n_groups <= 1 the rows rounded up to a multiple of 128. */
+int64_t fp8_block_padded_rows(int64_t rows, int32_t n_groups);
+
+/* Quantise activations or gradients x [rows x cols] (bf16 or fp32) into either
+ * or both of
+ *   row_q [rows x cols], row_s [ceil(cols/128) x rows]: blocks along each row,
+ *         the A operand of the forward and dgrad products;
+ *   col_q [cols x T], col_s [T/128 x cols], T = fp8_block_padded_rows(rows,
+ *         n_groups): blocks along each column, transposed, the operands of the
+ *         wgrad product.  Group g's rows take the next ceil128(length) columns;
+ *         its padding columns are zero codes.  Columns beyond the last group's
+ *         are not written.
+ * offsets/n_groups: NULL and 0 for the whole matrix.
+ * dbias [cols] fp32 receives the column sums of x (fixed order), or NULL; only
+ * without offsets; workspace of fp8_cast_workspace_size(rows, cols) bytes. */
+fp8dl_status fp8_block_quantize(const void *x, int32_t x_dtype, int64_t rows, int64_t cols,
+                                const int32_t *offsets, int32_t n_groups, int32_t out_dtype,
+                                uint8_t *row_q, float *row_s, uint8_t *col_q, float *col_s,
+                                float *dbias, void *workspace, size_t workspace_bytes,
+                                fp8dl_stream_t stream);
+
+/* Quantise n_mats weights w [n_mats x rows x cols] (bf16 or fp32) in 128 x 128
+ * blocks into either or both of
+ *   q   [n_mats x rows x cols], s   [n_mats x ceil(cols/128) x ceil(rows/128)]
+ *   q_t [n_mats x cols x rows], s_t [n_mats x ceil(rows/128) x ceil(cols/128)]
+ * q/s is the B operand of the forward product, q_t/s_t that of dgrad; q_t is
+ * q transposed, code by code.  1 <= n_mats <= 65535. */
+fp8dl_status fp8_block_quantize_weight(const void *w, int32_t w_dtype, int32_t n_mats, int64_t rows,
+                                       int64_t cols, int32_t out_dtype, uint8_t *q, float *s, uint8_t *q_t,
+                                       float *s_t, fp8dl_stream_t stream);
+
+/* Block-scaled FP8 GEMM:
+ *   D[m,n] = round_d( sum_b fl32(a_s[b][m] * b_s[b][n / b_rows]) * sum_{k in block b} A[m,k] * B[n,k]
+ *                     + bias[n] )
+ * Each block's 128 products are summed on the tcgen05 tensor cores in fp32;
+ * the sum over blocks is an fp32 fused multiply-add per block, in ascending
+ * order of b within each of the (1, 2, 4 or 8) contiguous parts that K may be
+ * split into for a product with few rows; the parts are added in order.
+ * Repeated calls give the same bits.
+ *   A [M x K] codes of a_dtype, a_s [ceil(K/128) x M]
+ *   B [N x K] codes of b_dtype, b_s [ceil(K/128) x ceil(N/b_rows)],
+ *     b_rows = 128 (a weight) or 1 (an activation or gradient)
+ *   bias [N] of bias_dtype, or NULL; D [M x N] of d_dtype; dev_status as for
+ *   fp8_gemm.  M >= 0; N and K positive multiples of 16. */
+fp8dl_status fp8_block_gemm(const uint8_t *A, int32_t a_dtype, const float *a_s, const uint8_t *B,
+                            int32_t b_dtype, const float *b_s, int32_t b_rows, int64_t M, int64_t N,
+                            int64_t K, const void *bias, int32_t bias_dtype, void *D, int32_t d_dtype,
+                            int32_t *dev_status, fp8dl_stream_t stream);
+
+/* The products of ragged groups of rows with their group's weight (the expert
+ * layers' forward product with q/s of the weights, dgrad with q_t/s_t):
+ *   D[m,:] = A[m,:] * B[g]^T for the rows m of group g, summed as above
+ *   A [M x K], a_s [ceil(K/128) x M]; B [n_groups x N x K],
+ *   b_s [n_groups x ceil(K/128) x ceil(N/128)]; D [M x N]. */
+fp8dl_status fp8_block_gemm_grouped(const uint8_t *A, int32_t a_dtype, const float *a_s, const uint8_t *B,
+                                    int32_t b_dtype, const float *b_s, const int32_t *offsets,
+                                    int32_t n_groups, int64_t M, int64_t N, int64_t K, void *D,
+                                    int32_t d_dtype, int32_t *dev_status, fp8dl_stream_t stream);
+
+/* The weight gradients of the groups (a ragged reduction over their tokens):
+ *   D[g,m,n] = sum over group g's token blocks b of
+ *              fl32(a_s[b][m] * b_s[b][n]) * sum_{t in block b} A[m,t] * B[n,t]
+ *   A [M x T] with a_s [T/128 x M] and B [N x T] with b_s [T/128 x N]: col_q
+ *   and col_s of fp8_block_quantize with the same offsets (A of grad_output,
+ *   B of the input), T its padded length, a multiple of 128 (0 if there are no
+ *   rows); D [n_groups x M x N]; a group without rows gets zeros.  M >= 1;
+ *   N a positive multiple of 16. */
+fp8dl_status fp8_block_gemm_grouped_wgrad(const uint8_t *A, int32_t a_dtype, const float *a_s, const uint8_t *B,
+                                          int32_t b_dtype, const float *b_s, const int32_t *offsets,
+                                          int32_t n_groups, int64_t M, int64_t N, int64_t T, void *D,
+                                          int32_t d_dtype, int32_t *dev_status, fp8dl_stream_t stream);
+
+/* ----------------------------------------------------------------------------
  * LayerNormMLP pieces.  The Transformer Engine tutorial builds its blocks
  * from te.LayerNormMLP (LayerNorm -> fc1 -> GELU -> fc2), mirrored in plain
  * PyTorch by nn.LayerNorm and nn.GELU (erf form).  Under delayed scaling the
