@@ -31,40 +31,52 @@ struct BlockGemmArgs {
     int d_dtype;
     int32_t *status;
     uint32_t idesc;
-    int raster_n;
-    int64_t group;
+    int along_n;     // tile order: bands along the columns (1) or rows (0) of D
+    uint32_t band;
 };
 
-// The groups' tables in shared memory: first[g], end[g] = the group's rows; pre[g] = units
-// (row tiles, or token blocks) of the groups before g.
+// The groups' tables in shared memory: off = the offsets clamped to the tensor, in order
+// (group g owns rows off[g] .. off[g+1]-1); pre[g] = units (row tiles, or token blocks) of
+// the groups before g.
 struct GroupTables {
-    int32_t *first, *end, *pre;
+    int32_t *off, *pre;
 };
-constexpr int kGroupTableBytes = 3 * 4 * (kMaxGroups + 4);
+constexpr int kGroupTableBytes = 2 * 4 * (kMaxGroups + 4);
 
 __device__ __forceinline__ GroupTables group_tables(uint8_t *smem) {
     int32_t *p = reinterpret_cast<int32_t *>(smem);
-    return {p, p + kMaxGroups + 4, p + 2 * (kMaxGroups + 4)};
+    return {p, p + kMaxGroups + 4};
 }
 
 // All threads of the block; `limit` caps the running sum (a reduction never reads past T).
 __device__ __forceinline__ void build_groups(const GroupTables &t, const int32_t *offsets, int n_groups, int64_t rows,
                                              int unit, int64_t limit) {
-    for (int g = threadIdx.x; g < n_groups; g += blockDim.x) {
-        int64_t first, end;
-        group_rows(offsets, g, rows, first, end);
-        t.first[g] = (int32_t)first;
-        t.end[g] = (int32_t)end;
-    }
-    __syncthreads();
     if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
         int64_t before = 0;
-        if (threadIdx.x == 0) t.pre[0] = 0;
+        int32_t from = 0;  // the running maximum: disordered offsets make empty groups, not overlaps
+        if (lane == 0) {
+            t.off[0] = from = (int32_t)min(max((int64_t)offsets[0], (int64_t)0), rows);
+            t.pre[0] = 0;
+        }
+        from = __shfl_sync(0xffffffffu, from, 0);
         for (int g0 = 0; g0 < n_groups; g0 += 32) {
-            const int g = g0 + threadIdx.x;
-            const int64_t n = g < n_groups ? ((int64_t)t.end[g] - t.first[g] + unit - 1) / unit : 0;
-            const int64_t sum = min(before + warp_inclusive_sum(n, threadIdx.x), limit);
-            if (g < n_groups) t.pre[g + 1] = (int32_t)sum;
+            const int g = g0 + lane;
+            int32_t end = g < n_groups ? (int32_t)min(max((int64_t)offsets[g + 1], (int64_t)0), rows) : 0;
+            end = max(end, from);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int32_t u = __shfl_up_sync(0xffffffffu, end, o);
+                if (lane >= o) end = max(end, u);
+            }
+            int32_t first = __shfl_up_sync(0xffffffffu, end, 1);
+            if (lane == 0) first = from;
+            const int64_t sum = min(before + warp_inclusive_sum(((int64_t)end - first + unit - 1) / unit, lane), limit);
+            if (g < n_groups) {
+                t.off[g + 1] = end;
+                t.pre[g + 1] = (int32_t)sum;
+            }
+            from = __shfl_sync(0xffffffffu, end, 31);
             before = __shfl_sync(0xffffffffu, sum, 31);
         }
     }
@@ -72,11 +84,11 @@ __device__ __forceinline__ void build_groups(const GroupTables &t, const int32_t
 }
 
 // The group that holds unit u: pre[g] <= u < pre[g + 1].
-__device__ __forceinline__ int find_group(const GroupTables &t, int n_groups, int64_t u) {
+__device__ __forceinline__ int find_group(const GroupTables &t, int n_groups, uint32_t u) {
     int lo = 0, hi = n_groups;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (t.pre[mid] <= u)
+        if ((uint32_t)t.pre[mid] <= u)
             lo = mid;
         else
             hi = mid;
@@ -85,164 +97,229 @@ __device__ __forceinline__ int find_group(const GroupTables &t, int n_groups, in
 }
 
 // Tiles in bands of `band` tiles along one dimension, which varies fastest inside a band: the
-// tiles in flight form a block whose operand panels are shared through L2.
-__device__ __forceinline__ void band_order(int64_t tile, int64_t tiles_m, int64_t tiles_n, int along_n, int64_t band,
-                                           int64_t &tm, int64_t &tn) {
-    const int64_t inner = along_n ? tiles_n : tiles_m, outer = along_n ? tiles_m : tiles_n;
-    const int64_t first = tile / (band * outer) * band;
-    const int64_t width = min(band, inner - first), r = tile - first * outer;
-    const int64_t i = first + r % width, o = r / width;
+// tiles in flight form a block whose operand panels are shared through L2.  32-bit arithmetic
+// (the host checks the tile count): a 64-bit division is a long subroutine, and every role of
+// the kernel decodes every tile.
+__device__ __forceinline__ void band_order(uint32_t tile, uint32_t tiles_m, uint32_t tiles_n, int along_n, uint32_t band,
+                                           uint32_t &tm, uint32_t &tn) {
+    const uint32_t inner = along_n ? tiles_n : tiles_m, outer = along_n ? tiles_m : tiles_n;
+    band = min(band, inner);
+    const uint32_t first = tile / (band * outer) * band;
+    const uint32_t width = min(band, inner - first), r = tile - first * outer;
+    const uint32_t o = r / width, i = first + r - o * width;
     tm = along_n ? o : i;
     tn = along_n ? i : o;
 }
 
 // One tile's work.
 struct BlockTile {
-    int64_t a_row, a_end;  // rows of A (and of D, but for BG_REDUCE) from a_row, valid below a_end
+    int64_t a_row, a_end;  // first row of A, and the end of the rows that are the tile's to write
     int64_t n0;            // first column of D
     int64_t b_row;         // its row of B
     int kb0, kbs;          // reduction blocks
     const float *b_s;      // factors of B of the tile's matrix
-    int64_t d_row0;        // added to A's row for D's row (BG_REDUCE)
+    int64_t d_row;         // a_row's row of D (BG_REDUCE: within all groups' matrices)
 };
 
 template <int TM, int TN>
-__device__ __forceinline__ int64_t block_tiles(const BlockGemmArgs &a, const GroupTables &t) {
-    const int64_t tiles_n = (a.N + TN - 1) / TN, tiles_m = (a.M + TM - 1) / TM;
+__device__ __forceinline__ uint32_t block_tiles(const BlockGemmArgs &a, const GroupTables &t) {
+    const uint32_t tiles_n = (uint32_t)((a.N + TN - 1) / TN), tiles_m = (uint32_t)((a.M + TM - 1) / TM);
     if (a.kind == BG_DENSE) return tiles_m * tiles_n;
-    if (a.kind == BG_ROWS) return (int64_t)t.pre[a.n_groups] * tiles_n;
-    return a.n_groups * tiles_m * tiles_n;
+    if (a.kind == BG_ROWS) return (uint32_t)t.pre[a.n_groups] * tiles_n;
+    return (uint32_t)a.n_groups * tiles_m * tiles_n;
+}
+
+// Reduction blocks of a tile.
+template <int TM, int TN>
+__device__ __forceinline__ int block_tile_kbs(const BlockGemmArgs &a, const GroupTables &t, uint32_t tile) {
+    if (a.kind != BG_REDUCE) return (int)((a.K + 127) / 128);
+    const uint32_t per = (uint32_t)((a.N + TN - 1) / TN) * (uint32_t)((a.M + TM - 1) / TM);
+    const uint32_t g = tile / per;
+    return t.pre[g + 1] - t.pre[g];
 }
 
 template <int TM, int TN>
-__device__ __forceinline__ BlockTile block_tile(const BlockGemmArgs &a, const GroupTables &t, int64_t tile) {
-    const int64_t tiles_n = (a.N + TN - 1) / TN;
+__device__ __forceinline__ BlockTile block_tile(const BlockGemmArgs &a, const GroupTables &t, uint32_t tile) {
+    const uint32_t tiles_n = (uint32_t)((a.N + TN - 1) / TN), tiles_m = (uint32_t)((a.M + TM - 1) / TM);
     BlockTile w;
-    int64_t tm, tn;
+    uint32_t tm, tn;
     const int kbs = (int)((a.K + 127) / 128);
     w.kb0 = 0;
     w.kbs = kbs;
     w.b_s = a.b_s;
-    w.d_row0 = 0;
     if (a.kind == BG_DENSE) {
-        band_order(tile, (a.M + TM - 1) / TM, tiles_n, a.raster_n, a.group, tm, tn);
-        w.a_row = tm * TM;
+        band_order(tile, tiles_m, tiles_n, a.along_n, a.band, tm, tn);
+        w.a_row = w.d_row = (int64_t)tm * TM;
         w.a_end = a.M;
-        w.n0 = w.b_row = tn * TN;
+        w.n0 = w.b_row = (int64_t)tn * TN;
     } else if (a.kind == BG_ROWS) {
         const int g = find_group(t, a.n_groups, tile / tiles_n);
-        band_order(tile - t.pre[g] * tiles_n, t.pre[g + 1] - t.pre[g], tiles_n, a.raster_n, a.group, tm, tn);
-        w.a_row = t.first[g] + tm * TM;
-        w.a_end = t.end[g];
-        w.n0 = tn * TN;
+        band_order(tile - t.pre[g] * tiles_n, t.pre[g + 1] - t.pre[g], tiles_n, a.along_n, a.band, tm, tn);
+        w.a_row = w.d_row = t.off[g] + (int64_t)tm * TM;
+        w.a_end = t.off[g + 1];
+        w.n0 = (int64_t)tn * TN;
         w.b_row = g * a.N + w.n0;
         w.b_s = a.b_s + (int64_t)g * kbs * a.b_ld;
     } else {
-        const int64_t tiles_m = (a.M + TM - 1) / TM;
-        const int64_t g = tile / (tiles_m * tiles_n);
-        band_order(tile - g * tiles_m * tiles_n, tiles_m, tiles_n, a.raster_n, a.group, tm, tn);
-        w.a_row = tm * TM;
+        const uint32_t g = tile / (tiles_m * tiles_n);
+        band_order(tile - g * tiles_m * tiles_n, tiles_m, tiles_n, a.along_n, a.band, tm, tn);
+        w.a_row = (int64_t)tm * TM;
         w.a_end = a.M;
-        w.n0 = w.b_row = tn * TN;
+        w.d_row = g * a.M + w.a_row;
+        w.n0 = w.b_row = (int64_t)tn * TN;
         w.kb0 = t.pre[g];
         w.kbs = t.pre[g + 1] - t.pre[g];
-        w.d_row0 = g * a.M;
     }
     return w;
 }
 
-// 32 consecutive columns n0 .. n0+31 of one row of D (bias added, rounded once).
-__device__ __forceinline__ void store_row32(const BlockGemmArgs &a, int64_t row, int64_t n0, const float2 *v) {
-    if (n0 >= a.N) return;
-    float y[32];
-#pragma unroll
-    for (int p = 0; p < 16; p++) y[2 * p] = v[p].x, y[2 * p + 1] = v[p].y;
+// 4- and 16-byte copies from global to shared memory.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// One arrival on an mbarrier of this CTA when the thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Columns c0 .. c0 + 31 of this thread's sums, bias added (n = their first column of D).
+__device__ __forceinline__ void add_bias32(const BlockGemmArgs &a, int64_t n, float2 (&v)[16]) {
     if (a.bias_dtype == FP8DL_BF16) {
-        const __nv_bfloat16 *b = static_cast<const __nv_bfloat16 *>(a.bias) + n0;
+        const __nv_bfloat16 *b = static_cast<const __nv_bfloat16 *>(a.bias) + n;
 #pragma unroll
         for (int g = 0; g < 4; g++)
-            if (n0 + 8 * g < a.N) {
+            if (n + 8 * g < a.N) {
                 const uint4 u = __ldg(reinterpret_cast<const uint4 *>(b + 8 * g));
                 const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                for (int q = 0; q < 4; q++) y[8 * g + 2 * q] += bf16_lo(w[q]), y[8 * g + 2 * q + 1] += bf16_hi(w[q]);
+                for (int q = 0; q < 4; q++)
+                    v[4 * g + q] = __fadd2_rn(v[4 * g + q], make_float2(bf16_lo(w[q]), bf16_hi(w[q])));
             }
     } else if (a.bias_dtype == FP8DL_F32) {
-        const float *b = static_cast<const float *>(a.bias) + n0;
+        const float *b = static_cast<const float *>(a.bias) + n;
 #pragma unroll
         for (int g = 0; g < 8; g++)
-            if (n0 + 4 * g < a.N) {
+            if (n + 4 * g < a.N) {
                 const float4 u = __ldg(reinterpret_cast<const float4 *>(b + 4 * g));
-                y[4 * g] += u.x, y[4 * g + 1] += u.y, y[4 * g + 2] += u.z, y[4 * g + 3] += u.w;
+                v[2 * g] = __fadd2_rn(v[2 * g], make_float2(u.x, u.y));
+                v[2 * g + 1] = __fadd2_rn(v[2 * g + 1], make_float2(u.z, u.w));
             }
     }
-    if (a.d_dtype == FP8DL_BF16) {
-        uint32_t w[16];
+}
+
+// One warp writes its 32 rows x 128 columns of D (lane = row; the sums in acc), rounded once.
+// Straight from the registers every store would touch 32 rows, a piece of a line each (the
+// stores of a 256 x 256 tile took 7200 cycles, a fifth of a tile with K = 4096).  Instead 64
+// bytes of each row at a time go through shared memory (16-byte chunks XOR-swizzled by row
+// pairs: conflict-free both ways) and leave as two whole sectors, eight rows per instruction.
+__device__ __forceinline__ void store_tile(const BlockGemmArgs &a, uint8_t *stage, int lane, int64_t d_row, int rows,
+                                           int64_t n0, float2 (&acc)[64]) {
+    const bool bf = a.d_dtype == FP8DL_BF16;
+    const int esz = bf ? 2 : 4;
+    const int sub = lane >> 2, ch = lane & 3;
+    uint8_t *base = static_cast<uint8_t *>(a.D) + ((d_row + sub) * a.N + n0) * esz + ch * 16;
+    const int64_t step = 8 * a.N * esz;
+    uint8_t *mine = stage + lane * 64;
+    const int swz = (lane >> 1) & 3, rswz = (sub >> 1) & 3;
+    auto flush = [&](int off, int64_t n) {  // the staged 64 bytes of each row, from column n on
+        __syncwarp();
+        const bool ok = n + ch * (16 / esz) < a.N;
 #pragma unroll
-        for (int p = 0; p < 16; p++) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * p], y[2 * p + 1]);
-            w[p] = *reinterpret_cast<const uint32_t *>(&h);
+        for (int i = 0; i < 4; i++) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(stage + (8 * i + sub) * 64 + ((ch ^ rswz) << 4));
+            if (ok && 8 * i + sub < rows) *reinterpret_cast<uint4 *>(base + i * step + off) = u;
         }
-        __nv_bfloat16 *d = static_cast<__nv_bfloat16 *>(a.D) + row * a.N + n0;
+        __syncwarp();
+    };
 #pragma unroll
-        for (int h = 0; h < 2; h++) {  // sixteen columns at a time (N is a multiple of 16)
-            if (n0 + 16 * h >= a.N) break;
-            *reinterpret_cast<uint4 *>(d + 16 * h) = make_uint4(w[8 * h], w[8 * h + 1], w[8 * h + 2], w[8 * h + 3]);
-            *reinterpret_cast<uint4 *>(d + 16 * h + 8) = make_uint4(w[8 * h + 4], w[8 * h + 5], w[8 * h + 6], w[8 * h + 7]);
+    for (int c = 0; c < 4; c++) {
+        const int64_t n = n0 + 32 * c;
+        if (n >= a.N) break;
+        float2 v[16];
+#pragma unroll
+        for (int p = 0; p < 16; p++) v[p] = acc[16 * c + p];
+        if (a.bias_dtype >= 0) add_bias32(a, n, v);
+        if (bf) {
+#pragma unroll
+            for (int g = 0; g < 4; g++) {
+                uint32_t w[4];
+#pragma unroll
+                for (int q = 0; q < 4; q++) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(v[4 * g + q].x, v[4 * g + q].y);
+                    w[q] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+                *reinterpret_cast<uint4 *>(mine + ((g ^ swz) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            flush(64 * c, n);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+#pragma unroll
+                for (int g = 0; g < 4; g++)
+                    *reinterpret_cast<float4 *>(mine + ((g ^ swz) << 4)) =
+                        make_float4(v[8 * h + 2 * g].x, v[8 * h + 2 * g].y, v[8 * h + 2 * g + 1].x, v[8 * h + 2 * g + 1].y);
+                flush(128 * c + 64 * h, n + 16 * h);
+            }
         }
-    } else {
-        float *d = static_cast<float *>(a.D) + row * a.N + n0;
-#pragma unroll
-        for (int g = 0; g < 8; g++)
-            if (n0 + 4 * g < a.N)
-                *reinterpret_cast<float4 *>(d + 4 * g) = make_float4(y[4 * g], y[4 * g + 1], y[4 * g + 2], y[4 * g + 3]);
     }
 }
 
 // ---------------------------------------------------------------------------
-// 256 x 256 tiles on CTA pairs.
-//   warp 0      TMA producer: 128 rows of A and 128 of B per CTA and k-block, six stages
-//   warp 1      the leader's MMA thread: per block four MMAs (M 256, N 256, K 32) into one
-//               of two 256-column tensor-memory buffers
+// 128 x 256 tiles, one persistent CTA per SM.
+//   warp 0      TMA producer: 128 rows of A and 256 of B per k-block, four stages
+//   warp 1      MMA thread: per block four MMAs (M 128, N 256, K 32) into one of two
+//               256-column tensor-memory buffers
+//   warp 2      copies the blocks' factors into a shared-memory ring
 //   warps 4-11  epilogue: warp w drains lane quarter w & 3 of column half (w - 4) / 4; a thread
 //               holds one row x 128 columns of the sum (64 fp32 pairs)
 // With 128 x 128 weight factors a thread's 128 columns share one factor per block: one
 // packed multiply-add per two values, half the MMAs' time on the FP32 pipe.  With factors per
 // row of B (BROWS, weight gradients) each column has its own: one more packed multiply.
+//
+// Why not CTA pairs (256 x 256 tiles): every block's buffer goes to the epilogue and back
+// through mbarriers, and between two SMs that costs more than the pair saves in operand
+// traffic: PAIRFIG.
 // ---------------------------------------------------------------------------
 namespace bp {
-constexpr int TM = 256, TN = 256, BK = 128, STAGES = 6;
-constexpr int A_BYTES = 128 * BK, B_BYTES = 128 * BK, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int TM = 128, TN = 256, BK = 128, STAGES = 4;
+constexpr int A_BYTES = TM * BK, B_BYTES = TN * BK, STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int THREADS = 384, EPI_WARPS = 8;
-constexpr int REGS_LAUNCH = 168, REGS_IO = 40, REGS_EPI = 232;  // 128 * 40 + 256 * 232 = 384 * 168
+constexpr int REGS_LAUNCH = 168, REGS_IO = 56, REGS_EPI = 224;  // 128 * 56 + 256 * 224 = 384 * 168
 static_assert(128 * REGS_IO + 256 * REGS_EPI <= THREADS * REGS_LAUNCH, "register split");
 constexpr int TMEM_COLS = 512;
-constexpr int CS_BYTES = EPI_WARPS * 2 * 128 * 4;  // column factors, double-buffered per warp
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + CS_BYTES + kGroupTableBytes + 1024;
+// The factors of the next blocks: 128 of A's, then one per column half, or (BROWS) 256, of B's.
+constexpr int RING = 4, SLOT_FLOATS = 128 + 256, RING_BYTES = RING * SLOT_FLOATS * 4;
+constexpr int OUT_BYTES = EPI_WARPS * 2048;        // 32 rows x 64 bytes of D per warp
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + OUT_BYTES + 1024 + RING_BYTES + kGroupTableBytes + 1024;
+static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 }  // namespace bp
 
 template <bool BROWS>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(bp::THREADS, 1)
-    block_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
-                           const BlockGemmArgs args) {
+__global__ void __launch_bounds__(bp::THREADS, 1)
+    block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+                      const BlockGemmArgs args) {
     using namespace bp;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
-    uint8_t *bar_area = smem + STAGES * STAGE_BYTES;
+    uint8_t *out_stage = smem + STAGES * STAGE_BYTES;
+    uint8_t *bar_area = out_stage + OUT_BYTES;
     uint64_t *full = reinterpret_cast<uint64_t *>(bar_area);
     uint64_t *empty = full + STAGES;
     uint64_t *tfull = empty + STAGES;
     uint64_t *tempty = tfull + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tempty + 2);
+    uint64_t *ffull = tempty + 2;
+    uint64_t *fempty = ffull + RING;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(fempty + RING);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    float *cs_all = reinterpret_cast<float *>(bar_area + 1024);
-    const GroupTables tab = group_tables(bar_area + 1024 + CS_BYTES);
+    float *ring = reinterpret_cast<float *>(bar_area + 1024);
+    const GroupTables tab = group_tables(bar_area + 1024 + RING_BYTES);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
-    const bool leader = rank == 0;
-    const int64_t pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; s++) {
@@ -251,7 +328,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(bp::THREADS, 1)
         }
         for (int a = 0; a < 2; a++) {
             mbar_init(smem_u32(&tfull[a]), 1);
-            mbar_init(smem_u32(&tempty[a]), 2 * EPI_WARPS);
+            mbar_init(smem_u32(&tempty[a]), EPI_WARPS);
+        }
+        for (int a = 0; a < RING; a++) {
+            mbar_init(smem_u32(&ffull[a]), 32);  // every lane of the copying warp
+            mbar_init(smem_u32(&fempty[a]), EPI_WARPS);
         }
         *abort_flag = 0;
         mbar_fence_init();
@@ -259,12 +340,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(bp::THREADS, 1)
         tma_prefetch_map(&tmap_b);
     }
     if (warp == 1) {
-        tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
-        tmem_relinquish_pair();
+        tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+        tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();  // both CTAs' barriers initialised before any cross-CTA signal
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     pdl_wait();
@@ -272,29 +352,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(bp::THREADS, 1)
     if (args.kind == BG_ROWS) build_groups(tab, args.offsets, args.n_groups, args.M, TM, 0x7fffffffll);
     if (args.kind == BG_REDUCE)
         build_groups(tab, args.offsets, args.n_groups, 0x7fffffffll, 128, args.K / 128);
-    const int64_t tiles = block_tiles<TM, TN>(args, tab);
+    const uint32_t tiles = block_tiles<TM, TN>(args, tab);
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_IO));
-        if (warp == 0 && lane == 0) {  // ------------------------------------- producer (both CTAs)
+        if (warp == 0 && lane == 0) {  // ------------------------------------- producer
             int s = 0;
             uint32_t ph = 0;
             int64_t issued = 0;
             bool ok = true;
-            for (int64_t tile = pair; tile < tiles && ok; tile += npairs) {
+            for (uint32_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
                 const BlockTile w = block_tile<TM, TN>(args, tab, tile);
-                const int32_t ra = (int32_t)(w.a_row + rank * 128), rb = (int32_t)(w.b_row + rank * 128);
                 for (int kb = 0; kb < w.kbs; kb++) {
                     if (!mbar_wait(smem_u32(&empty[s]), ph ^ 1, abort_flag, args.status)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t fb_local = smem_u32(&full[s]);
-                    const uint32_t fb = mapa_shared(fb_local, 0);
-                    if (leader) mbar_expect_tx(fb_local, 2 * STAGE_BYTES);
-                    const uint32_t sa = smem_u32(smem + s * STAGE_BYTES);
-                    tma_load_2d_pair(sa, &tmap_a, fb, (w.kb0 + kb) * BK, ra);
-                    tma_load_2d_pair(sa + A_BYTES, &tmap_b, fb, (w.kb0 + kb) * BK, rb);
+                    const uint32_t fb = smem_u32(&full[s]), sa = smem_u32(smem + s * STAGE_BYTES);
+                    mbar_expect_tx(fb, STAGE_BYTES);
+                    tma_load_2d(sa, &tmap_a, fb, (w.kb0 + kb) * BK, (int32_t)w.a_row);
+                    tma_load_2d(sa + A_BYTES, &tmap_b, fb, (w.kb0 + kb) * BK, (int32_t)w.b_row);
                     issued++;
                     if (++s == STAGES) {
                         s = 0;
@@ -302,17 +379,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(bp::THREADS, 1)
                     }
                 }
             }
-            if (!ok && leader)
+            if (!ok)
                 for (int64_t i = issued - 1; i >= 0 && i >= issued - STAGES; i--)
                     mbar_drain(smem_u32(&full[i % STAGES]), (uint32_t)((i / STAGES) & 1));
-        } else if (warp == 1 && lane == 0 && leader) {  // --------------------- MMA issuer (leader only)
+        } else if (warp == 1 && lane == 0) {  // ------------------------------- MMA issuer
             int s = 0, buf = 0;
             uint32_t ph = 0, bph = 0;
             bool ok = true, any = false;
             uint32_t last_bar = 0, last_par = 0;
             const SDesc desc0 = sdesc_k_sw128_split(smem_u32(smem));
-            for (int64_t tile = pair; tile < tiles && ok; tile += npairs) {
-                const int kbs = block_tile<TM, TN>(args, tab, tile).kbs;
+            for (uint32_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+                const int kbs = block_tile_kbs<TM, TN>(args, tab, tile);
                 for (int kb = 0; kb < kbs; kb++) {
                     if (!mbar_wait(smem_u32(&tempty[buf]), bph ^ 1, abort_flag, args.status) ||
                         !mbar_wait(smem_u32(&full[s]), ph, abort_flag, args.status)) {
@@ -324,10 +401,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(bp::THREADS, 1)
                     const uint32_t lo_b = lo_a + (A_BYTES >> 4);
 #pragma unroll
                     for (int kk = 0; kk < BK / 32; kk++)
-                        umma_f8f6f4_pair(tmem_base + (uint32_t)(buf * TN), sdesc_join(lo_a + 2 * kk, desc0.hi),
-                                         sdesc_join(lo_b + 2 * kk, desc0.hi), args.idesc, kk != 0);
-                    umma_commit_pair(smem_u32(&tfull[buf]), 0x3);
-                    umma_commit_pair(smem_u32(&empty[s]), 0x3);
+                        umma_f8f6f4(tmem_base + (uint32_t)(buf * TN), sdesc_join(lo_a + 2 * kk, desc0.hi),
+                                    sdesc_join(lo_b + 2 * kk, desc0.hi), args.idesc, kk != 0);
+                    umma_commit(smem_u32(&tfull[buf]));
+                    umma_commit(smem_u32(&empty[s]));
                     any = true;
                     last_bar = smem_u32(&empty[s]);
                     last_par = ph;
@@ -340,45 +417,87 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(bp::THREADS, 1)
                 }
             }
             if (!ok && any) mbar_drain(last_bar, last_par);
+        } else if (warp == 2) {  // --------------------------------------------- factors
+            // Rows and columns outside the matrix take a valid address: their sums are not stored.
+            int slot = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (uint32_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+                const BlockTile w = block_tile<TM, TN>(args, tab, tile);
+                const float *pa[4], *pb[2];
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const int64_t row = w.a_row + 32 * j + lane;
+                    pa[j] = args.a_s + (int64_t)w.kb0 * args.M + (row < w.a_end ? row : w.a_row);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; h++) {  // BROWS: four columns of each half per lane
+                    const int64_t n = w.n0 + 128 * h + (BROWS ? 4 * lane : 0);
+                    pb[h] = w.b_s + (int64_t)w.kb0 * args.b_ld + (n < args.N ? (BROWS ? n : n >> 7) : 0);
+                }
+                for (int kb = 0; kb < w.kbs; kb++) {
+                    if (!mbar_wait(smem_u32(&fempty[slot]), ph ^ 1, abort_flag, args.status)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t dst = smem_u32(ring + slot * SLOT_FLOATS);
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        cp_async4(dst + 4 * (32 * j + lane), pa[j]);
+                        pa[j] += args.M;
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        if (BROWS)
+                            cp_async16(dst + 512 + 512 * h + 16 * lane, pb[h]);
+                        else if (lane == 0)
+                            cp_async4(dst + 512 + 512 * h, pb[h]);
+                        pb[h] += args.b_ld;
+                    }
+                    cp_async_arrive(smem_u32(&ffull[slot]));
+                    if (++slot == RING) {
+                        slot = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            cp_async_wait_all();
         }
-    } else {  // ------------------------------------------------------------ epilogue (both CTAs)
+    } else {  // ------------------------------------------------------------ epilogue
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EPI));
         const int q = warp & 3, half = (warp - 4) >> 2;
         const uint32_t taddr0 = tmem_base + (uint32_t)(128 * half) + ((uint32_t)(32 * q) << 16);
-        const uint32_t tempty_leader[2] = {mapa_shared(smem_u32(&tempty[0]), 0), mapa_shared(smem_u32(&tempty[1]), 0)};
-        float *cs = cs_all + (warp - 4) * 256;
+        uint8_t *stage = out_stage + (warp - 4) * 2048;
+        const float *my_a = ring + 32 * q + lane, *my_b = ring + 128 + 128 * half;
+        int slot = 0;
+        uint32_t fph = 0;
+        // The next block's factors are there (they were copied blocks ago).
+        auto wait_factors = [&] { return mbar_wait(smem_u32(&ffull[slot]), fph, abort_flag, args.status); };
+        auto free_factors = [&] {  // this warp has read them
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&fempty[slot]));
+            if (++slot == RING) {
+                slot = 0;
+                fph ^= 1;
+            }
+        };
         int buf = 0;
         uint32_t bph = 0;
-        bool ok = true;
-        for (int64_t tile = pair; tile < tiles && ok; tile += npairs) {
-            const BlockTile w = block_tile<TM, TN>(args, tab, tile);
-            const int64_t row = w.a_row + rank * 128 + 32 * q + lane;
-            const bool row_ok = row < w.a_end;
-            const int64_t n0 = w.n0 + 128 * half;
-            // factors of block kb: the row's, and the column half's (or, BROWS, the lane's four columns')
-            const float *pa = args.a_s + (int64_t)w.kb0 * args.M + (row_ok ? row : 0);
-            const float *pb = BROWS ? w.b_s + (int64_t)w.kb0 * args.b_ld + n0 + 4 * lane : w.b_s + n0 / 128;
-            const bool b_ok = BROWS ? n0 + 4 * lane < args.N : n0 < args.N;
-            auto load_a = [&](int kb) { return row_ok && kb < w.kbs ? __ldg(pa + kb * args.M) : 0.0f; };
-            auto load_b = [&](int kb) -> float4 {
-                if (!b_ok || kb >= w.kbs) return make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (BROWS) return __ldg(reinterpret_cast<const float4 *>(pb + kb * args.b_ld));
-                return make_float4(__ldg(pb + kb * args.b_ld), 0.0f, 0.0f, 0.0f);
-            };
+        for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+            const int kbs = block_tile_kbs<TM, TN>(args, tab, tile);
             float2 acc[64];
 #pragma unroll
             for (int p = 0; p < 64; p++) acc[p] = make_float2(0.0f, 0.0f);
-            float sa0 = load_a(0), sa1 = load_a(1);
-            float4 sb0 = load_b(0), sb1 = load_b(1);
-            for (int kb = 0; kb < w.kbs; kb++) {
-                const float sa2 = load_a(kb + 2);
-                const float4 sb2 = load_b(kb + 2);
-                float *csb = cs + (kb & 1) * 128;
-                if (BROWS) {
-                    *reinterpret_cast<float4 *>(csb + 4 * lane) = sb0;
-                    __syncwarp();
+            bool ok = true;
+            for (int kb = 0; kb < kbs; kb++) {
+                if (!wait_factors()) {
+                    ok = false;
+                    break;
                 }
-                const float2 sc = f2(BROWS ? sa0 : __fmul_rn(sa0, sb0.x));
+                const float *fb = my_b + slot * SLOT_FLOATS;
+                const float fa = my_a[slot * SLOT_FLOATS];
+                const float2 sc = f2(BROWS ? fa : __fmul_rn(fa, fb[0]));
+                if (!BROWS) free_factors();
                 if (!mbar_wait(smem_u32(&tfull[buf]), bph, abort_flag, args.status)) {
                     ok = false;
                     break;
@@ -395,34 +514,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(bp::THREADS, 1)
                     } else {  // the buffer is read: the next block's MMAs may overwrite it
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(tempty_leader[buf]);
+                        if (lane == 0) mbar_arrive(smem_u32(&tempty[buf]));
                     }
 #pragma unroll
-                    for (int p = 0; p < 16; p++) {
-                        const float2 t = make_float2(__uint_as_float(r[c & 1][2 * p]), __uint_as_float(r[c & 1][2 * p + 1]));
-                        const float2 f = BROWS ? __fmul2_rn(sc, *reinterpret_cast<const float2 *>(csb + 32 * c + 2 * p)) : sc;
-                        acc[16 * c + p] = __ffma2_rn(t, f, acc[16 * c + p]);
+                    for (int p = 0; p < 16; p += 2) {
+                        float2 f0 = sc, f1 = sc;
+                        if (BROWS) {
+                            const float4 u = *reinterpret_cast<const float4 *>(fb + 32 * c + 2 * p);
+                            f0 = __fmul2_rn(sc, make_float2(u.x, u.y));
+                            f1 = __fmul2_rn(sc, make_float2(u.z, u.w));
+                        }
+                        const uint32_t *t = r[c & 1] + 2 * p;
+                        acc[16 * c + p] =
+                            __ffma2_rn(make_float2(__uint_as_float(t[0]), __uint_as_float(t[1])), f0, acc[16 * c + p]);
+                        acc[16 * c + p + 1] =
+                            __ffma2_rn(make_float2(__uint_as_float(t[2]), __uint_as_float(t[3])), f1, acc[16 * c + p + 1]);
                     }
                 }
-                sa0 = sa1, sa1 = sa2;
-                sb0 = sb1, sb1 = sb2;
+                if (BROWS) free_factors();
                 buf ^= 1;
                 if (buf == 0) bph ^= 1;
             }
-            if (ok && row_ok)
-#pragma unroll
-                for (int c = 0; c < 4; c++) store_row32(args, w.d_row0 + row, n0 + 32 * c, acc + 16 * c);
+            if (!ok) break;
+            const BlockTile w = block_tile<TM, TN>(args, tab, tile);
+            const int64_t first = 32 * q;
+            const int64_t rows = w.a_end - (w.a_row + first);  // the warp's rows to write
+            store_tile(args, stage, lane, w.d_row + first, (int)max(min(rows, (int64_t)32), (int64_t)0), w.n0 + 128 * half, acc);
         }
     }
 
     tc_fence_before();
     __syncwarp();
     __syncthreads();
-    cluster_sync();  // the peer's shared memory and TMEM stay live until the pair is done
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc_pair(tmem_base, TMEM_COLS);
+        tmem_dealloc(tmem_base, TMEM_COLS);
     }
 }
 
@@ -430,15 +557,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(bp::THREADS, 1)
 // host
 // ---------------------------------------------------------------------------
 static std::atomic<bool> g_block_set[64];
-static int g_block_pairs[64];
 
-static fp8dl_status block_gemm_setup(int dev, int sms) {
+static fp8dl_status block_gemm_setup(int dev) {
     if (g_block_set[dev].load(std::memory_order_acquire)) return FP8DL_OK;
     std::lock_guard<std::mutex> lock(init_mutex());
     if (g_block_set[dev].load(std::memory_order_relaxed)) return FP8DL_OK;
-    const void *pairs[] = {(const void *)block_gemm_pair_kernel<false>, (const void *)block_gemm_pair_kernel<true>};
-    int resident = 1 << 30;
-    for (const void *k : pairs) {
+    const void *kernels[] = {(const void *)block_gemm_kernel<false>, (const void *)block_gemm_kernel<true>};
+    for (const void *k : kernels) {
         cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bp::SMEM_BYTES);
         cudaFuncAttributes fa = {};
         if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, k);
@@ -446,19 +571,7 @@ static fp8dl_status block_gemm_setup(int dev, int sms) {
         // the epilogue's larger register share comes out of the launch's registers
         if (fa.numRegs < bp::REGS_LAUNCH)
             return fail(FP8DL_ERR_CUDA, "block GEMM: built with %d registers, %d needed", fa.numRegs, bp::REGS_LAUNCH);
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(sms / 2 * 2), 1, 1);
-        cfg.blockDim = dim3(bp::THREADS, 1, 1);
-        cfg.dynamicSmemBytes = bp::SMEM_BYTES;
-        int n = 0;
-        e = cudaOccupancyMaxActiveClusters(&n, k, &cfg);
-        if (e != cudaSuccess || n < 1) {
-            cudaGetLastError();
-            return fail(FP8DL_ERR_UNSUPPORTED_DEVICE, "the block GEMM needs resident CTA-pair clusters");
-        }
-        resident = n < resident ? n : resident;
     }
-    g_block_pairs[dev] = resident;
     g_block_set[dev].store(true, std::memory_order_release);
     return FP8DL_OK;
 }
@@ -480,20 +593,21 @@ static fp8dl_status launch_block_gemm(const uint8_t *A, int32_t a_dtype, int64_t
                                       BlockGemmArgs &args, cudaStream_t st, bool pdl, const char *what) {
     int dev = 0, sms = 0;
     FP8DL_TRY(current_device(&dev, &sms));
-    FP8DL_TRY(block_gemm_setup(dev, sms));
+    FP8DL_TRY(block_gemm_setup(dev));
     CUtensorMap ta, tb;
-    FP8DL_TRY(encode_tmap_2d_u8(&ta, A, (uint64_t)args.K, (uint64_t)a_rows, (uint64_t)args.K, 128, 128,
+    FP8DL_TRY(encode_tmap_2d_u8(&ta, A, (uint64_t)args.K, (uint64_t)a_rows, (uint64_t)args.K, bp::BK, bp::TM,
                                 CU_TENSOR_MAP_SWIZZLE_128B));
-    FP8DL_TRY(encode_tmap_2d_u8(&tb, B, (uint64_t)args.K, (uint64_t)b_rows, (uint64_t)args.K, 128, 128,
+    FP8DL_TRY(encode_tmap_2d_u8(&tb, B, (uint64_t)args.K, (uint64_t)b_rows, (uint64_t)args.K, bp::BK, bp::TN,
                                 CU_TENSOR_MAP_SWIZZLE_128B));
     args.idesc = (1u << 4) | ((uint32_t)a_dtype << 7) | ((uint32_t)b_dtype << 10) | ((uint32_t)(bp::TN >> 3) << 17) |
                  ((uint32_t)(bp::TM >> 4) << 24);
     const int64_t tiles_m = (args.M + bp::TM - 1) / bp::TM, tiles_n = (args.N + bp::TN - 1) / bp::TN;
-    args.raster_n = tiles_n < tiles_m;
-    args.group = args.K <= 8192 ? 16 : 8;
-    const int64_t pairs = tiles_bound < g_block_pairs[dev] ? tiles_bound : g_block_pairs[dev];
-    (void)launch_kernel(brows ? block_gemm_pair_kernel<true> : block_gemm_pair_kernel<false>, dim3((unsigned)(2 * pairs)),
-                        bp::THREADS, bp::SMEM_BYTES, st, 0, pdl, ta, tb, args);
+    args.along_n = 0;
+    args.band = 16;
+    if (tiles_bound > 0x7fffffffll) return fail(FP8DL_ERR_SHAPE, "%s: more than 2^31 - 1 output tiles", what);
+    (void)launch_kernel(brows ? block_gemm_kernel<true> : block_gemm_kernel<false>,
+                        dim3((unsigned)(tiles_bound < sms ? tiles_bound : sms)), bp::THREADS, bp::SMEM_BYTES, st, 0, pdl, ta,
+                        tb, args);
     note_launch();
     return check_launch(what);
 }
