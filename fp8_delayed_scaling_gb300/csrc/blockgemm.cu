@@ -173,6 +173,65 @@ __device__ __forceinline__ BlockTile block_tile(const BlockGemmArgs &a, const Gr
     return w;
 }
 
+// One k-block of the pair's tile by one elected lane of a converged warp: four MMAs (K = 32 each,
+// 32 bytes further into the swizzled rows, two descriptor units), the first one overwriting D,
+// and the commits that hand the buffer to the epilogue and the stage to the producer.
+__device__ __forceinline__ void umma_block_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t tfull,
+                                                uint32_t empty) {
+    asm volatile(
+        "{\n\t.reg .pred e, t, f;\n\t.reg .b64 a, b;\n\t.reg .b16 m;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.eq.u32 t, 0, 0;\n\tsetp.ne.u32 f, 0, 0;\n\tmov.u16 m, 3;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, f;\n\t"
+        "add.u64 a, %1, 2;\n\tadd.u64 b, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "add.u64 a, %1, 4;\n\tadd.u64 b, %2, 4;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "add.u64 a, %1, 6;\n\tadd.u64 b, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%4], m;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%5], m;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(tfull), "r"(empty)
+        : "memory");
+}
+
+// Arrive on an mbarrier of this CTA from the lanes with `who`, without a branch.
+__device__ __forceinline__ void arrive_if(uint32_t bar, bool who) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+                 "r"((uint32_t)who)
+                 : "memory");
+}
+
+// The same on another CTA's mbarrier (a shared::cluster address).  What it announces is that this
+// warp's tensor-memory loads are done, which tcgen05.wait::ld and the tcgen05 fence order; no
+// ordinary memory is handed over, so the release stays within the CTA: a release at cluster
+// scope waits for every global access in flight, once per k-block here (16384 x 16384 x 4096:
+// 1.92 ms with it, 0.92 without).
+__device__ __forceinline__ void arrive_remote_if(uint32_t cluster_addr, bool who) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t@p mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];\n\t}" ::"r"(
+            cluster_addr),
+        "r"((uint32_t)who)
+        : "memory");
+}
+
+// No use of r moves above this point: r belongs to a tcgen05.ld that has just been waited for.
+template <int L>
+__device__ __forceinline__ void regs_ready(uint32_t (&r)[L]) {
+#pragma unroll
+    for (int i = 0; i < L; i++) asm volatile("" : "+r"(r[i]));
+}
+
+// 32 lanes x 16 consecutive 32-bit columns of tensor memory.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
 // 4- and 16-byte copies from global to shared memory.
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -186,123 +245,138 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// Columns c0 .. c0 + 31 of this thread's sums, bias added (n = their first column of D).
-__device__ __forceinline__ void add_bias32(const BlockGemmArgs &a, int64_t n, float2 (&v)[16]) {
+// Sixteen consecutive columns' bias added to the sums, n = the first one's column of D.
+__device__ __forceinline__ void add_bias16(const BlockGemmArgs &a, int64_t n, float2 (&v)[8]) {
     if (a.bias_dtype == FP8DL_BF16) {
-        const __nv_bfloat16 *b = static_cast<const __nv_bfloat16 *>(a.bias) + n;
+        const uint4 *b = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.bias) + n);
 #pragma unroll
-        for (int g = 0; g < 4; g++)
-            if (n + 8 * g < a.N) {
-                const uint4 u = __ldg(reinterpret_cast<const uint4 *>(b + 8 * g));
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        for (int g = 0; g < 2; g++) {
+            const uint4 u = __ldg(b + g);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                for (int q = 0; q < 4; q++)
-                    v[4 * g + q] = __fadd2_rn(v[4 * g + q], make_float2(bf16_lo(w[q]), bf16_hi(w[q])));
-            }
-    } else if (a.bias_dtype == FP8DL_F32) {
-        const float *b = static_cast<const float *>(a.bias) + n;
+            for (int q = 0; q < 4; q++)
+                v[4 * g + q] = __fadd2_rn(v[4 * g + q], make_float2(bf16_lo(w[q]), bf16_hi(w[q])));
+        }
+    } else {
+        const float4 *b = reinterpret_cast<const float4 *>(static_cast<const float *>(a.bias) + n);
 #pragma unroll
-        for (int g = 0; g < 8; g++)
-            if (n + 4 * g < a.N) {
-                const float4 u = __ldg(reinterpret_cast<const float4 *>(b + 4 * g));
-                v[2 * g] = __fadd2_rn(v[2 * g], make_float2(u.x, u.y));
-                v[2 * g + 1] = __fadd2_rn(v[2 * g + 1], make_float2(u.z, u.w));
-            }
+        for (int g = 0; g < 4; g++) {
+            const float4 u = __ldg(b + g);
+            v[2 * g] = __fadd2_rn(v[2 * g], make_float2(u.x, u.y));
+            v[2 * g + 1] = __fadd2_rn(v[2 * g + 1], make_float2(u.z, u.w));
+        }
     }
 }
 
-// One warp writes its 32 rows x 128 columns of D (lane = row; the sums in acc), rounded once.
-// Straight from the registers every store would touch 32 rows, a piece of a line each (the
-// stores of a 256 x 256 tile took 7200 cycles, a fifth of a tile with K = 4096).  Instead 64
-// bytes of each row at a time go through shared memory (16-byte chunks XOR-swizzled by row
-// pairs: conflict-free both ways) and leave as two whole sectors, eight rows per instruction.
-__device__ __forceinline__ void store_tile(const BlockGemmArgs &a, uint8_t *stage, int lane, int64_t d_row, int rows,
-                                           int64_t n0, float2 (&acc)[64]) {
+// ---------------------------------------------------------------------------
+// 256 x 256 tiles on CTA pairs (tcgen05 cta_group::2, M 256, N 256, K 32).
+//   warp 0      TMA producer: 128 rows of A and 128 of B per CTA and k-block
+//   warp 1      the leader's MMA thread: four MMAs per block into one of two 256-column
+//               tensor-memory buffers
+//   warp 2      copies the blocks' factors into a shared-memory ring, blocks ahead
+//   warp 3      adds "the factors are there" to "the MMAs are done", so that the epilogue waits
+//               once per block: an mbarrier wait costs about 90 cycles even when it is over
+//   warps 4-11  epilogue: warp w drains lane quarter w & 3 of column half (w - 4) / 4; a thread
+//               holds one row x 128 columns of the sum (64 fp32 pairs)
+// TILEFIG
+// FP32 pipe: with 128 x 128 weight factors one packed multiply-add per two values; with
+// factors per row of B (BROWS, weight gradients) one packed multiply more.
+// ---------------------------------------------------------------------------
+namespace bp {
+constexpr int TM = 256, TN = 256, HALF = 128, BK = 128, STAGES = 4, BUFS = 2;
+constexpr int A_BYTES = 128 * BK, B_ROWS = TN / 2, STAGE_BYTES = A_BYTES + B_ROWS * BK;
+constexpr int THREADS = 384, EPI_WARPS = 8;
+constexpr int REGS_LAUNCH = 168, REGS_IO = 56, REGS_EPI = 224;  // 128 * 56 + 256 * 224 = 384 * 168
+static_assert(128 * REGS_IO + 256 * REGS_EPI <= THREADS * REGS_LAUNCH, "register split");
+constexpr int TMEM_COLS = 512;
+// The factors of the next blocks, FB blocks per ring slot: 128 of A's, then one per column half
+// of B's (padded to 16 bytes), or, BROWS, 256.
+template <bool BROWS>
+struct Ring {
+    static constexpr int FB = BROWS ? 2 : 4, SLOTS = 2, BLOCK = 128 + (BROWS ? TN : 4);
+    static constexpr int SLOT = FB * BLOCK;
+};
+constexpr int RING_BYTES = Ring<true>::SLOTS * Ring<true>::SLOT * 4;
+// One warp's 32 rows x 256 bytes of D on their way out, as two boxes of 128 bytes.
+constexpr int OUT_BOX = 32 * 128, OUT_WARP = 2 * OUT_BOX, OUT_BYTES = EPI_WARPS * OUT_WARP;
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + OUT_BYTES + 1024 + RING_BYTES + kGroupTableBytes + 1024;
+static_assert(SMEM_BYTES <= 227 * 1024 && Ring<false>::SLOTS * Ring<false>::SLOT * 4 <= RING_BYTES, "shared memory");
+}  // namespace bp
+
+// One warp's 32 rows x 128 columns of D (lane = row): rounded once, laid out in shared memory as
+// boxes of 128 bytes a row (16-byte chunk j of row r at j ^ (r & 7): the TMA's 128-byte
+// swizzle, free of bank conflicts) and stored by the TMA while the next tile is summed.  All
+// CTAs finish their tiles together, so stores that the epilogue waits for come in bursts at the
+// speed of L2: with stores from registers, or through 4 KB a warp, a tile's end cost 4000-7200
+// cycles, an eighth to a fifth of a tile with K = 4096.  Rows at a ragged group's end are
+// written by the warp itself.  The box is free once the TMA has read it: the wait is at the
+// next tile's end (two boxes hold 128 columns of bf16; fp32 takes two turns).
+__device__ __forceinline__ void store_tile(const BlockGemmArgs &a, const CUtensorMap *tmap_d, uint8_t *stage, int lane,
+                                           int64_t d_row, int rows, int64_t n0, float2 (&acc)[64]) {
+    using namespace bp;
     const bool bf = a.d_dtype == FP8DL_BF16;
     const int esz = bf ? 2 : 4;
-    const int sub = lane >> 2, ch = lane & 3;
-    uint8_t *base = static_cast<uint8_t *>(a.D) + ((d_row + sub) * a.N + n0) * esz + ch * 16;
-    const int64_t step = 8 * a.N * esz;
-    uint8_t *mine = stage + lane * 64;
-    const int swz = (lane >> 1) & 3, rswz = (sub >> 1) & 3;
-    auto flush = [&](int off, int64_t n) {  // the staged 64 bytes of each row, from column n on
-        __syncwarp();
-        const bool ok = n + ch * (16 / esz) < a.N;
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(stage + (8 * i + sub) * 64 + ((ch ^ rswz) << 4));
-            if (ok && 8 * i + sub < rows) *reinterpret_cast<uint4 *>(base + i * step + off) = u;
+    uint8_t *mine = stage + lane * 128;
+    const int swz = lane & 7;
+    auto flush = [&](uint8_t *box, int64_t n) {  // a box whose first column is n
+        if (rows == 32) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && n < a.N) {
+                tma_store_2d(tmap_d, smem_u32(box), (int32_t)(n * esz), (int32_t)d_row);
+                bulk_commit();
+            }
+        } else {
+            __syncwarp();
+            const int sub = lane >> 3, ch = lane & 7;
+            uint8_t *to = static_cast<uint8_t *>(a.D) + ((d_row + sub) * a.N + n) * esz + 16 * ch;
+            const bool ok = n + ch * (16 / esz) < a.N;
+            for (int r = sub; r < rows; r += 4, to += 4 * a.N * esz)
+                if (ok) *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(box + r * 128 + ((ch ^ (r & 7)) << 4));
+            __syncwarp();
         }
+    };
+    auto wait_free = [&] {
+        if (lane == 0) bulk_wait_read();
         __syncwarp();
     };
+    wait_free();
 #pragma unroll
-    for (int c = 0; c < 4; c++) {
-        const int64_t n = n0 + 32 * c;
-        if (n >= a.N) break;
-        float2 v[16];
+    for (int c = 0; c < 8; c++) {
+        float2 v[8];
 #pragma unroll
-        for (int p = 0; p < 16; p++) v[p] = acc[16 * c + p];
-        if (a.bias_dtype >= 0) add_bias32(a, n, v);
+        for (int p = 0; p < 8; p++) v[p] = acc[8 * c + p];
+        if (a.bias_dtype >= 0 && n0 + 16 * c < a.N) add_bias16(a, n0 + 16 * c, v);
         if (bf) {
 #pragma unroll
-            for (int g = 0; g < 4; g++) {
+            for (int g = 0; g < 2; g++) {
                 uint32_t w[4];
 #pragma unroll
                 for (int q = 0; q < 4; q++) {
                     const __nv_bfloat162 h = __floats2bfloat162_rn(v[4 * g + q].x, v[4 * g + q].y);
                     w[q] = *reinterpret_cast<const uint32_t *>(&h);
                 }
-                *reinterpret_cast<uint4 *>(mine + ((g ^ swz) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4 *>(mine + (c >> 2) * OUT_BOX + (((2 * (c & 3) + g) ^ swz) << 4)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
             }
-            flush(64 * c, n);
+            if ((c & 3) == 3) flush(stage + (c >> 2) * OUT_BOX, n0 + 64 * (c >> 2));
         } else {
+            if (c == 4) wait_free();
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-#pragma unroll
-                for (int g = 0; g < 4; g++)
-                    *reinterpret_cast<float4 *>(mine + ((g ^ swz) << 4)) =
-                        make_float4(v[8 * h + 2 * g].x, v[8 * h + 2 * g].y, v[8 * h + 2 * g + 1].x, v[8 * h + 2 * g + 1].y);
-                flush(128 * c + 64 * h, n + 16 * h);
-            }
+            for (int g = 0; g < 4; g++)
+                *reinterpret_cast<float4 *>(mine + ((c >> 1) & 1) * OUT_BOX + (((4 * (c & 1) + g) ^ swz) << 4)) =
+                    make_float4(v[2 * g].x, v[2 * g].y, v[2 * g + 1].x, v[2 * g + 1].y);
+            if (c & 1) flush(stage + ((c >> 1) & 1) * OUT_BOX, n0 + 32 * (c >> 1));
         }
     }
 }
 
-// ---------------------------------------------------------------------------
-// 128 x 256 tiles, one persistent CTA per SM.
-//   warp 0      TMA producer: 128 rows of A and 256 of B per k-block, four stages
-//   warp 1      MMA thread: per block four MMAs (M 128, N 256, K 32) into one of two
-//               256-column tensor-memory buffers
-//   warp 2      copies the blocks' factors into a shared-memory ring
-//   warps 4-11  epilogue: warp w drains lane quarter w & 3 of column half (w - 4) / 4; a thread
-//               holds one row x 128 columns of the sum (64 fp32 pairs)
-// With 128 x 128 weight factors a thread's 128 columns share one factor per block: one
-// packed multiply-add per two values, half the MMAs' time on the FP32 pipe.  With factors per
-// row of B (BROWS, weight gradients) each column has its own: one more packed multiply.
-//
-// Why not CTA pairs (256 x 256 tiles): every block's buffer goes to the epilogue and back
-// through mbarriers, and between two SMs that costs more than the pair saves in operand
-// traffic: PAIRFIG.
-// ---------------------------------------------------------------------------
-namespace bp {
-constexpr int TM = 128, TN = 256, BK = 128, STAGES = 4;
-constexpr int A_BYTES = TM * BK, B_BYTES = TN * BK, STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int THREADS = 384, EPI_WARPS = 8;
-constexpr int REGS_LAUNCH = 168, REGS_IO = 56, REGS_EPI = 224;  // 128 * 56 + 256 * 224 = 384 * 168
-static_assert(128 * REGS_IO + 256 * REGS_EPI <= THREADS * REGS_LAUNCH, "register split");
-constexpr int TMEM_COLS = 512;
-// The factors of the next blocks: 128 of A's, then one per column half, or (BROWS) 256, of B's.
-constexpr int RING = 4, SLOT_FLOATS = 128 + 256, RING_BYTES = RING * SLOT_FLOATS * 4;
-constexpr int OUT_BYTES = EPI_WARPS * 2048;        // 32 rows x 64 bytes of D per warp
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + OUT_BYTES + 1024 + RING_BYTES + kGroupTableBytes + 1024;
-static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
-}  // namespace bp
-
 template <bool BROWS>
 __global__ void __launch_bounds__(bp::THREADS, 1)
     block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
-                      const BlockGemmArgs args) {
+                      const __grid_constant__ CUtensorMap tmap_d, const BlockGemmArgs args) {
     using namespace bp;
+    using R = Ring<BROWS>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
@@ -311,26 +385,29 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
     uint64_t *full = reinterpret_cast<uint64_t *>(bar_area);
     uint64_t *empty = full + STAGES;
     uint64_t *tfull = empty + STAGES;
-    uint64_t *tempty = tfull + 2;
-    uint64_t *ffull = tempty + 2;
-    uint64_t *fempty = ffull + RING;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(fempty + RING);
+    uint64_t *tempty = tfull + BUFS;
+    uint64_t *ffull = tempty + BUFS;
+    uint64_t *fempty = ffull + R::SLOTS;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(fempty + R::SLOTS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     float *ring = reinterpret_cast<float *>(bar_area + 1024);
     const GroupTables tab = group_tables(bar_area + 1024 + RING_BYTES);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const uint32_t pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; s++) {
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
         }
-        for (int a = 0; a < 2; a++) {
-            mbar_init(smem_u32(&tfull[a]), 1);
-            mbar_init(smem_u32(&tempty[a]), EPI_WARPS);
+        for (int a = 0; a < BUFS; a++) {
+            mbar_init(smem_u32(&tfull[a]), 2);  // the MMAs' commit, and the relay's word for the factors
+            mbar_init(smem_u32(&tempty[a]), 2 * EPI_WARPS);
         }
-        for (int a = 0; a < RING; a++) {
+        for (int a = 0; a < R::SLOTS; a++) {
             mbar_init(smem_u32(&ffull[a]), 32);  // every lane of the copying warp
             mbar_init(smem_u32(&fempty[a]), EPI_WARPS);
         }
@@ -338,13 +415,15 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
         mbar_fence_init();
         tma_prefetch_map(&tmap_a);
         tma_prefetch_map(&tmap_b);
+        tma_prefetch_map(&tmap_d);
     }
     if (warp == 1) {
-        tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
-        tmem_relinquish();
+        tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
+        tmem_relinquish_pair();
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // both CTAs' barriers are initialised before any signal crosses
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     pdl_wait();
@@ -356,22 +435,25 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_IO));
-        if (warp == 0 && lane == 0) {  // ------------------------------------- producer
+        if (warp == 0 && lane == 0) {  // ------------------------------------- producer (both CTAs)
             int s = 0;
             uint32_t ph = 0;
             int64_t issued = 0;
             bool ok = true;
-            for (uint32_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+            for (uint32_t tile = pair; tile < tiles && ok; tile += npairs) {
                 const BlockTile w = block_tile<TM, TN>(args, tab, tile);
+                const int32_t ra = (int32_t)(w.a_row + rank * 128), rb = (int32_t)(w.b_row + rank * B_ROWS);
                 for (int kb = 0; kb < w.kbs; kb++) {
                     if (!mbar_wait(smem_u32(&empty[s]), ph ^ 1, abort_flag, args.status)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t fb = smem_u32(&full[s]), sa = smem_u32(smem + s * STAGE_BYTES);
-                    mbar_expect_tx(fb, STAGE_BYTES);
-                    tma_load_2d(sa, &tmap_a, fb, (w.kb0 + kb) * BK, (int32_t)w.a_row);
-                    tma_load_2d(sa + A_BYTES, &tmap_b, fb, (w.kb0 + kb) * BK, (int32_t)w.b_row);
+                    // both CTAs' loads complete on the leader's barrier
+                    const uint32_t fb = smem_u32(&full[s]), lb = mapa_shared(fb, 0);
+                    const uint32_t sa = smem_u32(smem + s * STAGE_BYTES);
+                    if (leader) mbar_expect_tx(fb, 2 * STAGE_BYTES);
+                    tma_load_2d_pair(sa, &tmap_a, lb, (w.kb0 + kb) * BK, ra);
+                    tma_load_2d_pair(sa + A_BYTES, &tmap_b, lb, (w.kb0 + kb) * BK, rb);
                     issued++;
                     if (++s == STAGES) {
                         s = 0;
@@ -379,32 +461,32 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
                     }
                 }
             }
-            if (!ok)
+            if (!ok && leader)
                 for (int64_t i = issued - 1; i >= 0 && i >= issued - STAGES; i--)
                     mbar_drain(smem_u32(&full[i % STAGES]), (uint32_t)((i / STAGES) & 1));
-        } else if (warp == 1 && lane == 0) {  // ------------------------------- MMA issuer
+        } else if (warp == 1 && leader) {  // ----------------------------------- MMA issuer (leader only)
+            // The whole warp runs the loop and one elected lane issues: the operands stay in uniform
+            // registers, where the MMA wants them (with a branch on the lane every MMA first moved
+            // them over, on a scheduler shared with two epilogue warps: 10 % of the kernel).
             int s = 0, buf = 0;
             uint32_t ph = 0, bph = 0;
             bool ok = true, any = false;
             uint32_t last_bar = 0, last_par = 0;
             const SDesc desc0 = sdesc_k_sw128_split(smem_u32(smem));
-            for (uint32_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+            for (uint32_t tile = pair; tile < tiles && ok; tile += npairs) {
                 const int kbs = block_tile_kbs<TM, TN>(args, tab, tile);
                 for (int kb = 0; kb < kbs; kb++) {
-                    if (!mbar_wait(smem_u32(&tempty[buf]), bph ^ 1, abort_flag, args.status) ||
-                        !mbar_wait(smem_u32(&full[s]), ph, abort_flag, args.status)) {
+                    // the operands first: they are there early, the buffer comes back last
+                    if (!mbar_wait(smem_u32(&full[s]), ph, abort_flag, args.status) ||
+                        !mbar_wait(smem_u32(&tempty[buf]), bph ^ 1, abort_flag, args.status)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t lo_a = desc0.lo + (uint32_t)s * (STAGE_BYTES >> 4);
-                    const uint32_t lo_b = lo_a + (A_BYTES >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < BK / 32; kk++)
-                        umma_f8f6f4(tmem_base + (uint32_t)(buf * TN), sdesc_join(lo_a + 2 * kk, desc0.hi),
-                                    sdesc_join(lo_b + 2 * kk, desc0.hi), args.idesc, kk != 0);
-                    umma_commit(smem_u32(&tfull[buf]));
-                    umma_commit(smem_u32(&empty[s]));
+                    umma_block_pair(tmem_base + (uint32_t)(buf * TN), sdesc_join(lo_a, desc0.hi),
+                                    sdesc_join(lo_a + (A_BYTES >> 4), desc0.hi), args.idesc, smem_u32(&tfull[0]) + 8 * buf,
+                                    smem_u32(&empty[0]) + 8 * s);
                     any = true;
                     last_bar = smem_u32(&empty[s]);
                     last_par = ph;
@@ -412,144 +494,166 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
                         s = 0;
                         ph ^= 1;
                     }
-                    buf ^= 1;
-                    if (buf == 0) bph ^= 1;
+                    if (++buf == BUFS) {
+                        buf = 0;
+                        bph ^= 1;
+                    }
                 }
             }
             if (!ok && any) mbar_drain(last_bar, last_par);
-        } else if (warp == 2) {  // --------------------------------------------- factors
+        } else if (warp == 2) {  // --------------------------------------------- factors (both CTAs)
             // Rows and columns outside the matrix take a valid address: their sums are not stored.
             int slot = 0;
             uint32_t ph = 0;
             bool ok = true;
-            for (uint32_t tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+            for (uint32_t tile = pair; tile < tiles && ok; tile += npairs) {
                 const BlockTile w = block_tile<TM, TN>(args, tab, tile);
-                const float *pa[4], *pb[2];
+                const int64_t row = w.a_row + rank * 128 + lane;
+                const float *pa = args.a_s + (int64_t)w.kb0 * args.M + w.a_row;
+                const float *pb = w.b_s + (int64_t)w.kb0 * args.b_ld + (BROWS ? w.n0 : w.n0 >> 7);
+                int oa[4], ob[2];  // from those: four rows, and (BROWS) two times four columns, or one block
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const int64_t row = w.a_row + 32 * j + lane;
-                    pa[j] = args.a_s + (int64_t)w.kb0 * args.M + (row < w.a_end ? row : w.a_row);
-                }
+                for (int j = 0; j < 4; j++) oa[j] = row + 32 * j < w.a_end ? (int)(rank * 128) + lane + 32 * j : 0;
+                if (BROWS) {
 #pragma unroll
-                for (int h = 0; h < 2; h++) {  // BROWS: four columns of each half per lane
-                    const int64_t n = w.n0 + 128 * h + (BROWS ? 4 * lane : 0);
-                    pb[h] = w.b_s + (int64_t)w.kb0 * args.b_ld + (n < args.N ? (BROWS ? n : n >> 7) : 0);
+                    for (int h = 0; h < 2; h++) ob[h] = w.n0 + 128 * h + 4 * lane < args.N ? 128 * h + 4 * lane : 0;
+                } else {
+                    ob[0] = (w.n0 >> 7) + lane < args.b_ld ? lane : 0;
                 }
-                for (int kb = 0; kb < w.kbs; kb++) {
+                for (int kb = 0; kb < w.kbs; kb += R::FB) {
                     if (!mbar_wait(smem_u32(&fempty[slot]), ph ^ 1, abort_flag, args.status)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t dst = smem_u32(ring + slot * SLOT_FLOATS);
+                    uint32_t dst = smem_u32(ring + slot * R::SLOT);
+                    for (int f = 0; f < R::FB && kb + f < w.kbs; f++, dst += 4 * R::BLOCK) {
 #pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        cp_async4(dst + 4 * (32 * j + lane), pa[j]);
-                        pa[j] += args.M;
-                    }
-#pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        if (BROWS)
-                            cp_async16(dst + 512 + 512 * h + 16 * lane, pb[h]);
-                        else if (lane == 0)
-                            cp_async4(dst + 512 + 512 * h, pb[h]);
-                        pb[h] += args.b_ld;
+                        for (int j = 0; j < 4; j++) cp_async4(dst + 4 * (32 * j + lane), pa + oa[j]);
+                        if (BROWS) {
+                            cp_async16(dst + 512 + 16 * lane, pb + ob[0]);
+                            cp_async16(dst + 1024 + 16 * lane, pb + ob[1]);
+                        } else if (lane < 2) {
+                            cp_async4(dst + 512 + 4 * lane, pb + ob[0]);
+                        }
+                        pa += args.M;
+                        pb += args.b_ld;
                     }
                     cp_async_arrive(smem_u32(&ffull[slot]));
-                    if (++slot == RING) {
+                    if (++slot == R::SLOTS) {
                         slot = 0;
                         ph ^= 1;
                     }
                 }
             }
             cp_async_wait_all();
+        } else if (warp == 3) {  // --------------------------------------------- relay (both CTAs)
+            // A block reaches the epilogue in one wait: its buffer is full when the MMAs have
+            // committed and this warp, which waits for the factors, has said so.  It arrives for
+            // a block once the buffer's last block is complete, well before the MMAs do.
+            int slot = 0, buf = 0;
+            uint32_t fph = 0, bph = 0;
+            bool ok = true;
+            for (uint32_t tile = pair; tile < tiles && ok; tile += npairs) {
+                const int kbs = block_tile_kbs<TM, TN>(args, tab, tile);
+                for (int kb = 0; kb < kbs; kb++) {
+                    if (kb % R::FB == 0) {
+                        ok = mbar_wait(smem_u32(&ffull[slot]), fph, abort_flag, args.status);
+                        if (++slot == R::SLOTS) {
+                            slot = 0;
+                            fph ^= 1;
+                        }
+                    }
+                    if (!ok || !(ok = mbar_wait(smem_u32(&tfull[buf]), bph ^ 1, abort_flag, args.status))) break;
+                    if (lane == 0) mbar_arrive(smem_u32(&tfull[buf]));
+                    __syncwarp();
+                    if (++buf == BUFS) {
+                        buf = 0;
+                        bph ^= 1;
+                    }
+                }
+            }
         }
-    } else {  // ------------------------------------------------------------ epilogue
+    } else {  // ------------------------------------------------------------ epilogue (both CTAs)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EPI));
         const int q = warp & 3, half = (warp - 4) >> 2;
-        const uint32_t taddr0 = tmem_base + (uint32_t)(128 * half) + ((uint32_t)(32 * q) << 16);
-        uint8_t *stage = out_stage + (warp - 4) * 2048;
-        const float *my_a = ring + 32 * q + lane, *my_b = ring + 128 + 128 * half;
-        int slot = 0;
-        uint32_t fph = 0;
-        // The next block's factors are there (they were copied blocks ago).
-        auto wait_factors = [&] { return mbar_wait(smem_u32(&ffull[slot]), fph, abort_flag, args.status); };
-        auto free_factors = [&] {  // this warp has read them
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&fempty[slot]));
-            if (++slot == RING) {
-                slot = 0;
-                fph ^= 1;
-            }
-        };
-        int buf = 0;
+        const uint32_t taddr0 = tmem_base + (uint32_t)(HALF * half) + ((uint32_t)(32 * q) << 16);
+        uint8_t *stage = out_stage + (warp - 4) * OUT_WARP;
+        const float *my_a = ring + 32 * q + lane, *my_b = ring + 128 + (BROWS ? HALF : 1) * half;
+        const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
+        int slot = 0, buf = 0;
         uint32_t bph = 0;
-        for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        for (uint32_t tile = pair; tile < tiles; tile += npairs) {
             const int kbs = block_tile_kbs<TM, TN>(args, tab, tile);
             float2 acc[64];
 #pragma unroll
             for (int p = 0; p < 64; p++) acc[p] = make_float2(0.0f, 0.0f);
             bool ok = true;
-            for (int kb = 0; kb < kbs; kb++) {
-                if (!wait_factors()) {
-                    ok = false;
-                    break;
-                }
-                const float *fb = my_b + slot * SLOT_FLOATS;
-                const float fa = my_a[slot * SLOT_FLOATS];
-                const float2 sc = f2(BROWS ? fa : __fmul_rn(fa, fb[0]));
-                if (!BROWS) free_factors();
-                if (!mbar_wait(smem_u32(&tfull[buf]), bph, abort_flag, args.status)) {
-                    ok = false;
-                    break;
-                }
+            for (int kb = 0; ok && kb < kbs; kb++) {
+                // after a wait that ran out this block's sums are garbage and the loop ends
+                ok = mbar_wait(smem_u32(&tfull[0]) + 8 * buf, bph, abort_flag, args.status);
                 tc_fence_after();
                 const uint32_t ta = taddr0 + (uint32_t)(buf * TN);
                 uint32_t r[2][32];
                 tmem_ld_32x32b_x32(ta, r[0]);
+                tmem_ld_32x32b_x32(ta + 32, r[1]);
+                const int at = slot * R::SLOT + (kb % R::FB) * R::BLOCK;
+                const float *fb = my_b + at;  // BROWS: the block's column factors
+                const float2 sc = f2(BROWS ? my_a[at] : __fmul_rn(my_a[at], fb[0]));
+                tmem_ld_wait_regs(r[0]);
+                regs_ready(r[1]);
+                // Chunks of 32 columns.  The buffer goes back as soon as the last one is in registers,
+                // and only two chunks' multiply-adds come before that.
 #pragma unroll
                 for (int c = 0; c < 4; c++) {
-                    tmem_ld_wait_regs(r[c & 1]);
-                    if (c < 3) {
-                        tmem_ld_32x32b_x32(ta + 32 * (c + 1), r[(c + 1) & 1]);
-                    } else {  // the buffer is read: the next block's MMAs may overwrite it
+                    if (c == 2) {
+                        tmem_ld_32x32b_x32(ta + 96, r[1]);
+                        tmem_ld_wait_regs(r[0]);
+                        regs_ready(r[1]);
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&tempty[buf]));
+                        arrive_remote_if(tempty0 + 8 * buf, lane == 0);
                     }
 #pragma unroll
                     for (int p = 0; p < 16; p += 2) {
-                        float2 f0 = sc, f1 = sc;
+                        float2 g0 = sc, g1 = sc;
                         if (BROWS) {
                             const float4 u = *reinterpret_cast<const float4 *>(fb + 32 * c + 2 * p);
-                            f0 = __fmul2_rn(sc, make_float2(u.x, u.y));
-                            f1 = __fmul2_rn(sc, make_float2(u.z, u.w));
+                            g0 = __fmul2_rn(sc, make_float2(u.x, u.y));
+                            g1 = __fmul2_rn(sc, make_float2(u.z, u.w));
                         }
                         const uint32_t *t = r[c & 1] + 2 * p;
                         acc[16 * c + p] =
-                            __ffma2_rn(make_float2(__uint_as_float(t[0]), __uint_as_float(t[1])), f0, acc[16 * c + p]);
+                            __ffma2_rn(make_float2(__uint_as_float(t[0]), __uint_as_float(t[1])), g0, acc[16 * c + p]);
                         acc[16 * c + p + 1] =
-                            __ffma2_rn(make_float2(__uint_as_float(t[2]), __uint_as_float(t[3])), f1, acc[16 * c + p + 1]);
+                            __ffma2_rn(make_float2(__uint_as_float(t[2]), __uint_as_float(t[3])), g1, acc[16 * c + p + 1]);
                     }
+                    if (c == 0) tmem_ld_32x32b_x32(ta + 64, r[0]);
                 }
-                if (BROWS) free_factors();
-                buf ^= 1;
-                if (buf == 0) bph ^= 1;
+                const bool last = kb % R::FB == R::FB - 1 || kb == kbs - 1;  // of the factor slot
+                __syncwarp();
+                arrive_if(smem_u32(&fempty[0]) + 8 * slot, lane == 0 && last);
+                slot = last ? (slot + 1) % R::SLOTS : slot;
+                bph ^= buf == BUFS - 1;
+                buf = buf == BUFS - 1 ? 0 : buf + 1;
             }
             if (!ok) break;
             const BlockTile w = block_tile<TM, TN>(args, tab, tile);
-            const int64_t first = 32 * q;
-            const int64_t rows = w.a_end - (w.a_row + first);  // the warp's rows to write
-            store_tile(args, stage, lane, w.d_row + first, (int)max(min(rows, (int64_t)32), (int64_t)0), w.n0 + 128 * half, acc);
+            const int64_t first = rank * 128 + 32 * q;
+            const int64_t rows = w.a_end - (w.a_row + first), n0 = w.n0 + HALF * half;
+            if (rows > 0 && n0 < args.N)
+                store_tile(args, &tmap_d, stage, lane, w.d_row + first, (int)min(rows, (int64_t)32), n0, acc);
         }
+        if (lane == 0) bulk_wait_all();
     }
 
     tc_fence_before();
     __syncwarp();
     __syncthreads();
+    cluster_sync();  // the peer's shared memory and TMEM stay live until the pair is done
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc(tmem_base, TMEM_COLS);
+        tmem_dealloc_pair(tmem_base, TMEM_COLS);
     }
 }
 
@@ -557,8 +661,9 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
 // host
 // ---------------------------------------------------------------------------
 static std::atomic<bool> g_block_set[64];
+static int g_block_pairs[64];
 
-static fp8dl_status block_gemm_setup(int dev) {
+static fp8dl_status block_gemm_setup(int dev, int sms) {
     if (g_block_set[dev].load(std::memory_order_acquire)) return FP8DL_OK;
     std::lock_guard<std::mutex> lock(init_mutex());
     if (g_block_set[dev].load(std::memory_order_relaxed)) return FP8DL_OK;
@@ -571,6 +676,24 @@ static fp8dl_status block_gemm_setup(int dev) {
         // the epilogue's larger register share comes out of the launch's registers
         if (fa.numRegs < bp::REGS_LAUNCH)
             return fail(FP8DL_ERR_CUDA, "block GEMM: built with %d registers, %d needed", fa.numRegs, bp::REGS_LAUNCH);
+        // persistent pairs: how many are resident at once
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(sms / 2 * 2), 1, 1);
+        cfg.blockDim = dim3(bp::THREADS, 1, 1);
+        cfg.dynamicSmemBytes = bp::SMEM_BYTES;
+        cudaLaunchAttribute at = {};
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = 2;
+        at.val.clusterDim.y = at.val.clusterDim.z = 1;
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, k, &cfg);
+        if (e != cudaSuccess || n < 1) {
+            cudaGetLastError();
+            return fail(FP8DL_ERR_UNSUPPORTED_DEVICE, "the block GEMM needs resident CTA-pair clusters");
+        }
+        g_block_pairs[dev] = g_block_pairs[dev] == 0 || n < g_block_pairs[dev] ? n : g_block_pairs[dev];
     }
     g_block_set[dev].store(true, std::memory_order_release);
     return FP8DL_OK;
@@ -589,25 +712,32 @@ static fp8dl_status check_block_gemm(const uint8_t *A, int32_t a_dtype, const fl
 
 // rows_b: rows of B in memory (all groups'); a_rows: rows of A.
 static fp8dl_status launch_block_gemm(const uint8_t *A, int32_t a_dtype, int64_t a_rows, const uint8_t *B,
-                                      int32_t b_dtype, int64_t b_rows, bool brows, int64_t tiles_bound,
-                                      BlockGemmArgs &args, cudaStream_t st, bool pdl, const char *what) {
+                                      int32_t b_dtype, int64_t b_rows, bool brows, BlockGemmArgs &args,
+                                      cudaStream_t st, bool pdl, const char *what) {
     int dev = 0, sms = 0;
     FP8DL_TRY(current_device(&dev, &sms));
-    FP8DL_TRY(block_gemm_setup(dev));
-    CUtensorMap ta, tb;
-    FP8DL_TRY(encode_tmap_2d_u8(&ta, A, (uint64_t)args.K, (uint64_t)a_rows, (uint64_t)args.K, bp::BK, bp::TM,
+    FP8DL_TRY(block_gemm_setup(dev, sms));
+    CUtensorMap ta, tb, td;
+    FP8DL_TRY(encode_tmap_2d_u8(&ta, A, (uint64_t)args.K, (uint64_t)a_rows, (uint64_t)args.K, bp::BK, 128,
                                 CU_TENSOR_MAP_SWIZZLE_128B));
-    FP8DL_TRY(encode_tmap_2d_u8(&tb, B, (uint64_t)args.K, (uint64_t)b_rows, (uint64_t)args.K, bp::BK, bp::TN,
+    FP8DL_TRY(encode_tmap_2d_u8(&tb, B, (uint64_t)args.K, (uint64_t)b_rows, (uint64_t)args.K, bp::BK, bp::B_ROWS,
                                 CU_TENSOR_MAP_SWIZZLE_128B));
+    const uint64_t d_ld = (uint64_t)args.N * (args.d_dtype == FP8DL_BF16 ? 2 : 4);
+    FP8DL_TRY(encode_tmap_2d_u8(&td, args.D, d_ld, (uint64_t)(args.kind == BG_REDUCE ? args.n_groups * args.M : args.M), d_ld, 128,
+                                32, CU_TENSOR_MAP_SWIZZLE_128B));
     args.idesc = (1u << 4) | ((uint32_t)a_dtype << 7) | ((uint32_t)b_dtype << 10) | ((uint32_t)(bp::TN >> 3) << 17) |
                  ((uint32_t)(bp::TM >> 4) << 24);
     const int64_t tiles_m = (args.M + bp::TM - 1) / bp::TM, tiles_n = (args.N + bp::TN - 1) / bp::TN;
     args.along_n = 0;
-    args.band = 16;
-    if (tiles_bound > 0x7fffffffll) return fail(FP8DL_ERR_SHAPE, "%s: more than 2^31 - 1 output tiles", what);
-    (void)launch_kernel(brows ? block_gemm_kernel<true> : block_gemm_kernel<false>,
-                        dim3((unsigned)(tiles_bound < sms ? tiles_bound : sms)), bp::THREADS, bp::SMEM_BYTES, st, 0, pdl, ta,
-                        tb, args);
+    args.band = 8;
+    const int64_t busy = args.n_groups < args.M ? args.n_groups : args.M;  // groups that can hold a row
+    const int64_t bound = args.kind == BG_DENSE  ? tiles_m * tiles_n
+                          : args.kind == BG_ROWS ? (args.M / bp::TM + busy) * tiles_n
+                                                 : args.n_groups * tiles_m * tiles_n;
+    if (bound > 0x7fffffffll) return fail(FP8DL_ERR_SHAPE, "%s: more than 2^31 - 1 output tiles", what);
+    const int64_t pairs = bound < g_block_pairs[dev] ? bound : g_block_pairs[dev];
+    (void)launch_kernel(brows ? block_gemm_kernel<true> : block_gemm_kernel<false>, dim3((unsigned)(2 * pairs)),
+                        bp::THREADS, bp::SMEM_BYTES, st, 2, pdl, ta, tb, td, args);
     note_launch();
     return check_launch(what);
 }
@@ -644,8 +774,7 @@ extern "C" fp8dl_status fp8_block_gemm(const uint8_t *A, int32_t a_dtype, const 
     a.D = D;
     a.d_dtype = d_dtype;
     a.status = dev_status;
-    const int64_t tiles = ((M + bp::TM - 1) / bp::TM) * ((N + bp::TN - 1) / bp::TN);
-    return launch_block_gemm(A, a_dtype, M, B, b_dtype, N, b_rows == 1, tiles, a, (cudaStream_t)stream,
+    return launch_block_gemm(A, a_dtype, M, B, b_dtype, N, b_rows == 1, a, (cudaStream_t)stream,
                              short_call_flops(2.0 * (double)M * (double)N * (double)K), "fp8_block_gemm");
 }
 
@@ -677,9 +806,7 @@ extern "C" fp8dl_status fp8_block_gemm_grouped(const uint8_t *A, int32_t a_dtype
     a.D = D;
     a.d_dtype = d_dtype;
     a.status = dev_status;
-    const int64_t busy = n_groups < M ? n_groups : M;  // groups that can hold a row
-    const int64_t tiles = (M / bp::TM + busy) * ((N + bp::TN - 1) / bp::TN);
-    return launch_block_gemm(A, a_dtype, M, B, b_dtype, N * n_groups, false, tiles, a, (cudaStream_t)stream,
+    return launch_block_gemm(A, a_dtype, M, B, b_dtype, N * n_groups, false, a, (cudaStream_t)stream,
                              short_call_flops(2.0 * (double)M * (double)N * (double)K), "fp8_block_gemm_grouped");
 }
 
@@ -717,7 +844,6 @@ extern "C" fp8dl_status fp8_block_gemm_grouped_wgrad(const uint8_t *A, int32_t a
     a.D = D;
     a.d_dtype = d_dtype;
     a.status = dev_status;
-    const int64_t tiles = n_groups * ((M + bp::TM - 1) / bp::TM) * ((N + bp::TN - 1) / bp::TN);
-    return launch_block_gemm(A, a_dtype, M, B, b_dtype, N, true, tiles, a, st,
+    return launch_block_gemm(A, a_dtype, M, B, b_dtype, N, true, a, st,
                              short_call_flops(2.0 * (double)M * (double)N * (double)T), "fp8_block_gemm_grouped_wgrad");
 }
