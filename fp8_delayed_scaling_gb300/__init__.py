@@ -382,26 +382,21 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _tensor(t, dtype, shape, name: str):
-    """t (or None) is a contiguous tensor of this dtype and shape; returns its device."""
+def _tensor(t, dtype, shape, dev: int, name: str):
+    """Address of t, a contiguous tensor of this dtype and shape on device `dev` (or None)."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s tensor of shape %s, got %s %s%s" % (
-            name, dtype, shape, t.dtype, tuple(t.shape), "" if t.is_contiguous() else " (strided)"))
-    return t.device
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on the device of the others, got %s %s on %s%s" % (
+            name, dtype, tuple(shape), t.dtype, tuple(t.shape), t.device, "" if t.is_contiguous() else ", strided"))
+    return t.data_ptr()
 
 
-def _one_device(devices) -> None:
-    """All tensors live on the current CUDA device (the one the kernels launch on)."""
-    have = {d for d in devices if d is not None}
-    if len(have) != 1 or next(iter(have)) != torch.device("cuda", torch.cuda.current_device() if torch.cuda.is_available() else 0):
-        raise ValueError("all tensors must be on the current CUDA device, got %s" % sorted(map(str, have)))
-
-
-def _offsets(offsets, name="offsets"):
-    _need(offsets.dim() == 1 and offsets.numel() >= 2, "%s must hold n_groups + 1 entries" % name)
-    return _tensor(offsets, torch.int32, (offsets.numel(),), name)
+def _launch(dev: int, stream):
+    """The stream to launch on; the tensors must be on the current CUDA device, where the kernels run."""
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("the tensors must be on the current CUDA device, got %s" % ("cuda:%d" % dev if dev >= 0 else "CPU tensors"))
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _blocks(n: int) -> int:
@@ -422,15 +417,16 @@ def fp8_block_quantize(x: torch.Tensor, out_dtype: int, row_q=None, row_s=None, 
     _need(x.dim() == 2 and x.is_contiguous(), "x must be a contiguous matrix")
     rows, cols = x.shape
     groups = 0 if offsets is None else offsets.numel() - 1
-    T = fp8_block_padded_rows(rows, groups)
-    _one_device((x.device, _tensor(row_q, torch.uint8, (rows, cols), "row_q"),
-                 _tensor(row_s, torch.float32, (_blocks(cols), rows), "row_s"),
-                 _tensor(col_q, torch.uint8, (cols, T), "col_q"),
-                 _tensor(col_s, torch.float32, (T // 128, cols), "col_s"),
-                 None if offsets is None else _offsets(offsets), _tensor(dbias, torch.float32, (cols,), "dbias")))
-    _check(_lib.fp8_block_quantize(_p(x), _hp(x), rows, cols, _p(offsets), groups, out_dtype, _p(row_q), _p(row_s),
-                                   _p(col_q), _p(col_s), _p(dbias), _p(workspace), _nbytes(workspace),
-                                   _stream(stream)), "fp8_block_quantize")
+    _need(groups >= 1 or offsets is None, "offsets must hold n_groups + 1 entries")
+    dev, T = x.get_device(), _lib.fp8_block_padded_rows(rows, groups)
+    _need(workspace is None or workspace.get_device() == dev, "workspace must be on the device of x")
+    args = (x.data_ptr(), _hp(x), rows, cols, _tensor(offsets, torch.int32, (groups + 1,), dev, "offsets"), groups,
+            out_dtype, _tensor(row_q, torch.uint8, (rows, cols), dev, "row_q"),
+            _tensor(row_s, torch.float32, (_blocks(cols), rows), dev, "row_s"),
+            _tensor(col_q, torch.uint8, (cols, T), dev, "col_q"),
+            _tensor(col_s, torch.float32, (T // 128, cols), dev, "col_s"),
+            _tensor(dbias, torch.float32, (cols,), dev, "dbias"), _p(workspace), _nbytes(workspace))
+    _check(_lib.fp8_block_quantize(*args, _launch(dev, stream)), "fp8_block_quantize")
 
 
 def fp8_block_quantize_weight(w: torch.Tensor, out_dtype: int, q=None, s=None, q_t=None, s_t=None,
@@ -439,12 +435,17 @@ def fp8_block_quantize_weight(w: torch.Tensor, out_dtype: int, q=None, s=None, q
     (the B operand of the forward product), and transposed, q_t [(E x) C x R] with s_t [(E x) R/128 x C/128] (dgrad)."""
     _need(w.dim() in (2, 3) and w.is_contiguous(), "w must be a contiguous [R x C] or [E x R x C] tensor")
     lead, (rows, cols) = tuple(w.shape[:-2]), w.shape[-2:]
-    _one_device((w.device, _tensor(q, torch.uint8, lead + (rows, cols), "q"),
-                 _tensor(s, torch.float32, lead + (_blocks(cols), _blocks(rows)), "s"),
-                 _tensor(q_t, torch.uint8, lead + (cols, rows), "q_t"),
-                 _tensor(s_t, torch.float32, lead + (_blocks(rows), _blocks(cols)), "s_t")))
-    _check(_lib.fp8_block_quantize_weight(_p(w), _hp(w), lead[0] if lead else 1, rows, cols, out_dtype, _p(q), _p(s),
-                                          _p(q_t), _p(s_t), _stream(stream)), "fp8_block_quantize_weight")
+    dev = w.get_device()
+    args = (w.data_ptr(), _hp(w), lead[0] if lead else 1, rows, cols, out_dtype,
+            _tensor(q, torch.uint8, lead + (rows, cols), dev, "q"),
+            _tensor(s, torch.float32, lead + (_blocks(cols), _blocks(rows)), dev, "s"),
+            _tensor(q_t, torch.uint8, lead + (cols, rows), dev, "q_t"),
+            _tensor(s_t, torch.float32, lead + (_blocks(rows), _blocks(cols)), dev, "s_t"))
+    _check(_lib.fp8_block_quantize_weight(*args, _launch(dev, stream)), "fp8_block_quantize_weight")
+
+
+def _status(dev_status, dev: int):
+    return None if dev_status is None else _tensor(dev_status, torch.int32, dev_status.shape, dev, "dev_status")
 
 
 def fp8_block_gemm(A: torch.Tensor, a_dtype: int, a_s: torch.Tensor, B: torch.Tensor, b_dtype: int, b_s: torch.Tensor,
@@ -452,15 +453,14 @@ def fp8_block_gemm(A: torch.Tensor, a_dtype: int, a_s: torch.Tensor, B: torch.Te
     """D[M,N] = sum over blocks of 128 of (A_blk * B_blk^T) * a_s * b_s, + bias.  A [M x K], a_s [K/128 x M];
     B [N x K], b_s [K/128 x N/128] (a weight) or [K/128 x N] (an activation or gradient)."""
     _need(A.dim() == 2 and B.dim() == 2 and A.shape[1] == B.shape[1], "A [M x K] and B [N x K] must share K")
-    (M, K), N = A.shape, B.shape[0]
-    b_rows = 1 if b_s.shape[-1] == N else 128
-    _one_device((_tensor(A, torch.uint8, (M, K), "A"), _tensor(a_s, torch.float32, (_blocks(K), M), "a_s"),
-                 _tensor(B, torch.uint8, (N, K), "B"),
-                 _tensor(b_s, torch.float32, (_blocks(K), N if b_rows == 1 else _blocks(N)), "b_s"),
-                 _tensor(D, D.dtype, (M, N), "D"), None if bias is None else _tensor(bias, bias.dtype, (N,), "bias")))
-    _check(_lib.fp8_block_gemm(_p(A), a_dtype, _p(a_s), _p(B), b_dtype, _p(b_s), b_rows, M, N, K, _p(bias),
-                               _hp(bias) if bias is not None else BF16, _p(D), _hp(D), _p(dev_status),
-                               _stream(stream)), "fp8_block_gemm")
+    (M, K), N, dev = A.shape, B.shape[0], A.get_device()
+    b_rows = 1 if b_s.shape[-1:] == (N,) else 128
+    args = (_tensor(A, torch.uint8, (M, K), dev, "A"), a_dtype, _tensor(a_s, torch.float32, (_blocks(K), M), dev, "a_s"),
+            _tensor(B, torch.uint8, (N, K), dev, "B"), b_dtype,
+            _tensor(b_s, torch.float32, (_blocks(K), N if b_rows == 1 else _blocks(N)), dev, "b_s"), b_rows, M, N, K,
+            None if bias is None else _tensor(bias, bias.dtype, (N,), dev, "bias"),
+            BF16 if bias is None else _hp(bias), _tensor(D, D.dtype, (M, N), dev, "D"), _hp(D), _status(dev_status, dev))
+    _check(_lib.fp8_block_gemm(*args, _launch(dev, stream)), "fp8_block_gemm")
 
 
 def fp8_block_gemm_grouped(A: torch.Tensor, a_dtype: int, a_s: torch.Tensor, B: torch.Tensor, b_dtype: int,
@@ -469,14 +469,13 @@ def fp8_block_gemm_grouped(A: torch.Tensor, a_dtype: int, a_s: torch.Tensor, B: 
     """D[m] = A[m] * B[g]^T for the rows m of group g: A [M x K], a_s [K/128 x M]; B [G x N x K],
     b_s [G x K/128 x N/128]; offsets int32 [G + 1]; D [M x N].  Rows outside the groups keep their values."""
     _need(A.dim() == 2 and B.dim() == 3 and A.shape[1] == B.shape[2], "A [M x K] and B [G x N x K] must share K")
-    (M, K), (G, N) = A.shape, B.shape[:2]
-    _need(offsets.numel() == G + 1, "offsets must hold %d entries, one more than B has matrices" % (G + 1))
-    _one_device((_tensor(A, torch.uint8, (M, K), "A"), _tensor(a_s, torch.float32, (_blocks(K), M), "a_s"),
-                 _tensor(B, torch.uint8, (G, N, K), "B"),
-                 _tensor(b_s, torch.float32, (G, _blocks(K), _blocks(N)), "b_s"), _offsets(offsets),
-                 _tensor(D, D.dtype, (M, N), "D")))
-    _check(_lib.fp8_block_gemm_grouped(_p(A), a_dtype, _p(a_s), _p(B), b_dtype, _p(b_s), _p(offsets), G, M, N, K,
-                                       _p(D), _hp(D), _p(dev_status), _stream(stream)), "fp8_block_gemm_grouped")
+    (M, K), (G, N, _), dev = A.shape, B.shape, A.get_device()
+    args = (_tensor(A, torch.uint8, (M, K), dev, "A"), a_dtype, _tensor(a_s, torch.float32, (_blocks(K), M), dev, "a_s"),
+            _tensor(B, torch.uint8, (G, N, K), dev, "B"), b_dtype,
+            _tensor(b_s, torch.float32, (G, _blocks(K), _blocks(N)), dev, "b_s"),
+            _tensor(offsets, torch.int32, (G + 1,), dev, "offsets"), G, M, N, K, _tensor(D, D.dtype, (M, N), dev, "D"),
+            _hp(D), _status(dev_status, dev))
+    _check(_lib.fp8_block_gemm_grouped(*args, _launch(dev, stream)), "fp8_block_gemm_grouped")
 
 
 def fp8_block_gemm_grouped_wgrad(A: torch.Tensor, a_dtype: int, a_s: torch.Tensor, B: torch.Tensor, b_dtype: int,
@@ -485,13 +484,12 @@ def fp8_block_gemm_grouped_wgrad(A: torch.Tensor, a_dtype: int, a_s: torch.Tenso
     """D[g] = A_g * B_g^T over group g's tokens: A [M x T], a_s [T/128 x M] and B [N x T], b_s [T/128 x N] are col_q and
     col_s of fp8_block_quantize with these offsets (int32 [G + 1]); D [G x M x N], zeros for a group without rows."""
     _need(A.dim() == 2 and B.dim() == 2 and A.shape[1] == B.shape[1], "A [M x T] and B [N x T] must share T")
-    (M, T), N, G = A.shape, B.shape[0], offsets.numel() - 1
-    _one_device((_tensor(A, torch.uint8, (M, T), "A"), _tensor(a_s, torch.float32, (_blocks(T), M), "a_s"),
-                 _tensor(B, torch.uint8, (N, T), "B"), _tensor(b_s, torch.float32, (_blocks(T), N), "b_s"),
-                 _offsets(offsets), _tensor(D, D.dtype, (G, M, N), "D")))
-    _check(_lib.fp8_block_gemm_grouped_wgrad(_p(A), a_dtype, _p(a_s), _p(B), b_dtype, _p(b_s), _p(offsets), G, M, N,
-                                             T, _p(D), _hp(D), _p(dev_status), _stream(stream)),
-           "fp8_block_gemm_grouped_wgrad")
+    (M, T), N, G, dev = A.shape, B.shape[0], offsets.numel() - 1, A.get_device()
+    args = (_tensor(A, torch.uint8, (M, T), dev, "A"), a_dtype, _tensor(a_s, torch.float32, (_blocks(T), M), dev, "a_s"),
+            _tensor(B, torch.uint8, (N, T), dev, "B"), b_dtype, _tensor(b_s, torch.float32, (_blocks(T), N), dev, "b_s"),
+            _tensor(offsets, torch.int32, (G + 1,), dev, "offsets"), G, M, N, T,
+            _tensor(D, D.dtype, (G, M, N), dev, "D"), _hp(D), _status(dev_status, dev))
+    _check(_lib.fp8_block_gemm_grouped_wgrad(*args, _launch(dev, stream)), "fp8_block_gemm_grouped_wgrad")
 
 
 # --------------------------------------------------------------------------

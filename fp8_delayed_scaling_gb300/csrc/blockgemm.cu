@@ -194,6 +194,25 @@ __device__ __forceinline__ void umma_block_pair(uint32_t d, uint64_t a, uint64_t
         : "memory");
 }
 
+// The same on one CTA.
+__device__ __forceinline__ void umma_block(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t tfull,
+                                                uint32_t empty) {
+    asm volatile(
+        "{\n\t.reg .pred e, t, f;\n\t.reg .b64 a, b;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.eq.u32 t, 0, 0;\n\tsetp.ne.u32 f, 0, 0;\n\t\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, f;\n\t"
+        "add.u64 a, %1, 2;\n\tadd.u64 b, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "add.u64 a, %1, 4;\n\tadd.u64 b, %2, 4;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "add.u64 a, %1, 6;\n\tadd.u64 b, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(tfull), "r"(empty)
+        : "memory");
+}
+
 // Arrive on an mbarrier of this CTA from the lanes with `who`, without a branch.
 __device__ __forceinline__ void arrive_if(uint32_t bar, bool who) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
@@ -244,6 +263,17 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+__device__ __forceinline__ float load_bias1(const BlockGemmArgs &a, int64_t n) {
+    return a.bias_dtype == FP8DL_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(a.bias)[n])
+                                      : static_cast<const float *>(a.bias)[n];
+}
+__device__ __forceinline__ void store1(const BlockGemmArgs &a, int64_t at, float v) {
+    if (a.d_dtype == FP8DL_BF16)
+        static_cast<__nv_bfloat16 *>(a.D)[at] = __float2bfloat16_rn(v);
+    else
+        static_cast<float *>(a.D)[at] = v;
+}
 
 // Sixteen consecutive columns' bias added to the sums, n = the first one's column of D.
 __device__ __forceinline__ void add_bias16(const BlockGemmArgs &a, int64_t n, float2 (&v)[8]) {
@@ -658,6 +688,290 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
 }
 
 // ---------------------------------------------------------------------------
+// Few rows of A (decoding, small groups of tokens): the weight takes the MMA's M side, 128 of its
+// rows a tile, and BT rows of A (16, 32 or 64) its N side, so that a tile computes little
+// more than the rows there are and the kernel runs at the speed the weight arrives.
+//   warp 0      TMA producer: 128 weight rows and BT rows of A per k-block
+//   warp 1      MMA thread: four MMAs (M 128, N BT, K 32) per block into one of NB buffers
+//   warp 2      copies the blocks' factors (one per row of A, one of the weight's) into a ring
+//   warps 4-7   epilogue: a thread holds one weight row x BT rows of A; the two factors are
+//               multiplied and applied per block as in the tile kernel
+// Split: where the tiles alone would leave SMs without a weight to read, the CTAs of a cluster
+// share a tile, each with a contiguous part of the blocks, and add their sums in rank order
+// through distributed shared memory: no workspace, one launch, the same bits every time.
+// Two CTAs fit an SM: one's start and end hide behind the other's loads.
+// ---------------------------------------------------------------------------
+namespace bf {
+constexpr int TW = 128, BK = 128;
+template <int BT>
+struct Shape {
+    static constexpr int EPI_WARPS = 4, THREADS = 32 * (4 + EPI_WARPS);
+    static constexpr int STAGE_BYTES = TW * BK + BT * BK;
+    static constexpr int STAGES = BT <= 32 ? 5 : 4;
+    static constexpr int NB = 4, TMEM_COLS = NB * BT;
+    static constexpr int RING = 8, SLOT = BT + 4;              // factors per block: BT of A's, one of B's
+    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + RING * SLOT * 4 + kGroupTableBytes + 1024;
+    static_assert(2 * SMEM_BYTES <= 227 * 1024 && 2 * TMEM_COLS <= 512, "two CTAs per SM");
+    static_assert(STAGES * STAGE_BYTES >= BT * TW * 4, "the sums of a split tile take the operands' place");
+};
+}  // namespace bf
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+template <int BT>
+__global__ void __launch_bounds__(bf::Shape<BT>::THREADS, 2)
+    block_gemm_few_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+                          const BlockGemmArgs args) {
+    using namespace bf;
+    using S = Shape<BT>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t *smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
+    uint8_t *bar_area = smem + S::STAGES * S::STAGE_BYTES;
+    uint64_t *full = reinterpret_cast<uint64_t *>(bar_area);
+    uint64_t *empty = full + S::STAGES;
+    uint64_t *tfull = empty + S::STAGES;
+    uint64_t *tempty = tfull + S::NB;
+    uint64_t *ffull = tempty + S::NB;
+    uint64_t *fempty = ffull + S::RING;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(fempty + S::RING);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    float *ring = reinterpret_cast<float *>(bar_area + 1024);
+    const GroupTables tab = group_tables(bar_area + 1024 + S::RING * S::SLOT * 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t split = cluster_nctarank(), rank = cluster_ctarank();
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::STAGES; i++) {
+            mbar_init(smem_u32(&full[i]), 1);
+            mbar_init(smem_u32(&empty[i]), 1);
+        }
+        for (int i = 0; i < S::NB; i++) {
+            mbar_init(smem_u32(&tfull[i]), 1);
+            mbar_init(smem_u32(&tempty[i]), S::EPI_WARPS);
+        }
+        for (int i = 0; i < S::RING; i++) {
+            mbar_init(smem_u32(&ffull[i]), 32);
+            mbar_init(smem_u32(&fempty[i]), S::EPI_WARPS);
+        }
+        *abort_flag = 0;
+        mbar_fence_init();
+        tma_prefetch_map(&tmap_a);
+        tma_prefetch_map(&tmap_b);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), S::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    pdl_wait();
+    pdl_trigger();
+    if (args.kind == BG_ROWS) build_groups(tab, args.offsets, args.n_groups, args.M, BT, 0x7fffffffll);
+    const uint32_t tiles = block_tiles<BT, TW>(args, tab);
+    const uint32_t tile0 = blockIdx.x / split, step = gridDim.x / split;  // a split launch has a tile per cluster at most
+    const int all_kbs = (int)((args.K + BK - 1) / BK);
+    const int kb0 = (int)((int64_t)all_kbs * rank / split), kb1 = (int)((int64_t)all_kbs * (rank + 1) / split);
+
+    if (warp == 0) {
+        if (lane == 0) {  // ---------------------------------------------------- producer
+            int s = 0;
+            uint32_t ph = 0;
+            int64_t issued = 0;
+            bool ok = true;
+            for (uint32_t tile = tile0; tile < tiles && ok; tile += step) {
+                const BlockTile w = block_tile<BT, TW>(args, tab, tile);
+                for (int kb = kb0; kb < kb1; kb++) {
+                    if (!mbar_wait(smem_u32(&empty[s]), ph ^ 1, abort_flag, args.status)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = smem_u32(&full[s]), dst = smem_u32(smem + s * S::STAGE_BYTES);
+                    mbar_expect_tx(fb, S::STAGE_BYTES);
+                    tma_load_2d(dst, &tmap_b, fb, kb * BK, (int32_t)w.b_row);
+                    tma_load_2d(dst + TW * BK, &tmap_a, fb, kb * BK, (int32_t)w.a_row);
+                    issued++;
+                    if (++s == S::STAGES) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            if (!ok)
+                for (int64_t i = issued - 1; i >= 0 && i >= issued - S::STAGES; i--)
+                    mbar_drain(smem_u32(&full[i % S::STAGES]), (uint32_t)((i / S::STAGES) & 1));
+        }
+    } else if (warp == 1) {  // ------------------------------------------------- MMA issuer
+        int s = 0, buf = 0;
+        uint32_t ph = 0, bph = 0;
+        bool ok = true, any = false;
+        uint32_t last_bar = 0, last_par = 0;
+        const SDesc desc0 = sdesc_k_sw128_split(smem_u32(smem));
+        for (uint32_t tile = tile0; tile < tiles && ok; tile += step) {
+            for (int kb = kb0; kb < kb1; kb++) {
+                if (!mbar_wait(smem_u32(&full[s]), ph, abort_flag, args.status) ||
+                    !mbar_wait(smem_u32(&tempty[buf]), bph ^ 1, abort_flag, args.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t lo = desc0.lo + (uint32_t)s * (S::STAGE_BYTES >> 4);
+                umma_block(tmem_base + (uint32_t)(buf * BT), sdesc_join(lo, desc0.hi),
+                           sdesc_join(lo + (TW * BK >> 4), desc0.hi), args.idesc, smem_u32(&tfull[0]) + 8 * buf,
+                           smem_u32(&empty[0]) + 8 * s);
+                any = true;
+                last_bar = smem_u32(&empty[s]);
+                last_par = ph;
+                if (++s == S::STAGES) {
+                    s = 0;
+                    ph ^= 1;
+                }
+                if (++buf == S::NB) {
+                    buf = 0;
+                    bph ^= 1;
+                }
+            }
+        }
+        if (!ok && any) mbar_drain(last_bar, last_par);
+    } else if (warp == 2) {  // ------------------------------------------------- factors
+        int slot = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (uint32_t tile = tile0; tile < tiles && ok; tile += step) {
+            const BlockTile w = block_tile<BT, TW>(args, tab, tile);
+            const float *pa = args.a_s + (int64_t)kb0 * args.M + w.a_row;
+            const float *pb = w.b_s + (int64_t)kb0 * args.b_ld + (w.n0 >> 7);
+            for (int kb = kb0; kb < kb1; kb++, pa += args.M, pb += args.b_ld) {
+                if (!mbar_wait(smem_u32(&fempty[slot]), ph ^ 1, abort_flag, args.status)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t dst = smem_u32(ring + slot * S::SLOT);
+#pragma unroll
+                for (int t = 0; t < BT; t += 32)  // rows behind the last take the first one's factor
+                    if (t + lane < BT) cp_async4(dst + 4 * (t + lane), pa + (w.a_row + t + lane < w.a_end ? t + lane : 0));
+                if (lane == 0) cp_async4(dst + 4 * BT, pb);
+                cp_async_arrive(smem_u32(&ffull[slot]));
+                if (++slot == S::RING) {
+                    slot = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+        cp_async_wait_all();
+    } else if (warp >= 4) {  // ------------------------------------------------- epilogue
+        const int q = warp & 3;
+        const int row = 32 * q + lane;  // of the weight tile
+        const uint32_t taddr0 = tmem_base + ((uint32_t)(32 * q) << 16);
+        int slot = 0, buf = 0;
+        uint32_t fph = 0, bph = 0;
+        for (uint32_t tile = tile0; tile < tiles; tile += step) {
+            float2 acc[BT / 2];
+#pragma unroll
+            for (int p = 0; p < BT / 2; p++) acc[p] = make_float2(0.0f, 0.0f);
+            bool ok = true;
+            for (int kb = kb0; kb < kb1; kb++) {
+                if (!mbar_wait(smem_u32(&ffull[slot]), fph, abort_flag, args.status) ||
+                    !mbar_wait(smem_u32(&tfull[buf]), bph, abort_flag, args.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t ta = taddr0 + (uint32_t)(buf * BT);
+                const float *fac = ring + slot * S::SLOT;
+                const float2 fb = f2(fac[BT]);
+                constexpr int LD = BT < 32 ? 16 : 32;
+#pragma unroll
+                for (int c = 0; c < BT; c += LD) {
+                    uint32_t r[LD];
+                    if constexpr (LD == 16)
+                        tmem_ld_32x32b_x16(ta + c, r);
+                    else
+                        tmem_ld_32x32b_x32(ta + c, r);
+                    tmem_ld_wait();
+                    regs_ready(r);
+#pragma unroll
+                    for (int j = 0; j < LD; j += 4) {
+                        const float4 fa = *reinterpret_cast<const float4 *>(fac + c + j);
+                        const float2 s0 = __fmul2_rn(make_float2(fa.x, fa.y), fb), s1 = __fmul2_rn(make_float2(fa.z, fa.w), fb);
+                        acc[(c + j) / 2] = __ffma2_rn(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), s0,
+                                                      acc[(c + j) / 2]);
+                        acc[(c + j) / 2 + 1] = __ffma2_rn(
+                            make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), s1, acc[(c + j) / 2 + 1]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                arrive_if(smem_u32(&tempty[buf]), lane == 0);
+                arrive_if(smem_u32(&fempty[slot]), lane == 0);
+                if (++slot == S::RING) {
+                    slot = 0;
+                    fph ^= 1;
+                }
+                if (++buf == S::NB) {
+                    buf = 0;
+                    bph ^= 1;
+                }
+            }
+            if (split > 1) {  // this rank's sums, where the operands were: all its MMAs are done
+                float *red = reinterpret_cast<float *>(smem);
+#pragma unroll
+                for (int p = 0; p < BT / 2; p++) {
+                    red[2 * p * TW + row] = acc[p].x;
+                    red[(2 * p + 1) * TW + row] = acc[p].y;
+                }
+                break;  // joined below; the one tile of this cluster
+            }
+            if (!ok) break;
+            const BlockTile w = block_tile<BT, TW>(args, tab, tile);
+            const int rows = (int)min(w.a_end - w.a_row, (int64_t)BT);
+            if (w.n0 + row < args.N) {
+                const float bias = args.bias_dtype >= 0 ? load_bias1(args, w.n0 + row) : 0.0f;
+                const int64_t at = w.d_row * args.N + w.n0 + row;
+#pragma unroll
+                for (int p = 0; p < BT / 2; p++) {
+                    if (2 * p < rows) store1(args, at + 2 * p * args.N, acc[p].x + bias);
+                    if (2 * p + 1 < rows) store1(args, at + (2 * p + 1) * args.N, acc[p].y + bias);
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncwarp();
+    __syncthreads();
+    if (split > 1) {
+        cluster_sync();  // every rank's sums are there
+        if (tile0 < tiles) {
+            const BlockTile w = block_tile<BT, TW>(args, tab, tile0);
+            const int rows = (int)min(w.a_end - w.a_row, (int64_t)BT);
+            const uint32_t red = smem_u32(smem);
+            // rank r joins every split-th row of A, 128 consecutive columns of D per row
+            for (int i = threadIdx.x; i < (BT / (int)split) * TW; i += S::THREADS) {
+                const int t = (i / TW) * (int)split + (int)rank, col = i % TW;
+                if (t >= rows || w.n0 + col >= args.N) continue;
+                float v = 0.0f;
+                for (uint32_t r = 0; r < split; r++) v += ld_cluster_f32(mapa_shared(red + 4 * (t * TW + col), r));
+                if (args.bias_dtype >= 0) v += load_bias1(args, w.n0 + col);
+                store1(args, (w.d_row + t) * args.N + w.n0 + col, v);
+            }
+        }
+        cluster_sync();  // nobody's sums go away while they are read
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem_base, S::TMEM_COLS);
+    }
+}
+
+// ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
 static std::atomic<bool> g_block_set[64];
@@ -695,8 +1009,71 @@ static fp8dl_status block_gemm_setup(int dev, int sms) {
         }
         g_block_pairs[dev] = g_block_pairs[dev] == 0 || n < g_block_pairs[dev] ? n : g_block_pairs[dev];
     }
+    const void *few[] = {(const void *)block_gemm_few_kernel<16>, (const void *)block_gemm_few_kernel<32>,
+                         (const void *)block_gemm_few_kernel<64>};
+    const int bytes[] = {bf::Shape<16>::SMEM_BYTES, bf::Shape<32>::SMEM_BYTES, bf::Shape<64>::SMEM_BYTES};
+    for (int i = 0; i < 3; i++) {
+        const cudaError_t e = cudaFuncSetAttribute(few[i], cudaFuncAttributeMaxDynamicSharedMemorySize, bytes[i]);
+        if (e != cudaSuccess) return fail(FP8DL_ERR_CUDA, "block GEMM set-up: %s", cudaGetErrorString(e));
+    }
     g_block_set[dev].store(true, std::memory_order_release);
     return FP8DL_OK;
+}
+
+// Rows of A per tile of the few-row kernel, or 0 for the 256 x 256 tiles.  Times in us, weights from
+// DRAM, 16 / 32 / 64 rows a tile against 256 x 256 tiles:
+//   N 4096, K 4096      M 1: 7.2 / 7.5 / 8.4, 17.8;  M 64: 10.2 / 9.3 / 10.0, 17.4;  M 256: - / 15.2 / 17.3, 18.1;
+//                       M 384: - / - / 21.0, 18.2
+//   N 2048, K 7168      M 512: - / - / 22.7, 26.8;  M 768: no gain
+//   N 11008, K 4096     M 48: 13.7 / 15.9 / 17.6, 19.5;  M 96: 22.7 / 16.3 / 21.8, 19.6;  M 128: 30.8 / 24.5 / 21.7, 19.9
+//   N 16384, K 4096     M 32: 16.3 / 18.4 / 19.2, 21.2;  M 64: 23.2 / 17.6 / 21.2, 21.7;  M 96: 31.9 / 26.8 / 22.7, 22.0
+//   64 groups, N 2048, K 4096, rows a group  16: 105 / 107 / 113, 138;  64: 146 / 113 / 117, 138;
+//                       96: 207 / 140 / 142, 139;  128: 269 / 171 / 141, 142
+// One product: the fewest rows a tile whose tiles run at once (or all rows in one tile), up to
+// 96 rows; more rows only while 256 x 256 tiles would occupy no more than 16 of the 76 pairs.
+// Groups: by their mean length (the host does not see the offsets).
+static int few_rows(const BlockGemmArgs &a, int sms) {
+    if (a.kind == BG_REDUCE) return 0;
+    if (a.kind == BG_ROWS) {
+        const int64_t busy = a.n_groups < a.M ? a.n_groups : a.M;
+        const int64_t mean = (a.M + busy - 1) / busy;
+        return mean <= 16 ? 16 : mean <= 48 ? 32 : mean <= 96 ? 64 : 0;
+    }
+    const int64_t pair_tiles = ((a.M + bp::TM - 1) / bp::TM) * ((a.N + bp::TN - 1) / bp::TN);
+    if (a.M > 96 && pair_tiles > 16) return 0;
+    for (int bt = 16; bt <= 64; bt *= 2) {
+        const int64_t row_tiles = (a.M + bt - 1) / bt;
+        if (row_tiles == 1 || row_tiles * ((a.N + bf::TW - 1) / bf::TW) <= 2 * sms) return bt;
+    }
+    return a.M <= 64 ? 64 : 0;
+}
+
+template <int BT>
+static fp8dl_status launch_few(const uint8_t *A, int32_t a_dtype, const uint8_t *B, int32_t b_dtype, int64_t b_rows,
+                               BlockGemmArgs &args, int sms, cudaStream_t st, bool pdl, const char *what) {
+    using S = bf::Shape<BT>;
+    CUtensorMap ta, tb;
+    FP8DL_TRY(encode_tmap_2d_u8(&ta, A, (uint64_t)args.K, (uint64_t)args.M, (uint64_t)args.K, bf::BK, BT,
+                                CU_TENSOR_MAP_SWIZZLE_128B));
+    FP8DL_TRY(encode_tmap_2d_u8(&tb, B, (uint64_t)args.K, (uint64_t)b_rows, (uint64_t)args.K, bf::BK, bf::TW,
+                                CU_TENSOR_MAP_SWIZZLE_128B));
+    args.idesc = (1u << 4) | ((uint32_t)b_dtype << 7) | ((uint32_t)a_dtype << 10) | ((uint32_t)(BT >> 3) << 17) |
+                 ((uint32_t)(bf::TW >> 4) << 24);
+    const int64_t tiles_w = (args.N + bf::TW - 1) / bf::TW;
+    const int64_t busy = args.n_groups < args.M ? args.n_groups : args.M;
+    const int64_t bound = args.kind == BG_DENSE ? (args.M + BT - 1) / BT * tiles_w : (args.M / BT + busy) * tiles_w;
+    if (bound > 0x7fffffffll) return fail(FP8DL_ERR_SHAPE, "%s: more than 2^31 - 1 output tiles", what);
+    args.along_n = 0;  // the token tiles of a weight tile follow one another
+    args.band = 0x7fffffffu;
+    // Split a tile's blocks over a cluster while the CTAs fit the SMs together and each keeps
+    // four blocks at least.
+    const int64_t resident = 2 * (int64_t)sms, kbs = (args.K + 127) / 128;
+    int split = 1;
+    while (split < 8 && bound * split * 2 <= resident && kbs >= 8 * split) split *= 2;
+    const int64_t ctas = split > 1 ? bound * split : bound < resident ? bound : resident;
+    (void)launch_kernel(block_gemm_few_kernel<BT>, dim3((unsigned)ctas), S::THREADS, S::SMEM_BYTES, st, split, pdl, ta, tb, args);
+    note_launch();
+    return check_launch(what);
 }
 
 static fp8dl_status check_block_gemm(const uint8_t *A, int32_t a_dtype, const float *a_s, const uint8_t *B,
@@ -717,6 +1094,10 @@ static fp8dl_status launch_block_gemm(const uint8_t *A, int32_t a_dtype, int64_t
     int dev = 0, sms = 0;
     FP8DL_TRY(current_device(&dev, &sms));
     FP8DL_TRY(block_gemm_setup(dev, sms));
+    const int bt = brows ? 0 : few_rows(args, sms);
+    if (bt == 16) return launch_few<16>(A, a_dtype, B, b_dtype, b_rows, args, sms, st, pdl, what);
+    if (bt == 32) return launch_few<32>(A, a_dtype, B, b_dtype, b_rows, args, sms, st, pdl, what);
+    if (bt == 64) return launch_few<64>(A, a_dtype, B, b_dtype, b_rows, args, sms, st, pdl, what);
     CUtensorMap ta, tb, td;
     FP8DL_TRY(encode_tmap_2d_u8(&ta, A, (uint64_t)args.K, (uint64_t)a_rows, (uint64_t)args.K, bp::BK, 128,
                                 CU_TENSOR_MAP_SWIZZLE_128B));
@@ -816,8 +1197,8 @@ extern "C" fp8dl_status fp8_block_gemm_grouped_wgrad(const uint8_t *A, int32_t a
                                                      int64_t T, void *D, int32_t d_dtype, int32_t *dev_status,
                                                      fp8dl_stream_t stream) {
     FP8DL_NVTX("fp8_block_gemm_grouped_wgrad");
-    if (!dim_ok(M, 1) || !block_tokens_ok(M) || !dim_ok(N, 16) || !block_tokens_ok(T) || T % 128 != 0)
-        return fail(FP8DL_ERR_SHAPE, "M (%lld) must be positive, N (%lld) a positive multiple of 16 and T (%lld) a multiple of 128",
+    if (!dim_ok(M, 1) || !block_tokens_ok(M) || !block_tokens_ok(M * (n_groups < 1 ? 1 : n_groups)) || !dim_ok(N, 16) || !block_tokens_ok(T) || T % 128 != 0)
+        return fail(FP8DL_ERR_SHAPE, "M (%lld) must be positive, n_groups * M below 2^31, N (%lld) a positive multiple of 16 and T (%lld) a multiple of 128",
                     (long long)M, (long long)N, (long long)T);
     FP8DL_TRY(check_block_groups(offsets, n_groups, false));
     FP8DL_CHECK_ARG(D, "D is NULL");
