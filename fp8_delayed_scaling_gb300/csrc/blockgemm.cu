@@ -316,7 +316,7 @@ namespace bp {
 constexpr int TM = 256, TN = 256, HALF = 128, BK = 128, STAGES = 4, BUFS = 2;
 constexpr int A_BYTES = 128 * BK, B_ROWS = TN / 2, STAGE_BYTES = A_BYTES + B_ROWS * BK;
 constexpr int THREADS = 384, EPI_WARPS = 8;
-constexpr int REGS_LAUNCH = 168, REGS_IO = 56, REGS_EPI = 224;  // 128 * 56 + 256 * 224 = 384 * 168
+constexpr int REGS_LAUNCH = 168, REGS_IO = 72, REGS_EPI = 216;  // 128 * 72 + 256 * 216 = 384 * 168
 static_assert(128 * REGS_IO + 256 * REGS_EPI <= THREADS * REGS_LAUNCH, "register split");
 constexpr int TMEM_COLS = 512;
 // The factors of the next blocks, FB blocks per ring slot: 128 of A's, then one per column half
@@ -329,9 +329,22 @@ struct Ring {
 constexpr int RING_BYTES = Ring<true>::SLOTS * Ring<true>::SLOT * 4;
 // One warp's 32 rows x 256 bytes of D on their way out, as two boxes of 128 bytes.
 constexpr int OUT_BOX = 32 * 128, OUT_WARP = 2 * OUT_BOX, OUT_BYTES = EPI_WARPS * OUT_WARP;
+// What the epilogue needs of a tile, decoded by the relay warp (the decoding's divisions took
+// 600-900 cycles at each tile's end): the CTA's first row of D, how many rows are its to write,
+// the first column.  The relay is at most four blocks ahead of the epilogue, four tiles if
+// each has one block.
+struct TileOut {
+    int64_t d_row, n0;
+    int64_t rows;
+};
+constexpr int TILE_RING = 8;
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + OUT_BYTES + 1024 + RING_BYTES + kGroupTableBytes + 1024;
 static_assert(SMEM_BYTES <= 227 * 1024 && Ring<false>::SLOTS * Ring<false>::SLOT * 4 <= RING_BYTES, "shared memory");
 }  // namespace bp
+
+__device__ __forceinline__ bp::TileOut tile_out_of(const BlockTile &w, uint32_t rank) {
+    return {w.d_row + rank * 128, w.n0, w.a_end - (w.a_row + rank * 128)};
+}
 
 // One warp's 32 rows x 128 columns of D (lane = row): rounded once, laid out in shared memory as
 // boxes of 128 bytes a row (16-byte chunk j of row r at j ^ (r & 7): the TMA's 128-byte
@@ -401,6 +414,23 @@ __device__ __forceinline__ void store_tile(const BlockGemmArgs &a, const CUtenso
     }
 }
 
+// acc[C .. C+L) += r * factor: the factor sc, or (BROWS) sc times the columns' own.
+template <bool BROWS, int C, int L>
+__device__ __forceinline__ void add_block(float2 (&acc)[64], const uint32_t (&r)[L], float2 sc, const float *fb) {
+#pragma unroll
+    for (int j = 0; j < L; j += 4) {
+        float2 g0 = sc, g1 = sc;
+        if (BROWS) {
+            const float4 u = *reinterpret_cast<const float4 *>(fb + C + j);
+            g0 = __fmul2_rn(sc, make_float2(u.x, u.y));
+            g1 = __fmul2_rn(sc, make_float2(u.z, u.w));
+        }
+        float2 &a = acc[(C + j) / 2], &b = acc[(C + j) / 2 + 1];
+        a = __ffma2_rn(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), g0, a);
+        b = __ffma2_rn(make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), g1, b);
+    }
+}
+
 template <bool BROWS>
 __global__ void __launch_bounds__(bp::THREADS, 1)
     block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
@@ -418,6 +448,7 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
     uint64_t *tempty = tfull + BUFS;
     uint64_t *ffull = tempty + BUFS;
     uint64_t *fempty = ffull + R::SLOTS;
+    TileOut *tile_out = reinterpret_cast<TileOut *>(bar_area + 512);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(fempty + R::SLOTS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     float *ring = reinterpret_cast<float *>(bar_area + 1024);
@@ -583,8 +614,12 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
             int slot = 0, buf = 0;
             uint32_t fph = 0, bph = 0;
             bool ok = true;
-            for (uint32_t tile = pair; tile < tiles && ok; tile += npairs) {
-                const int kbs = block_tile_kbs<TM, TN>(args, tab, tile);
+            uint32_t seq = 0;
+            for (uint32_t tile = pair; tile < tiles && ok; tile += npairs, seq++) {
+                const BlockTile w = block_tile<TM, TN>(args, tab, tile);
+                const int kbs = w.kbs;
+                if (lane == 0 && kbs > 0)  // handed over with the first block's arrival
+                    tile_out[seq % TILE_RING] = tile_out_of(w, rank);
                 for (int kb = 0; kb < kbs; kb++) {
                     if (kb % R::FB == 0) {
                         ok = mbar_wait(smem_u32(&ffull[slot]), fph, abort_flag, args.status);
@@ -611,8 +646,8 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
         const float *my_a = ring + 32 * q + lane, *my_b = ring + 128 + (BROWS ? HALF : 1) * half;
         const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
         int slot = 0, buf = 0;
-        uint32_t bph = 0;
-        for (uint32_t tile = pair; tile < tiles; tile += npairs) {
+        uint32_t bph = 0, seq = 0;
+        for (uint32_t tile = pair; tile < tiles; tile += npairs, seq++) {
             const int kbs = block_tile_kbs<TM, TN>(args, tab, tile);
             float2 acc[64];
 #pragma unroll
@@ -623,42 +658,31 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
                 ok = mbar_wait(smem_u32(&tfull[0]) + 8 * buf, bph, abort_flag, args.status);
                 tc_fence_after();
                 const uint32_t ta = taddr0 + (uint32_t)(buf * TN);
-                uint32_t r[2][32];
-                tmem_ld_32x32b_x32(ta, r[0]);
-                tmem_ld_32x32b_x32(ta + 32, r[1]);
+                // Columns 0-31, 32-47, 48-79, 80-95, 96-127 through two sets of registers (48 beside
+                // the 128 sums: with 64 the compiler spills).  The buffer goes back as soon as the last
+                // ones are loaded, before their multiply-adds and those of columns 80-95.
+                uint32_t ra[32], rb[16];
+                tmem_ld_32x32b_x32(ta, ra);
+                tmem_ld_32x32b_x16(ta + 32, rb);
                 const int at = slot * R::SLOT + (kb % R::FB) * R::BLOCK;
                 const float *fb = my_b + at;  // BROWS: the block's column factors
                 const float2 sc = f2(BROWS ? my_a[at] : __fmul_rn(my_a[at], fb[0]));
-                tmem_ld_wait_regs(r[0]);
-                regs_ready(r[1]);
-                // Chunks of 32 columns.  The buffer goes back as soon as the last one is in registers,
-                // and only two chunks' multiply-adds come before that.
-#pragma unroll
-                for (int c = 0; c < 4; c++) {
-                    if (c == 2) {
-                        tmem_ld_32x32b_x32(ta + 96, r[1]);
-                        tmem_ld_wait_regs(r[0]);
-                        regs_ready(r[1]);
-                        tc_fence_before();
-                        __syncwarp();
-                        arrive_remote_if(tempty0 + 8 * buf, lane == 0);
-                    }
-#pragma unroll
-                    for (int p = 0; p < 16; p += 2) {
-                        float2 g0 = sc, g1 = sc;
-                        if (BROWS) {
-                            const float4 u = *reinterpret_cast<const float4 *>(fb + 32 * c + 2 * p);
-                            g0 = __fmul2_rn(sc, make_float2(u.x, u.y));
-                            g1 = __fmul2_rn(sc, make_float2(u.z, u.w));
-                        }
-                        const uint32_t *t = r[c & 1] + 2 * p;
-                        acc[16 * c + p] =
-                            __ffma2_rn(make_float2(__uint_as_float(t[0]), __uint_as_float(t[1])), g0, acc[16 * c + p]);
-                        acc[16 * c + p + 1] =
-                            __ffma2_rn(make_float2(__uint_as_float(t[2]), __uint_as_float(t[3])), g1, acc[16 * c + p + 1]);
-                    }
-                    if (c == 0) tmem_ld_32x32b_x32(ta + 64, r[0]);
-                }
+                tmem_ld_wait_regs(ra);
+                regs_ready(rb);
+                add_block<BROWS, 0>(acc, ra, sc, fb);
+                tmem_ld_32x32b_x32(ta + 48, ra);
+                add_block<BROWS, 32>(acc, rb, sc, fb);
+                tmem_ld_32x32b_x16(ta + 80, rb);
+                tmem_ld_wait_regs(ra);
+                regs_ready(rb);
+                add_block<BROWS, 48>(acc, ra, sc, fb);
+                tmem_ld_32x32b_x32(ta + 96, ra);
+                tmem_ld_wait_regs(ra);
+                tc_fence_before();
+                __syncwarp();
+                arrive_remote_if(tempty0 + 8 * buf, lane == 0);
+                add_block<BROWS, 80>(acc, rb, sc, fb);
+                add_block<BROWS, 96>(acc, ra, sc, fb);
                 const bool last = kb % R::FB == R::FB - 1 || kb == kbs - 1;  // of the factor slot
                 __syncwarp();
                 arrive_if(smem_u32(&fempty[0]) + 8 * slot, lane == 0 && last);
@@ -667,11 +691,11 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
                 buf = buf == BUFS - 1 ? 0 : buf + 1;
             }
             if (!ok) break;
-            const BlockTile w = block_tile<TM, TN>(args, tab, tile);
-            const int64_t first = rank * 128 + 32 * q;
-            const int64_t rows = w.a_end - (w.a_row + first), n0 = w.n0 + HALF * half;
+            const TileOut out = kbs > 0 ? tile_out[seq % TILE_RING]
+                                        : tile_out_of(block_tile<TM, TN>(args, tab, tile), rank);  // nothing to sum: zeros
+            const int64_t rows = out.rows - 32 * q, n0 = out.n0 + HALF * half;
             if (rows > 0 && n0 < args.N)
-                store_tile(args, &tmap_d, stage, lane, w.d_row + first, (int)min(rows, (int64_t)32), n0, acc);
+                store_tile(args, &tmap_d, stage, lane, out.d_row + 32 * q, (int)min(rows, (int64_t)32), n0, acc);
         }
         if (lane == 0) bulk_wait_all();
     }

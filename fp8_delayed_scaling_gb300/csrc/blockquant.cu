@@ -43,10 +43,66 @@ __device__ __forceinline__ float finite_abs(float v) {
     return a <= 3.402823466e38f ? a : 0.0f;
 }
 
+// A thread's 8 x 8 values as they were loaded: bf16 stays packed (32 registers instead of 64, so
+// three CTAs fit an SM and their loads overlap), and its maxima are taken on the packed words.
+template <int XKIND>
+struct Values;
+template <>
+struct Values<FP8DL_BF16> {
+    uint32_t w[8][4];
+    __device__ __forceinline__ void load(int i, const char *p, bool ok) {
+        const uint4 u = ok ? ldg_stream(p) : make_uint4(0u, 0u, 0u, 0u);
+        w[i][0] = u.x, w[i][1] = u.y, w[i][2] = u.z, w[i][3] = u.w;
+    }
+    __device__ __forceinline__ float2 pair(int i, int q) const { return make_float2(bf16_lo(w[i][q]), bf16_hi(w[i][q])); }
+    __device__ __forceinline__ void maxima(float (&rmax)[8], float (&cmax)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const uint32_t m = bf16x2_absmax(bf16x2_absmax(w[i][0], w[i][1]), bf16x2_absmax(w[i][2], w[i][3]));
+            rmax[i] = fmaxf(fabsf(bf16_lo(m)), fabsf(bf16_hi(m)));
+        }
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            uint32_t m = w[0][q];
+#pragma unroll
+            for (int i = 1; i < 8; i++) m = bf16x2_absmax(m, w[i][q]);
+            cmax[2 * q] = fabsf(bf16_lo(m)), cmax[2 * q + 1] = fabsf(bf16_hi(m));
+        }
+    }
+};
+template <>
+struct Values<FP8DL_F32> {
+    float2 v[8][4];
+    __device__ __forceinline__ void load(int i, const char *p, bool ok) {
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const uint4 u = ok ? ldg_stream(p + 16 * h) : make_uint4(0u, 0u, 0u, 0u);
+            v[i][2 * h] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+            v[i][2 * h + 1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+        }
+    }
+    __device__ __forceinline__ float2 pair(int i, int q) const { return v[i][q]; }
+    __device__ __forceinline__ void maxima(float (&rmax)[8], float (&cmax)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; i++) rmax[i] = cmax[i] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const float a = fabsf(v[i][q].x), b = fabsf(v[i][q].y);  // fmaxf ignores NaN
+                rmax[i] = fmaxf(rmax[i], fmaxf(a, b));
+                cmax[2 * q] = fmaxf(cmax[2 * q], a);
+                cmax[2 * q + 1] = fmaxf(cmax[2 * q + 1], b);
+            }
+    }
+};
+
 // One CTA converts one 128 x 128 tile: x is read once, both copies of the codes are written.
 //   Threads  16 x 16, thread (rr, cc) holds rows 8rr .. 8rr+7 and columns 8cc .. 8cc+7: its
 //            eight loads are 16 (bf16) or 32 (fp32) bytes and a warp covers whole 128-byte
 //            lines; all eight are in flight at once.
+//   Maxima   ignoring NaN; where an infinity shows up the thread takes them again over its
+//            finite values.
 //   Row      maxima over the 16 lanes of a half-warp by a halving exchange (8 shuffles for
 //   blocks   8 rows instead of 32), after which each lane owns one row's maximum, takes its
 //            scale once and the others fetch it by shuffle.
@@ -58,9 +114,10 @@ __device__ __forceinline__ float finite_abs(float v) {
 //            8-byte chunks XOR-swizzled by column group (conflict-free both ways), and leave
 //            as whole 128-byte lines.
 // WEIGHT: one scale for the tile instead, for both copies.
-// Bound: HBM (read esz, write 2 bytes per value).
+// Bound: HBM (read esz, write 2 bytes per value).  QUANTFIG
 template <int XKIND, int FMT, bool WEIGHT>
-__global__ void __launch_bounds__(bq::THREADS) block_quantize_kernel(const BlockQuantArgs args) {
+__global__ void __launch_bounds__(bq::THREADS, XKIND == FP8DL_BF16 || WEIGHT ? 3 : 2)
+    block_quantize_kernel(const BlockQuantArgs args) {
     using namespace bq;
     pdl_wait();
     pdl_trigger();
@@ -87,40 +144,34 @@ __global__ void __launch_bounds__(bq::THREADS) block_quantize_kernel(const Block
     const int64_t c0 = tile_c * TILE + 8 * cc;
     const bool col_ok = c0 < args.cols;  // columns come in sixteens
     const char *px = static_cast<const char *>(args.x) + ((mat * args.rows + r0 + 8 * rr) * args.cols + c0) * ESZ;
-    float v[8][8];
+    Values<XKIND> v;
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const bool ok = col_ok && 8 * rr + i < nrows;
-        if (ESZ == 2) {
-            const uint4 u = ok ? ldg_stream(px + i * args.cols * ESZ) : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int q = 0; q < 4; q++) v[i][2 * q] = bf16_lo(w[q]), v[i][2 * q + 1] = bf16_hi(w[q]);
-        } else {
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const uint4 u = ok ? ldg_stream(px + i * args.cols * ESZ + 16 * h) : make_uint4(0u, 0u, 0u, 0u);
-                v[i][4 * h] = __uint_as_float(u.x), v[i][4 * h + 1] = __uint_as_float(u.y);
-                v[i][4 * h + 2] = __uint_as_float(u.z), v[i][4 * h + 3] = __uint_as_float(u.w);
-            }
-        }
-    }
+    for (int i = 0; i < 8; i++) v.load(i, px + i * args.cols * ESZ, col_ok && 8 * rr + i < nrows);
     float rmax[8], cmax[8];
+    v.maxima(rmax, cmax);
+    float top = rmax[0];
 #pragma unroll
-    for (int i = 0; i < 8; i++) rmax[i] = cmax[i] = 0.0f;
+    for (int i = 1; i < 8; i++) top = fmaxf(top, rmax[i]);
+    if (top > 3.402823466e38f) {  // an infinity: the maxima over the finite values
 #pragma unroll
-    for (int i = 0; i < 8; i++)
+        for (int i = 0; i < 8; i++) rmax[i] = cmax[i] = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const float a = finite_abs(v[i][j]);
-            rmax[i] = fmaxf(rmax[i], a);
-            cmax[j] = fmaxf(cmax[j], a);
-        }
+        for (int i = 0; i < 8; i++)
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const float2 p = v.pair(i, q);
+                const float a = finite_abs(p.x), b = finite_abs(p.y);
+                rmax[i] = fmaxf(rmax[i], fmaxf(a, b));
+                cmax[2 * q] = fmaxf(cmax[2 * q], a);
+                cmax[2 * q + 1] = fmaxf(cmax[2 * q + 1], b);
+            }
+        top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; i++) top = fmaxf(top, rmax[i]);
+    }
+    float tile_scale = 0.0f;
     if (WEIGHT) {
-        float m = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; i++) m = fmaxf(m, rmax[i]);
-        m = warp_max(m);
+        float m = warp_max(top);
         if (lane == 0) cscale[warp] = m;
         __syncthreads();
 #pragma unroll
@@ -131,13 +182,17 @@ __global__ void __launch_bounds__(bq::THREADS) block_quantize_kernel(const Block
             if (args.row_s) args.row_s[e + tile_c * args.row_blocks + tile_r] = sc.y;
             if (args.col_s) args.col_s[e + tile_r * args.tiles_c + tile_c] = sc.y;
         }
+        tile_scale = sc.x;
+    }
+    if (!WEIGHT && args.col_q) {  // column maxima of the warp; joined after the row-wise stores are on their way
 #pragma unroll
-        for (int i = 0; i < 8; i++)
-#pragma unroll
-            for (int j = 0; j < 8; j++) v[i][j] = __fmul_rn(v[i][j], sc.x);
+        for (int j = 0; j < 8; j++) {
+            cmax[j] = fmaxf(cmax[j], __shfl_xor_sync(0xffffffffu, cmax[j], 16));
+            if (lane < 16) part[warp][8 * cc + j] = cmax[j];
+        }
     }
     if (args.row_q) {
-        float s8[8];
+        float own = tile_scale;
         if (!WEIGHT) {
             // halving exchange: after steps 8, 4, 2 lane cc holds row (cc >> 1) of its eight
 #pragma unroll
@@ -160,45 +215,41 @@ __global__ void __launch_bounds__(bq::THREADS) block_quantize_kernel(const Block
             const float2 sc = block_scale<FMT>(fmaxf(rmax[0], __shfl_xor_sync(0xffffffffu, rmax[0], 1)));
             const int row = 8 * rr + (cc >> 1);
             if (!(cc & 1) && row < nrows) args.row_s[tile_c * args.rows + r0 + row] = sc.y;
-#pragma unroll
-            for (int i = 0; i < 8; i++) s8[i] = __shfl_sync(0xffffffffu, sc.x, (lane & 16) + 2 * i);
+            own = sc.x;
         }
         uint8_t *qrow = args.row_q + (mat * args.rows + r0 + 8 * rr) * args.cols + c0;
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-            if (!col_ok || 8 * rr + i >= nrows) continue;
-            float y[8];
+            const float2 s2 = f2(WEIGHT ? own : __shfl_sync(0xffffffffu, own, (lane & 16) + 2 * i));
+            float2 y[4];
 #pragma unroll
-            for (int j = 0; j < 8; j++) y[j] = WEIGHT ? v[i][j] : __fmul_rn(v[i][j], s8[i]);
-            *reinterpret_cast<uint2 *>(qrow + i * args.cols) =
-                make_uint2(pack4<FMT>(y[0], y[1], y[2], y[3]), pack4<FMT>(y[4], y[5], y[6], y[7]));
+            for (int q = 0; q < 4; q++) y[q] = __fmul2_rn(v.pair(i, q), s2);
+            if (col_ok && 8 * rr + i < nrows)
+                *reinterpret_cast<uint2 *>(qrow + i * args.cols) = make_uint2(
+                    pack4<FMT>(y[0].x, y[0].y, y[1].x, y[1].y), pack4<FMT>(y[2].x, y[2].y, y[3].x, y[3].y));
         }
     }
     if (!WEIGHT && args.ws) {  // column sums of the tile, rows in a fixed order
+        float *sums = reinterpret_cast<float *>(tcode);  // [8][TILE], before the codes take the place
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            float s = v[0][j];
+        for (int q = 0; q < 4; q++) {
+            float2 s = v.pair(0, q);
 #pragma unroll
-            for (int i = 1; i < 8; i++) s += v[i][j];
-            s += __shfl_xor_sync(0xffffffffu, s, 16);
-            if (lane < 16) part[warp][8 * cc + j] = s;
+            for (int i = 1; i < 8; i++) s = __fadd2_rn(s, v.pair(i, q));
+            s.x += __shfl_xor_sync(0xffffffffu, s.x, 16);
+            s.y += __shfl_xor_sync(0xffffffffu, s.y, 16);
+            if (lane < 16) *reinterpret_cast<float2 *>(sums + warp * TILE + 8 * cc + 2 * q) = s;
         }
         __syncthreads();
         if (tid < TILE && tile_c * TILE + tid < args.cols) {
-            float s = part[0][tid];
+            float s = sums[tid];
 #pragma unroll
-            for (int w = 1; w < 8; w++) s += part[w][tid];
+            for (int w = 1; w < 8; w++) s += sums[w * TILE + tid];
             args.ws[tile_r * args.cols + tile_c * TILE + tid] = s;
         }
-        __syncthreads();
     }
     if (!args.col_q) return;
     if (!WEIGHT) {
-#pragma unroll
-        for (int j = 0; j < 8; j++) {
-            cmax[j] = fmaxf(cmax[j], __shfl_xor_sync(0xffffffffu, cmax[j], 16));
-            if (lane < 16) part[warp][8 * cc + j] = cmax[j];
-        }
         __syncthreads();
         if (tid < TILE) {
             float m = part[0][tid];
@@ -211,13 +262,16 @@ __global__ void __launch_bounds__(bq::THREADS) block_quantize_kernel(const Block
         __syncthreads();
     }
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
-        const float s = WEIGHT ? 1.0f : cscale[8 * cc + j];
-        float y[8];
+    for (int q = 0; q < 4; q++) {  // columns 8cc + 2q and the next
+        const float2 s2 = WEIGHT ? f2(tile_scale) : *reinterpret_cast<const float2 *>(cscale + 8 * cc + 2 * q);
+        float2 y[8];
 #pragma unroll
-        for (int i = 0; i < 8; i++) y[i] = WEIGHT ? v[i][j] : __fmul_rn(v[i][j], s);
-        *reinterpret_cast<uint2 *>(tcode + (8 * cc + j) * TILE + ((rr ^ cc) << 3)) =
-            make_uint2(pack4<FMT>(y[0], y[1], y[2], y[3]), pack4<FMT>(y[4], y[5], y[6], y[7]));
+        for (int i = 0; i < 8; i++) y[i] = __fmul2_rn(v.pair(i, q), s2);
+        uint8_t *at = tcode + (8 * cc + 2 * q) * TILE + ((rr ^ cc) << 3);
+        *reinterpret_cast<uint2 *>(at) =
+            make_uint2(pack4<FMT>(y[0].x, y[1].x, y[2].x, y[3].x), pack4<FMT>(y[4].x, y[5].x, y[6].x, y[7].x));
+        *reinterpret_cast<uint2 *>(at + TILE) =
+            make_uint2(pack4<FMT>(y[0].y, y[1].y, y[2].y, y[3].y), pack4<FMT>(y[4].y, y[5].y, y[6].y, y[7].y));
     }
     __syncthreads();
     // weights: r0 .. r0+127 of q_t's rows (sixteens); groups: the tile's 128 padded columns
