@@ -275,26 +275,13 @@ __device__ __forceinline__ void store1(const BlockGemmArgs &a, int64_t at, float
         static_cast<float *>(a.D)[at] = v;
 }
 
-// Sixteen consecutive columns' bias added to the sums, n = the first one's column of D.
-__device__ __forceinline__ void add_bias16(const BlockGemmArgs &a, int64_t n, float2 (&v)[8]) {
-    if (a.bias_dtype == FP8DL_BF16) {
-        const uint4 *b = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.bias) + n);
+// Sixteen consecutive columns' bias (in shared memory) added to the sums.
+__device__ __forceinline__ void add_bias16(const float *bias, float2 (&v)[8]) {
 #pragma unroll
-        for (int g = 0; g < 2; g++) {
-            const uint4 u = __ldg(b + g);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int q = 0; q < 4; q++)
-                v[4 * g + q] = __fadd2_rn(v[4 * g + q], make_float2(bf16_lo(w[q]), bf16_hi(w[q])));
-        }
-    } else {
-        const float4 *b = reinterpret_cast<const float4 *>(static_cast<const float *>(a.bias) + n);
-#pragma unroll
-        for (int g = 0; g < 4; g++) {
-            const float4 u = __ldg(b + g);
-            v[2 * g] = __fadd2_rn(v[2 * g], make_float2(u.x, u.y));
-            v[2 * g + 1] = __fadd2_rn(v[2 * g + 1], make_float2(u.z, u.w));
-        }
+    for (int g = 0; g < 4; g++) {
+        const float4 u = *reinterpret_cast<const float4 *>(bias + 4 * g);
+        v[2 * g] = __fadd2_rn(v[2 * g], make_float2(u.x, u.y));
+        v[2 * g + 1] = __fadd2_rn(v[2 * g + 1], make_float2(u.z, u.w));
     }
 }
 
@@ -338,7 +325,8 @@ struct TileOut {
     int64_t rows;
 };
 constexpr int TILE_RING = 8;
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + OUT_BYTES + 1024 + RING_BYTES + kGroupTableBytes + 1024;
+constexpr int BIAS_BYTES = TILE_RING * TN * 4;  // and the tile's bias as fp32, if there is one
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + OUT_BYTES + 1024 + RING_BYTES + BIAS_BYTES + kGroupTableBytes + 1024;
 static_assert(SMEM_BYTES <= 227 * 1024 && Ring<false>::SLOTS * Ring<false>::SLOT * 4 <= RING_BYTES, "shared memory");
 }  // namespace bp
 
@@ -355,7 +343,8 @@ __device__ __forceinline__ bp::TileOut tile_out_of(const BlockTile &w, uint32_t 
 // written by the warp itself.  The box is free once the TMA has read it: the wait is at the
 // next tile's end (two boxes hold 128 columns of bf16; fp32 takes two turns).
 __device__ __forceinline__ void store_tile(const BlockGemmArgs &a, const CUtensorMap *tmap_d, uint8_t *stage, int lane,
-                                           int64_t d_row, int rows, int64_t n0, float2 (&acc)[64]) {
+                                           int64_t d_row, int rows, int64_t n0, const float *bias,
+                                           float2 (&acc)[64]) {
     using namespace bp;
     const bool bf = a.d_dtype == FP8DL_BF16;
     const int esz = bf ? 2 : 4;
@@ -389,7 +378,7 @@ __device__ __forceinline__ void store_tile(const BlockGemmArgs &a, const CUtenso
         float2 v[8];
 #pragma unroll
         for (int p = 0; p < 8; p++) v[p] = acc[8 * c + p];
-        if (a.bias_dtype >= 0 && n0 + 16 * c < a.N) add_bias16(a, n0 + 16 * c, v);
+        if (a.bias_dtype >= 0) add_bias16(bias + 16 * c, v);
         if (bf) {
 #pragma unroll
             for (int g = 0; g < 2; g++) {
@@ -452,7 +441,8 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(fempty + R::SLOTS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     float *ring = reinterpret_cast<float *>(bar_area + 1024);
-    const GroupTables tab = group_tables(bar_area + 1024 + RING_BYTES);
+    float *bias_ring = reinterpret_cast<float *>(bar_area + 1024 + RING_BYTES);
+    const GroupTables tab = group_tables(bar_area + 1024 + RING_BYTES + BIAS_BYTES);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -618,8 +608,16 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
             for (uint32_t tile = pair; tile < tiles && ok; tile += npairs, seq++) {
                 const BlockTile w = block_tile<TM, TN>(args, tab, tile);
                 const int kbs = w.kbs;
-                if (lane == 0 && kbs > 0)  // handed over with the first block's arrival
-                    tile_out[seq % TILE_RING] = tile_out_of(w, rank);
+                if (kbs > 0) {  // handed over with the first block's arrival
+                    if (lane == 0) tile_out[seq % TILE_RING] = tile_out_of(w, rank);
+                    if (args.bias_dtype >= 0) {
+#pragma unroll
+                        for (int j = 0; j < TN / 32; j++)
+                            if (w.n0 + 32 * j + lane < args.N)
+                                bias_ring[seq % TILE_RING * TN + 32 * j + lane] = load_bias1(args, w.n0 + 32 * j + lane);
+                    }
+                    __syncwarp();
+                }
                 for (int kb = 0; kb < kbs; kb++) {
                     if (kb % R::FB == 0) {
                         ok = mbar_wait(smem_u32(&ffull[slot]), fph, abort_flag, args.status);
@@ -695,7 +693,8 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
                                         : tile_out_of(block_tile<TM, TN>(args, tab, tile), rank);  // nothing to sum: zeros
             const int64_t rows = out.rows - 32 * q, n0 = out.n0 + HALF * half;
             if (rows > 0 && n0 < args.N)
-                store_tile(args, &tmap_d, stage, lane, out.d_row + 32 * q, (int)min(rows, (int64_t)32), n0, acc);
+                store_tile(args, &tmap_d, stage, lane, out.d_row + 32 * q, (int)min(rows, (int64_t)32), n0,
+                           bias_ring + seq % TILE_RING * TN + HALF * half, acc);
         }
         if (lane == 0) bulk_wait_all();
     }
