@@ -318,8 +318,10 @@ constexpr int RING_BYTES = Ring<true>::SLOTS * Ring<true>::SLOT * 4;
 constexpr int OUT_BOX = 32 * 128, OUT_WARP = 2 * OUT_BOX, OUT_BYTES = EPI_WARPS * OUT_WARP;
 // What the epilogue needs of a tile, decoded by the relay warp (the decoding's divisions took
 // 600-900 cycles at each tile's end): the CTA's first row of D, how many rows are its to write,
-// the first column.  The relay is at most four blocks ahead of the epilogue, four tiles if
-// each has one block.
+// the first column.  The relay writes a tile's entry at most five blocks ahead of the last one
+// that the epilogue has loaded (it waits for block i - 3 before it gets to block i, whose MMAs
+// waited for the release of block i - 5): five tiles if each has one block.  Tiles without
+// blocks take no entry.
 struct TileOut {
     int64_t d_row, n0;
     int64_t rows;
@@ -403,20 +405,40 @@ __device__ __forceinline__ void store_tile(const BlockGemmArgs &a, const CUtenso
     }
 }
 
-// acc[C .. C+L) += r * factor: the factor sc, or (BROWS) sc times the columns' own.
-template <bool BROWS, int C, int L>
-__device__ __forceinline__ void add_block(float2 (&acc)[64], const uint32_t (&r)[L], float2 sc, const float *fb) {
+// Eight columns' factors from shared memory, in program order with the other volatile accesses.
+__device__ __forceinline__ void load_factors(float4 (&f)[2], const float *p) {
 #pragma unroll
-    for (int j = 0; j < L; j += 4) {
-        float2 g0 = sc, g1 = sc;
-        if (BROWS) {
-            const float4 u = *reinterpret_cast<const float4 *>(fb + C + j);
-            g0 = __fmul2_rn(sc, make_float2(u.x, u.y));
-            g1 = __fmul2_rn(sc, make_float2(u.z, u.w));
+    for (int i = 0; i < 2; i++)
+        asm volatile("ld.volatile.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(f[i].x), "=f"(f[i].y), "=f"(f[i].z), "=f"(f[i].w)
+                     : "r"(smem_u32(p + 4 * i)));
+}
+
+// acc[C .. C+L) += r * factor: the factor sc, or (BROWS) sc times the columns' own, of which f0 and f1
+// hold the next sixteen; they are loaded sixteen columns ahead of their use, which with two
+// warps a scheduler hides most of it (1205 cycles a block with the loads at their use, 1141 so,
+// 907 if there were none).
+template <bool BROWS, int C, int L>
+__device__ __forceinline__ void add_block(float2 (&acc)[64], const uint32_t (&r)[L], float2 sc, const float *fb,
+                                          float4 (&f0)[2], float4 (&f1)[2]) {
+#pragma unroll
+    for (int g = 0; g < L / 8; g++) {
+        float2 m[4] = {sc, sc, sc, sc};
+        if constexpr (BROWS) {
+            float4(&f)[2] = ((C / 8 + g) & 1) ? f1 : f0;
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                m[2 * i] = __fmul2_rn(sc, make_float2(f[i].x, f[i].y));
+                m[2 * i + 1] = __fmul2_rn(sc, make_float2(f[i].z, f[i].w));
+            }
+            if (C + 8 * g + 16 < bp::HALF) load_factors(f, fb + C + 8 * g + 16);
         }
-        float2 &a = acc[(C + j) / 2], &b = acc[(C + j) / 2 + 1];
-        a = __ffma2_rn(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), g0, a);
-        b = __ffma2_rn(make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), g1, b);
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const int j = 8 * g + 2 * k;
+            float2 &a = acc[(C + j) / 2];
+            a = __ffma2_rn(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), m[k], a);
+        }
     }
 }
 
@@ -605,7 +627,7 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
             uint32_t fph = 0, bph = 0;
             bool ok = true;
             uint32_t seq = 0;
-            for (uint32_t tile = pair; tile < tiles && ok; tile += npairs, seq++) {
+            for (uint32_t tile = pair; tile < tiles && ok; tile += npairs) {
                 const BlockTile w = block_tile<TM, TN>(args, tab, tile);
                 const int kbs = w.kbs;
                 if (kbs > 0) {  // handed over with the first block's arrival
@@ -617,6 +639,7 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
                                 bias_ring[seq % TILE_RING * TN + 32 * j + lane] = load_bias1(args, w.n0 + 32 * j + lane);
                     }
                     __syncwarp();
+                    seq++;
                 }
                 for (int kb = 0; kb < kbs; kb++) {
                     if (kb % R::FB == 0) {
@@ -644,8 +667,8 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
         const float *my_a = ring + 32 * q + lane, *my_b = ring + 128 + (BROWS ? HALF : 1) * half;
         const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
         int slot = 0, buf = 0;
-        uint32_t bph = 0, seq = 0;
-        for (uint32_t tile = pair; tile < tiles; tile += npairs, seq++) {
+        uint32_t bph = 0, seq = 0;  // seq: tiles with blocks so far, as the relay counts them
+        for (uint32_t tile = pair; tile < tiles; tile += npairs) {
             const int kbs = block_tile_kbs<TM, TN>(args, tab, tile);
             float2 acc[64];
 #pragma unroll
@@ -665,22 +688,27 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
                 const int at = slot * R::SLOT + (kb % R::FB) * R::BLOCK;
                 const float *fb = my_b + at;  // BROWS: the block's column factors
                 const float2 sc = f2(BROWS ? my_a[at] : __fmul_rn(my_a[at], fb[0]));
+                float4 f0[2], f1[2];
+                if (BROWS) {
+                    load_factors(f0, fb);
+                    load_factors(f1, fb + 8);
+                }
                 tmem_ld_wait_regs(ra);
                 regs_ready(rb);
-                add_block<BROWS, 0>(acc, ra, sc, fb);
+                add_block<BROWS, 0>(acc, ra, sc, fb, f0, f1);
                 tmem_ld_32x32b_x32(ta + 48, ra);
-                add_block<BROWS, 32>(acc, rb, sc, fb);
+                add_block<BROWS, 32>(acc, rb, sc, fb, f0, f1);
                 tmem_ld_32x32b_x16(ta + 80, rb);
                 tmem_ld_wait_regs(ra);
                 regs_ready(rb);
-                add_block<BROWS, 48>(acc, ra, sc, fb);
+                add_block<BROWS, 48>(acc, ra, sc, fb, f0, f1);
                 tmem_ld_32x32b_x32(ta + 96, ra);
                 tmem_ld_wait_regs(ra);
                 tc_fence_before();
                 __syncwarp();
                 arrive_remote_if(tempty0 + 8 * buf, lane == 0);
-                add_block<BROWS, 80>(acc, rb, sc, fb);
-                add_block<BROWS, 96>(acc, ra, sc, fb);
+                add_block<BROWS, 80>(acc, rb, sc, fb, f0, f1);
+                add_block<BROWS, 96>(acc, ra, sc, fb, f0, f1);
                 const bool last = kb % R::FB == R::FB - 1 || kb == kbs - 1;  // of the factor slot
                 __syncwarp();
                 arrive_if(smem_u32(&fempty[0]) + 8 * slot, lane == 0 && last);
@@ -695,6 +723,7 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
             if (rows > 0 && n0 < args.N)
                 store_tile(args, &tmap_d, stage, lane, out.d_row + 32 * q, (int)min(rows, (int64_t)32), n0,
                            bias_ring + seq % TILE_RING * TN + HALF * half, acc);
+            seq += kbs > 0;
         }
         if (lane == 0) bulk_wait_all();
     }

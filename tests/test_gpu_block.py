@@ -270,3 +270,31 @@ def test_grouped_wgrad(off, rows, M, N, dtype):
         if hi == lo:
             assert torch.all(D[e] == 0.0)
         at += 128 * n
+
+
+def test_grouped_wgrad_with_mostly_empty_groups():
+    """More tiles than the GPU runs at once, most of them of groups without rows, and the rest one or two blocks long."""
+    fd, dev = _fd()
+    G, M, N = 1000, 256, 272
+    rng = np.random.default_rng(9)
+    lens = np.where(rng.random(G) < 0.12, rng.integers(1, 200, G), 0)
+    off = np.concatenate([[0], np.cumsum(lens)])
+    rows = int(off[-1])
+    o = torch.tensor(off, dtype=torch.int32, device=dev)
+    ops = []
+    for cols, fmt in ((M, 1), (N, 0)):
+        q, s, _ = br.cols(_x(rows, cols, torch.float32, "sparse%d" % cols).numpy(), fmt, off)
+        ops += [q, s]
+    t = _dev(dev, *ops)
+    D = torch.full((G, M, N), 7.0, device=dev)
+    fd.fp8_block_gemm_grouped_wgrad(t[0], 1, t[1], t[2], 0, t[3], o, D)
+    at = 0
+    for e in range(G):
+        n = br.blocks(int(lens[e]))
+        if n == 0:
+            assert torch.all(D[e] == 0.0)
+            continue
+        av = br.values(ops[0][:, at:at + 128 * n], 1, ops[1][at // 128:at // 128 + n], 1)
+        bv = br.values(ops[2][:, at:at + 128 * n], 0, ops[3][at // 128:at // 128 + n], 1)
+        br.check(D[e], av @ bv.T, np.abs(av) @ np.abs(bv).T, 128 * n, "wgrad of group %d" % e)
+        at += 128 * n
