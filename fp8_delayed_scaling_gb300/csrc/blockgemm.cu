@@ -295,9 +295,23 @@ __device__ __forceinline__ void add_bias16(const float *bias, float2 (&v)[8]) {
 //               once per block: an mbarrier wait costs about 90 cycles even when it is over
 //   warps 4-11  epilogue: warp w drains lane quarter w & 3 of column half (w - 4) / 4; a thread
 //               holds one row x 128 columns of the sum (64 fp32 pairs)
-// TILEFIG
-// FP32 pipe: with 128 x 128 weight factors one packed multiply-add per two values; with
-// factors per row of B (BROWS, weight gradients) one packed multiply more.
+// Every block's sums go to the epilogue and the buffer back to the MMAs, about 1270 cycles for the
+// two buffers with an epilogue that does nothing: 638 a block, where the MMAs alone take 566.
+// This kernel takes 742 (8192 x 8192 x 16384, 3050 TFLOP/s in a burst, 2630 under the power cap).  What got it there:
+//   - a release at CTA scope on the leader's barrier (1.92 -> 0.92 ms at 16384 x 16384 x 4096),
+//   - MMA operands in uniform registers (one elected lane, no branch: 10 %),
+//   - one wait per block for sums and factors, no branches in the loop (a wait costs 90 cycles),
+//   - the buffer given back before the last three eighths of the multiply-adds,
+//   - no spilled register: 128 sums, 48 loads and 40 others are what 216 registers hold,
+//   - the store, the tile's decoding and its bias out of the epilogue's way (see store_tile).
+// Tried and slower: 128 x 256 tiles on single CTAs (shared memory: 96 KB written and read a block,
+// 750 cycles at 128 bytes a clock; 826-900 measured), 256 x 160 tiles with three buffers (the
+// fixed 500 cycles an MMA thread spends per block weigh more: 990 per 256 columns).
+// FP32 pipe: with 128 x 128 weight factors one packed multiply-add per two values (2.25 cycles each: 290
+// a block); with factors per row of B (BROWS, weight gradients) one packed multiply more, and the
+// columns' factors from shared memory: 1141 cycles a block.  Reading tensor memory in shapes that
+// give a thread four rows and a quarter of the columns (16x128b, 16x256b: half and a quarter of
+// the 32x32b shape's speed) needs fewer factors but came out no faster.
 // ---------------------------------------------------------------------------
 namespace bp {
 constexpr int TM = 256, TN = 256, HALF = 128, BK = 128, STAGES = 4, BUFS = 2;
@@ -1161,8 +1175,11 @@ static fp8dl_status launch_block_gemm(const uint8_t *A, int32_t a_dtype, int64_t
     args.idesc = (1u << 4) | ((uint32_t)a_dtype << 7) | ((uint32_t)b_dtype << 10) | ((uint32_t)(bp::TN >> 3) << 17) |
                  ((uint32_t)(bp::TM >> 4) << 24);
     const int64_t tiles_m = (args.M + bp::TM - 1) / bp::TM, tiles_n = (args.N + bp::TN - 1) / bp::TN;
-    args.along_n = 0;
-    args.band = 8;
+    // Bands of 16 tiles along the dimension with fewer of them, 8 where a panel is long (16384 x 16384 x
+    // 4096: 838 us with 16, 857 with 8, under the power cap; 16384 x 4096 x 16384: 833 along the
+    // columns with 8, 848 with 16, 850 along the rows).  A group's row tiles are few: along the rows.
+    args.along_n = args.kind != BG_ROWS && tiles_n < tiles_m;
+    args.band = args.kind == BG_REDUCE || args.K <= 8192 ? 16 : 8;
     const int64_t busy = args.n_groups < args.M ? args.n_groups : args.M;  // groups that can hold a row
     const int64_t bound = args.kind == BG_DENSE  ? tiles_m * tiles_n
                           : args.kind == BG_ROWS ? (args.M / bp::TM + busy) * tiles_n
