@@ -418,7 +418,7 @@ def fp8_block_quantize(x: torch.Tensor, out_dtype: int, row_q=None, row_s=None, 
     rows, cols = x.shape
     groups = 0 if offsets is None else offsets.numel() - 1
     _need(groups >= 1 or offsets is None, "offsets must hold n_groups + 1 entries")
-    dev, T = x.get_device(), _lib.fp8_block_padded_rows(rows, groups)
+    dev, T = x.get_device(), (rows + 127 * min(max(groups, 1), rows)) // 128 * 128  # fp8_block_padded_rows
     _need(workspace is None or workspace.get_device() == dev, "workspace must be on the device of x")
     args = (x.data_ptr(), _hp(x), rows, cols, _tensor(offsets, torch.int32, (groups + 1,), dev, "offsets"), groups,
             out_dtype, _tensor(row_q, torch.uint8, (rows, cols), dev, "row_q"),

@@ -173,6 +173,13 @@ __device__ __forceinline__ BlockTile block_tile(const BlockGemmArgs &a, const Gr
     return w;
 }
 
+// mbar_wait by a whole warp, with one answer for all its lanes: where a wait runs out, lanes that
+// saw the abort and lanes that saw the phase complete would part, and the warp-wide operations
+// that follow wait for lanes that never come.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, int32_t *status) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
+}
+
 // One k-block of the pair's tile by one elected lane of a converged warp: four MMAs (K = 32 each,
 // 32 bytes further into the swizzled rows, two descriptor units), the first one overwriting D,
 // and the commits that hand the buffer to the epilogue and the stage to the producer.
@@ -564,8 +571,8 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
                 const int kbs = block_tile_kbs<TM, TN>(args, tab, tile);
                 for (int kb = 0; kb < kbs; kb++) {
                     // the operands first: they are there early, the buffer comes back last
-                    if (!mbar_wait(smem_u32(&full[s]), ph, abort_flag, args.status) ||
-                        !mbar_wait(smem_u32(&tempty[buf]), bph ^ 1, abort_flag, args.status)) {
+                    if (!warp_wait(smem_u32(&full[s]), ph, abort_flag, args.status) ||
+                        !warp_wait(smem_u32(&tempty[buf]), bph ^ 1, abort_flag, args.status)) {
                         ok = false;
                         break;
                     }
@@ -608,7 +615,7 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
                     ob[0] = (w.n0 >> 7) + lane < args.b_ld ? lane : 0;
                 }
                 for (int kb = 0; kb < w.kbs; kb += R::FB) {
-                    if (!mbar_wait(smem_u32(&fempty[slot]), ph ^ 1, abort_flag, args.status)) {
+                    if (!warp_wait(smem_u32(&fempty[slot]), ph ^ 1, abort_flag, args.status)) {
                         ok = false;
                         break;
                     }
@@ -657,13 +664,13 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
                 }
                 for (int kb = 0; kb < kbs; kb++) {
                     if (kb % R::FB == 0) {
-                        ok = mbar_wait(smem_u32(&ffull[slot]), fph, abort_flag, args.status);
+                        ok = warp_wait(smem_u32(&ffull[slot]), fph, abort_flag, args.status);
                         if (++slot == R::SLOTS) {
                             slot = 0;
                             fph ^= 1;
                         }
                     }
-                    if (!ok || !(ok = mbar_wait(smem_u32(&tfull[buf]), bph ^ 1, abort_flag, args.status))) break;
+                    if (!ok || !(ok = warp_wait(smem_u32(&tfull[buf]), bph ^ 1, abort_flag, args.status))) break;
                     if (lane == 0) mbar_arrive(smem_u32(&tfull[buf]));
                     __syncwarp();
                     if (++buf == BUFS) {
@@ -690,7 +697,7 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
             bool ok = true;
             for (int kb = 0; ok && kb < kbs; kb++) {
                 // after a wait that ran out this block's sums are garbage and the loop ends
-                ok = mbar_wait(smem_u32(&tfull[0]) + 8 * buf, bph, abort_flag, args.status);
+                ok = warp_wait(smem_u32(&tfull[0]) + 8 * buf, bph, abort_flag, args.status);
                 tc_fence_after();
                 const uint32_t ta = taddr0 + (uint32_t)(buf * TN);
                 // Columns 0-31, 32-47, 48-79, 80-95, 96-127 through two sets of registers (48 beside
@@ -881,8 +888,8 @@ __global__ void __launch_bounds__(bf::Shape<BT>::THREADS, 2)
         const SDesc desc0 = sdesc_k_sw128_split(smem_u32(smem));
         for (uint32_t tile = tile0; tile < tiles && ok; tile += step) {
             for (int kb = kb0; kb < kb1; kb++) {
-                if (!mbar_wait(smem_u32(&full[s]), ph, abort_flag, args.status) ||
-                    !mbar_wait(smem_u32(&tempty[buf]), bph ^ 1, abort_flag, args.status)) {
+                if (!warp_wait(smem_u32(&full[s]), ph, abort_flag, args.status) ||
+                    !warp_wait(smem_u32(&tempty[buf]), bph ^ 1, abort_flag, args.status)) {
                     ok = false;
                     break;
                 }
@@ -914,7 +921,7 @@ __global__ void __launch_bounds__(bf::Shape<BT>::THREADS, 2)
             const float *pa = args.a_s + (int64_t)kb0 * args.M + w.a_row;
             const float *pb = w.b_s + (int64_t)kb0 * args.b_ld + (w.n0 >> 7);
             for (int kb = kb0; kb < kb1; kb++, pa += args.M, pb += args.b_ld) {
-                if (!mbar_wait(smem_u32(&fempty[slot]), ph ^ 1, abort_flag, args.status)) {
+                if (!warp_wait(smem_u32(&fempty[slot]), ph ^ 1, abort_flag, args.status)) {
                     ok = false;
                     break;
                 }
@@ -943,8 +950,8 @@ __global__ void __launch_bounds__(bf::Shape<BT>::THREADS, 2)
             for (int p = 0; p < BT / 2; p++) acc[p] = make_float2(0.0f, 0.0f);
             bool ok = true;
             for (int kb = kb0; kb < kb1; kb++) {
-                if (!mbar_wait(smem_u32(&ffull[slot]), fph, abort_flag, args.status) ||
-                    !mbar_wait(smem_u32(&tfull[buf]), bph, abort_flag, args.status)) {
+                if (!warp_wait(smem_u32(&ffull[slot]), fph, abort_flag, args.status) ||
+                    !warp_wait(smem_u32(&tfull[buf]), bph, abort_flag, args.status)) {
                     ok = false;
                     break;
                 }
@@ -1028,6 +1035,7 @@ __global__ void __launch_bounds__(bf::Shape<BT>::THREADS, 2)
                 store1(args, (w.d_row + t) * args.N + w.n0 + col, v);
             }
         }
+        __syncwarp();
         cluster_sync();  // nobody's sums go away while they are read
     }
     if (warp == 1) {
@@ -1142,6 +1150,9 @@ static fp8dl_status launch_few(const uint8_t *A, int32_t a_dtype, const uint8_t 
     return check_launch(what);
 }
 
+// Columns of D: a row's bytes are a 32-bit coordinate of the stores.
+static bool block_cols_ok(int64_t n) { return dim_ok(n, 16) && n < (int64_t(1) << 29); }
+
 static fp8dl_status check_block_gemm(const uint8_t *A, int32_t a_dtype, const float *a_s, const uint8_t *B,
                                      int32_t b_dtype, const float *b_s, const void *D, int32_t d_dtype, bool tokens) {
     FP8DL_CHECK_ARG((a_dtype == FP8DL_E4M3 || a_dtype == FP8DL_E5M2) && (b_dtype == FP8DL_E4M3 || b_dtype == FP8DL_E5M2),
@@ -1201,8 +1212,8 @@ extern "C" fp8dl_status fp8_block_gemm(const uint8_t *A, int32_t a_dtype, const 
                                        int64_t K, const void *bias, int32_t bias_dtype, void *D, int32_t d_dtype,
                                        int32_t *dev_status, fp8dl_stream_t stream) {
     FP8DL_NVTX("fp8_block_gemm");
-    if (!block_tokens_ok(M) || !dim_ok(N, 16) || !dim_ok(K, 16))
-        return fail(FP8DL_ERR_SHAPE, "M (%lld) must be in [0, 2^31), N and K (%lld, %lld) positive multiples of 16",
+    if (!block_tokens_ok(M) || !block_cols_ok(N) || !dim_ok(K, 16))
+        return fail(FP8DL_ERR_SHAPE, "M (%lld) must be in [0, 2^31), N (%lld) and K (%lld) positive multiples of 16, N < 2^29",
                     (long long)M, (long long)N, (long long)K);
     FP8DL_TRY(check_block_gemm(A, a_dtype, a_s, B, b_dtype, b_s, D, d_dtype, M > 0));
     FP8DL_CHECK_ARG(b_rows == 1 || b_rows == 128, "b_rows must be 1 or 128");
@@ -1233,8 +1244,8 @@ extern "C" fp8dl_status fp8_block_gemm_grouped(const uint8_t *A, int32_t a_dtype
                                                int32_t n_groups, int64_t M, int64_t N, int64_t K, void *D,
                                                int32_t d_dtype, int32_t *dev_status, fp8dl_stream_t stream) {
     FP8DL_NVTX("fp8_block_gemm_grouped");
-    if (!block_tokens_ok(M) || !dim_ok(N, 16) || !dim_ok(K, 16))
-        return fail(FP8DL_ERR_SHAPE, "M (%lld) must be in [0, 2^31), N and K (%lld, %lld) positive multiples of 16",
+    if (!block_tokens_ok(M) || !block_cols_ok(N) || !dim_ok(K, 16))
+        return fail(FP8DL_ERR_SHAPE, "M (%lld) must be in [0, 2^31), N (%lld) and K (%lld) positive multiples of 16, N < 2^29",
                     (long long)M, (long long)N, (long long)K);
     FP8DL_TRY(check_block_groups(offsets, n_groups, false));
     FP8DL_TRY(check_block_gemm(A, a_dtype, a_s, B, b_dtype, b_s, D, d_dtype, M > 0));
@@ -1266,8 +1277,8 @@ extern "C" fp8dl_status fp8_block_gemm_grouped_wgrad(const uint8_t *A, int32_t a
                                                      int64_t T, void *D, int32_t d_dtype, int32_t *dev_status,
                                                      fp8dl_stream_t stream) {
     FP8DL_NVTX("fp8_block_gemm_grouped_wgrad");
-    if (!dim_ok(M, 1) || !block_tokens_ok(M) || !block_tokens_ok(M * (n_groups < 1 ? 1 : n_groups)) || !dim_ok(N, 16) || !block_tokens_ok(T) || T % 128 != 0)
-        return fail(FP8DL_ERR_SHAPE, "M (%lld) must be positive, n_groups * M below 2^31, N (%lld) a positive multiple of 16 and T (%lld) a multiple of 128",
+    if (!dim_ok(M, 1) || !block_tokens_ok(M) || !block_tokens_ok(M * (n_groups < 1 ? 1 : n_groups)) || !block_cols_ok(N) || !block_tokens_ok(T) || T % 128 != 0)
+        return fail(FP8DL_ERR_SHAPE, "M (%lld) must be positive, n_groups * M < 2^31, N (%lld) a positive multiple of 16 < 2^29, T (%lld) a multiple of 128",
                     (long long)M, (long long)N, (long long)T);
     FP8DL_TRY(check_block_groups(offsets, n_groups, false));
     FP8DL_CHECK_ARG(D, "D is NULL");

@@ -115,7 +115,7 @@ struct Values<FP8DL_F32> {
 //            as whole 128-byte lines.
 // WEIGHT: one scale for the tile instead, for both copies.
 // Bound: HBM (read esz, write 2 bytes per value).  8192 x 4096 bf16, both copies: 25.6 us, 5.3 TB/s;
-// weights 16384 x 4096 bf16: 44.9 us, 6.0 TB/s; 32 of 1008 x 2048 fp32: 62.7 us, 6.3 TB/s.
+// weights 16384 x 4096 bf16: 44.9 us, 6.0 TB/s; 32 of 1008 x 2048 fp32: 64.8 us, 6.1 TB/s.
 template <int XKIND, int FMT, bool WEIGHT>
 __global__ void __launch_bounds__(bq::THREADS, XKIND == FP8DL_BF16 || WEIGHT ? 3 : 2)
     block_quantize_kernel(const BlockQuantArgs args) {

@@ -340,7 +340,7 @@ fp8dl_status mxfp8_gemm(const uint8_t *A, const uint8_t *A_s, const uint8_t *B, 
  *
  * Token dimensions may have any length, also 0 (nothing is written, except
  * sums over no tokens, which are zeros; the tensors may then be NULL).
- * Feature dimensions are positive multiples of 16.
+ * Feature dimensions are positive multiples of 16, those of D below 2^29.
  *
  * Groups: offsets is a DEVICE array of n_groups + 1 non-decreasing int32 with
  * offsets[0] >= 0 and offsets[n_groups] <= rows; group g owns rows
