@@ -129,17 +129,22 @@ __device__ __forceinline__ uint32_t block_tiles(const BlockGemmArgs &a, const Gr
     return (uint32_t)a.n_groups * tiles_m * tiles_n;
 }
 
-// Reduction blocks of a tile.
+// Reduction blocks of a tile, or of share `share` of `split` (of one product only).
 template <int TM, int TN>
-__device__ __forceinline__ int block_tile_kbs(const BlockGemmArgs &a, const GroupTables &t, uint32_t tile) {
-    if (a.kind != BG_REDUCE) return (int)((a.K + 127) / 128);
+__device__ __forceinline__ int block_tile_kbs(const BlockGemmArgs &a, const GroupTables &t, uint32_t tile, int split = 1,
+                                              int share = 0) {
+    if (a.kind != BG_REDUCE) {
+        const int kbs = (int)((a.K + 127) / 128);
+        return kbs * (share + 1) / split - kbs * share / split;
+    }
     const uint32_t per = (uint32_t)((a.N + TN - 1) / TN) * (uint32_t)((a.M + TM - 1) / TM);
     const uint32_t g = tile / per;
     return t.pre[g + 1] - t.pre[g];
 }
 
 template <int TM, int TN>
-__device__ __forceinline__ BlockTile block_tile(const BlockGemmArgs &a, const GroupTables &t, uint32_t tile) {
+__device__ __forceinline__ BlockTile block_tile(const BlockGemmArgs &a, const GroupTables &t, uint32_t tile, int split = 1,
+                                                int share = 0) {
     const uint32_t tiles_n = (uint32_t)((a.N + TN - 1) / TN), tiles_m = (uint32_t)((a.M + TM - 1) / TM);
     BlockTile w;
     uint32_t tm, tn;
@@ -152,6 +157,8 @@ __device__ __forceinline__ BlockTile block_tile(const BlockGemmArgs &a, const Gr
         w.a_row = w.d_row = (int64_t)tm * TM;
         w.a_end = a.M;
         w.n0 = w.b_row = (int64_t)tn * TN;
+        w.kb0 = kbs * share / split;
+        w.kbs = kbs * (share + 1) / split - w.kb0;
     } else if (a.kind == BG_ROWS) {
         const int g = find_group(t, a.n_groups, tile / tiles_n);
         band_order(tile - t.pre[g] * tiles_n, t.pre[g + 1] - t.pre[g], tiles_n, a.along_n, a.band, tm, tn);
@@ -184,10 +191,10 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 // 32 bytes further into the swizzled rows, two descriptor units), the first one overwriting D,
 // and the commits that hand the buffer to the epilogue and the stage to the producer.
 __device__ __forceinline__ void umma_block_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t tfull,
-                                                uint32_t empty) {
+                                                uint32_t empty, uint16_t ctas) {
     asm volatile(
-        "{\n\t.reg .pred e, t, f;\n\t.reg .b64 a, b;\n\t.reg .b16 m;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\tsetp.eq.u32 t, 0, 0;\n\tsetp.ne.u32 f, 0, 0;\n\tmov.u16 m, 3;\n\t"
+        "{\n\t.reg .pred e, t, f;\n\t.reg .b64 a, b;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.eq.u32 t, 0, 0;\n\tsetp.ne.u32 f, 0, 0;\n\t\n\t"
         "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, f;\n\t"
         "add.u64 a, %1, 2;\n\tadd.u64 b, %2, 2;\n\t"
         "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
@@ -195,9 +202,9 @@ __device__ __forceinline__ void umma_block_pair(uint32_t d, uint64_t a, uint64_t
         "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
         "add.u64 a, %1, 6;\n\tadd.u64 b, %2, 6;\n\t"
         "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
-        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%4], m;\n\t"
-        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%5], m;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(tfull), "r"(empty)
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%4], %6;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%5], %6;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(tfull), "r"(empty), "h"(ctas)
         : "memory");
 }
 
@@ -256,6 +263,18 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr)
         : "memory");
+}
+
+// Loads from shared memory of a CTA of the cluster (addresses from mapa_shared).
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
 }
 
 // 4- and 16-byte copies from global to shared memory.
@@ -463,7 +482,59 @@ __device__ __forceinline__ void add_block(float2 (&acc)[64], const uint32_t (&r)
     }
 }
 
-template <bool BROWS>
+// A split tile's end: one thread's row, the 128 / SPLIT columns that its share stores; the shares' sums
+// (sixteen bytes at 512 k from `sums`, in the CTAs of the same rank of every pair) are added in
+// order.  Sixteen columns' loads are under way at once: one at a time their latency
+// made the join as long as the products it saved.
+template <int SPLIT>
+__device__ __forceinline__ void join_shares(const BlockGemmArgs &a, uint32_t sums, uint32_t rank, int share, int64_t row,
+                                            int64_t n0, const float *bias) {
+    constexpr int PIECES = 32 / SPLIT;
+    uint32_t from[SPLIT];
+#pragma unroll
+    for (int o = 0; o < SPLIT; o++) from[o] = mapa_shared(sums + 512 * PIECES * share, 2 * o + rank);
+    for (int k = 0; k < PIECES; k += 4) {
+        const int col = 4 * (PIECES * share + k);
+        const int64_t n = n0 + col;
+        if (n >= a.N) break;
+        float4 v[SPLIT][4];
+#pragma unroll
+        for (int o = 0; o < SPLIT; o++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) v[o][i] = ld_cluster_f32x4(from[o] + 512 * (k + i));
+        float y[16];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            float4 s = v[0][i];
+#pragma unroll
+            for (int o = 1; o < SPLIT; o++) s.x += v[o][i].x, s.y += v[o][i].y, s.z += v[o][i].z, s.w += v[o][i].w;
+            if (a.bias_dtype >= 0) {
+                const float4 u = *reinterpret_cast<const float4 *>(bias + col + 4 * i);
+                s.x += u.x, s.y += u.y, s.z += u.z, s.w += u.w;
+            }
+            y[4 * i] = s.x, y[4 * i + 1] = s.y, y[4 * i + 2] = s.z, y[4 * i + 3] = s.w;
+        }
+        if (a.d_dtype == FP8DL_BF16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            uint4 *d = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.D) + row * a.N + n);
+            d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        } else {
+            float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(a.D) + row * a.N + n);
+#pragma unroll
+            for (int i = 0; i < 4; i++) d[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+        }
+    }
+}
+
+// SPLIT: the cluster's pairs share a tile (a kernel of its own: with the shares as run-time numbers
+// the others lost 3 %).
+template <bool BROWS, bool SPLIT>
 __global__ void __launch_bounds__(bp::THREADS, 1)
     block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                       const __grid_constant__ CUtensorMap tmap_d, const BlockGemmArgs args) {
@@ -488,9 +559,12 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
     const GroupTables tab = group_tables(bar_area + 1024 + RING_BYTES + BIAS_BYTES);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
+    // A cluster is one pair, or (SPLIT) several that share a tile, each with a part of its blocks.
+    const uint32_t cluster_rank = cluster_ctarank(), cluster_size = SPLIT ? cluster_nctarank() : 2u;
+    const uint32_t rank = SPLIT ? cluster_rank & 1 : cluster_rank, leader_rank = SPLIT ? cluster_rank & ~1u : 0u;
     const bool leader = rank == 0;
-    const uint32_t pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    const int split = SPLIT ? (int)(cluster_size >> 1) : 1, share = SPLIT ? (int)(cluster_rank >> 1) : 0;
+    const uint32_t pair = blockIdx.x / cluster_size, npairs = gridDim.x / cluster_size;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; s++) {
@@ -535,7 +609,7 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
             int64_t issued = 0;
             bool ok = true;
             for (uint32_t tile = pair; tile < tiles && ok; tile += npairs) {
-                const BlockTile w = block_tile<TM, TN>(args, tab, tile);
+                const BlockTile w = block_tile<TM, TN>(args, tab, tile, split, share);
                 const int32_t ra = (int32_t)(w.a_row + rank * 128), rb = (int32_t)(w.b_row + rank * B_ROWS);
                 for (int kb = 0; kb < w.kbs; kb++) {
                     if (!mbar_wait(smem_u32(&empty[s]), ph ^ 1, abort_flag, args.status)) {
@@ -543,7 +617,7 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
                         break;
                     }
                     // both CTAs' loads complete on the leader's barrier
-                    const uint32_t fb = smem_u32(&full[s]), lb = mapa_shared(fb, 0);
+                    const uint32_t fb = smem_u32(&full[s]), lb = mapa_shared(fb, leader_rank);
                     const uint32_t sa = smem_u32(smem + s * STAGE_BYTES);
                     if (leader) mbar_expect_tx(fb, 2 * STAGE_BYTES);
                     tma_load_2d_pair(sa, &tmap_a, lb, (w.kb0 + kb) * BK, ra);
@@ -568,7 +642,7 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
             uint32_t last_bar = 0, last_par = 0;
             const SDesc desc0 = sdesc_k_sw128_split(smem_u32(smem));
             for (uint32_t tile = pair; tile < tiles && ok; tile += npairs) {
-                const int kbs = block_tile_kbs<TM, TN>(args, tab, tile);
+                const int kbs = block_tile_kbs<TM, TN>(args, tab, tile, split, share);
                 for (int kb = 0; kb < kbs; kb++) {
                     // the operands first: they are there early, the buffer comes back last
                     if (!warp_wait(smem_u32(&full[s]), ph, abort_flag, args.status) ||
@@ -580,7 +654,7 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
                     const uint32_t lo_a = desc0.lo + (uint32_t)s * (STAGE_BYTES >> 4);
                     umma_block_pair(tmem_base + (uint32_t)(buf * TN), sdesc_join(lo_a, desc0.hi),
                                     sdesc_join(lo_a + (A_BYTES >> 4), desc0.hi), args.idesc, smem_u32(&tfull[0]) + 8 * buf,
-                                    smem_u32(&empty[0]) + 8 * s);
+                                    smem_u32(&empty[0]) + 8 * s, (uint16_t)(0x3u << leader_rank));
                     any = true;
                     last_bar = smem_u32(&empty[s]);
                     last_par = ph;
@@ -601,7 +675,7 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
             uint32_t ph = 0;
             bool ok = true;
             for (uint32_t tile = pair; tile < tiles && ok; tile += npairs) {
-                const BlockTile w = block_tile<TM, TN>(args, tab, tile);
+                const BlockTile w = block_tile<TM, TN>(args, tab, tile, split, share);
                 const int64_t row = w.a_row + rank * 128 + lane;
                 const float *pa = args.a_s + (int64_t)w.kb0 * args.M + w.a_row;
                 const float *pb = w.b_s + (int64_t)w.kb0 * args.b_ld + (BROWS ? w.n0 : w.n0 >> 7);
@@ -649,7 +723,7 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
             bool ok = true;
             uint32_t seq = 0;
             for (uint32_t tile = pair; tile < tiles && ok; tile += npairs) {
-                const BlockTile w = block_tile<TM, TN>(args, tab, tile);
+                const BlockTile w = block_tile<TM, TN>(args, tab, tile, split, share);
                 const int kbs = w.kbs;
                 if (kbs > 0) {  // handed over with the first block's arrival
                     if (lane == 0) tile_out[seq % TILE_RING] = tile_out_of(w, rank);
@@ -686,11 +760,11 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
         const uint32_t taddr0 = tmem_base + (uint32_t)(HALF * half) + ((uint32_t)(32 * q) << 16);
         uint8_t *stage = out_stage + (warp - 4) * OUT_WARP;
         const float *my_a = ring + 32 * q + lane, *my_b = ring + 128 + (BROWS ? HALF : 1) * half;
-        const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
+        const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), leader_rank);
         int slot = 0, buf = 0;
         uint32_t bph = 0, seq = 0;  // seq: tiles with blocks so far, as the relay counts them
         for (uint32_t tile = pair; tile < tiles; tile += npairs) {
-            const int kbs = block_tile_kbs<TM, TN>(args, tab, tile);
+            const int kbs = block_tile_kbs<TM, TN>(args, tab, tile, split, share);
             float2 acc[64];
 #pragma unroll
             for (int p = 0; p < 64; p++) acc[p] = make_float2(0.0f, 0.0f);
@@ -737,9 +811,18 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
                 bph ^= buf == BUFS - 1;
                 buf = buf == BUFS - 1 ? 0 : buf + 1;
             }
+            if (SPLIT) {
+                // this share's sums, where the operands were (all its MMAs are done): sixteen bytes of
+                // lane l's row at 512 k + 16 l, free of bank conflicts for the writer and the readers
+#pragma unroll
+                for (int k = 0; k < 32; k++)
+                    *reinterpret_cast<float4 *>(smem + (warp - 4) * 16384 + 512 * k + 16 * lane) =
+                        make_float4(acc[2 * k].x, acc[2 * k].y, acc[2 * k + 1].x, acc[2 * k + 1].y);
+                break;  // the cluster's one tile; joined below
+            }
             if (!ok) break;
             const TileOut out = kbs > 0 ? tile_out[seq % TILE_RING]
-                                        : tile_out_of(block_tile<TM, TN>(args, tab, tile), rank);  // nothing to sum: zeros
+                                        : tile_out_of(block_tile<TM, TN>(args, tab, tile, split, share), rank);  // nothing to sum: zeros
             const int64_t rows = out.rows - 32 * q, n0 = out.n0 + HALF * half;
             if (rows > 0 && n0 < args.N)
                 store_tile(args, &tmap_d, stage, lane, out.d_row + 32 * q, (int)min(rows, (int64_t)32), n0,
@@ -752,7 +835,22 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
     tc_fence_before();
     __syncwarp();
     __syncthreads();
-    cluster_sync();  // the peer's shared memory and TMEM stay live until the pair is done
+    if (SPLIT) {
+        cluster_sync();  // every share's sums are there
+        if (warp >= 4 && pair < tiles) {
+            const TileOut out = tile_out[0];
+            const int q = warp & 3, half = (warp - 4) >> 2;
+            const uint8_t *sums = smem + (warp - 4) * 16384 + 16 * lane;
+            if (32 * q + lane < out.rows && split == 2)
+                join_shares<2>(args, smem_u32(sums), rank, share, out.d_row + 32 * q + lane, out.n0 + HALF * half,
+                               bias_ring + HALF * half);
+            if (32 * q + lane < out.rows && split == 4)
+                join_shares<4>(args, smem_u32(sums), rank, share, out.d_row + 32 * q + lane, out.n0 + HALF * half,
+                               bias_ring + HALF * half);
+        }
+        __syncwarp();
+    }
+    cluster_sync();  // the peers' shared memory and TMEM stay live until the cluster is done
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
@@ -788,12 +886,6 @@ struct Shape {
     static_assert(STAGES * STAGE_BYTES >= BT * TW * 4, "the sums of a split tile take the operands' place");
 };
 }  // namespace bf
-
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
 
 template <int BT>
 __global__ void __launch_bounds__(bf::Shape<BT>::THREADS, 2)
@@ -1049,13 +1141,15 @@ __global__ void __launch_bounds__(bf::Shape<BT>::THREADS, 2)
 // host
 // ---------------------------------------------------------------------------
 static std::atomic<bool> g_block_set[64];
-static int g_block_pairs[64];
+static int g_block_pairs[64][3];  // clusters of 2, 4 and 8 CTAs resident at once
 
 static fp8dl_status block_gemm_setup(int dev, int sms) {
     if (g_block_set[dev].load(std::memory_order_acquire)) return FP8DL_OK;
     std::lock_guard<std::mutex> lock(init_mutex());
     if (g_block_set[dev].load(std::memory_order_relaxed)) return FP8DL_OK;
-    const void *kernels[] = {(const void *)block_gemm_kernel<false>, (const void *)block_gemm_kernel<true>};
+    int resident[3] = {1 << 30, 1 << 30, 1 << 30};
+    const void *kernels[] = {(const void *)block_gemm_kernel<false, false>, (const void *)block_gemm_kernel<true, false>,
+                             (const void *)block_gemm_kernel<false, true>, (const void *)block_gemm_kernel<true, true>};
     for (const void *k : kernels) {
         cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bp::SMEM_BYTES);
         cudaFuncAttributes fa = {};
@@ -1066,23 +1160,27 @@ static fp8dl_status block_gemm_setup(int dev, int sms) {
             return fail(FP8DL_ERR_CUDA, "block GEMM: built with %d registers, %d needed", fa.numRegs, bp::REGS_LAUNCH);
         // persistent pairs: how many are resident at once
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(sms / 2 * 2), 1, 1);
         cfg.blockDim = dim3(bp::THREADS, 1, 1);
         cfg.dynamicSmemBytes = bp::SMEM_BYTES;
         cudaLaunchAttribute at = {};
         at.id = cudaLaunchAttributeClusterDimension;
-        at.val.clusterDim.x = 2;
         at.val.clusterDim.y = at.val.clusterDim.z = 1;
         cfg.attrs = &at;
         cfg.numAttrs = 1;
-        int n = 0;
-        e = cudaOccupancyMaxActiveClusters(&n, k, &cfg);
-        if (e != cudaSuccess || n < 1) {
-            cudaGetLastError();
-            return fail(FP8DL_ERR_UNSUPPORTED_DEVICE, "the block GEMM needs resident CTA-pair clusters");
+        for (int i = 0; i < 3; i++) {
+            at.val.clusterDim.x = 2u << i;
+            cfg.gridDim = dim3((unsigned)(sms / (2 << i) * (2 << i)), 1, 1);
+            int n = 0;
+            e = cudaOccupancyMaxActiveClusters(&n, k, &cfg);
+            if (e != cudaSuccess) {
+                cudaGetLastError();
+                n = 0;
+            }
+            if (i == 0 && n < 1) return fail(FP8DL_ERR_UNSUPPORTED_DEVICE, "the block GEMM needs resident CTA-pair clusters");
+            resident[i] = n < resident[i] ? n : resident[i];
         }
-        g_block_pairs[dev] = g_block_pairs[dev] == 0 || n < g_block_pairs[dev] ? n : g_block_pairs[dev];
     }
+    for (int i = 0; i < 3; i++) g_block_pairs[dev][i] = resident[i];
     const void *few[] = {(const void *)block_gemm_few_kernel<16>, (const void *)block_gemm_few_kernel<32>,
                          (const void *)block_gemm_few_kernel<64>};
     const int bytes[] = {bf::Shape<16>::SMEM_BYTES, bf::Shape<32>::SMEM_BYTES, bf::Shape<64>::SMEM_BYTES};
@@ -1095,17 +1193,19 @@ static fp8dl_status block_gemm_setup(int dev, int sms) {
 }
 
 // Rows of A per tile of the few-row kernel, or 0 for the 256 x 256 tiles.  Times in us, weights from
-// DRAM, 16 / 32 / 64 rows a tile against 256 x 256 tiles:
-//   N 4096, K 4096      M 1: 7.2 / 7.5 / 8.4, 17.8;  M 64: 10.2 / 9.3 / 10.0, 17.4;  M 256: - / 15.2 / 17.3, 18.1;
-//                       M 384: - / - / 21.0, 18.2
-//   N 2048, K 7168      M 512: - / - / 22.7, 26.8;  M 768: no gain
+// DRAM, 16 / 32 / 64 rows a tile against 256 x 256 tiles (shared by pairs where that helps):
+//   N 4096, K 4096      M 1: 7.2 / 7.5 / 8.4, 17;  M 64: 10.2 / 9.4 / 10.2, 13.3;  M 128: - / 12.7 / 12.1, 14.8;
+//                       M 256: - / 15.7 / 17.8, 14.9
+//   N 1024, K 4096      M 256: - / 8.7 / 9.1, 12.4;  M 512: - / 12.2 / 11.6, 13.1;  M 1024: - / - / 17.5, 14.3
+//   N 2048, K 7168      M 256: - / 16.6 / 15.0, 15.9;  M 512: - / 23.6 / 23.5, 19.0
 //   N 11008, K 4096     M 48: 13.7 / 15.9 / 17.6, 19.5;  M 96: 22.7 / 16.3 / 21.8, 19.6;  M 128: 30.8 / 24.5 / 21.7, 19.9
 //   N 16384, K 4096     M 32: 16.3 / 18.4 / 19.2, 21.2;  M 64: 23.2 / 17.6 / 21.2, 21.7;  M 96: 31.9 / 26.8 / 22.7, 22.0
 //   64 groups, N 2048, K 4096, rows a group  16: 105 / 107 / 113, 138;  64: 146 / 113 / 117, 138;
 //                       96: 207 / 140 / 142, 139;  128: 269 / 171 / 141, 142
 // One product: the fewest rows a tile whose tiles run at once (or all rows in one tile), up to
-// 96 rows; more rows only while 256 x 256 tiles would occupy no more than 16 of the 76 pairs.
-// Groups: by their mean length (the host does not see the offsets).
+// 96 rows, or 128 where 256 x 256 tiles would occupy at most 16 of the 76 pairs, or any number
+// where they would occupy at most 8.  Groups: by their mean length (the host does not see the
+// offsets).
 static int few_rows(const BlockGemmArgs &a, int sms) {
     if (a.kind == BG_REDUCE) return 0;
     if (a.kind == BG_ROWS) {
@@ -1114,7 +1214,7 @@ static int few_rows(const BlockGemmArgs &a, int sms) {
         return mean <= 16 ? 16 : mean <= 48 ? 32 : mean <= 96 ? 64 : 0;
     }
     const int64_t pair_tiles = ((a.M + bp::TM - 1) / bp::TM) * ((a.N + bp::TN - 1) / bp::TN);
-    if (a.M > 96 && pair_tiles > 16) return 0;
+    if (a.M > 96 && !(a.M <= 128 && pair_tiles <= 16) && pair_tiles > 8) return 0;
     for (int bt = 16; bt <= 64; bt *= 2) {
         const int64_t row_tiles = (a.M + bt - 1) / bt;
         if (row_tiles == 1 || row_tiles * ((a.N + bf::TW - 1) / bf::TW) <= 2 * sms) return bt;
@@ -1196,9 +1296,21 @@ static fp8dl_status launch_block_gemm(const uint8_t *A, int32_t a_dtype, int64_t
                           : args.kind == BG_ROWS ? (args.M / bp::TM + busy) * tiles_n
                                                  : args.n_groups * tiles_m * tiles_n;
     if (bound > 0x7fffffffll) return fail(FP8DL_ERR_SHAPE, "%s: more than 2^31 - 1 output tiles", what);
-    const int64_t pairs = bound < g_block_pairs[dev] ? bound : g_block_pairs[dev];
-    (void)launch_kernel(brows ? block_gemm_kernel<true> : block_gemm_kernel<false>, dim3((unsigned)(2 * pairs)),
-                        bp::THREADS, bp::SMEM_BYTES, st, 2, pdl, ta, tb, td, args);
+    // One product with too few tiles for the pairs: two or four pairs share each tile, as long as
+    // all their clusters run at once and the blocks they save are worth the join.  us with 1 / 2 / 4
+    // pairs a tile:  M 512, N 4096, K 4096 (32 tiles) 17.9 / 16.0;  M 256, N 4096, K 11008 (16 tiles)
+    // 38.0 / 25.7, 37.9 with 4 (not all at once);  M 256, N 2048, K 7168 (8 tiles) 26.0 / 18.8 / 15.9;
+    // M 512, N 1024, K 4096 (8 tiles) 17.0 / 14.0 / 13.1;  M 512, N 1536, K 1536 (12 tiles) 9.8 / 10.7 / 11.5.
+    int split = 1;
+    if (args.kind == BG_DENSE) {
+        const int64_t kbs = (args.K + 127) / 128;
+        if (bound <= g_block_pairs[dev][1] && kbs >= 24) split = 2;
+        if (bound <= g_block_pairs[dev][2] && kbs >= 32) split = 4;
+    }
+    const int64_t clusters = split > 1 || bound < g_block_pairs[dev][0] ? bound : g_block_pairs[dev][0];
+    (void)launch_kernel(split > 1 ? (brows ? block_gemm_kernel<true, true> : block_gemm_kernel<false, true>)
+                                  : (brows ? block_gemm_kernel<true, false> : block_gemm_kernel<false, false>),
+                        dim3((unsigned)(2 * split * clusters)), bp::THREADS, bp::SMEM_BYTES, st, 2 * split, pdl, ta, tb, td, args);
     note_launch();
     return check_launch(what);
 }

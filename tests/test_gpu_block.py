@@ -160,6 +160,11 @@ GEMMS = [  # M, N, K, fmt_a, b per row, bias dtype, D dtype
     (272, 1008, 1040, 0, True, torch.bfloat16, torch.bfloat16),
     (640, 528, 384, 1, True, None, torch.float32),
     (20000, 48, 256, 0, False, None, torch.float32),
+    # few tiles and a long reduction: pairs share a tile's blocks (uneven shares, ragged rows and columns)
+    (600, 1040, 4112, 0, False, torch.bfloat16, torch.bfloat16),
+    (700, 2064, 3088, 1, False, torch.float32, torch.float32),
+    (300, 528, 6160, 0, True, torch.bfloat16, torch.float32),
+    (513, 1296, 4240, 1, True, None, torch.bfloat16),
 ]
 
 
