@@ -266,11 +266,6 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
 }
 
 // Loads from shared memory of a CTA of the cluster (addresses from mapa_shared).
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
@@ -864,9 +859,9 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
 // more than the rows there are and the kernel runs at the speed the weight arrives.
 //   warp 0      TMA producer: 128 weight rows and BT rows of A per k-block
 //   warp 1      MMA thread: four MMAs (M 128, N BT, K 32) per block into one of NB buffers
-//   warp 2      copies the blocks' factors (one per row of A, one of the weight's) into a ring
-//   warps 4-7   epilogue: a thread holds one weight row x BT rows of A; the two factors are
-//               multiplied and applied per block as in the tile kernel
+//   warp 2      multiplies the blocks' factors (one per row of A with the weight's) into a ring
+//   warp 3      relay: a block's one signal to the epilogue, as in the tile kernel
+//   warps 4-7   epilogue: a thread holds one weight row x BT rows of A
 // Split: where the tiles alone would leave SMs without a weight to read, the CTAs of a cluster
 // share a tile, each with a contiguous part of the blocks, and add their sums in rank order
 // through distributed shared memory: no workspace, one launch, the same bits every time.
@@ -880,12 +875,42 @@ struct Shape {
     static constexpr int STAGE_BYTES = TW * BK + BT * BK;
     static constexpr int STAGES = BT <= 32 ? 5 : 4;
     static constexpr int NB = 4, TMEM_COLS = NB * BT;
-    static constexpr int RING = 8, SLOT = BT + 4;              // factors per block: BT of A's, one of B's
+    static constexpr int RING = 8, SLOT = BT;                  // the factors of eight blocks, BT each
     static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + RING * SLOT * 4 + kGroupTableBytes + 1024;
     static_assert(2 * SMEM_BYTES <= 227 * 1024 && 2 * TMEM_COLS <= 512, "two CTAs per SM");
     static_assert(STAGES * STAGE_BYTES >= BT * TW * 4, "the sums of a split tile take the operands' place");
 };
 }  // namespace bf
+
+// A split tile's end: the cluster's sums (row t of A at 512 t bytes from `sums` in every CTA) are added in
+// rank order; rank r stores every SPLIT-th row, four columns a thread, the loads of all ranks
+// under way at once.
+template <int SPLIT>
+__device__ __forceinline__ void join_few(const BlockGemmArgs &a, uint32_t sums, uint32_t rank, const BlockTile &w, int rows) {
+    uint32_t from[SPLIT];
+#pragma unroll
+    for (int o = 0; o < SPLIT; o++) from[o] = mapa_shared(sums, o);
+    const int col = 4 * (threadIdx.x & 31);
+    const int64_t n = w.n0 + col;
+    if (n >= a.N) return;
+    for (int t = SPLIT * (threadIdx.x >> 5) + (int)rank; t < rows; t += SPLIT * 8) {
+        float4 v[SPLIT];
+#pragma unroll
+        for (int o = 0; o < SPLIT; o++) v[o] = ld_cluster_f32x4(from[o] + 4 * (t * bf::TW + col));
+#pragma unroll
+        for (int o = 1; o < SPLIT; o++) v[0].x += v[o].x, v[0].y += v[o].y, v[0].z += v[o].z, v[0].w += v[o].w;
+        if (a.bias_dtype >= 0)
+            v[0].x += load_bias1(a, n), v[0].y += load_bias1(a, n + 1), v[0].z += load_bias1(a, n + 2), v[0].w += load_bias1(a, n + 3);
+        const int64_t at = (w.d_row + t) * a.N + n;
+        if (a.d_dtype == FP8DL_BF16) {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0].x, v[0].y), hi = __floats2bfloat162_rn(v[0].z, v[0].w);
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.D) + at) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+        } else {
+            *reinterpret_cast<float4 *>(static_cast<float *>(a.D) + at) = v[0];
+        }
+    }
+}
 
 template <int BT>
 __global__ void __launch_bounds__(bf::Shape<BT>::THREADS, 2)
@@ -916,11 +941,11 @@ __global__ void __launch_bounds__(bf::Shape<BT>::THREADS, 2)
             mbar_init(smem_u32(&empty[i]), 1);
         }
         for (int i = 0; i < S::NB; i++) {
-            mbar_init(smem_u32(&tfull[i]), 1);
+            mbar_init(smem_u32(&tfull[i]), 2);  // the MMAs' commit, and the relay's word for the factors
             mbar_init(smem_u32(&tempty[i]), S::EPI_WARPS);
         }
         for (int i = 0; i < S::RING; i++) {
-            mbar_init(smem_u32(&ffull[i]), 32);
+            mbar_init(smem_u32(&ffull[i]), 1);
             mbar_init(smem_u32(&fempty[i]), S::EPI_WARPS);
         }
         *abort_flag = 0;
@@ -1005,6 +1030,9 @@ __global__ void __launch_bounds__(bf::Shape<BT>::THREADS, 2)
         }
         if (!ok && any) mbar_drain(last_bar, last_par);
     } else if (warp == 2) {  // ------------------------------------------------- factors
+        // The two factors of every row and block, multiplied once for all the weight's rows.  Four
+        // blocks' are loaded at a time, four blocks before they are needed.
+        constexpr int PER = (BT + 31) / 32, AHEAD = 4;
         int slot = 0;
         uint32_t ph = 0;
         bool ok = true;
@@ -1012,45 +1040,80 @@ __global__ void __launch_bounds__(bf::Shape<BT>::THREADS, 2)
             const BlockTile w = block_tile<BT, TW>(args, tab, tile);
             const float *pa = args.a_s + (int64_t)kb0 * args.M + w.a_row;
             const float *pb = w.b_s + (int64_t)kb0 * args.b_ld + (w.n0 >> 7);
-            for (int kb = kb0; kb < kb1; kb++, pa += args.M, pb += args.b_ld) {
-                if (!warp_wait(smem_u32(&fempty[slot]), ph ^ 1, abort_flag, args.status)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t dst = smem_u32(ring + slot * S::SLOT);
+            float fa[AHEAD][PER], fb[AHEAD], na[AHEAD][PER], nb[AHEAD];
+            auto load = [&](int kb, float(&a)[AHEAD][PER], float(&b)[AHEAD]) {
 #pragma unroll
-                for (int t = 0; t < BT; t += 32)  // rows behind the last take the first one's factor
-                    if (t + lane < BT) cp_async4(dst + 4 * (t + lane), pa + (w.a_row + t + lane < w.a_end ? t + lane : 0));
-                if (lane == 0) cp_async4(dst + 4 * BT, pb);
-                cp_async_arrive(smem_u32(&ffull[slot]));
-                if (++slot == S::RING) {
-                    slot = 0;
-                    ph ^= 1;
+                for (int i = 0; i < AHEAD; i++, pa += args.M, pb += args.b_ld) {
+                    b[i] = kb + i < kb1 ? __ldg(pb) : 0.0f;
+#pragma unroll
+                    for (int t = 0; t < PER; t++)  // rows behind the last: zeros, not stored
+                        a[i][t] = kb + i < kb1 && 32 * t + lane < BT && w.a_row + 32 * t + lane < w.a_end
+                                      ? __ldg(pa + 32 * t + lane)
+                                      : 0.0f;
+                }
+            };
+            load(kb0, fa, fb);
+            for (int kb = kb0; kb < kb1 && ok; kb += AHEAD) {
+                load(kb + AHEAD, na, nb);
+#pragma unroll
+                for (int i = 0; i < AHEAD; i++) {
+                    if (kb + i >= kb1 || !(ok = warp_wait(smem_u32(&fempty[slot]), ph ^ 1, abort_flag, args.status))) break;
+#pragma unroll
+                    for (int t = 0; t < PER; t++)
+                        if (32 * t + lane < BT) ring[slot * S::SLOT + 32 * t + lane] = __fmul_rn(fa[i][t], fb[i]);
+                    __syncwarp();
+                    arrive_if(smem_u32(&ffull[slot]), lane == 0);
+                    if (++slot == S::RING) {
+                        slot = 0;
+                        ph ^= 1;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < AHEAD; i++) {
+                    fb[i] = nb[i];
+#pragma unroll
+                    for (int t = 0; t < PER; t++) fa[i][t] = na[i][t];
                 }
             }
         }
-        cp_async_wait_all();
+    } else if (warp == 3) {  // ------------------------------------------------- relay (as in the tile kernel)
+        int slot = 0, buf = 0;
+        uint32_t fph = 0, bph = 0;
+        bool ok = true;
+        for (uint32_t tile = tile0; tile < tiles && ok; tile += step)
+            for (int kb = kb0; kb < kb1; kb++) {
+                ok = warp_wait(smem_u32(&ffull[slot]), fph, abort_flag, args.status) &&
+                     warp_wait(smem_u32(&tfull[buf]), bph ^ 1, abort_flag, args.status);
+                if (!ok) break;
+                arrive_if(smem_u32(&tfull[buf]), lane == 0);
+                if (++slot == S::RING) {
+                    slot = 0;
+                    fph ^= 1;
+                }
+                if (++buf == S::NB) {
+                    buf = 0;
+                    bph ^= 1;
+                }
+            }
     } else if (warp >= 4) {  // ------------------------------------------------- epilogue
         const int q = warp & 3;
         const int row = 32 * q + lane;  // of the weight tile
         const uint32_t taddr0 = tmem_base + ((uint32_t)(32 * q) << 16);
         int slot = 0, buf = 0;
-        uint32_t fph = 0, bph = 0;
+        uint32_t bph = 0;
         for (uint32_t tile = tile0; tile < tiles; tile += step) {
             float2 acc[BT / 2];
 #pragma unroll
             for (int p = 0; p < BT / 2; p++) acc[p] = make_float2(0.0f, 0.0f);
             bool ok = true;
             for (int kb = kb0; kb < kb1; kb++) {
-                if (!warp_wait(smem_u32(&ffull[slot]), fph, abort_flag, args.status) ||
-                    !warp_wait(smem_u32(&tfull[buf]), bph, abort_flag, args.status)) {
+                if (!warp_wait(smem_u32(&tfull[buf]), bph, abort_flag, args.status)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t ta = taddr0 + (uint32_t)(buf * BT);
                 const float *fac = ring + slot * S::SLOT;
-                const float2 fb = f2(fac[BT]);
                 constexpr int LD = BT < 32 ? 16 : 32;
 #pragma unroll
                 for (int c = 0; c < BT; c += LD) {
@@ -1063,22 +1126,17 @@ __global__ void __launch_bounds__(bf::Shape<BT>::THREADS, 2)
                     regs_ready(r);
 #pragma unroll
                     for (int j = 0; j < LD; j += 4) {
-                        const float4 fa = *reinterpret_cast<const float4 *>(fac + c + j);
-                        const float2 s0 = __fmul2_rn(make_float2(fa.x, fa.y), fb), s1 = __fmul2_rn(make_float2(fa.z, fa.w), fb);
-                        acc[(c + j) / 2] = __ffma2_rn(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), s0,
-                                                      acc[(c + j) / 2]);
-                        acc[(c + j) / 2 + 1] = __ffma2_rn(
-                            make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), s1, acc[(c + j) / 2 + 1]);
+                        const float4 f = *reinterpret_cast<const float4 *>(fac + c + j);
+                        float2 &a = acc[(c + j) / 2], &b = acc[(c + j) / 2 + 1];
+                        a = __ffma2_rn(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), make_float2(f.x, f.y), a);
+                        b = __ffma2_rn(make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), make_float2(f.z, f.w), b);
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
                 arrive_if(smem_u32(&tempty[buf]), lane == 0);
                 arrive_if(smem_u32(&fempty[slot]), lane == 0);
-                if (++slot == S::RING) {
-                    slot = 0;
-                    fph ^= 1;
-                }
+                if (++slot == S::RING) slot = 0;
                 if (++buf == S::NB) {
                     buf = 0;
                     bph ^= 1;
@@ -1116,16 +1174,9 @@ __global__ void __launch_bounds__(bf::Shape<BT>::THREADS, 2)
         if (tile0 < tiles) {
             const BlockTile w = block_tile<BT, TW>(args, tab, tile0);
             const int rows = (int)min(w.a_end - w.a_row, (int64_t)BT);
-            const uint32_t red = smem_u32(smem);
-            // rank r joins every split-th row of A, 128 consecutive columns of D per row
-            for (int i = threadIdx.x; i < (BT / (int)split) * TW; i += S::THREADS) {
-                const int t = (i / TW) * (int)split + (int)rank, col = i % TW;
-                if (t >= rows || w.n0 + col >= args.N) continue;
-                float v = 0.0f;
-                for (uint32_t r = 0; r < split; r++) v += ld_cluster_f32(mapa_shared(red + 4 * (t * TW + col), r));
-                if (args.bias_dtype >= 0) v += load_bias1(args, w.n0 + col);
-                store1(args, (w.d_row + t) * args.N + w.n0 + col, v);
-            }
+            if (split == 2) join_few<2>(args, smem_u32(smem), rank, w, rows);
+            if (split == 4) join_few<4>(args, smem_u32(smem), rank, w, rows);
+            if (split == 8) join_few<8>(args, smem_u32(smem), rank, w, rows);
         }
         __syncwarp();
         cluster_sync();  // nobody's sums go away while they are read
@@ -1192,34 +1243,63 @@ static fp8dl_status block_gemm_setup(int dev, int sms) {
     return FP8DL_OK;
 }
 
-// Rows of A per tile of the few-row kernel, or 0 for the 256 x 256 tiles.  Times in us, weights from
-// DRAM, 16 / 32 / 64 rows a tile against 256 x 256 tiles (shared by pairs where that helps):
-//   N 4096, K 4096      M 1: 7.2 / 7.5 / 8.4, 17;  M 64: 10.2 / 9.4 / 10.2, 13.3;  M 128: - / 12.7 / 12.1, 14.8;
-//                       M 256: - / 15.7 / 17.8, 14.9
-//   N 1024, K 4096      M 256: - / 8.7 / 9.1, 12.4;  M 512: - / 12.2 / 11.6, 13.1;  M 1024: - / - / 17.5, 14.3
-//   N 2048, K 7168      M 256: - / 16.6 / 15.0, 15.9;  M 512: - / 23.6 / 23.5, 19.0
-//   N 11008, K 4096     M 48: 13.7 / 15.9 / 17.6, 19.5;  M 96: 22.7 / 16.3 / 21.8, 19.6;  M 128: 30.8 / 24.5 / 21.7, 19.9
-//   N 16384, K 4096     M 32: 16.3 / 18.4 / 19.2, 21.2;  M 64: 23.2 / 17.6 / 21.2, 21.7;  M 96: 31.9 / 26.8 / 22.7, 22.0
-//   64 groups, N 2048, K 4096, rows a group  16: 105 / 107 / 113, 138;  64: 146 / 113 / 117, 138;
-//                       96: 207 / 140 / 142, 139;  128: 269 / 171 / 141, 142
-// One product: the fewest rows a tile whose tiles run at once (or all rows in one tile), up to
-// 96 rows, or 128 where 256 x 256 tiles would occupy at most 16 of the 76 pairs, or any number
-// where they would occupy at most 8.  Groups: by their mean length (the host does not see the
-// offsets).
-static int few_rows(const BlockGemmArgs &a, int sms) {
+// How many CTAs share a tile of the few-row kernel: as many as run at once, while each keeps four
+// blocks (us at M 1, N 4096, K 4096 with 1 / 2 / 4 / 8: 10.8 / 8.3 / 7.2 / 7.3; at M 64, N 2048, K 7168:
+// 16.8 / 11.2 / 8.7 / 8.5).
+static int few_split(int64_t tiles, int64_t kbs, int sms) {
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= 2 * (int64_t)sms && kbs >= 8 * split) split *= 2;
+    return split;
+}
+
+// Pairs that share a 256 x 256 tile of one product: two or four where tiles are few and the reduction
+// long, as long as all their clusters run at once.  us with 1 / 2 / 4 pairs a tile:  M 512, N 4096, K 4096
+// (32 tiles) 17.9 / 16.0;  M 512, N 4096, K 11008 38.4 / 26.9;  M 256, N 4096, K 11008 (16 tiles) 38.0 / 25.7,
+// 37.9 with 4 (not all at once);  M 256, N 2048, K 7168 (8 tiles) 26.0 / 18.8 / 15.9;  M 512, N 1536, K 1536
+// (12 tiles) 9.8 / 10.7 / 11.5.
+static int pair_split(int64_t tiles, int64_t kbs, const int (&resident)[3]) {
+    if (tiles <= resident[2] && kbs >= 32) return 4;
+    return tiles <= resident[1] && kbs >= 24 ? 2 : 1;
+}
+
+// Rows of A per tile of the few-row kernel, or 0 for the 256 x 256 tiles.
+// Groups: by their mean length (the host does not see the offsets).  64 groups, N 2048, K 4096, us with
+// 16 / 32 / 64 rows a tile and with 256 x 256 tiles: 16 rows a group 105 / 107 / 113, 138;  64 rows 146 /
+// 113 / 117, 138;  96 rows 207 / 140 / 142, 139;  128 rows 269 / 171 / 141, 142.
+// One product: by what the two kernels' times follow.  The few-row kernel's: the bytes that pass the
+// SM with the most CTAs (weight and rows of A, its CTAs' share of the blocks), and the rows a
+// tile (epilogue and join): 4.5 us + 7.5 us per 1000 of (KB + 6 a row).  The tiles': 0.42 us a block, 6 us
+// of start and end, 2 for a join.  us, 16 / 32 / 64 rows a tile, 256 x 256 tiles:
+//   N 11008, K 4096   M 17: 14.2 / 12.4 / 15.6, 19.6;  M 37: 14.5 / 14.9 / 13.8, 19.6;  M 80: - / 15.2 / 19.5, 19.6;
+//                     M 128: - / - / 19.6, 19.9
+//   N 4096, K 4096    M 37: 9.8 / 8.5 / 8.7, 13.3;  M 128: - / 10.4 / 10.6, 14.8;  M 256: - / - / 12.9, 14.9;  M 512: - / - / 21, 16.0
+//   N 2048, K 7168    M 64: 9.3 / 8.5 / 10.0, 13.6;  M 256: - / - / 12.8, 15.9
+//   N 1536, K 1536    M 64: 5.7 / 6.0 / 7.0, 8.9;  M 256: - / 6.9 / 7.2, 9.8
+//   N 16384, K 4096   M 64: - / 17.3 / 17.4, 21.7;  M 128: - / - / 20.7, 22.1
+static int few_rows(const BlockGemmArgs &a, int sms, const int (&resident)[3]) {
     if (a.kind == BG_REDUCE) return 0;
     if (a.kind == BG_ROWS) {
         const int64_t busy = a.n_groups < a.M ? a.n_groups : a.M;
         const int64_t mean = (a.M + busy - 1) / busy;
         return mean <= 16 ? 16 : mean <= 48 ? 32 : mean <= 96 ? 64 : 0;
     }
+    const int64_t kbs = (a.K + 127) / 128, tiles_w = (a.N + bf::TW - 1) / bf::TW;
     const int64_t pair_tiles = ((a.M + bp::TM - 1) / bp::TM) * ((a.N + bp::TN - 1) / bp::TN);
-    if (a.M > 96 && !(a.M <= 128 && pair_tiles <= 16) && pair_tiles > 8) return 0;
+    const int pairs = pair_split(pair_tiles, kbs, resident);
+    const int64_t waves = (pair_tiles * pairs + resident[0] - 1) / resident[0];
+    double best = 6.0 + 0.42 * (double)(waves * ((kbs + pairs - 1) / pairs)) + (pairs > 1 ? 2.0 : 0.0);
+    int rows = 0;
     for (int bt = 16; bt <= 64; bt *= 2) {
-        const int64_t row_tiles = (a.M + bt - 1) / bt;
-        if (row_tiles == 1 || row_tiles * ((a.N + bf::TW - 1) / bf::TW) <= 2 * sms) return bt;
+        const int64_t tiles = (a.M + bt - 1) / bt * tiles_w;
+        const int split = few_split(tiles, kbs, sms);
+        const double kb = 0.125 * (double)((tiles * split + sms - 1) / sms * ((kbs + split - 1) / split) * (bf::TW + bt));
+        const double us = 4.5 + 0.0075 * (kb + 6.0 * bt);
+        if (us < best) {
+            best = us;
+            rows = bt;
+        }
     }
-    return a.M <= 64 ? 64 : 0;
+    return rows;
 }
 
 template <int BT>
@@ -1239,11 +1319,8 @@ static fp8dl_status launch_few(const uint8_t *A, int32_t a_dtype, const uint8_t 
     if (bound > 0x7fffffffll) return fail(FP8DL_ERR_SHAPE, "%s: more than 2^31 - 1 output tiles", what);
     args.along_n = 0;  // the token tiles of a weight tile follow one another
     args.band = 0x7fffffffu;
-    // Split a tile's blocks over a cluster while the CTAs fit the SMs together and each keeps
-    // four blocks at least.
-    const int64_t resident = 2 * (int64_t)sms, kbs = (args.K + 127) / 128;
-    int split = 1;
-    while (split < 8 && bound * split * 2 <= resident && kbs >= 8 * split) split *= 2;
+    const int64_t resident = 2 * (int64_t)sms;
+    const int split = few_split(bound, (args.K + 127) / 128, sms);
     const int64_t ctas = split > 1 ? bound * split : bound < resident ? bound : resident;
     (void)launch_kernel(block_gemm_few_kernel<BT>, dim3((unsigned)ctas), S::THREADS, S::SMEM_BYTES, st, split, pdl, ta, tb, args);
     note_launch();
@@ -1271,7 +1348,7 @@ static fp8dl_status launch_block_gemm(const uint8_t *A, int32_t a_dtype, int64_t
     int dev = 0, sms = 0;
     FP8DL_TRY(current_device(&dev, &sms));
     FP8DL_TRY(block_gemm_setup(dev, sms));
-    const int bt = brows ? 0 : few_rows(args, sms);
+    const int bt = brows ? 0 : few_rows(args, sms, g_block_pairs[dev]);
     if (bt == 16) return launch_few<16>(A, a_dtype, B, b_dtype, b_rows, args, sms, st, pdl, what);
     if (bt == 32) return launch_few<32>(A, a_dtype, B, b_dtype, b_rows, args, sms, st, pdl, what);
     if (bt == 64) return launch_few<64>(A, a_dtype, B, b_dtype, b_rows, args, sms, st, pdl, what);
@@ -1296,17 +1373,7 @@ static fp8dl_status launch_block_gemm(const uint8_t *A, int32_t a_dtype, int64_t
                           : args.kind == BG_ROWS ? (args.M / bp::TM + busy) * tiles_n
                                                  : args.n_groups * tiles_m * tiles_n;
     if (bound > 0x7fffffffll) return fail(FP8DL_ERR_SHAPE, "%s: more than 2^31 - 1 output tiles", what);
-    // One product with too few tiles for the pairs: two or four pairs share each tile, as long as
-    // all their clusters run at once and the blocks they save are worth the join.  us with 1 / 2 / 4
-    // pairs a tile:  M 512, N 4096, K 4096 (32 tiles) 17.9 / 16.0;  M 256, N 4096, K 11008 (16 tiles)
-    // 38.0 / 25.7, 37.9 with 4 (not all at once);  M 256, N 2048, K 7168 (8 tiles) 26.0 / 18.8 / 15.9;
-    // M 512, N 1024, K 4096 (8 tiles) 17.0 / 14.0 / 13.1;  M 512, N 1536, K 1536 (12 tiles) 9.8 / 10.7 / 11.5.
-    int split = 1;
-    if (args.kind == BG_DENSE) {
-        const int64_t kbs = (args.K + 127) / 128;
-        if (bound <= g_block_pairs[dev][1] && kbs >= 24) split = 2;
-        if (bound <= g_block_pairs[dev][2] && kbs >= 32) split = 4;
-    }
+    const int split = args.kind == BG_DENSE ? pair_split(bound, (args.K + 127) / 128, g_block_pairs[dev]) : 1;
     const int64_t clusters = split > 1 || bound < g_block_pairs[dev][0] ? bound : g_block_pairs[dev][0];
     (void)launch_kernel(split > 1 ? (brows ? block_gemm_kernel<true, true> : block_gemm_kernel<false, true>)
                                   : (brows ? block_gemm_kernel<true, false> : block_gemm_kernel<false, false>),
