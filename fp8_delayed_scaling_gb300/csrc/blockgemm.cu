@@ -1264,8 +1264,9 @@ static int pair_split(int64_t tiles, int64_t kbs, const int (&resident)[3]) {
 
 // Rows of A per tile of the few-row kernel, or 0 for the 256 x 256 tiles.
 // Groups: by their mean length (the host does not see the offsets).  64 groups, N 2048, K 4096, us with
-// 16 / 32 / 64 rows a tile and with 256 x 256 tiles: 16 rows a group 105 / 107 / 113, 138;  64 rows 146 /
-// 113 / 117, 138;  96 rows 207 / 140 / 142, 139;  128 rows 269 / 171 / 141, 142.
+// 16 / 32 / 64 rows a tile and with 256 x 256 tiles: 16 rows a group 87 / 88 / 93, 116;  32 rows 94 / 89 /
+// 95, 116;  64 rows 138 / 99 / 97, 118;  96 rows 200 / 122 / 117, 121;  128 rows - / 151 / 120, 122;  192 rows
+// - / 220 / 172, 125.
 // One product: by what the two kernels' times follow.  The few-row kernel's: the bytes that pass the
 // SM with the most CTAs (weight and rows of A, its CTAs' share of the blocks), and the rows a
 // tile (epilogue and join): 4.5 us + 7.5 us per 1000 of (KB + 6 a row).  The tiles': 0.42 us a block, 6 us
