@@ -9,7 +9,6 @@
 // buffer, and the epilogue warps multiply it into fp32 registers while the next block's MMAs
 // run.  The tile's whole sum lives in registers; tensor memory only passes the blocks on.
 #include <cuda_bf16.h>
-#include <stdlib.h>
 
 #include "block.cuh"
 #include "tc.cuh"
@@ -883,22 +882,21 @@ struct Shape {
 }  // namespace bf
 
 // A split tile's end: the cluster's sums (row t of A at 512 t bytes from `sums` in every CTA) are added in
-// rank order; rank r stores every SPLIT-th row, four columns a thread, the loads of all ranks
+// rank order; rank r stores every split-th row, four columns a thread, the loads of all ranks
 // under way at once.
-template <int SPLIT>
-__device__ __forceinline__ void join_few(const BlockGemmArgs &a, uint32_t sums, uint32_t rank, const BlockTile &w, int rows) {
-    uint32_t from[SPLIT];
-#pragma unroll
-    for (int o = 0; o < SPLIT; o++) from[o] = mapa_shared(sums, o);
+__device__ __forceinline__ void join_few(const BlockGemmArgs &a, uint32_t sums, int split, int rank, const BlockTile &w,
+                                         int rows) {
     const int col = 4 * (threadIdx.x & 31);
     const int64_t n = w.n0 + col;
     if (n >= a.N) return;
-    for (int t = SPLIT * (threadIdx.x >> 5) + (int)rank; t < rows; t += SPLIT * 8) {
-        float4 v[SPLIT];
+    for (int t = split * (int)(threadIdx.x >> 5) + rank; t < rows; t += split * 8) {
+        float4 v[8];
 #pragma unroll
-        for (int o = 0; o < SPLIT; o++) v[o] = ld_cluster_f32x4(from[o] + 4 * (t * bf::TW + col));
+        for (int o = 0; o < 8; o++)
+            if (o < split) v[o] = ld_cluster_f32x4(mapa_shared(sums, o) + 4 * (t * bf::TW + col));
 #pragma unroll
-        for (int o = 1; o < SPLIT; o++) v[0].x += v[o].x, v[0].y += v[o].y, v[0].z += v[o].z, v[0].w += v[o].w;
+        for (int o = 1; o < 8; o++)
+            if (o < split) v[0].x += v[o].x, v[0].y += v[o].y, v[0].z += v[o].z, v[0].w += v[o].w;
         if (a.bias_dtype >= 0)
             v[0].x += load_bias1(a, n), v[0].y += load_bias1(a, n + 1), v[0].z += load_bias1(a, n + 2), v[0].w += load_bias1(a, n + 3);
         const int64_t at = (w.d_row + t) * a.N + n;
@@ -1174,9 +1172,7 @@ __global__ void __launch_bounds__(bf::Shape<BT>::THREADS, 2)
         if (tile0 < tiles) {
             const BlockTile w = block_tile<BT, TW>(args, tab, tile0);
             const int rows = (int)min(w.a_end - w.a_row, (int64_t)BT);
-            if (split == 2) join_few<2>(args, smem_u32(smem), rank, w, rows);
-            if (split == 4) join_few<4>(args, smem_u32(smem), rank, w, rows);
-            if (split == 8) join_few<8>(args, smem_u32(smem), rank, w, rows);
+            join_few(args, smem_u32(smem), (int)split, (int)rank, w, rows);
         }
         __syncwarp();
         cluster_sync();  // nobody's sums go away while they are read
@@ -1243,13 +1239,15 @@ static fp8dl_status block_gemm_setup(int dev, int sms) {
     return FP8DL_OK;
 }
 
-// How many CTAs share a tile of the few-row kernel: as many as run at once, while each keeps four
-// blocks (us at M 1, N 4096, K 4096 with 1 / 2 / 4 / 8: 10.8 / 8.3 / 7.2 / 7.3; at M 64, N 2048, K 7168:
-// 16.8 / 11.2 / 8.7 / 8.5).
+// How many CTAs share a tile of the few-row kernel, each with two blocks at least: as many as give every SM
+// one CTA, or, where the tiles alone fill more than half the SMs, two.  More than six cost
+// more than they save.  us with 1 / 2 / 3 / 4 / 5 / 6 / 8:
+//   M 16, N 4096, K 4096 (32 tiles) 11.0 / 8.5 / 7.9 / 7.5 / 8.0 / 7.9 / 7.9;  M 64 14.8 / 10.8 / 9.7 / 9.0 / 10.1 / 10.1 / 10.3
+//   M 64, N 2048, K 7168 (16 tiles) 21.6 / 13.9 / 11.4 / 9.9 / 9.5 / 9.2 / 10.1;  M 64, N 11008, K 4096 (86 tiles) 16.6 / 14.5 / 13.9
 static int few_split(int64_t tiles, int64_t kbs, int sms) {
-    int split = 1;
-    while (split < 8 && tiles * split * 2 <= 2 * (int64_t)sms && kbs >= 8 * split) split *= 2;
-    return split;
+    const int64_t most = kbs / 2 < 6 ? kbs / 2 : 6;
+    const int64_t split = (2 * tiles > sms ? 2 * (int64_t)sms : (int64_t)sms) / tiles;
+    return split < 1 || most < 1 ? 1 : (int)(split < most ? split : most);
 }
 
 // Pairs that share a 256 x 256 tile of one product: two or four where tiles are few and the reduction

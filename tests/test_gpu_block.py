@@ -165,6 +165,11 @@ GEMMS = [  # M, N, K, fmt_a, b per row, bias dtype, D dtype
     (700, 2064, 3088, 1, False, torch.float32, torch.float32),
     (300, 528, 6160, 0, True, torch.bfloat16, torch.float32),
     (513, 1296, 4240, 1, True, None, torch.bfloat16),
+    # a weight tile's blocks over three, four, five and six CTAs (uneven shares, ragged rows)
+    (19, 6016, 528, 0, False, torch.float32, torch.float32),
+    (61, 4096, 1168, 1, False, None, torch.bfloat16),
+    (50, 3600, 1424, 0, False, torch.bfloat16, torch.bfloat16),
+    (9, 1040, 2576, 0, False, torch.bfloat16, torch.float32),
     # more tiles than run at once
     (2500, 2064, 400, 0, False, torch.bfloat16, torch.float32),
     (2310, 2320, 256, 1, True, torch.float32, torch.bfloat16),
