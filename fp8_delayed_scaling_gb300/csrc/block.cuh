@@ -37,29 +37,55 @@ __device__ __forceinline__ int64_t warp_inclusive_sum(int64_t v, int lane) {
     return v;
 }
 
-// Called by one whole warp: the rows behind 128-row block `block` of the padded order (every
-// group rounded up to a multiple of 128): first row and how many (0 behind the last group).
-__device__ __forceinline__ void group_of_block(const int32_t *offsets, int n_groups, int64_t rows, int64_t block,
-                                               int64_t &first_row, int64_t &count) {
-    const int lane = threadIdx.x & 31;
-    int64_t before = 0;  // blocks of the groups already passed
-    for (int g0 = 0; g0 < n_groups; g0 += 32) {
-        int64_t first = 0, end = 0;
-        if (g0 + lane < n_groups) group_rows(offsets, g0 + lane, rows, first, end);
-        const int64_t blocks = (end - first + 127) / 128;
-        const int64_t sum = before + warp_inclusive_sum(blocks, lane);
-        const unsigned hit = __ballot_sync(0xffffffffu, block < sum);
-        if (hit) {
-            const int src = __ffs((int)hit) - 1;
-            const int64_t r = first + (block - (sum - blocks)) * 128;
-            first_row = __shfl_sync(0xffffffffu, r, src);
-            count = min(__shfl_sync(0xffffffffu, end, src) - first_row, (int64_t)128);
-            return;
+// Called by all 256 threads of a block: the rows behind 128-row block `block` of the padded order (every
+// group rounded up to a multiple of 128): first row and how many (0 behind the last group).  A
+// thread takes up to four groups, so every offset is loaded at once and few instructions are issued
+// (a search by every warp for itself cost twice the time with 200 groups).  Offsets in disorder may wrap
+// the 32-bit sums; the rows returned are a group's, clamped to the tensor, all the same.
+__device__ __forceinline__ void group_of_block(const int32_t *offsets, int n_groups, int64_t rows, uint32_t block,
+                                               int64_t &first_row, int &count) {
+    __shared__ uint32_t warp_sum[8];
+    __shared__ int32_t found[2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = (int)rows;
+    const int per = (n_groups + 255) / 256, g0 = (int)threadIdx.x * per;
+    int32_t first[4], length[4];
+    uint32_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        first[i] = length[i] = 0;
+        if (i < per && g0 + i < n_groups) {
+            first[i] = min(max(offsets[g0 + i], 0), n);
+            length[i] = min(max(offsets[g0 + i + 1], first[i]), n) - first[i];
         }
-        before = __shfl_sync(0xffffffffu, sum, 31);
+        mine += ((uint32_t)length[i] + 127) >> 7;
     }
-    first_row = 0;
-    count = 0;
+    uint32_t sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += u;
+    }
+    if (lane == 31) warp_sum[warp] = sum;
+    if (threadIdx.x == 0) found[1] = 0;
+    __syncthreads();
+    uint32_t at = block - (sum - mine);  // within this thread's blocks, if below `mine`
+#pragma unroll
+    for (int w = 0; w < 7; w++) at -= w < warp ? warp_sum[w] : 0;
+    if (at < mine) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint32_t blocks = ((uint32_t)length[i] + 127) >> 7;
+            if (at < blocks) {
+                found[0] = first[i] + (int32_t)(at * 128);
+                found[1] = min(length[i] - (int32_t)(at * 128), 128);
+                break;
+            }
+            at -= blocks;
+        }
+    }
+    __syncthreads();
+    first_row = found[0];
+    count = found[1];
 }
 
 }  // namespace fp8dl

@@ -12,6 +12,7 @@ namespace fp8dl {
 
 namespace bq {
 constexpr int THREADS = 256, TILE = 128;
+enum { TOKENS, GROUPS, WEIGHT };
 }
 
 struct BlockQuantArgs {
@@ -114,34 +115,56 @@ struct Values<FP8DL_F32> {
 //            8-byte chunks XOR-swizzled by column group (conflict-free both ways), and leave
 //            as whole 128-byte lines.
 // WEIGHT: one scale for the tile instead, for both copies.
-// Bound: HBM (read esz, write 2 bytes per value).  8192 x 4096 bf16, both copies: 25.6 us, 5.3 TB/s;
-// weights 16384 x 4096 bf16: 44.9 us, 6.0 TB/s; 32 of 1008 x 2048 fp32: 64.8 us, 6.1 TB/s.
-template <int XKIND, int FMT, bool WEIGHT>
-__global__ void __launch_bounds__(bq::THREADS, XKIND == FP8DL_BF16 || WEIGHT ? 3 : 2)
+// GROUPS: a tile is a group's; where groups are short, most warps of a CTA would have no rows.  A tile of
+// up to 16, 32 or 64 rows takes 1, 2 or 4 warps and the CTA the next 8, 4 or 2 column tiles; their
+// own CTAs write the padding behind the rows' 32-byte sectors (500 rows of 200 groups, 4096 columns fp32:
+// 72 us with a CTA for every tile, 43 so; 4096 rows 80 and 53; 24 groups of 2999 rows no change).
+// Bound: HBM (read esz, write 2 bytes per value).  8192 x 4096 bf16, both copies: 25.1 us, 5.4 TB/s;
+// weights 16384 x 4096 bf16: 44.0 us, 6.1 TB/s; 32 of 1008 x 2048 fp32: 63.9 us, 6.2 TB/s.
+template <int XKIND, int FMT, int KIND>
+__global__ void __launch_bounds__(bq::THREADS, XKIND == FP8DL_BF16 || KIND == bq::WEIGHT ? 3 : 2)
     block_quantize_kernel(const BlockQuantArgs args) {
     using namespace bq;
     pdl_wait();
     pdl_trigger();
     constexpr int ESZ = XKIND == FP8DL_BF16 ? 2 : 4;
+    constexpr int MOST = KIND == GROUPS ? 8 : 1;    // column tiles of a CTA
     __shared__ __align__(16) uint8_t tcode[TILE * TILE];
     __shared__ __align__(16) float part[8][TILE];   // column maxima (or sums) per warp
-    __shared__ __align__(16) float cscale[TILE];
-    __shared__ int64_t where[2];                    // ragged groups: first row and row count of the tile
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cc = tid & 15, rr = tid >> 4;
-    const int64_t tile_r = blockIdx.x / args.tiles_c, tile_c = blockIdx.x % args.tiles_c;
+    __shared__ __align__(16) float cscale[MOST * TILE];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cc = tid & 15;
+    const uint32_t tiles_c = (uint32_t)args.tiles_c;
+    const uint32_t tile_r = blockIdx.x / tiles_c, tile_c0 = blockIdx.x % tiles_c;
     const int64_t mat = blockIdx.y;
-    int64_t r0 = tile_r * TILE, nrows = min((int64_t)TILE, args.rows - r0);
-    if (!WEIGHT && args.offsets) {
-        if (warp == 0) {
-            int64_t first, n;
-            group_of_block(args.offsets, args.n_groups, args.rows, tile_r, first, n);
-            if (lane == 0) where[0] = first, where[1] = n;
+    int64_t r0 = (int64_t)tile_r * TILE;
+    int nrows = (int)min((int64_t)TILE, args.rows - r0);
+    int wlog = 3;  // log2 of the warps of a tile
+    if (KIND == GROUPS) {
+        if (args.col_q) {
+            group_of_block(args.offsets, args.n_groups, args.rows, tile_r, r0, nrows);
+        } else {  // rows alone: the groups' borders do not matter, where the first begins and the last ends does
+            int64_t first, end;
+            group_rows(args.offsets, 0, args.rows, first, end);
+            end = min(max((int64_t)args.offsets[args.n_groups], first), args.rows);
+            r0 += first;
+            nrows = (int)min((int64_t)TILE, end - r0);
         }
-        __syncthreads();
-        r0 = where[0];
-        nrows = where[1];
         if (nrows <= 0) return;  // behind the last group
+        wlog = nrows <= 16 ? 0 : nrows <= 32 ? 1 : nrows <= 64 ? 2 : 3;
+        if (tile_c0 & ((8u >> wlog) - 1)) {  // another CTA's, but for the padding behind its rows' sectors
+            const int ch = tid & 7;
+            if (args.col_q && ch >= 2 * ((nrows + 31) / 32)) {
+                uint8_t *to = args.col_q + ((int64_t)tile_c0 * TILE + (tid >> 3)) * args.col_ld + (int64_t)tile_r * TILE + 16 * ch;
+                for (int64_t c = (int64_t)tile_c0 * TILE + (tid >> 3), k = 0; k < 4 && c < args.cols; k++, c += 32, to += 32 * args.col_ld)
+                    *reinterpret_cast<uint4 *>(to) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            return;
+        }
     }
+    const int sub = KIND == GROUPS ? warp >> wlog : 0, lw = warp - (sub << wlog);  // the warp's tile, its place there
+    const int rr = KIND == GROUPS ? 2 * lw + (lane >> 4) : tid >> 4;
+    const int64_t tile_c = tile_c0 + sub;
+    const bool live = KIND != GROUPS || (16 * lw < nrows && tile_c < args.tiles_c);
     const int64_t c0 = tile_c * TILE + 8 * cc;
     const bool col_ok = c0 < args.cols;  // columns come in sixteens
     const char *px = static_cast<const char *>(args.x) + ((mat * args.rows + r0 + 8 * rr) * args.cols + c0) * ESZ;
@@ -171,7 +194,7 @@ __global__ void __launch_bounds__(bq::THREADS, XKIND == FP8DL_BF16 || WEIGHT ? 3
         for (int i = 0; i < 8; i++) top = fmaxf(top, rmax[i]);
     }
     float tile_scale = 0.0f;
-    if (WEIGHT) {
+    if (KIND == WEIGHT) {
         float m = warp_max(top);
         if (lane == 0) cscale[warp] = m;
         __syncthreads();
@@ -185,16 +208,16 @@ __global__ void __launch_bounds__(bq::THREADS, XKIND == FP8DL_BF16 || WEIGHT ? 3
         }
         tile_scale = sc.x;
     }
-    if (!WEIGHT && args.col_q) {  // column maxima of the warp; joined after the row-wise stores are on their way
+    if (KIND != WEIGHT && args.col_q) {  // column maxima of the warp; joined after the row-wise stores are on their way
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             cmax[j] = fmaxf(cmax[j], __shfl_xor_sync(0xffffffffu, cmax[j], 16));
             if (lane < 16) part[warp][8 * cc + j] = cmax[j];
         }
     }
-    if (args.row_q) {
+    if (args.row_q && live) {
         float own = tile_scale;
-        if (!WEIGHT) {
+        if (KIND != WEIGHT) {
             // halving exchange: after steps 8, 4, 2 lane cc holds row (cc >> 1) of its eight
 #pragma unroll
             for (int i = 0; i < 4; i++) {
@@ -221,7 +244,7 @@ __global__ void __launch_bounds__(bq::THREADS, XKIND == FP8DL_BF16 || WEIGHT ? 3
         uint8_t *qrow = args.row_q + (mat * args.rows + r0 + 8 * rr) * args.cols + c0;
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-            const float2 s2 = f2(WEIGHT ? own : __shfl_sync(0xffffffffu, own, (lane & 16) + 2 * i));
+            const float2 s2 = f2(KIND == WEIGHT ? own : __shfl_sync(0xffffffffu, own, (lane & 16) + 2 * i));
             float2 y[4];
 #pragma unroll
             for (int q = 0; q < 4; q++) y[q] = __fmul2_rn(v.pair(i, q), s2);
@@ -230,7 +253,7 @@ __global__ void __launch_bounds__(bq::THREADS, XKIND == FP8DL_BF16 || WEIGHT ? 3
                     pack4<FMT>(y[0].x, y[0].y, y[1].x, y[1].y), pack4<FMT>(y[2].x, y[2].y, y[3].x, y[3].y));
         }
     }
-    if (!WEIGHT && args.ws) {  // column sums of the tile, rows in a fixed order
+    if (KIND != WEIGHT && args.ws) {  // column sums of the tile, rows in a fixed order
         float *sums = reinterpret_cast<float *>(tcode);  // [8][TILE], before the codes take the place
 #pragma unroll
         for (int q = 0; q < 4; q++) {
@@ -250,56 +273,70 @@ __global__ void __launch_bounds__(bq::THREADS, XKIND == FP8DL_BF16 || WEIGHT ? 3
         }
     }
     if (!args.col_q) return;
-    if (!WEIGHT) {
+    const int width = TILE << (3 - wlog);  // the CTA's columns
+    if (KIND != WEIGHT) {
         __syncthreads();
-        if (tid < TILE) {
-            float m = part[0][tid];
-#pragma unroll
-            for (int w = 1; w < 8; w++) m = fmaxf(m, part[w][tid]);
+        for (int c = tid; c < width; c += THREADS) {
+            const int w0 = (c >> 7) << wlog, w1 = w0 + (1 << wlog);
+            float m = part[w0][c & 127];
+            for (int w = w0 + 1; w < w1; w++) m = fmaxf(m, part[w][c & 127]);
             const float2 sc = block_scale<FMT>(m);
-            cscale[tid] = sc.x;
-            if (tile_c * TILE + tid < args.cols) args.col_s[tile_r * args.cols + tile_c * TILE + tid] = sc.y;
+            cscale[c] = sc.x;
+            const int64_t col = (int64_t)tile_c0 * TILE + c;
+            if (col < args.cols) args.col_s[tile_r * args.cols + col] = sc.y;
         }
         __syncthreads();
     }
+    if (live) {
+        const float *cs = cscale + sub * TILE + 8 * cc;
 #pragma unroll
-    for (int q = 0; q < 4; q++) {  // columns 8cc + 2q and the next
-        const float2 s2 = WEIGHT ? f2(tile_scale) : *reinterpret_cast<const float2 *>(cscale + 8 * cc + 2 * q);
-        float2 y[8];
+        for (int q = 0; q < 4; q++) {  // columns 8cc + 2q and the next
+            const float2 s2 = KIND == WEIGHT ? f2(tile_scale) : *reinterpret_cast<const float2 *>(cs + 2 * q);
+            float2 y[8];
 #pragma unroll
-        for (int i = 0; i < 8; i++) y[i] = __fmul2_rn(v.pair(i, q), s2);
-        uint8_t *at = tcode + (8 * cc + 2 * q) * TILE + ((rr ^ cc) << 3);
-        *reinterpret_cast<uint2 *>(at) =
-            make_uint2(pack4<FMT>(y[0].x, y[1].x, y[2].x, y[3].x), pack4<FMT>(y[4].x, y[5].x, y[6].x, y[7].x));
-        *reinterpret_cast<uint2 *>(at + TILE) =
-            make_uint2(pack4<FMT>(y[0].y, y[1].y, y[2].y, y[3].y), pack4<FMT>(y[4].y, y[5].y, y[6].y, y[7].y));
+            for (int i = 0; i < 8; i++) y[i] = __fmul2_rn(v.pair(i, q), s2);
+            uint8_t *at = tcode + (8 * cc + 2 * q) * TILE + (((tid >> 4) ^ cc) << 3);
+            *reinterpret_cast<uint2 *>(at) =
+                make_uint2(pack4<FMT>(y[0].x, y[1].x, y[2].x, y[3].x), pack4<FMT>(y[4].x, y[5].x, y[6].x, y[7].x));
+            *reinterpret_cast<uint2 *>(at + TILE) =
+                make_uint2(pack4<FMT>(y[0].y, y[1].y, y[2].y, y[3].y), pack4<FMT>(y[4].y, y[5].y, y[6].y, y[7].y));
+        }
     }
     __syncthreads();
-    // weights: r0 .. r0+127 of q_t's rows (sixteens); groups: the tile's 128 padded columns
-    const int64_t out0 = tile_r * TILE;
-    uint8_t *qcol = args.col_q + (mat * args.cols + tile_c * TILE) * args.col_ld + out0;
+    // weights: r0 .. r0+127 of q_t's rows (sixteens); tokens: the tile's 128 padded columns, of
+    // which sixteen are one warp's rows
+    const int64_t out0 = (int64_t)tile_r * TILE;
+    const int ch = tid & 7, first = tid >> 3, left = (int)min((int64_t)width, args.cols - (int64_t)tile_c0 * TILE);
+    const bool has = KIND != GROUPS || 16 * ch < nrows;  // chunk ch holds warp ch's rows; the rest is zeros
+    if (KIND == WEIGHT && out0 + 16 * ch >= args.col_ld) return;
+    uint8_t *to = args.col_q + (mat * args.cols + (int64_t)tile_c0 * TILE + first) * args.col_ld + out0 + 16 * ch;
+    for (int c0 = first; c0 < width; c0 += 128) {
+        uint4 u[4];
 #pragma unroll
-    for (int k = 0; k < 4; k++) {
-        const int col = 32 * k + (tid >> 3), ch = tid & 7, g = col >> 3;
-        uint4 u = *reinterpret_cast<const uint4 *>(tcode + col * TILE + ((ch ^ (g >> 1)) << 4));
-        if (g & 1) u = make_uint4(u.z, u.w, u.x, u.y);
-        if (tile_c * TILE + col < args.cols && out0 + 16 * ch < args.col_ld)
-            *reinterpret_cast<uint4 *>(qcol + col * args.col_ld + 16 * ch) = u;
+        for (int k = 0; k < 4; k++) {
+            const int c = first + 32 * k, g = c >> 3, w = KIND == GROUPS ? ((c0 >> 7) << wlog) + ch : ch;
+            u[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (has) u[k] = *reinterpret_cast<const uint4 *>(tcode + c * TILE + ((w ^ (g >> 1)) << 4));
+            if (g & 1) u[k] = make_uint4(u[k].z, u[k].w, u[k].x, u[k].y);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; k++, to += 32 * args.col_ld)
+            if (c0 + 32 * k < left && (KIND != GROUPS || c0 < TILE || ch < 2 * ((nrows + 31) / 32))) *reinterpret_cast<uint4 *>(to) = u[k];
     }
 }
 
-template <bool WEIGHT>
+template <int KIND>
 static void launch_block_quantize(int32_t x_dtype, int32_t out_dtype, dim3 grid, cudaStream_t st, bool pdl,
                                   const BlockQuantArgs &a) {
     const bool e4 = out_dtype == FP8DL_E4M3;
     if (x_dtype == FP8DL_BF16 && e4)
-        (void)launch_kernel(block_quantize_kernel<FP8DL_BF16, FP8DL_E4M3, WEIGHT>, grid, bq::THREADS, 0, st, 0, pdl, a);
+        (void)launch_kernel(block_quantize_kernel<FP8DL_BF16, FP8DL_E4M3, KIND>, grid, bq::THREADS, 0, st, 0, pdl, a);
     else if (x_dtype == FP8DL_BF16)
-        (void)launch_kernel(block_quantize_kernel<FP8DL_BF16, FP8DL_E5M2, WEIGHT>, grid, bq::THREADS, 0, st, 0, pdl, a);
+        (void)launch_kernel(block_quantize_kernel<FP8DL_BF16, FP8DL_E5M2, KIND>, grid, bq::THREADS, 0, st, 0, pdl, a);
     else if (e4)
-        (void)launch_kernel(block_quantize_kernel<FP8DL_F32, FP8DL_E4M3, WEIGHT>, grid, bq::THREADS, 0, st, 0, pdl, a);
+        (void)launch_kernel(block_quantize_kernel<FP8DL_F32, FP8DL_E4M3, KIND>, grid, bq::THREADS, 0, st, 0, pdl, a);
     else
-        (void)launch_kernel(block_quantize_kernel<FP8DL_F32, FP8DL_E5M2, WEIGHT>, grid, bq::THREADS, 0, st, 0, pdl, a);
+        (void)launch_kernel(block_quantize_kernel<FP8DL_F32, FP8DL_E5M2, KIND>, grid, bq::THREADS, 0, st, 0, pdl, a);
     note_launch();
 }
 
@@ -348,7 +385,7 @@ extern "C" fp8dl_status fp8_block_quantize(const void *x, int32_t x_dtype, int64
     a.rows = rows;
     a.cols = cols;
     a.tiles_c = (cols + 127) / 128;
-    a.row_blocks = fp8_block_padded_rows(rows, n_groups) / 128;
+    a.row_blocks = fp8_block_padded_rows(rows, col_q ? n_groups : 0) / 128;
     a.offsets = offsets;
     a.n_groups = n_groups;
     a.row_q = row_q;
@@ -360,7 +397,11 @@ extern "C" fp8dl_status fp8_block_quantize(const void *x, int32_t x_dtype, int64
     if (a.tiles_c * a.row_blocks > 0x7fffffffll)
         return fail(FP8DL_ERR_SHAPE, "%lld x %lld is more than 2^31 - 1 tiles", (long long)rows, (long long)cols);
     const bool pdl = short_call_bytes((double)rows * (double)cols * (x_dtype == FP8DL_BF16 ? 4.0 : 6.0));
-    launch_block_quantize<false>(x_dtype, out_dtype, dim3((unsigned)(a.tiles_c * a.row_blocks)), st, pdl, a);
+    const dim3 grid((unsigned)(a.tiles_c * a.row_blocks));
+    if (offsets)
+        launch_block_quantize<bq::GROUPS>(x_dtype, out_dtype, grid, st, pdl, a);
+    else
+        launch_block_quantize<bq::TOKENS>(x_dtype, out_dtype, grid, st, pdl, a);
     FP8DL_TRY(check_launch("fp8_block_quantize"));
     if (dbias) {
         colsum_reduce(a.ws, (rows + 127) / 128, cols, dbias, st, pdl);
@@ -398,7 +439,7 @@ extern "C" fp8dl_status fp8_block_quantize_weight(const void *w, int32_t w_dtype
         return fail(FP8DL_ERR_SHAPE, "%lld x %lld is more than 2^31 - 1 tiles", (long long)rows, (long long)cols);
     FP8DL_TRY(current_device(nullptr, nullptr));
     const bool pdl = short_call_bytes((double)n_mats * (double)rows * (double)cols * (w_dtype == FP8DL_BF16 ? 4.0 : 6.0));
-    launch_block_quantize<true>(w_dtype, out_dtype, dim3((unsigned)(a.tiles_c * a.row_blocks), (unsigned)n_mats),
+    launch_block_quantize<bq::WEIGHT>(w_dtype, out_dtype, dim3((unsigned)(a.tiles_c * a.row_blocks), (unsigned)n_mats),
                                 (cudaStream_t)stream, pdl, a);
     return check_launch("fp8_block_quantize_weight");
 }

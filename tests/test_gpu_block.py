@@ -108,6 +108,51 @@ def test_quantize_groups(off):
     assert np.array_equal(got["col_s"][:used // 128], st[:used // 128]) and np.all(got["col_s"][used // 128:] == 7.0)
 
 
+SHORT = [[0, 1, 17, 33, 65, 66, 129, 290], [4] + [4 + 3 * i for i in range(1, 300)], list(range(0, 1025)),
+         [0, 16, 32, 64, 128, 256, 256]]
+
+
+@pytest.mark.parametrize("dtype,fmt", [(torch.bfloat16, 1), (torch.float32, 0)])
+@pytest.mark.parametrize("off", SHORT, ids=range(len(SHORT)))
+def test_quantize_short_groups(off, dtype, fmt):
+    """Groups of a few rows share a block of threads between column tiles; eleven of those, the last one narrow."""
+    fd, dev = _fd()
+    rows, cols = off[-1] + 3, 1296
+    x = _x(rows, cols, dtype, "s%s" % off[:6])
+    x[off[0] + 1, 600] = float("inf")
+    b = _buffers(fd, rows, cols, len(off) - 1, dev)
+    o = torch.tensor(off, dtype=torch.int32, device=dev)
+    fd.fp8_block_quantize(x.to(dev), fmt, offsets=o, **b)
+    xf = x.float().numpy()
+    q, s = br.rows(xf, fmt)
+    qt, st, used = br.cols(xf, fmt, off)
+    inside = slice(off[0], off[-1])
+    got = {k: v.cpu().numpy() for k, v in b.items()}
+    assert np.array_equal(got["row_q"][inside], q[inside]) and np.array_equal(got["row_s"][:, inside], s[:, inside])
+    assert np.array_equal(got["col_q"][:, :used], qt[:, :used]) and np.all(got["col_q"][:, used:] == 0xAA)
+    assert np.array_equal(got["col_s"][:used // 128], st[:used // 128]) and np.all(got["col_s"][used // 128:] == 7.0)
+    one = _buffers(fd, rows, cols, len(off) - 1, dev)  # either direction alone: the same bits, the same rows left alone
+    fd.fp8_block_quantize(x.to(dev), fmt, row_q=one["row_q"], row_s=one["row_s"], offsets=o)
+    fd.fp8_block_quantize(x.to(dev), fmt, col_q=one["col_q"], col_s=one["col_s"], offsets=o)
+    for k in one:
+        assert torch.equal(one[k], b[k]), k
+
+
+def test_quantize_wrong_offsets_stay_inside():
+    """Offsets in disorder or behind the last row give wrong codes, and no access outside the tensors."""
+    fd, dev = _fd()
+    rows, cols, off = 300, 272, [7, 900, 100, -5, 250, 5000, -2 ** 31, 2 ** 31 - 1]
+    x = _x(rows, cols, torch.bfloat16, "wrong").to(dev)
+    T = fd.fp8_block_padded_rows(rows, len(off) - 1)
+    sizes = dict(row_q=(torch.uint8, (rows, cols)), row_s=(torch.float32, (br.blocks(cols), rows)),
+                 col_q=(torch.uint8, (cols, T)), col_s=(torch.float32, (T // 128, cols)))
+    whole = {k: torch.full((shape[0] * shape[1] + 8192,), 7, dtype=t, device=dev) for k, (t, shape) in sizes.items()}
+    view = {k: whole[k][4096:-4096].view(shape) for k, (t, shape) in sizes.items()}
+    fd.fp8_block_quantize(x, 0, offsets=torch.tensor(off, dtype=torch.int32, device=dev), **view)
+    for v in whole.values():
+        assert torch.all(v[:4096] == 7) and torch.all(v[-4096:] == 7)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("shape", [(16, 16), (128, 128), (144, 400), (1, 1008, 272), (5, 48, 1040)])
 @pytest.mark.parametrize("fmt", [0, 1])
@@ -311,3 +356,25 @@ def test_grouped_wgrad_with_mostly_empty_groups():
         bv = br.values(ops[2][:, at:at + 128 * n], 0, ops[3][at // 128:at // 128 + n], 1)
         br.check(D[e], av @ bv.T, np.abs(av) @ np.abs(bv).T, 128 * n, "wgrad of group %d" % e)
         at += 128 * n
+
+
+@pytest.mark.parametrize("rows", [40, 900])  # the kernels for few and for many rows a group
+def test_grouped_products_wrong_offsets_stay_inside(rows):
+    fd, dev = _fd()
+    off, N, K = torch.tensor([7, 600, 100, -5, 250, 5000, -2 ** 31, 2 ** 31 - 1], dtype=torch.int32, device=dev), 272, 400
+    G = off.numel() - 1
+    a, a_s = _operand(rows, K, 0, "wa")
+    b, b_s = _operand(G * N, K, 0, "wb")
+    t = _dev(dev, a, a_s, b)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    whole = torch.full((rows * N + 8192,), 7.0, device=dev)
+    fd.fp8_block_gemm_grouped(t[0], 0, t[1], t[2].view(G, N, K), 0, torch.ones((G, br.blocks(K), br.blocks(N)), device=dev), off,
+                              whole[4096:-4096].view(rows, N), dev_status=status)
+    T = fd.fp8_block_padded_rows(rows, G)
+    A, B = (torch.full((n, T), 0x38, dtype=torch.uint8, device=dev) for n in (144, N))
+    grads = torch.full((G * 144 * N + 8192,), 7.0, device=dev)
+    fd.fp8_block_gemm_grouped_wgrad(A, 0, torch.ones((T // 128, 144), device=dev), B, 0, torch.ones((T // 128, N), device=dev), off,
+                                    grads[4096:-4096].view(G, 144, N), dev_status=status)
+    for v in (whole, grads):
+        assert torch.all(v[:4096] == 7) and torch.all(v[-4096:] == 7)
+    assert status.item() == 0
