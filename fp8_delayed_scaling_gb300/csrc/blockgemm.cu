@@ -32,6 +32,7 @@ struct BlockGemmArgs {
     uint32_t idesc;
     int along_n;     // tile order: bands along the columns (1) or rows (0) of D
     uint32_t band;
+    uint32_t first, end;  // the launch's tiles (256 x 256)
 };
 
 // The groups' tables in shared memory: off = the offsets clamped to the tensor, in order
@@ -558,7 +559,7 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
     const uint32_t rank = SPLIT ? cluster_rank & 1 : cluster_rank, leader_rank = SPLIT ? cluster_rank & ~1u : 0u;
     const bool leader = rank == 0;
     const int split = SPLIT ? (int)(cluster_size >> 1) : 1, share = SPLIT ? (int)(cluster_rank >> 1) : 0;
-    const uint32_t pair = blockIdx.x / cluster_size, npairs = gridDim.x / cluster_size;
+    const uint32_t pair = args.first + blockIdx.x / cluster_size, npairs = gridDim.x / cluster_size;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; s++) {
@@ -593,7 +594,7 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
     if (args.kind == BG_ROWS) build_groups(tab, args.offsets, args.n_groups, args.M, TM, 0x7fffffffll);
     if (args.kind == BG_REDUCE)
         build_groups(tab, args.offsets, args.n_groups, 0x7fffffffll, 128, args.K / 128);
-    const uint32_t tiles = block_tiles<TM, TN>(args, tab);
+    const uint32_t tiles = min(block_tiles<TM, TN>(args, tab), args.end);
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_IO));
@@ -1250,14 +1251,19 @@ static int few_split(int64_t tiles, int64_t kbs, int sms) {
     return split < 1 || most < 1 ? 1 : (int)(split < most ? split : most);
 }
 
-// Pairs that share a 256 x 256 tile of one product: two or four where tiles are few and the reduction
-// long, as long as all their clusters run at once.  us with 1 / 2 / 4 pairs a tile:  M 512, N 4096, K 4096
-// (32 tiles) 17.9 / 16.0;  M 512, N 4096, K 11008 38.4 / 26.9;  M 256, N 4096, K 11008 (16 tiles) 38.0 / 25.7,
-// 37.9 with 4 (not all at once);  M 256, N 2048, K 7168 (8 tiles) 26.0 / 18.8 / 15.9;  M 512, N 1536, K 1536
-// (12 tiles) 9.8 / 10.7 / 11.5.
-static int pair_split(int64_t tiles, int64_t kbs, const int (&resident)[3]) {
-    if (tiles <= resident[2] && kbs >= 32) return 4;
-    return tiles <= resident[1] && kbs >= 24 ? 2 : 1;
+// Tiles of one product that are left when every pair has had the same number, if several pairs share each of
+// them (`split`: two or four, each with a part of the blocks), else 0: where the reduction is long and all
+// their clusters run at once.  us with 1 / 2 / 4 pairs a tile:
+//   all tiles:  M 512, N 4096, K 4096 (32 tiles) 17.9 / 16.0;  K 11008 38.4 / 26.9;  M 256, N 4096, K 11008 (16 tiles) 38.0 / 25.7,
+//     37.9 with 4 (not all at once);  M 256, N 2048, K 7168 (8 tiles) 26.0 / 18.8 / 15.9;  M 512, N 1536, K 1536 (12 tiles)
+//     9.8 / 10.7 / 11.5
+//   the last of them, in a launch of their own, without and with:  M 1280, N 4096, K 11008 (4 of 80 tiles) 72.2, 58.2;
+//     M 1536 (20 of 96) 72.2, 65.0;  M 2048, N 2560, K 8192 (4 of 80) 55.4, 46.6;  M 512, N 11008, K 4096 (10 of 86) 32.7, 33.9
+static int64_t shared_tiles(int64_t tiles, int64_t kbs, const int (&resident)[3], int &split) {
+    const int64_t tail = tiles % resident[0];
+    split = tail <= resident[2] && kbs >= 32 ? 4 : tail <= resident[1] && kbs >= 24 ? 2 : 1;
+    if (tail < tiles && kbs - (kbs + split - 1) / split < 32) split = 1;
+    return split > 1 ? tail : 0;
 }
 
 // Rows of A per tile of the few-row kernel, or 0 for the 256 x 256 tiles.
@@ -1284,9 +1290,10 @@ static int few_rows(const BlockGemmArgs &a, int sms, const int (&resident)[3]) {
     }
     const int64_t kbs = (a.K + 127) / 128, tiles_w = (a.N + bf::TW - 1) / bf::TW;
     const int64_t pair_tiles = ((a.M + bp::TM - 1) / bp::TM) * ((a.N + bp::TN - 1) / bp::TN);
-    const int pairs = pair_split(pair_tiles, kbs, resident);
-    const int64_t waves = (pair_tiles * pairs + resident[0] - 1) / resident[0];
-    double best = 6.0 + 0.42 * (double)(waves * ((kbs + pairs - 1) / pairs)) + (pairs > 1 ? 2.0 : 0.0);
+    int share;
+    const int64_t shared = shared_tiles(pair_tiles, kbs, resident, share);
+    const int64_t waves = (pair_tiles - shared + resident[0] - 1) / resident[0];
+    double best = 6.0 + 0.42 * (double)(waves * kbs + (shared ? (kbs + share - 1) / share : 0)) + (shared ? 2.0 : 0.0);
     int rows = 0;
     for (int bt = 16; bt <= 64; bt *= 2) {
         const int64_t tiles = (a.M + bt - 1) / bt * tiles_w;
@@ -1372,12 +1379,25 @@ static fp8dl_status launch_block_gemm(const uint8_t *A, int32_t a_dtype, int64_t
                           : args.kind == BG_ROWS ? (args.M / bp::TM + busy) * tiles_n
                                                  : args.n_groups * tiles_m * tiles_n;
     if (bound > 0x7fffffffll) return fail(FP8DL_ERR_SHAPE, "%s: more than 2^31 - 1 output tiles", what);
-    const int split = args.kind == BG_DENSE ? pair_split(bound, (args.K + 127) / 128, g_block_pairs[dev]) : 1;
-    const int64_t clusters = split > 1 || bound < g_block_pairs[dev][0] ? bound : g_block_pairs[dev][0];
-    (void)launch_kernel(split > 1 ? (brows ? block_gemm_kernel<true, true> : block_gemm_kernel<false, true>)
-                                  : (brows ? block_gemm_kernel<true, false> : block_gemm_kernel<false, false>),
-                        dim3((unsigned)(2 * split * clusters)), bp::THREADS, bp::SMEM_BYTES, st, 2 * split, pdl, ta, tb, td, args);
-    note_launch();
+    const int64_t pairs = g_block_pairs[dev][0];
+    int split = 1;
+    const int64_t shared = args.kind == BG_DENSE ? shared_tiles(bound, (args.K + 127) / 128, g_block_pairs[dev], split) : 0;
+    const int64_t whole = bound - shared;
+    args.end = (uint32_t)whole;
+    if (whole) {
+        (void)launch_kernel(brows ? block_gemm_kernel<true, false> : block_gemm_kernel<false, false>,
+                            dim3((unsigned)(2 * (whole < pairs ? whole : pairs))), bp::THREADS, bp::SMEM_BYTES, st, 2, pdl, ta, tb,
+                            td, args);
+        note_launch();
+    }
+    if (shared) {
+        args.first = (uint32_t)whole;
+        args.end = (uint32_t)bound;
+        (void)launch_kernel(brows ? block_gemm_kernel<true, true> : block_gemm_kernel<false, true>,
+                            dim3((unsigned)(2 * split * shared)), bp::THREADS, bp::SMEM_BYTES, st, 2 * split, pdl || whole, ta, tb,
+                            td, args);
+        note_launch();
+    }
     return check_launch(what);
 }
 

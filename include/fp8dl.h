@@ -388,7 +388,7 @@ fp8dl_status fp8_block_quantize_weight(const void *w, int32_t w_dtype, int32_t n
  * Each block's 128 products are summed on the tcgen05 tensor cores in fp32;
  * the sum over blocks is an fp32 fused multiply-add per block, in ascending
  * order of b within each of the up to six contiguous parts that K may be
- * split into where D has few tiles; the parts are added in order.
+ * split into for a tile of D; the parts are added in order.
  * Repeated calls give the same bits.
  *   A [M x K] codes of a_dtype, a_s [ceil(K/128) x M]
  *   B [N x K] codes of b_dtype, b_s [ceil(K/128) x ceil(N/b_rows)],

@@ -218,6 +218,9 @@ GEMMS = [  # M, N, K, fmt_a, b per row, bias dtype, D dtype
     # more tiles than run at once
     (2500, 2064, 400, 0, False, torch.bfloat16, torch.float32),
     (2310, 2320, 256, 1, True, torch.float32, torch.bfloat16),
+    # and a long reduction: the tiles left at the end are shared
+    (1290, 3344, 5520, 0, False, torch.float32, torch.bfloat16),
+    (1100, 4112, 5648, 1, True, torch.bfloat16, torch.float32),
 ]
 
 
