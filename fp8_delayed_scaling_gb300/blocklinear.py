@@ -136,7 +136,8 @@ class BlockLinear(_BlockLayer):
 
 
 class BlockExperts(_BlockLayer):
-    """weight [G x N x K]; x's rows sorted by group.  Rows outside the groups keep what the output buffers held."""
+    """weight [G x N x K]; x's rows sorted by group.  Rows outside the groups keep what the output buffers held.
+    backward() reads the forward's offsets again: they keep their values until it has run."""
 
     def __init__(self, weight: torch.Tensor, tokens: int, out_dtype=torch.bfloat16, grad_dtype: int = E4M3):
         super().__init__(weight, tokens, weight.shape[0], out_dtype, grad_dtype)

@@ -1275,12 +1275,12 @@ static int64_t shared_tiles(int64_t tiles, int64_t kbs, const int (&resident)[3]
 // SM with the most CTAs (weight and rows of A, its CTAs' share of the blocks), and the rows a
 // tile (epilogue and join): 4.5 us + 7.5 us per 1000 of (KB + 6 a row).  The tiles': 0.42 us a block, 6 us
 // of start and end, 2 for a join.  us, 16 / 32 / 64 rows a tile, 256 x 256 tiles:
-//   N 11008, K 4096   M 17: 14.2 / 12.4 / 15.6, 19.6;  M 37: 14.5 / 14.9 / 13.8, 19.6;  M 80: - / 15.2 / 19.5, 19.6;
-//                     M 128: - / - / 19.6, 19.9
-//   N 4096, K 4096    M 37: 9.8 / 8.5 / 8.7, 13.3;  M 128: - / 10.4 / 10.6, 14.8;  M 256: - / - / 12.9, 14.9;  M 512: - / - / 21, 16.0
-//   N 2048, K 7168    M 64: 9.3 / 8.5 / 10.0, 13.6;  M 256: - / - / 12.8, 15.9
-//   N 1536, K 1536    M 64: 5.7 / 6.0 / 7.0, 8.9;  M 256: - / 6.9 / 7.2, 9.8
-//   N 16384, K 4096   M 64: - / 17.3 / 17.4, 21.7;  M 128: - / - / 20.7, 22.1
+//   N 11008, K 4096   M 16: 12.2 / 12.3 / 13.5, 20.6;  M 37: 14.7 / 15.1 / 13.1, 18.8;  M 96: 24.1 / 15.6 / 19.4, 19.3;
+//                     M 128: 33.3 / 24.0 / 19.7, 19.6
+//   N 4096, K 4096    M 37: 8.7 / 9.0 / 8.8, 12.5;  M 128: 13.7 / 10.5 / 10.9, 14.4;  M 256: - / 14.6 / 13.0, 14.5;  M 384: - / - / 19.0, 15.3
+//   N 2048, K 7168    M 64: 10.8 / 8.7 / 9.2, 13.2;  M 256: - / 14.0 / 14.1, 15.3
+//   N 2048, K 2048    M 64: 6.2 / 6.1 / 6.8, 10.7;  M 256: - / 7.7 / 8.0, 11.1
+//   N 16384, K 4096   M 64: 24.8 / 17.2 / 17.6, 21.0;  M 128: - / 25.9 / 20.8, 21.6
 static int few_rows(const BlockGemmArgs &a, int sms, const int (&resident)[3]) {
     if (a.kind == BG_REDUCE) return 0;
     if (a.kind == BG_ROWS) {

@@ -381,3 +381,47 @@ def test_grouped_products_wrong_offsets_stay_inside(rows):
     for v in (whole, grads):
         assert torch.all(v[:4096] == 7) and torch.all(v[-4096:] == 7)
     assert status.item() == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(50, 3600, 1424), (600, 1040, 4112), (1100, 4112, 5648), (2500, 2064, 400)])
+def test_products_in_order_and_captured(M, N, K):
+    """A chain of quantisation, product and a reader of D on one stream, each launch behind the one before it; then the same
+    chain replayed from a graph over changed inputs.  Products in one launch, shared ones, and one of two launches."""
+    fd, dev = _fd()
+    b, b_s = _operand(N, K, 0, "chain", 128)
+    b, b_s = _dev(dev, b, b_s)
+    x = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    q, s = torch.empty((M, K), dtype=torch.uint8, device=dev), torch.empty((br.blocks(K), M), device=dev)
+    D, out = (torch.empty((M, N), dtype=torch.bfloat16, device=dev) for _ in range(2))
+    xs = [_x(M, K, torch.bfloat16, "chain%d" % i).to(dev) for i in range(3)]
+
+    def chain(src):
+        x.copy_(src)
+        fd.fp8_block_quantize(x, 0, row_q=q, row_s=s)
+        fd.fp8_block_gemm(q, 0, s, b, 0, b_s, D)
+        out.copy_(D)
+        D.fill_(7.0)
+
+    want = []
+    for src in xs:  # with a wait after every step
+        x.copy_(src)
+        torch.cuda.synchronize()
+        fd.fp8_block_quantize(x, 0, row_q=q, row_s=s)
+        torch.cuda.synchronize()
+        fd.fp8_block_gemm(q, 0, s, b, 0, b_s, D)
+        torch.cuda.synchronize()
+        want.append(D.clone())
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        for _ in range(3):
+            for src, w in zip(xs, want):
+                chain(src)
+                assert torch.equal(out, w)
+        src = xs[0].clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            chain(src)
+        for new, w in zip(xs[::-1], want[::-1]):
+            src.copy_(new)
+            graph.replay()
+            assert torch.equal(out, w)
