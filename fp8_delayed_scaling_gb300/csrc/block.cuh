@@ -40,8 +40,11 @@ __device__ __forceinline__ int64_t warp_inclusive_sum(int64_t v, int lane) {
 // Called by all 256 threads of a block: the rows behind 128-row block `block` of the padded order (every
 // group rounded up to a multiple of 128): first row and how many (0 behind the last group).  A
 // thread takes up to four groups, so every offset is loaded at once and few instructions are issued
-// (a search by every warp for itself cost twice the time with 200 groups).  Offsets in disorder may wrap
-// the 32-bit sums; the rows returned are a group's, clamped to the tensor, all the same.
+// (a search by every warp for itself cost twice the time with 200 groups).  Offsets in disorder may make
+// groups overlap: a warp's 128 groups then have up to 2^30 blocks (every other group 2^24), and all 1024 up
+// to 2^33.  So that 32 bits hold the sums, a warp counts for 2^28 at most, which is more than there are blocks to
+// look for (2^25): the warps after it find nothing, as they should.  One thread at most answers; two answers
+// could mix into rows behind the tensor's end.
 __device__ __forceinline__ void group_of_block(const int32_t *offsets, int n_groups, int64_t rows, uint32_t block,
                                                int64_t &first_row, int &count) {
     __shared__ uint32_t warp_sum[8];
@@ -65,7 +68,7 @@ __device__ __forceinline__ void group_of_block(const int32_t *offsets, int n_gro
         const uint32_t u = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += u;
     }
-    if (lane == 31) warp_sum[warp] = sum;
+    if (lane == 31) warp_sum[warp] = min(sum, 1u << 28);
     if (threadIdx.x == 0) found[1] = 0;
     __syncthreads();
     uint32_t at = block - (sum - mine);  // within this thread's blocks, if below `mine`
