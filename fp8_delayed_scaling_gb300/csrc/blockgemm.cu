@@ -868,7 +868,7 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
 // Two CTAs fit an SM: one's start and end hide behind the other's loads.
 // ---------------------------------------------------------------------------
 namespace bf {
-constexpr int TW = 128, BK = 128;
+constexpr int TW = 128, BK = 128, MOST_SHARES = 6;  // CTAs of a weight tile
 template <int BT>
 struct Shape {
     static constexpr int EPI_WARPS = 4, THREADS = 32 * (4 + EPI_WARPS);
@@ -891,12 +891,12 @@ __device__ __forceinline__ void join_few(const BlockGemmArgs &a, uint32_t sums, 
     const int64_t n = w.n0 + col;
     if (n >= a.N) return;
     for (int t = split * (int)(threadIdx.x >> 5) + rank; t < rows; t += split * 8) {
-        float4 v[8];
+        float4 v[bf::MOST_SHARES];
 #pragma unroll
-        for (int o = 0; o < 8; o++)
+        for (int o = 0; o < bf::MOST_SHARES; o++)
             if (o < split) v[o] = ld_cluster_f32x4(mapa_shared(sums, o) + 4 * (t * bf::TW + col));
 #pragma unroll
-        for (int o = 1; o < 8; o++)
+        for (int o = 1; o < bf::MOST_SHARES; o++)
             if (o < split) v[0].x += v[o].x, v[0].y += v[o].y, v[0].z += v[o].z, v[0].w += v[o].w;
         if (a.bias_dtype >= 0)
             v[0].x += load_bias1(a, n), v[0].y += load_bias1(a, n + 1), v[0].z += load_bias1(a, n + 2), v[0].w += load_bias1(a, n + 3);
@@ -1246,7 +1246,7 @@ static fp8dl_status block_gemm_setup(int dev, int sms) {
 //   M 16, N 4096, K 4096 (32 tiles) 11.0 / 8.5 / 7.9 / 7.5 / 8.0 / 7.9 / 7.9;  M 64 14.8 / 10.8 / 9.7 / 9.0 / 10.1 / 10.1 / 10.3
 //   M 64, N 2048, K 7168 (16 tiles) 21.6 / 13.9 / 11.4 / 9.9 / 9.5 / 9.2 / 10.1;  M 64, N 11008, K 4096 (86 tiles) 16.6 / 14.5 / 13.9
 static int few_split(int64_t tiles, int64_t kbs, int sms) {
-    const int64_t most = kbs / 2 < 6 ? kbs / 2 : 6;
+    const int64_t most = kbs / 2 < bf::MOST_SHARES ? kbs / 2 : bf::MOST_SHARES;
     const int64_t split = (2 * tiles > sms ? 2 * (int64_t)sms : (int64_t)sms) / tiles;
     return split < 1 || most < 1 ? 1 : (int)(split < most ? split : most);
 }
