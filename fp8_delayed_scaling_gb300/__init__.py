@@ -71,6 +71,7 @@ _SIGS = {
     "fp8_block_quantize_weight": (_i32, [_vp, _i32, _i32, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp]),
     "fp8_block_gemm": (_i32, [_vp, _i32, _vp, _vp, _i32, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp, _i32, _vp,
                               _vp]),
+    "fp8_block_gemm_plan": (_i32, [_i32, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp]),
     "fp8_block_gemm_grouped": (_i32, [_vp, _i32, _vp, _vp, _i32, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp,
                                       _vp]),
     "fp8_block_gemm_grouped_wgrad": (_i32, [_vp, _i32, _vp, _vp, _i32, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _i32,
@@ -461,6 +462,16 @@ def fp8_block_gemm(A: torch.Tensor, a_dtype: int, a_s: torch.Tensor, B: torch.Te
             None if bias is None else _tensor(bias, bias.dtype, (N,), dev, "bias"),
             BF16 if bias is None else _hp(bias), _tensor(D, D.dtype, (M, N), dev, "D"), _hp(D), _status(dev_status, dev))
     _check(_lib.fp8_block_gemm(*args, _launch(dev, stream)), "fp8_block_gemm")
+
+
+def fp8_block_gemm_plan(M: int, N: int, K: int, n_groups: int = 0, b_rows: int = 128) -> tuple[int, int, int, int]:
+    """What fp8_block_gemm (or, with groups, fp8_block_gemm_grouped) runs a product as on the current device: rows of A
+    a tile (16, 32, 64 or 256), CTAs (256: CTA pairs) that share each of the shared tiles, tiles computed alone, shared
+    tiles.  Launches nothing."""
+    rows, shares, whole, shared = _i32(), _i32(), _i64(), _i64()
+    _check(_lib.fp8_block_gemm_plan(b_rows, n_groups, M, N, K, ctypes.byref(rows), ctypes.byref(shares), ctypes.byref(whole),
+                                    ctypes.byref(shared)), "fp8_block_gemm_plan")
+    return rows.value, shares.value, whole.value, shared.value
 
 
 def fp8_block_gemm_grouped(A: torch.Tensor, a_dtype: int, a_s: torch.Tensor, B: torch.Tensor, b_dtype: int,

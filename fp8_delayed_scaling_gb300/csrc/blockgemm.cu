@@ -1308,9 +1308,36 @@ static int few_rows(const BlockGemmArgs &a, int sms, const int (&resident)[3]) {
     return rows;
 }
 
+// What a product runs as.  Groups: the tiles are the most there can be, wherever the groups' borders lie.
+struct BlockPlan {
+    int rows;               // of A per tile: 16, 32 or 64 (few-row kernel), or 256
+    int split;              // CTAs (few-row kernel) or CTA pairs that share each of the shared tiles
+    int64_t whole, shared;  // tiles that one of them computes alone, and shared ones
+};
+
+static BlockPlan plan_block_gemm(const BlockGemmArgs &a, bool brows, int sms, const int (&resident)[3]) {
+    BlockPlan p = {brows ? 0 : few_rows(a, sms, resident), 1, 0, 0};
+    const bool few = p.rows > 0;
+    if (!few) p.rows = bp::TM;
+    const int64_t tw = few ? bf::TW : bp::TN, tiles_m = (a.M + p.rows - 1) / p.rows, tiles_n = (a.N + tw - 1) / tw;
+    const int64_t busy = a.n_groups < a.M ? a.n_groups : a.M;  // groups that can hold a row
+    const int64_t tiles = a.kind == BG_DENSE  ? tiles_m * tiles_n
+                          : a.kind == BG_ROWS ? (a.M / p.rows + busy) * tiles_n
+                                              : a.n_groups * tiles_m * tiles_n;
+    const int64_t kbs = (a.K + 127) / 128;
+    if (few) {
+        p.split = few_split(tiles, kbs, sms);
+        p.shared = p.split > 1 ? tiles : 0;
+    } else if (a.kind == BG_DENSE) {
+        p.shared = shared_tiles(tiles, kbs, resident, p.split);
+    }
+    p.whole = tiles - p.shared;
+    return p;
+}
+
 template <int BT>
 static fp8dl_status launch_few(const uint8_t *A, int32_t a_dtype, const uint8_t *B, int32_t b_dtype, int64_t b_rows,
-                               BlockGemmArgs &args, int sms, cudaStream_t st, bool pdl, const char *what) {
+                               BlockGemmArgs &args, const BlockPlan &plan, int sms, cudaStream_t st, bool pdl, const char *what) {
     using S = bf::Shape<BT>;
     CUtensorMap ta, tb;
     FP8DL_TRY(encode_tmap_2d_u8(&ta, A, (uint64_t)args.K, (uint64_t)args.M, (uint64_t)args.K, bf::BK, BT,
@@ -1319,16 +1346,11 @@ static fp8dl_status launch_few(const uint8_t *A, int32_t a_dtype, const uint8_t 
                                 CU_TENSOR_MAP_SWIZZLE_128B));
     args.idesc = (1u << 4) | ((uint32_t)b_dtype << 7) | ((uint32_t)a_dtype << 10) | ((uint32_t)(BT >> 3) << 17) |
                  ((uint32_t)(bf::TW >> 4) << 24);
-    const int64_t tiles_w = (args.N + bf::TW - 1) / bf::TW;
-    const int64_t busy = args.n_groups < args.M ? args.n_groups : args.M;
-    const int64_t bound = args.kind == BG_DENSE ? (args.M + BT - 1) / BT * tiles_w : (args.M / BT + busy) * tiles_w;
-    if (bound > 0x7fffffffll) return fail(FP8DL_ERR_SHAPE, "%s: more than 2^31 - 1 output tiles", what);
     args.along_n = 0;  // the token tiles of a weight tile follow one another
     args.band = 0x7fffffffu;
     const int64_t resident = 2 * (int64_t)sms;
-    const int split = few_split(bound, (args.K + 127) / 128, sms);
-    const int64_t ctas = split > 1 ? bound * split : bound < resident ? bound : resident;
-    (void)launch_kernel(block_gemm_few_kernel<BT>, dim3((unsigned)ctas), S::THREADS, S::SMEM_BYTES, st, split, pdl, ta, tb, args);
+    const int64_t ctas = plan.shared ? plan.shared * plan.split : plan.whole < resident ? plan.whole : resident;
+    (void)launch_kernel(block_gemm_few_kernel<BT>, dim3((unsigned)ctas), S::THREADS, S::SMEM_BYTES, st, plan.split, pdl, ta, tb, args);
     note_launch();
     return check_launch(what);
 }
@@ -1354,10 +1376,11 @@ static fp8dl_status launch_block_gemm(const uint8_t *A, int32_t a_dtype, int64_t
     int dev = 0, sms = 0;
     FP8DL_TRY(current_device(&dev, &sms));
     FP8DL_TRY(block_gemm_setup(dev, sms));
-    const int bt = brows ? 0 : few_rows(args, sms, g_block_pairs[dev]);
-    if (bt == 16) return launch_few<16>(A, a_dtype, B, b_dtype, b_rows, args, sms, st, pdl, what);
-    if (bt == 32) return launch_few<32>(A, a_dtype, B, b_dtype, b_rows, args, sms, st, pdl, what);
-    if (bt == 64) return launch_few<64>(A, a_dtype, B, b_dtype, b_rows, args, sms, st, pdl, what);
+    const BlockPlan plan = plan_block_gemm(args, brows, sms, g_block_pairs[dev]);
+    if (plan.whole + plan.shared > 0x7fffffffll) return fail(FP8DL_ERR_SHAPE, "%s: more than 2^31 - 1 output tiles", what);
+    if (plan.rows == 16) return launch_few<16>(A, a_dtype, B, b_dtype, b_rows, args, plan, sms, st, pdl, what);
+    if (plan.rows == 32) return launch_few<32>(A, a_dtype, B, b_dtype, b_rows, args, plan, sms, st, pdl, what);
+    if (plan.rows == 64) return launch_few<64>(A, a_dtype, B, b_dtype, b_rows, args, plan, sms, st, pdl, what);
     CUtensorMap ta, tb, td;
     FP8DL_TRY(encode_tmap_2d_u8(&ta, A, (uint64_t)args.K, (uint64_t)a_rows, (uint64_t)args.K, bp::BK, 128,
                                 CU_TENSOR_MAP_SWIZZLE_128B));
@@ -1374,27 +1397,20 @@ static fp8dl_status launch_block_gemm(const uint8_t *A, int32_t a_dtype, int64_t
     // columns with 8, 848 with 16, 850 along the rows).  A group's row tiles are few: along the rows.
     args.along_n = args.kind != BG_ROWS && tiles_n < tiles_m;
     args.band = args.kind == BG_REDUCE || args.K <= 8192 ? 16 : 8;
-    const int64_t busy = args.n_groups < args.M ? args.n_groups : args.M;  // groups that can hold a row
-    const int64_t bound = args.kind == BG_DENSE  ? tiles_m * tiles_n
-                          : args.kind == BG_ROWS ? (args.M / bp::TM + busy) * tiles_n
-                                                 : args.n_groups * tiles_m * tiles_n;
-    if (bound > 0x7fffffffll) return fail(FP8DL_ERR_SHAPE, "%s: more than 2^31 - 1 output tiles", what);
     const int64_t pairs = g_block_pairs[dev][0];
-    int split = 1;
-    const int64_t shared = args.kind == BG_DENSE ? shared_tiles(bound, (args.K + 127) / 128, g_block_pairs[dev], split) : 0;
-    const int64_t whole = bound - shared;
-    args.end = (uint32_t)whole;
-    if (whole) {
+    args.end = (uint32_t)plan.whole;
+    if (plan.whole) {
         (void)launch_kernel(brows ? block_gemm_kernel<true, false> : block_gemm_kernel<false, false>,
-                            dim3((unsigned)(2 * (whole < pairs ? whole : pairs))), bp::THREADS, bp::SMEM_BYTES, st, 2, pdl, ta, tb,
+                            dim3((unsigned)(2 * (plan.whole < pairs ? plan.whole : pairs))), bp::THREADS, bp::SMEM_BYTES, st, 2, pdl, ta, tb,
                             td, args);
         note_launch();
     }
-    if (shared) {
-        args.first = (uint32_t)whole;
-        args.end = (uint32_t)bound;
+    if (plan.shared) {
+        args.first = (uint32_t)plan.whole;
+        args.end = (uint32_t)(plan.whole + plan.shared);
         (void)launch_kernel(brows ? block_gemm_kernel<true, true> : block_gemm_kernel<false, true>,
-                            dim3((unsigned)(2 * split * shared)), bp::THREADS, bp::SMEM_BYTES, st, 2 * split, pdl || whole, ta, tb,
+                            dim3((unsigned)(2 * plan.split * plan.shared)), bp::THREADS, bp::SMEM_BYTES, st, 2 * plan.split,
+                            pdl || plan.whole, ta, tb,
                             td, args);
         note_launch();
     }
@@ -1435,6 +1451,31 @@ extern "C" fp8dl_status fp8_block_gemm(const uint8_t *A, int32_t a_dtype, const 
     a.status = dev_status;
     return launch_block_gemm(A, a_dtype, M, B, b_dtype, N, b_rows == 1, a, (cudaStream_t)stream,
                              short_call_flops(2.0 * (double)M * (double)N * (double)K), "fp8_block_gemm");
+}
+
+extern "C" fp8dl_status fp8_block_gemm_plan(int32_t b_rows, int32_t n_groups, int64_t M, int64_t N, int64_t K,
+                                            int32_t *tile_rows, int32_t *shares, int64_t *whole, int64_t *shared) {
+    if (!dim_ok(M, 1) || !block_tokens_ok(M) || !block_cols_ok(N) || !dim_ok(K, 16))
+        return fail(FP8DL_ERR_SHAPE, "M (%lld) must be in [1, 2^31), N (%lld) and K (%lld) positive multiples of 16, N < 2^29",
+                    (long long)M, (long long)N, (long long)K);
+    FP8DL_CHECK_ARG(n_groups >= 0 && n_groups <= kMaxGroups, "n_groups must be in [0, %d]", kMaxGroups);
+    FP8DL_CHECK_ARG(b_rows == 128 || (b_rows == 1 && n_groups == 0), "b_rows must be 128, or 1 without groups");
+    FP8DL_CHECK_ARG(tile_rows && shares && whole && shared, "tile_rows, shares, whole and shared must be non-NULL");
+    int dev = 0, sms = 0;
+    FP8DL_TRY(current_device(&dev, &sms));
+    FP8DL_TRY(block_gemm_setup(dev, sms));
+    BlockGemmArgs a = {};
+    a.kind = n_groups ? BG_ROWS : BG_DENSE;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.n_groups = n_groups;
+    const BlockPlan p = plan_block_gemm(a, b_rows == 1, sms, g_block_pairs[dev]);
+    *tile_rows = p.rows;
+    *shares = p.split;
+    *whole = p.whole;
+    *shared = p.shared;
+    return FP8DL_OK;
 }
 
 extern "C" fp8dl_status fp8_block_gemm_grouped(const uint8_t *A, int32_t a_dtype, const float *a_s, const uint8_t *B,
