@@ -137,7 +137,8 @@ class BlockLinear(_BlockLayer):
 
 class BlockExperts(_BlockLayer):
     """weight [G x N x K]; x's rows sorted by group.  Rows outside the groups keep what the output buffers held.
-    backward() reads the forward's offsets again: they keep their values until it has run."""
+    backward() reads the forward's offsets again: they keep their values until it has run.  The products are laid out
+    for all of x's rows, since the host does not know how many the groups hold."""
 
     def __init__(self, weight: torch.Tensor, tokens: int, out_dtype=torch.bfloat16, grad_dtype: int = E4M3):
         super().__init__(weight, tokens, weight.shape[0], out_dtype, grad_dtype)

@@ -320,11 +320,14 @@ __device__ __forceinline__ void add_bias16(const float *bias, float2 (&v)[8]) {
 // two buffers with an epilogue that does nothing: 638 a block, where the MMAs alone take 566.
 // This kernel takes 742 (8192 x 8192 x 16384, 3050 TFLOP/s in a burst, 2630 under the power cap).  What got it there:
 //   - a release at CTA scope on the leader's barrier (1.92 -> 0.92 ms at 16384 x 16384 x 4096),
-//   - MMA operands in uniform registers (one elected lane, no branch: 10 %),
+//   - MMAs issued by one elected lane of the whole warp, without a branch on the lane (10 %),
 //   - one wait per block for sums and factors, no branches in the loop (a wait costs 90 cycles),
 //   - the buffer given back before the last three eighths of the multiply-adds,
-//   - no spilled register: 128 sums, 48 loads and 40 others are what 216 registers hold,
+//   - no spilled register in the kernels of whole tiles: 128 sums, 48 loads and 40 others are what 216
+//     registers hold (the SPLIT kernels spill 20 bytes),
 //   - the store, the tile's decoding and its bias out of the epilogue's way (see store_tile).
+// A tile costs 0.376 us a block (0.545 with BROWS) and 2.0 us (2.2) beside them, for its first block's way through
+// and its store (8192 x 4864, eight tiles a pair, K 512 to 8192): 14 % of it at K = 4096, 25 % at 2048.
 // Tried and slower: 128 x 256 tiles on single CTAs (shared memory: 96 KB written and read a block,
 // 750 cycles at 128 bytes a clock; 826-900 measured), 256 x 160 tiles with three buffers (the
 // fixed 500 cycles an MMA thread spends per block weigh more: 990 per 256 columns).
@@ -628,9 +631,9 @@ __global__ void __launch_bounds__(bp::THREADS, 1)
                 for (int64_t i = issued - 1; i >= 0 && i >= issued - STAGES; i--)
                     mbar_drain(smem_u32(&full[i % STAGES]), (uint32_t)((i / STAGES) & 1));
         } else if (warp == 1 && leader) {  // ----------------------------------- MMA issuer (leader only)
-            // The whole warp runs the loop and one elected lane issues: the operands stay in uniform
-            // registers, where the MMA wants them (with a branch on the lane every MMA first moved
-            // them over, on a scheduler shared with two epilogue warps: 10 % of the kernel).
+            // The whole warp runs the loop and one elected lane issues, so that the operands are the same
+            // for all lanes and no branch on the lane stands before an MMA, on a scheduler shared with
+            // two epilogue warps: 10 % of the kernel.
             int s = 0, buf = 0;
             uint32_t ph = 0, bph = 0;
             bool ok = true, any = false;
@@ -1267,7 +1270,8 @@ static int64_t shared_tiles(int64_t tiles, int64_t kbs, const int (&resident)[3]
 }
 
 // Rows of A per tile of the few-row kernel, or 0 for the 256 x 256 tiles.
-// Groups: by their mean length (the host does not see the offsets).  64 groups, N 2048, K 4096, us with
+// Groups: by their mean length in A's M rows (the host sees neither the offsets nor how many rows lie behind the
+// last group: 128 rows in 64 groups of a buffer of 128 to 1024 rows 84 us, of 4096 90, of 16384 118).  64 groups, N 2048, K 4096, us with
 // 16 / 32 / 64 rows a tile and with 256 x 256 tiles: 16 rows a group 87 / 88 / 93, 116;  32 rows 94 / 89 /
 // 95, 116;  64 rows 138 / 99 / 97, 118;  96 rows 200 / 122 / 117, 121;  128 rows - / 151 / 120, 122;  192 rows
 // - / 220 / 172, 125.

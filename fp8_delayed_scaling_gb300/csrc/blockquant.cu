@@ -114,7 +114,7 @@ struct Values<FP8DL_F32> {
 //            registers, so no byte transpose is needed), staged in shared memory with the
 //            8-byte chunks XOR-swizzled by column group (conflict-free both ways), and leave
 //            as whole 128-byte lines.
-// WEIGHT: one scale for the tile instead, for both copies.
+// WEIGHT: one scale for the tile instead, for both copies.  (fp32 at three CTAs an SM spills 20 bytes.)
 // GROUPS: a tile is a group's; where groups are short, most warps of a CTA would have no rows.  A tile of
 // up to 16, 32 or 64 rows takes 1, 2 or 4 warps and the CTA the next 8, 4 or 2 column tiles; their
 // own CTAs write the padding behind the rows' 32-byte sectors (500 rows of 200 groups, 4096 columns fp32:

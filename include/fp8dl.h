@@ -347,7 +347,9 @@ fp8dl_status mxfp8_gemm(const uint8_t *A, const uint8_t *A_s, const uint8_t *B, 
  * offsets[g] .. offsets[g+1]-1, possibly none; 1 <= n_groups <= 1024.  Rows
  * outside every group are neither read nor written.  The host does not see
  * the values: the kernels clamp them to the tensor, so wrong offsets give
- * wrong results but no access out of bounds. */
+ * wrong results but no access out of bounds.  For the same reason a grouped
+ * product is laid out for all rows of its tensor: one that is much longer than
+ * its groups costs time. */
 
 /* Columns of the transposed codes of fp8_block_quantize: every group is padded
  * to a multiple of 128, at most floor128(rows + 127 * min(n_groups, rows)) in
