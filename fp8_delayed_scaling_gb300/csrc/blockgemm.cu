@@ -1265,7 +1265,7 @@ static int few_split(int64_t tiles, int64_t kbs, int sms) {
 static int64_t shared_tiles(int64_t tiles, int64_t kbs, const int (&resident)[3], int &split) {
     const int64_t tail = tiles % resident[0];
     split = tail <= resident[2] && kbs >= 32 ? 4 : tail <= resident[1] && kbs >= 24 ? 2 : 1;
-    if (tail < tiles && kbs - (kbs + split - 1) / split < 32) split = 1;
+    if (tail == 0 || (tail < tiles && kbs - (kbs + split - 1) / split < 32)) split = 1;
     return split > 1 ? tail : 0;
 }
 

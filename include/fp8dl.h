@@ -405,8 +405,8 @@ fp8dl_status fp8_block_gemm(const uint8_t *A, int32_t a_dtype, const float *a_s,
 /* What fp8_block_gemm (n_groups 0) or fp8_block_gemm_grouped (b_rows 128) runs
  * a product as on the current device; launches nothing.  *tile_rows rows of A
  * are a tile's: 16, 32 or 64 where they are few, else 256; *whole tiles are
- * computed alone and *shared tiles by *shares CTAs (256 rows: CTA pairs), each
- * with a part of K.  Groups: the most tiles there can be, whatever the
+ * computed alone and *shared tiles by *shares CTAs (256 rows: CTA pairs; 1 if no
+ * tile is shared), each with a part of K.  Groups: the most tiles there can be, whatever the
  * offsets.  M >= 1. */
 fp8dl_status fp8_block_gemm_plan(int32_t b_rows, int32_t n_groups, int64_t M, int64_t N, int64_t K,
                                  int32_t *tile_rows, int32_t *shares, int64_t *whole, int64_t *shared);

@@ -125,6 +125,19 @@ def _offsets(G, rows):
     return [2] + [2 + sum(lens[:g + 1]) for g in range(G - 1)] + [rows - 3]
 
 
+def test_plan_names_shares_only_where_tiles_are_shared():
+    """Tiles that fill the pairs exactly leave none to share, however long the reduction; and sizes of all kinds."""
+    fd, dev = _fd()
+    _expect(fd.fp8_block_gemm_plan(19 * 256, 4 * 256, 8192), (256, 1, 76, 0), dev)
+    rng = np.random.default_rng(17)
+    for _ in range(2000):
+        M, N, K = (int(np.exp(rng.uniform(0, np.log(v)))) for v in (20000, 800, 800))
+        groups = int(rng.integers(0, 2) * rng.integers(1, 100))
+        rows, shares, whole, shared = fd.fp8_block_gemm_plan(M, 16 * N, 16 * K, n_groups=groups)
+        assert rows in (16, 32, 64, 256) and whole >= 0 and shared >= 0 and whole + shared > 0
+        assert (shares > 1) == (shared > 0) and 1 <= shares <= (4 if rows == 256 else 6)
+
+
 @pytest.mark.parametrize("G,rows,N,K,plan,fa,fb,dtype", GROUPED)
 def test_grouped(G, rows, N, K, plan, fa, fb, dtype):
     fd, dev = _fd()
