@@ -31,6 +31,7 @@ E4M3, E5M2 = 0, 1
 F32, BF16 = 0, 1
 FORMAT_E4M3, FORMAT_HYBRID = 0, 1
 FP8_MAX = {E4M3: 448.0, E5M2: 57344.0}
+ACT_GELU, ACT_SILU, ACT_GEGLU, ACT_SWIGLU = range(4)
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 
@@ -76,6 +77,16 @@ _SIGS = {
                                       _vp]),
     "fp8_block_gemm_grouped_wgrad": (_i32, [_vp, _i32, _vp, _vp, _i32, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _i32,
                                             _vp, _vp]),
+    "moe_route_workspace_size": (_sz, [_i64, _i32]),
+    "moe_route": (_i32, [_vp, _i32, _i64, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_route_bwd": (_i32, [_vp, _i32, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "fp8_block_dispatch": (_i32, [_vp, _i32, _i64, _i64, _i32, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "moe_combine": (_i32, [_vp, _i32, _i64, _i64, _vp, _vp, _i64, _i32, _vp, _vp]),
+    "moe_combine_bwd": (_i32, [_vp, _vp, _i32, _i64, _i64, _vp, _vp, _i64, _i32, _vp, _vp, _vp]),
+    "fp8_block_act": (_i32, [_vp, _i32, _i32, _i64, _i64, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp]),
+    "fp8_block_dact": (_i32, [_vp, _i32, _i32, _i64, _i64, _vp, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                              _vp, _vp, _sz, _vp]),
+    "fp8_block_recode": (_i32, [_vp, _i32, _vp, _i64, _i64, _i64, _vp, _vp, _i32, _i32, _vp, _vp, _vp]),
     "fp8_layernorm_cast": (_i32, [_vp, _i64, _i64, _vp, _vp, ctypes.c_float, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
                                   _vp, _vp]),
     "fp8_gelu_cast": (_i32, [_vp, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _vp]),
@@ -501,6 +512,135 @@ def fp8_block_gemm_grouped_wgrad(A: torch.Tensor, a_dtype: int, a_s: torch.Tenso
             _tensor(offsets, torch.int32, (G + 1,), dev, "offsets"), G, M, N, T,
             _tensor(D, D.dtype, (G, M, N), dev, "D"), _hp(D), _status(dev_status, dev))
     _check(_lib.fp8_block_gemm_grouped_wgrad(*args, _launch(dev, stream)), "fp8_block_gemm_grouped_wgrad")
+
+
+# --------------------------------------------------------------------------
+# expert routing: choice of experts, balance loss, tokens to their rows and back
+# --------------------------------------------------------------------------
+def moe_route_workspace_size(tokens: int, n_experts: int) -> int:
+    return _lib.moe_route_workspace_size(int(tokens), int(n_experts))
+
+
+def moe_route(logits: torch.Tensor, expert: torch.Tensor, weight: torch.Tensor, position: torch.Tensor, token: torch.Tensor,
+              offsets: torch.Tensor, counts=None, slope=None, loss=None, workspace=None, valid=None, normalize: bool = True,
+              stream=None) -> None:
+    """The k largest logits [T x E] of each token, k = expert.shape[1]: expert, weight, position [T x k], token [T * k],
+    offsets [E + 1] (int32, weight fp32; -1 and 0 where there is no choice), counts [E]; slope [E] and loss [1]: the
+    balance loss and its gradient by the probabilities.  valid (bool or uint8 [T]): zero for padding.  workspace:
+    moe_route_workspace_size bytes."""
+    _need(logits.dim() == 2 and logits.is_contiguous() and expert.dim() == 2, "logits [T x E] and expert [T x k] must be matrices")
+    (T, E), k, dev, i32, f32 = logits.shape, expert.shape[1], logits.get_device(), torch.int32, torch.float32
+    _need(workspace is None or workspace.get_device() == dev, "workspace must be on the device of logits")
+    args = (logits.data_ptr(), _hp(logits), T, E, k,
+            None if valid is None else _tensor(valid, torch.bool if valid.dtype is torch.bool else torch.uint8, (T,), dev, "valid"),
+            1 if normalize else 0, _tensor(expert, i32, (T, k), dev, "expert"), _tensor(weight, f32, (T, k), dev, "weight"),
+            _tensor(position, i32, (T, k), dev, "position"), _tensor(token, i32, (T * k,), dev, "token"),
+            _tensor(offsets, i32, (E + 1,), dev, "offsets"), _tensor(counts, i32, (E,), dev, "counts"),
+            _tensor(slope, f32, (E,), dev, "slope"), _tensor(loss, f32, (1,), dev, "loss"), _p(workspace), _nbytes(workspace))
+    _check(_lib.moe_route(*args, _launch(dev, stream)), "moe_route")
+
+
+def moe_route_bwd(logits: torch.Tensor, expert: torch.Tensor, weight: torch.Tensor, dlogits: torch.Tensor, dweight=None,
+                  slope=None, dloss=None, normalize: bool = True, stream=None) -> None:
+    """dlogits [T x E] from dweight [T x k] and dloss (fp32 [1]); expert, weight and slope as moe_route wrote them."""
+    _need(logits.dim() == 2 and logits.is_contiguous() and expert.dim() == 2, "logits [T x E] and expert [T x k] must be matrices")
+    (T, E), k, dev, f32 = logits.shape, expert.shape[1], logits.get_device(), torch.float32
+    args = (logits.data_ptr(), _hp(logits), T, E, k, 1 if normalize else 0, _tensor(expert, torch.int32, (T, k), dev, "expert"),
+            _tensor(weight, f32, (T, k), dev, "weight"), _tensor(dweight, f32, (T, k), dev, "dweight"),
+            _tensor(slope, f32, (E,), dev, "slope"), _tensor(dloss, f32, (1,), dev, "dloss"),
+            _tensor(dlogits, logits.dtype, (T, E), dev, "dlogits"))
+    _check(_lib.moe_route_bwd(*args, _launch(dev, stream)), "moe_route_bwd")
+
+
+def fp8_block_dispatch(x: torch.Tensor, out_dtype: int, position: torch.Tensor, row_q: torch.Tensor, row_s: torch.Tensor,
+                       q=None, s=None, stream=None) -> None:
+    """Codes and factors of tokens x [T x C] into their experts' rows: row_q [R x C], row_s [C/128 x R] at position
+    [T x k] (int32; skipped outside [0, R)), and in token order: q [T x C], s [C/128 x T]."""
+    _need(x.dim() == 2 and x.is_contiguous() and position.dim() == 2 and row_q.dim() == 2,
+          "x [T x C], position [T x k] and row_q [R x C] must be matrices")
+    (T, C), k, R, dev = x.shape, position.shape[1], row_q.shape[0], x.get_device()
+    args = (x.data_ptr(), _hp(x), T, C, out_dtype, _tensor(position, torch.int32, (T, k), dev, "position"), k, R,
+            _tensor(row_q, torch.uint8, (R, C), dev, "row_q"), _tensor(row_s, torch.float32, (_blocks(C), R), dev, "row_s"),
+            _tensor(q, torch.uint8, (T, C), dev, "q"), _tensor(s, torch.float32, (_blocks(C), T), dev, "s"))
+    _check(_lib.fp8_block_dispatch(*args, _launch(dev, stream)), "fp8_block_dispatch")
+
+
+def moe_combine(y: torch.Tensor, position: torch.Tensor, out: torch.Tensor, weight=None, stream=None) -> None:
+    """out[t] = sum_j weight[t, j] * y[position[t, j]]: y [R x C], position [T x k] (int32), weight [T x k] fp32 or None
+    (ones), out [T x C]."""
+    _need(y.dim() == 2 and y.is_contiguous() and position.dim() == 2, "y [R x C] and position [T x k] must be matrices")
+    (R, C), (T, k), dev = y.shape, position.shape, y.get_device()
+    args = (y.data_ptr(), _hp(y), R, C, _tensor(position, torch.int32, (T, k), dev, "position"),
+            _tensor(weight, torch.float32, (T, k), dev, "weight"), T, k, _tensor(out, y.dtype, (T, C), dev, "out"))
+    _check(_lib.moe_combine(*args, _launch(dev, stream)), "moe_combine")
+
+
+def moe_combine_bwd(dout: torch.Tensor, y, position: torch.Tensor, weight, dy=None, dweight=None, stream=None) -> None:
+    """dy[position[t, j]] = weight[t, j] * dout[t] (dy [R x C]) and dweight[t, j] = <dout[t], y[position[t, j]]>."""
+    _need(dout.dim() == 2 and dout.is_contiguous() and position.dim() == 2, "dout [T x C] and position [T x k] must be matrices")
+    _need(dy is not None or dweight is not None, "dy and dweight are both None")
+    (T, C), k, dev = dout.shape, position.shape[1], dout.get_device()
+    R = (y if dy is None else dy).shape[0]
+    args = (dout.data_ptr(), _tensor(y, dout.dtype, (R, C), dev, "y"), _hp(dout), R, C,
+            _tensor(position, torch.int32, (T, k), dev, "position"), _tensor(weight, torch.float32, (T, k), dev, "weight"), T, k,
+            _tensor(dy, dout.dtype, (R, C), dev, "dy"), _tensor(dweight, torch.float32, (T, k), dev, "dweight"))
+    _check(_lib.moe_combine_bwd(*args, _launch(dev, stream)), "moe_combine_bwd")
+
+
+# --------------------------------------------------------------------------
+# activations kept in 8 bits between block-scaled products
+# --------------------------------------------------------------------------
+def _groups(offsets) -> int:
+    groups = 0 if offsets is None else offsets.numel() - 1
+    _need(groups >= 1 or offsets is None, "offsets must hold n_groups + 1 entries")
+    return groups
+
+
+def fp8_block_act(h: torch.Tensor, act: int, out_dtype: int, g_q: torch.Tensor, g_s: torch.Tensor, h_q=None, h_s=None,
+                  offsets=None, stream=None) -> None:
+    """Codes of g = act(h) along the rows, g_q [R x C], g_s [C/128 x R]; act is ACT_GELU or ACT_SILU (h [R x C]), ACT_GEGLU
+    or ACT_SWIGLU (h [R x 2C], g = act(left half) * right half).  h_q, h_s: codes of h along the rows (the checkpoint)."""
+    _need(h.dim() == 2 and h.is_contiguous() and g_q.dim() == 2, "h must be a contiguous matrix and g_q a matrix")
+    (R, W), C, G, dev = h.shape, g_q.shape[1], _groups(offsets), h.get_device()
+    _need(W == (2 * C if act >= ACT_GEGLU else C), "h has %d columns, g_q %d" % (W, C))
+    args = (h.data_ptr(), _hp(h), act, R, C, _tensor(offsets, torch.int32, (G + 1,), dev, "offsets"), G, out_dtype,
+            _tensor(g_q, torch.uint8, (R, C), dev, "g_q"), _tensor(g_s, torch.float32, (_blocks(C), R), dev, "g_s"),
+            _tensor(h_q, torch.uint8, (R, W), dev, "h_q"), _tensor(h_s, torch.float32, (_blocks(W), R), dev, "h_s"))
+    _check(_lib.fp8_block_act(*args, _launch(dev, stream)), "fp8_block_act")
+
+
+def fp8_block_dact(dg: torch.Tensor, h_q: torch.Tensor, h_fp8: int, h_s: torch.Tensor, act: int, out_dtype: int, dh_q=None,
+                   dh_s=None, dh_qt=None, dh_st=None, g_qt=None, g_st=None, offsets=None, dbias=None,
+                   workspace=None, stream=None) -> None:
+    """The gradient dh of an activation from dg [R x C] and the checkpoint h_q [R x W], h_s [W/128 x R] (W = C, or 2C for a
+    gated act): its codes along the rows (dh_q, dh_s) and transposed (dh_qt [W x T], dh_st [T/128 x W]), the activation's
+    transposed codes (g_qt [C x T], g_st [T/128 x C]), and dh's column sums dbias [W] (without offsets; workspace:
+    fp8_cast_workspace_size(R, W) bytes).  T = fp8_block_padded_rows(R, groups)."""
+    _need(dg.dim() == 2 and dg.is_contiguous(), "dg must be a contiguous matrix")
+    (R, C), G, dev, u8, f32 = dg.shape, _groups(offsets), dg.get_device(), torch.uint8, torch.float32
+    W, T = 2 * C if act >= ACT_GEGLU else C, (R + 127 * min(max(G, 1), R)) // 128 * 128
+    _need(workspace is None or workspace.get_device() == dev, "workspace must be on the device of dg")
+    args = (dg.data_ptr(), _hp(dg), act, R, C, _tensor(h_q, u8, (R, W), dev, "h_q"), h_fp8,
+            _tensor(h_s, f32, (_blocks(W), R), dev, "h_s"), _tensor(offsets, torch.int32, (G + 1,), dev, "offsets"), G, out_dtype,
+            _tensor(dh_q, u8, (R, W), dev, "dh_q"), _tensor(dh_s, f32, (_blocks(W), R), dev, "dh_s"),
+            _tensor(dh_qt, u8, (W, T), dev, "dh_qt"), _tensor(dh_st, f32, (T // 128, W), dev, "dh_st"),
+            _tensor(g_qt, u8, (C, T), dev, "g_qt"), _tensor(g_st, f32, (T // 128, C), dev, "g_st"),
+            _tensor(dbias, f32, (W,), dev, "dbias"), _p(workspace), _nbytes(workspace))
+    _check(_lib.fp8_block_dact(*args, _launch(dev, stream)), "fp8_block_dact")
+
+
+def fp8_block_recode(q: torch.Tensor, q_fp8: int, s: torch.Tensor, out_dtype: int, col_q: torch.Tensor, col_s: torch.Tensor,
+                     offsets=None, index=None, stream=None) -> None:
+    """Transposed codes col_q [C x T], col_s [T/128 x C] of the values that q [S x C], s [C/128 x S] stand for: of its rows in
+    order, or of rows index[r] (int32 [R]; zeros outside [0, S)).  T = fp8_block_padded_rows(R, groups)."""
+    _need(q.dim() == 2, "q must be a matrix")
+    (S, C), G, dev = q.shape, _groups(offsets), q.get_device()
+    R = S if index is None else index.numel()
+    T = (R + 127 * min(max(G, 1), R)) // 128 * 128
+    args = (_tensor(q, torch.uint8, (S, C), dev, "q"), q_fp8, _tensor(s, torch.float32, (_blocks(C), S), dev, "s"), S, R, C,
+            _tensor(index, torch.int32, (R,), dev, "index"), _tensor(offsets, torch.int32, (G + 1,), dev, "offsets"), G,
+            out_dtype, _tensor(col_q, torch.uint8, (C, T), dev, "col_q"), _tensor(col_s, torch.float32, (T // 128, C), dev, "col_s"))
+    _check(_lib.fp8_block_recode(*args, _launch(dev, stream)), "fp8_block_recode")
 
 
 # --------------------------------------------------------------------------

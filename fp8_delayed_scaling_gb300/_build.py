@@ -11,7 +11,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfp8dl.so")
 SOURCES = ["abi.cu", "scaling.cu", "cast.cu", "gemm.cu", "mxfp8.cu", "lnmlp.cu",
-           "blockquant.cu", "blockgemm.cu"]
+           "blockquant.cu", "blockgemm.cu", "route.cu", "exchange.cu", "blockact.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-ftz=false", "-prec-div=true",
               "-prec-sqrt=true", "-I", os.path.join(ROOT, "include"), "-I", CSRC]

@@ -1,5 +1,5 @@
-// block.cuh — what the block-scaled FP8 kernels share: the ragged groups' tables and the
-// host checks of their arguments.
+// block.cuh — what the block-scaled FP8 kernels share: a block's scale, the ragged groups' tables and
+// the host checks of their arguments.
 #pragma once
 
 #include "common.cuh"
@@ -8,6 +8,7 @@ namespace fp8dl {
 
 constexpr int kMaxGroups = 1024;
 
+inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline bool block_tokens_ok(int64_t n) { return n >= 0 && n < (int64_t(1) << 31); }
 
 // offsets/n_groups of a call; `optional`: NULL and 0 stand for no groups.
@@ -37,7 +38,23 @@ __device__ __forceinline__ int64_t warp_inclusive_sum(int64_t v, int lane) {
     return v;
 }
 
-// Called by all 256 threads of a block: the rows behind 128-row block `block` of the padded order (every
+// (scale, stored factor) of a block whose largest finite magnitude is amax: both are
+// correctly rounded divisions.  A maximum below 2^-100 counts as 2^-100, so that the scale
+// stays finite; an all-zero block has scale 1.
+template <int FMT>
+__device__ __forceinline__ float2 block_scale(float amax) {
+    constexpr float FMAX = FMT == FP8DL_E4M3 ? 448.0f : 57344.0f;
+    const float sc = amax > 0.0f ? __fdiv_rn(FMAX, fmaxf(amax, 7.888609052210118e-31f)) : 1.0f;
+    return make_float2(sc, __frcp_rn(sc));
+}
+
+// |v|, or 0 if v is not finite (blocks that hold infinities or NaN only).
+__device__ __forceinline__ float finite_abs(float v) {
+    const float a = fabsf(v);
+    return a <= 3.402823466e38f ? a : 0.0f;
+}
+
+// Called by all threads of a block of 256 or 512 (the first 256 hold the groups): the rows behind 128-row block `block` of the padded order (every
 // group rounded up to a multiple of 128): first row and how many (0 behind the last group).  A
 // thread takes up to four groups, so every offset is loaded at once and few instructions are issued
 // (a search by every warp for itself cost twice the time with 200 groups).  Offsets in disorder may make
@@ -68,7 +85,7 @@ __device__ __forceinline__ void group_of_block(const int32_t *offsets, int n_gro
         const uint32_t u = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += u;
     }
-    if (lane == 31) warp_sum[warp] = min(sum, 1u << 28);
+    if (lane == 31 && warp < 8) warp_sum[warp] = min(sum, 1u << 28);
     if (threadIdx.x == 0) found[1] = 0;
     __syncthreads();
     uint32_t at = block - (sum - mine);  // within this thread's blocks, if below `mine`

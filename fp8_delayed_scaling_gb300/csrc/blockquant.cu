@@ -28,22 +28,6 @@ struct BlockQuantArgs {
     float *ws;               // column sums per 128-row tile, or NULL
 };
 
-// (scale, stored factor) of a block whose largest finite magnitude is amax: both are
-// correctly rounded divisions.  A maximum below 2^-100 counts as 2^-100, so that the scale
-// stays finite; an all-zero block has scale 1.
-template <int FMT>
-__device__ __forceinline__ float2 block_scale(float amax) {
-    constexpr float FMAX = FMT == FP8DL_E4M3 ? 448.0f : 57344.0f;
-    const float sc = amax > 0.0f ? __fdiv_rn(FMAX, fmaxf(amax, 7.888609052210118e-31f)) : 1.0f;
-    return make_float2(sc, __frcp_rn(sc));
-}
-
-// |v|, or 0 if v is not finite (blocks that hold infinities or NaN only).
-__device__ __forceinline__ float finite_abs(float v) {
-    const float a = fabsf(v);
-    return a <= 3.402823466e38f ? a : 0.0f;
-}
-
 // A thread's 8 x 8 values as they were loaded: bf16 stays packed (32 registers instead of 64, so
 // three CTAs fit an SM and their loads overlap), and its maxima are taken on the packed words.
 template <int XKIND>

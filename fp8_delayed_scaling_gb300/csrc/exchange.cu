@@ -1,0 +1,299 @@
+// exchange.cu — tokens to their experts' rows and back.
+//
+//   dispatch     row_q[position[t,j]] = codes of x[t] (1 x 128 blocks), quantised once for all its copies
+//   combine      out[t] = sum_j weight[t,j] y[position[t,j]]
+//   combine_bwd  dy[position[t,j]] = weight[t,j] dout[t],  dweight[t,j] = <dout[t], y[position[t,j]]>
+//
+// All three walk the tokens, so that a token's values are read once whatever k is, no row needs a
+// search for its token, and nothing is added with atomics.  Bound: HBM.
+#include "block.cuh"
+
+namespace fp8dl {
+
+// Eight consecutive values of a row: 16 (bf16) or 32 (fp32) bytes.
+template <int XKIND>
+struct Eight;
+template <>
+struct Eight<FP8DL_BF16> {
+    uint4 u;
+    __device__ __forceinline__ void load(const void *base, int64_t at) {
+        u = ldg_stream(static_cast<const char *>(base) + at * 2);
+    }
+    __device__ __forceinline__ void zero() { u = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ float2 pair(int q) const {
+        const uint32_t w = q == 0 ? u.x : q == 1 ? u.y : q == 2 ? u.z : u.w;
+        return make_float2(bf16_lo(w), bf16_hi(w));
+    }
+    static __device__ __forceinline__ void store(void *base, int64_t at, const float2 (&v)[4]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[q].x, v[q].y);
+            w[q] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        *reinterpret_cast<uint4 *>(static_cast<char *>(base) + at * 2) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+template <>
+struct Eight<FP8DL_F32> {
+    uint4 u[2];
+    __device__ __forceinline__ void load(const void *base, int64_t at) {
+        const char *p = static_cast<const char *>(base) + at * 4;
+        u[0] = ldg_stream(p);
+        u[1] = ldg_stream(p + 16);
+    }
+    __device__ __forceinline__ void zero() { u[0] = u[1] = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ float2 pair(int q) const {
+        const uint4 &w = u[q >> 1];
+        return q & 1 ? make_float2(__uint_as_float(w.z), __uint_as_float(w.w))
+                     : make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+    }
+    static __device__ __forceinline__ void store(void *base, int64_t at, const float2 (&v)[4]) {
+        float4 *p = reinterpret_cast<float4 *>(static_cast<char *>(base) + at * 4);
+        p[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+        p[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+    }
+};
+
+struct DispatchArgs {
+    const void *x;
+    int64_t tokens, cols, rows, chunks;  // chunks of 1024 columns in a row
+    const int32_t *position;
+    int k;
+    uint8_t *row_q, *q;
+    float *row_s, *s;
+};
+
+// A warp quantises 1024 columns of a token: four loads under way at once, 16 lanes a block of 128.
+template <int XKIND, int FMT>
+__global__ void __launch_bounds__(256) block_dispatch_kernel(const DispatchArgs a) {
+    constexpr int U = 4;
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), t = w / a.chunks;
+    if (t >= a.tokens) return;
+    const int64_t c0 = (w - t * a.chunks) * 1024 + 8 * lane;
+    const int64_t at = lane < a.k ? a.position[t * a.k + lane] : -1;  // lane j: where copy j goes
+    Eight<XKIND> v[U];
+#pragma unroll
+    for (int i = 0; i < U; i++) {
+        v[i].zero();
+        if (c0 + 256 * i < a.cols) v[i].load(a.x, t * a.cols + c0 + 256 * i);
+    }
+    uint2 code[U];
+    float inv[U];
+#pragma unroll
+    for (int i = 0; i < U; i++) {
+        float m = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 4; q++) m = fmaxf(m, fmaxf(finite_abs(v[i].pair(q).x), finite_abs(v[i].pair(q).y)));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float2 sc = block_scale<FMT>(m);
+        inv[i] = sc.y;
+        float2 y[4];
+#pragma unroll
+        for (int q = 0; q < 4; q++) y[q] = __fmul2_rn(v[i].pair(q), f2(sc.x));
+        code[i] = make_uint2(pack4<FMT>(y[0].x, y[0].y, y[1].x, y[1].y), pack4<FMT>(y[2].x, y[2].y, y[3].x, y[3].y));
+    }
+    for (int j = a.q ? -1 : 0; j < a.k; j++) {
+        int64_t row = t;
+        if (j >= 0) row = __shfl_sync(0xffffffffu, at, j);
+        if (j >= 0 && (row < 0 || row >= a.rows)) continue;
+        uint8_t *q = j < 0 ? a.q : a.row_q;
+        float *s = j < 0 ? a.s : a.row_s;
+        const int64_t ld = j < 0 ? a.tokens : a.rows;
+#pragma unroll
+        for (int i = 0; i < U; i++) {
+            const int64_t c = c0 + 256 * i;
+            if (c >= a.cols) continue;
+            *reinterpret_cast<uint2 *>(q + row * a.cols + c) = code[i];
+            if ((lane & 15) == 0) s[(c >> 7) * ld + row] = inv[i];
+        }
+    }
+}
+
+struct CombineArgs {
+    const void *y, *dout;
+    int64_t rows, cols, tokens;
+    const int32_t *position;
+    const float *weight;
+    int k;
+    void *out, *dy;
+    float *dweight;
+};
+
+// A thread sums eight columns of a token, four rows of y under way at once.
+template <int XKIND>
+__global__ void __launch_bounds__(256) moe_combine_kernel(const CombineArgs a) {
+    constexpr int U = 4;
+    pdl_wait();
+    pdl_trigger();
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, per = a.cols / 8, t = i / per;
+    if (t >= a.tokens) return;
+    const int64_t c = (i - t * per) * 8;
+    float2 sum[4];
+#pragma unroll
+    for (int q = 0; q < 4; q++) sum[q] = f2(0.0f);
+    for (int j0 = 0; j0 < a.k; j0 += U) {
+        Eight<XKIND> v[U];
+        float w[U];
+        bool has[U];
+#pragma unroll
+        for (int j = 0; j < U; j++) {
+            const int64_t row = j0 + j < a.k ? a.position[t * a.k + j0 + j] : -1;
+            has[j] = row >= 0 && row < a.rows;
+            w[j] = !has[j] ? 0.0f : a.weight ? a.weight[t * a.k + j0 + j] : 1.0f;
+            v[j].zero();
+            if (has[j]) v[j].load(a.y, row * a.cols + c);
+        }
+#pragma unroll
+        for (int j = 0; j < U; j++)
+            if (has[j]) {
+#pragma unroll
+                for (int q = 0; q < 4; q++) sum[q] = __ffma2_rn(v[j].pair(q), f2(w[j]), sum[q]);
+            }
+    }
+    Eight<XKIND>::store(a.out, t * a.cols + c, sum);
+}
+
+// A warp walks a token's row, 256 columns a step, J choices at once (more: again, dout from L1).  The sums
+// run over a lane's columns in order, then over the lanes in a fixed tree.
+template <int XKIND, int J>
+__global__ void __launch_bounds__(256) moe_combine_bwd_kernel(const CombineArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (t >= a.tokens) return;
+    for (int j0 = 0; j0 < a.k; j0 += J) {
+        int64_t row[J];
+        float w[J], sum[J];
+#pragma unroll
+        for (int j = 0; j < J; j++) {
+            row[j] = j0 + j < a.k ? a.position[t * a.k + j0 + j] : -1;
+            if (row[j] >= a.rows) row[j] = -1;
+            w[j] = a.dy && row[j] >= 0 ? a.weight[t * a.k + j0 + j] : 0.0f;
+            sum[j] = 0.0f;
+        }
+        for (int64_t c = 8 * lane; c < a.cols; c += 256) {
+            Eight<XKIND> d, v[J];
+            d.load(a.dout, t * a.cols + c);
+#pragma unroll
+            for (int j = 0; j < J; j++) {
+                v[j].zero();
+                if (a.dweight && row[j] >= 0) v[j].load(a.y, row[j] * a.cols + c);
+            }
+#pragma unroll
+            for (int j = 0; j < J; j++) {
+                if (row[j] < 0) continue;
+                float2 s[4], part = f2(0.0f);
+#pragma unroll
+                for (int q = 0; q < 4; q++) {
+                    s[q] = __fmul2_rn(d.pair(q), f2(w[j]));
+                    part = __ffma2_rn(d.pair(q), v[j].pair(q), part);
+                }
+                if (a.dy) Eight<XKIND>::store(a.dy, row[j] * a.cols + c, s);
+                sum[j] += part.x + part.y;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < J; j++) {
+            if (!a.dweight || j0 + j >= a.k) break;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
+            if (lane == 0) a.dweight[t * a.k + j0 + j] = row[j] >= 0 ? sum[j] : 0.0f;
+        }
+    }
+}
+
+static fp8dl_status check_exchange(int32_t dtype, int64_t tokens, int64_t rows, int64_t cols, const int32_t *position,
+                                   int32_t k) {
+    FP8DL_CHECK_ARG(dtype == FP8DL_F32 || dtype == FP8DL_BF16, "the type must be FP8DL_F32 or FP8DL_BF16");
+    FP8DL_CHECK_ARG(k >= 1 && k <= 32, "k must be in [1, 32]");
+    if (!block_tokens_ok(tokens) || !block_tokens_ok(rows) || !dim_ok(cols, 16))
+        return fail(FP8DL_ERR_SHAPE, "tokens (%lld) and rows (%lld) must be in [0, 2^31) and cols (%lld) a positive multiple of 16",
+                    (long long)tokens, (long long)rows, (long long)cols);
+    FP8DL_CHECK_ARG(tokens == 0 || position, "position is NULL");
+    if (!aligned4(position)) return fail(FP8DL_ERR_ALIGN, "position must be 4-byte aligned");
+    return FP8DL_OK;
+}
+
+static fp8dl_status exchange_grid(int64_t ctas) {
+    if (ctas > 0x7fffffffll) return fail(FP8DL_ERR_SHAPE, "%lld blocks of threads are more than 2^31 - 1", (long long)ctas);
+    return FP8DL_OK;
+}
+
+}  // namespace fp8dl
+
+using namespace fp8dl;
+
+extern "C" fp8dl_status fp8_block_dispatch(const void *x, int32_t x_dtype, int64_t tokens, int64_t cols, int32_t out_dtype,
+                                           const int32_t *position, int32_t k, int64_t rows, uint8_t *row_q,
+                                           float *row_s, uint8_t *q, float *s, fp8dl_stream_t stream) {
+    FP8DL_NVTX("fp8_block_dispatch");
+    FP8DL_TRY(check_exchange(x_dtype, tokens, rows, cols, position, k));
+    FP8DL_CHECK_ARG(out_dtype == FP8DL_E4M3 || out_dtype == FP8DL_E5M2, "out_dtype must be E4M3 or E5M2");
+    FP8DL_CHECK_ARG(tokens == 0 || x, "x is NULL");
+    FP8DL_CHECK_ARG(tokens == 0 || rows == 0 || (row_q && row_s), "row_q and row_s must be non-NULL");
+    FP8DL_CHECK_ARG(!q == !s, "q and s come together");
+    if (!aligned16(x) || !aligned16(row_q) || !aligned16(row_s) || !aligned16(q) || !aligned16(s))
+        return fail(FP8DL_ERR_ALIGN, "x, row_q, row_s, q and s must be 16-byte aligned");
+    FP8DL_TRY(current_device(nullptr, nullptr));
+    if (tokens == 0) return FP8DL_OK;
+    DispatchArgs a = {x, tokens, cols, rows, (cols + 1023) / 1024, position, k, row_q, q, row_s, s};
+    const int64_t ctas = (tokens * a.chunks + 7) / 8;
+    FP8DL_TRY(exchange_grid(ctas));
+    const bool pdl = short_call_bytes((double)tokens * (double)cols * ((x_dtype == FP8DL_BF16 ? 2.0 : 4.0) + k));
+    auto *kernel = x_dtype == FP8DL_BF16
+                       ? (out_dtype == FP8DL_E4M3 ? block_dispatch_kernel<FP8DL_BF16, FP8DL_E4M3>
+                                                  : block_dispatch_kernel<FP8DL_BF16, FP8DL_E5M2>)
+                       : (out_dtype == FP8DL_E4M3 ? block_dispatch_kernel<FP8DL_F32, FP8DL_E4M3>
+                                                  : block_dispatch_kernel<FP8DL_F32, FP8DL_E5M2>);
+    (void)launch_kernel(kernel, dim3((unsigned)ctas), dim3(256), 0, (cudaStream_t)stream, 0, pdl, a);
+    note_launch();
+    return check_launch("fp8_block_dispatch");
+}
+
+extern "C" fp8dl_status moe_combine(const void *y, int32_t dtype, int64_t rows, int64_t cols, const int32_t *position,
+                                    const float *weight, int64_t tokens, int32_t k, void *out, fp8dl_stream_t stream) {
+    FP8DL_NVTX("moe_combine");
+    FP8DL_TRY(check_exchange(dtype, tokens, rows, cols, position, k));
+    FP8DL_CHECK_ARG(tokens == 0 || (out && (y || rows == 0)), "y and out must be non-NULL");
+    if (!aligned16(y) || !aligned16(out) || !aligned4(weight))
+        return fail(FP8DL_ERR_ALIGN, "y and out must be 16-byte aligned, weight 4-byte");
+    FP8DL_TRY(current_device(nullptr, nullptr));
+    if (tokens == 0) return FP8DL_OK;
+    CombineArgs a = {y, nullptr, rows, cols, tokens, position, weight, k, out, nullptr, nullptr};
+    const int64_t ctas = (tokens * (cols / 8) + 255) / 256;
+    FP8DL_TRY(exchange_grid(ctas));
+    const bool pdl = short_call_bytes((double)tokens * (double)cols * (dtype == FP8DL_BF16 ? 2.0 : 4.0) * (k + 1));
+    (void)launch_kernel(dtype == FP8DL_BF16 ? moe_combine_kernel<FP8DL_BF16> : moe_combine_kernel<FP8DL_F32>,
+                        dim3((unsigned)ctas), dim3(256), 0, (cudaStream_t)stream, 0, pdl, a);
+    note_launch();
+    return check_launch("moe_combine");
+}
+
+extern "C" fp8dl_status moe_combine_bwd(const void *dout, const void *y, int32_t dtype, int64_t rows, int64_t cols,
+                                        const int32_t *position, const float *weight, int64_t tokens, int32_t k,
+                                        void *dy, float *dweight, fp8dl_stream_t stream) {
+    FP8DL_NVTX("moe_combine_bwd");
+    FP8DL_TRY(check_exchange(dtype, tokens, rows, cols, position, k));
+    FP8DL_CHECK_ARG(tokens == 0 || dout, "dout is NULL");
+    FP8DL_CHECK_ARG(tokens == 0 || rows == 0 || dy || dweight, "dy and dweight are both NULL");
+    FP8DL_CHECK_ARG(tokens == 0 || rows == 0 || ((!dy || weight) && (!dweight || y)), "dy needs weight, dweight needs y");
+    if (!aligned16(dout) || !aligned16(y) || !aligned16(dy) || !aligned4(weight) || !aligned4(dweight))
+        return fail(FP8DL_ERR_ALIGN, "dout, y and dy must be 16-byte aligned, weight and dweight 4-byte");
+    FP8DL_TRY(current_device(nullptr, nullptr));
+    if (tokens == 0) return FP8DL_OK;
+    CombineArgs a = {y, dout, rows, cols, tokens, position, weight, k, nullptr, dy, dweight};
+    const int64_t ctas = (tokens + 7) / 8;
+    const bool pdl = short_call_bytes((double)tokens * (double)cols * (dtype == FP8DL_BF16 ? 2.0 : 4.0) * (2 * k + 1));
+    auto *kernel = dtype == FP8DL_BF16
+                       ? (k <= 2 ? moe_combine_bwd_kernel<FP8DL_BF16, 2> : moe_combine_bwd_kernel<FP8DL_BF16, 4>)
+                       : (k <= 2 ? moe_combine_bwd_kernel<FP8DL_F32, 2> : moe_combine_bwd_kernel<FP8DL_F32, 4>);
+    (void)launch_kernel(kernel, dim3((unsigned)ctas), dim3(256), 0, (cudaStream_t)stream, 0, pdl, a);
+    note_launch();
+    return check_launch("moe_combine_bwd");
+}

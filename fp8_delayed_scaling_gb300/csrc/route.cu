@@ -1,0 +1,633 @@
+// route.cu — expert routing: the k largest logits of each token, their weights, every
+// expert's rows, the balance loss, and the gradient of weights and loss by the logits.
+//
+// The expert layers' products (fp8_block_gemm_grouped and its weight gradient) read rows
+// sorted by expert and each group's first row; these kernels make both from the logits.
+//
+//   p = softmax(l), chosen = the k largest l;  weight_j = p_j (or p_j / sum of the chosen p)
+//   loss = sum_e slope_e sum_t p_te,  slope_e = E counts_e / (C N)
+//   dl = p (dp - <p, dp>),  dp_e = dloss slope_e + (chosen: dw_j, or (dw_j - <dw, w>) / sum of the chosen p)
+//
+// Rows are given out without atomics whose order matters: a group of lanes walks a run of
+// tokens in order and counts per expert in shared memory; prefixes over the runs of a CTA,
+// then over the CTAs, turn the counts into rows.  Sums of probabilities add up in the same
+// fixed order.
+#include "block.cuh"
+
+namespace fp8dl {
+
+namespace rt {
+constexpr int MAX_TILES = 160;  // CTAs of the first kernel (workspace rows); one per SM fits every GB300
+constexpr int MAX_K = 32;       // choices of a token: one per lane
+constexpr float NEG_INF = -__builtin_huge_valf();
+}
+
+struct RouteArgs {
+    const void *logits;
+    int64_t tokens;
+    int experts, k, normalize, vec;
+    const uint8_t *valid;
+    int32_t *expert, *position, *token, *offsets, *counts;
+    float *weight, *slope, *loss;
+    int32_t *hist;  // [tiles][experts + 1]: the tile's choices of each expert, its tokens with a choice
+    float *psum;    // [tiles][experts]: the tile's sums of p, or NULL
+    int64_t per;    // tokens of a run
+};
+
+// Order-preserving key of a float, 0 for what is never chosen (-infinity, NaN); -0 counts as 0.
+__device__ __forceinline__ uint32_t route_key(float v) {
+    const uint32_t b = __float_as_uint(v + 0.0f);
+    return v > rt::NEG_INF ? b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u) : 0u;
+}
+__device__ __forceinline__ float route_value(uint32_t key) {
+    return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
+
+// S consecutive logits of a row from element i0 on (lane-contiguous, so that the lowest lane
+// among equal maxima holds the lowest expert); -infinity behind the row's end.
+template <int XKIND, int S>
+__device__ __forceinline__ void route_load(const void *base, int64_t row, int E, int i0, bool vec, float (&v)[S]) {
+    constexpr int ESZ = XKIND == FP8DL_BF16 ? 2 : 4, BYTES = S * ESZ;
+    const char *p = static_cast<const char *>(base) + (row * E + i0) * ESZ;
+#pragma unroll
+    for (int s = 0; s < S; s++) v[s] = rt::NEG_INF;
+    if (vec && BYTES >= 4) {
+        if (i0 < E) {  // E is a multiple of S: all of the lane's or none
+            uint32_t w[BYTES >= 4 ? BYTES / 4 : 1];
+            if constexpr (BYTES >= 16) {
+#pragma unroll
+                for (int q = 0; q < BYTES / 16; q++) {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(p + 16 * q);
+                    w[4 * q] = u.x, w[4 * q + 1] = u.y, w[4 * q + 2] = u.z, w[4 * q + 3] = u.w;
+                }
+            } else if constexpr (BYTES == 8) {
+                const uint2 u = *reinterpret_cast<const uint2 *>(p);
+                w[0] = u.x, w[1] = u.y;
+            } else if constexpr (BYTES == 4) {
+                w[0] = *reinterpret_cast<const uint32_t *>(p);
+            }
+#pragma unroll
+            for (int s = 0; s < S; s++)
+                v[s] = XKIND == FP8DL_BF16 ? ((s & 1) ? bf16_hi(w[s / 2]) : bf16_lo(w[s / 2])) : __uint_as_float(w[s]);
+        }
+    } else {
+#pragma unroll
+        for (int s = 0; s < S; s++)
+            if (i0 + s < E)
+                v[s] = XKIND == FP8DL_BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p)[s])
+                                           : reinterpret_cast<const float *>(p)[s];
+    }
+}
+
+// Sum over the G lanes of a group, the same in all of them.
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Exclusive prefix sums of total[0 .. n) into first[0 .. n], by all threads of a block of THREADS
+// >= 32 threads (a multiple of 32); n <= 1024.  `warps` holds THREADS / 32 entries.
+template <int THREADS>
+__device__ __forceinline__ void scan_experts(const int32_t *total, int32_t *first, int n, int32_t *warps) {
+    constexpr int PER = 1024 / THREADS;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i0 = threadIdx.x * PER;
+    int32_t own[PER], sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; i++) {
+        own[i] = i0 + i < n ? total[i0 + i] : 0;
+        sum += own[i];
+    }
+    int32_t run = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t u = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += u;
+    }
+    if (lane == 31) warps[warp] = run;
+    __syncthreads();
+    int32_t before = run - sum;
+    for (int w = 0; w < warp; w++) before += warps[w];
+#pragma unroll
+    for (int i = 0; i < PER; i++) {
+        if (i0 + i < n) first[i0 + i] = before;
+        before += own[i];
+        if (i0 + i == n - 1) first[n] = before;
+    }
+    __syncthreads();
+}
+
+// slope and loss from every expert's count and sum of p, by a block of THREADS threads.
+template <int THREADS>
+__device__ __forceinline__ void balance(const RouteArgs &a, const int32_t *total, const float *p, int counted, int choices,
+                                        float *warps) {
+    const float unit = counted > 0 ? __fdiv_rn((float)a.experts, (float)choices * (float)counted) : 0.0f;
+    float sum = 0.0f;
+    for (int e = threadIdx.x; e < a.experts; e += THREADS) {
+        const float s = (float)total[e] * unit;
+        a.slope[e] = s;
+        sum = fmaf(s, p[e], sum);
+    }
+    sum = group_sum<32>(sum);
+    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < THREADS / 32; w++) sum += warps[w];
+        a.loss[0] = sum;
+    }
+}
+
+// One CTA routes a tile of tokens: G lanes a token, lane l the experts l S .. l S + S - 1, a run of
+// a.per consecutive tokens per group of lanes.
+//   choice   k rounds of a maximum over the lanes (redux) of the lanes' own best keys; the
+//            lowest lane that holds it takes its lowest such expert out.  Lane j keeps choice j.
+//   row      rank within the run from the CTA's shared counters (a token's experts differ, so its
+//            lanes never meet), plus the runs before it after the last token.
+//   SINGLE   the tile is all there is: rows, counts and the loss are finished here, one launch.
+// The runs' counters and then the runs' sums of p share one buffer [runs][experts].
+template <int XKIND, int G, int S, int THREADS, bool SINGLE>
+__global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
+    constexpr int NG = THREADS / G;
+    extern __shared__ int32_t cnt[];
+    __shared__ int32_t total[SINGLE ? 1024 : 1], first[SINGLE ? 1025 : 1], warps[THREADS / 32], counted;
+    const int E = a.experts, k = a.k, tid = threadIdx.x, lane = tid & 31, run = tid / G, l = tid % G;
+    const uint32_t gmask = G == 32 ? 0xffffffffu : ((1u << (G & 31)) - 1u) << (lane & ~(G - 1));
+    pdl_wait();
+    pdl_trigger();
+    for (int i = tid; i < NG * E; i += THREADS) cnt[i] = 0;
+    if (tid == 0) counted = 0;
+    __syncthreads();
+    const int64_t t0 = ((int64_t)blockIdx.x * NG + run) * a.per;
+    int32_t *mine = cnt + run * E;
+    float ps[S];
+#pragma unroll
+    for (int s = 0; s < S; s++) ps[s] = 0.0f;
+    int n_counted = 0;
+    for (int64_t i = 0; i < a.per; i++) {
+        const int64_t t = t0 + i;
+        const bool here = t < a.tokens, live = here && (!a.valid || a.valid[t]);
+        float v[S];
+        uint32_t key[S], best = 0;
+        if (live) {
+            route_load<XKIND, S>(a.logits, t, E, l * S, a.vec, v);
+        } else {
+#pragma unroll
+            for (int s = 0; s < S; s++) v[s] = rt::NEG_INF;
+        }
+#pragma unroll
+        for (int s = 0; s < S; s++) {
+            key[s] = route_key(v[s]);
+            best = max(best, key[s]);
+        }
+        uint32_t choice = 0;  // lane j: the key and the expert of choice j
+        int32_t pick = -1;
+        for (int j = 0; j < k; j++) {
+            const uint32_t top = __reduce_max_sync(gmask, best);
+            const int winner = __ffs(__ballot_sync(0xffffffffu, best == top) & gmask) - 1;
+            int slot = 0;
+#pragma unroll
+            for (int s = S - 1; s >= 0; s--)
+                if (key[s] == top) slot = s;
+            slot = __shfl_sync(0xffffffffu, slot, winner);
+            if (l == j && top != 0) {
+                choice = top;
+                pick = (winner & (G - 1)) * S + slot;
+            }
+            if (lane == winner) {
+                best = 0;
+#pragma unroll
+                for (int s = 0; s < S; s++) {
+                    if (s == slot) key[s] = 0;
+                    best = max(best, key[s]);
+                }
+            }
+        }
+        const uint32_t top = __shfl_sync(0xffffffffu, choice, lane & ~(G - 1));
+        const float m = top ? route_value(top) : 0.0f;
+        float z = 0.0f;
+#pragma unroll
+        for (int s = 0; s < S; s++) {
+            v[s] = top ? expf(v[s] - m) : v[s] == v[s] ? 0.0f : v[s];  // nothing to choose: 0, or NaN
+            z += v[s];
+        }
+        z = group_sum<G>(z);
+        const float inv = top ? __frcp_rn(z) : 1.0f;
+#pragma unroll
+        for (int s = 0; s < S; s++) ps[s] = fmaf(v[s], inv, ps[s]);
+        const float e = pick >= 0 ? expf(route_value(choice) - m) : 0.0f;
+        const float chosen = group_sum<G>(e);
+        if (l == 0 && top) n_counted++;
+        if (here && l < k) {
+            float w = 0.0f;
+            int32_t rank = -1;
+            if (pick >= 0) {
+                w = z == z ? (a.normalize ? __fdiv_rn(e, chosen) : e * inv) : z;
+                rank = mine[pick];
+                mine[pick] = rank + 1;
+            }
+            a.expert[t * k + l] = pick;
+            a.weight[t * k + l] = w;
+            a.position[t * k + l] = rank;
+        }
+        __syncwarp();
+    }
+    if (n_counted) atomicAdd(&counted, n_counted);
+    __syncthreads();
+    for (int e = tid; e < E; e += THREADS) {  // the runs before each run
+        int32_t sum = 0;
+        for (int g = 0; g < NG; g++) {
+            const int32_t c = cnt[g * E + e];
+            cnt[g * E + e] = sum;
+            sum += c;
+        }
+        if (SINGLE)
+            total[e] = sum;
+        else
+            a.hist[(int64_t)blockIdx.x * (E + 1) + e] = sum;
+    }
+    if (!SINGLE && tid == 0) a.hist[(int64_t)blockIdx.x * (E + 1) + E] = counted;
+    __syncthreads();
+    if (SINGLE) {
+        scan_experts<THREADS>(total, first, E, warps);
+        for (int e = tid; e <= E; e += THREADS) {
+            a.offsets[e] = first[e];
+            if (e < E && a.counts) a.counts[e] = total[e];
+        }
+    }
+    if (l < k) {
+        for (int64_t i = 0; i < a.per; i++) {
+            const int64_t t = t0 + i;
+            if (t >= a.tokens) break;
+            const int32_t e = a.expert[t * k + l];
+            if (e < 0) continue;
+            const int32_t at = a.position[t * k + l] + mine[e] + (SINGLE ? first[e] : 0);
+            a.position[t * k + l] = at;
+            if (SINGLE) a.token[at] = (int32_t)t;
+        }
+    }
+    if (!(SINGLE ? (void *)a.slope : (void *)a.psum)) return;
+    __syncthreads();
+    float *pf = reinterpret_cast<float *>(cnt);
+#pragma unroll
+    for (int s = 0; s < S; s++)
+        if (l * S + s < E) pf[run * E + l * S + s] = ps[s];
+    __syncthreads();
+    for (int e = tid; e < E; e += THREADS) {
+        float sum = 0.0f;
+        for (int g = 0; g < NG; g++) sum += pf[g * E + e];
+        if (SINGLE)
+            pf[e] = sum;  // (run 0's own entry, read by this thread alone)
+        else
+            a.psum[(int64_t)blockIdx.x * E + e] = sum;
+    }
+    if (SINGLE) {
+        __syncthreads();
+        balance<THREADS>(a, total, pf, counted, first[E], reinterpret_cast<float *>(warps));
+    }
+}
+
+// The rows of every tile: CTA i adds up the counts of the tiles before its own and of all tiles, and the
+// experts' first rows; its tokens' ranks become rows.  The CTA behind the last tile makes the loss.
+__global__ void __launch_bounds__(1024) route_rows_kernel(const RouteArgs a, int tiles, int64_t tile_tokens) {
+    __shared__ int32_t before[1024], total[1024], first[1025], warps[32];
+    __shared__ float sums[1024];
+    pdl_wait();
+    pdl_trigger();
+    const int E = a.experts, tid = threadIdx.x, tile = blockIdx.x;
+    int wide = 32;  // threads across the experts; the rest share out the tiles
+    while (wide < E) wide *= 2;
+    const int parts = 1024 / wide, part = tid / wide, e = tid % wide;
+    int32_t b = 0, n = 0;
+    float p = 0.0f;
+    if (e < E) {
+#pragma unroll 8
+        for (int i = part; i < tiles; i += parts) {
+            const int32_t c = a.hist[(int64_t)i * (E + 1) + e];
+            n += c;
+            b += i < tile ? c : 0;
+        }
+        if (tile == tiles) {
+#pragma unroll 8
+            for (int i = part; i < tiles; i += parts) p += a.psum[(int64_t)i * E + e];
+        }
+    }
+    before[tid] = b, total[tid] = n, sums[tid] = p;
+    __syncthreads();
+    if (tid < E) {
+        for (int q = 1; q < parts; q++) {
+            b += before[q * wide + tid];
+            n += total[q * wide + tid];
+            p += sums[q * wide + tid];
+        }
+    }
+    __syncthreads();
+    if (tid < E) before[tid] = b, total[tid] = n, sums[tid] = p;
+    __syncthreads();
+    scan_experts<1024>(total, first, E, warps);
+    if (tile == tiles) {
+        int32_t c = 0;
+        for (int i = tid; i < tiles; i += 1024) c += a.hist[(int64_t)i * (E + 1) + E];  // at most one each
+        __shared__ int32_t counted;
+        if (tid == 0) counted = 0;
+        __syncthreads();
+        if (c) atomicAdd(&counted, c);
+        __syncthreads();
+        balance<1024>(a, total, sums, counted, first[E], reinterpret_cast<float *>(warps));
+        return;
+    }
+    if (tile == 0) {
+        if (tid < E) {
+            a.offsets[tid] = first[tid];
+            if (a.counts) a.counts[tid] = total[tid];
+        }
+        if (tid == 0) a.offsets[E] = first[E];
+    }
+    if (tid < E) before[tid] += first[tid];
+    __syncthreads();
+    const int64_t lo = tile * tile_tokens * a.k, hi = min((tile + 1) * tile_tokens, a.tokens) * a.k;
+    for (int64_t i = lo + tid; i < hi; i += 1024) {
+        const int32_t x = a.expert[i];
+        if (x < 0) continue;
+        const int32_t at = a.position[i] + before[x];
+        a.position[i] = at;
+        a.token[at] = (int32_t)((uint32_t)i / (uint32_t)a.k);
+    }
+}
+
+// G lanes a token; the chosen experts' extra gradient reaches its lanes through shared memory, a row
+// of zeros per group of lanes that is cleared again.
+template <int XKIND, int G, int S>
+__global__ void __launch_bounds__(256) route_bwd_kernel(const RouteArgs a, const float *dweight, const float *dloss,
+                                                        void *dlogits) {
+    constexpr int NG = 256 / G, ESZ = XKIND == FP8DL_BF16 ? 2 : 4;
+    __shared__ float extra[NG][G * S];
+    const int E = a.experts, k = a.k, lane = threadIdx.x & 31, run = threadIdx.x / G, l = threadIdx.x % G, i0 = l * S;
+    float *mine = extra[run];
+#pragma unroll
+    for (int s = 0; s < S; s++) mine[i0 + s] = 0.0f;
+    pdl_wait();
+    pdl_trigger();
+    const float dl = dloss ? *dloss : 0.0f;
+    float even[S];
+#pragma unroll
+    for (int s = 0; s < S; s++) even[s] = dloss && i0 + s < E ? dl * a.slope[i0 + s] : 0.0f;
+    __syncwarp();
+    const int64_t step = (int64_t)gridDim.x * NG, rounds = (a.tokens + step - 1) / step;
+    for (int64_t r = 0; r < rounds; r++) {
+        const int64_t t = r * step + (int64_t)blockIdx.x * NG + run;
+        const bool here = t < a.tokens;
+        int32_t pick = -1;
+        float w = 0.0f, dw = 0.0f, vj = 0.0f;
+        if (here && l < k) {
+            pick = a.expert[t * k + l];
+            pick = pick < E ? pick : -1;
+            if (pick >= 0) {
+                w = a.weight[t * k + l];
+                dw = dweight ? dweight[t * k + l] : 0.0f;
+                vj = XKIND == FP8DL_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(a.logits)[t * E + pick])
+                                         : static_cast<const float *>(a.logits)[t * E + pick];
+            }
+        }
+        const bool some = __shfl_sync(0xffffffffu, pick, lane & ~(G - 1)) >= 0;
+        const float m = __shfl_sync(0xffffffffu, vj, lane & ~(G - 1));
+        float v[S], z = 0.0f;
+        if (some) {
+            route_load<XKIND, S>(a.logits, t, E, i0, a.vec, v);
+        } else {
+#pragma unroll
+            for (int s = 0; s < S; s++) v[s] = rt::NEG_INF;
+        }
+#pragma unroll
+        for (int s = 0; s < S; s++) {
+            v[s] = expf(v[s] - m);
+            z += v[s];
+        }
+        z = group_sum<G>(z);
+        const float inv = some ? __frcp_rn(z) : 0.0f;
+        float d = dw;
+        if (a.normalize) {
+            const float chosen = group_sum<G>(pick >= 0 ? expf(vj - m) : 0.0f), dot = group_sum<G>(dw * w);
+            d = (dw - dot) * __fdiv_rn(z, chosen);
+        }
+        if (pick >= 0) mine[pick] = d;
+        __syncwarp();
+        float dp[S], dot = 0.0f;
+#pragma unroll
+        for (int s = 0; s < S; s++) {
+            dp[s] = even[s] + mine[i0 + s];
+            v[s] *= inv;
+            dot = fmaf(v[s], dp[s], dot);
+        }
+        dot = group_sum<G>(dot);
+        __syncwarp();
+        if (pick >= 0) mine[pick] = 0.0f;
+        if (here && i0 < E) {
+#pragma unroll
+            for (int s = 0; s < S; s++) v[s] = some ? v[s] * (dp[s] - dot) : 0.0f;
+            char *to = static_cast<char *>(dlogits) + (t * E + i0) * ESZ;
+            if (a.vec && S * ESZ >= 4) {
+                uint32_t u[S * ESZ >= 4 ? S * ESZ / 4 : 1];
+                if constexpr (XKIND == FP8DL_BF16) {
+#pragma unroll
+                    for (int s = 0; s + 1 < S; s += 2) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(v[s], v[s + 1]);
+                        u[s / 2] = *reinterpret_cast<const uint32_t *>(&h);
+                    }
+                } else {
+#pragma unroll
+                    for (int s = 0; s < S; s++) u[s] = __float_as_uint(v[s]);
+                }
+                if constexpr (S * ESZ >= 16) {
+#pragma unroll
+                    for (int q = 0; q < S * ESZ / 16; q++)
+                        *reinterpret_cast<uint4 *>(to + 16 * q) = make_uint4(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]);
+                } else if constexpr (S * ESZ == 8) {
+                    *reinterpret_cast<uint2 *>(to) = make_uint2(u[0], u[1]);
+                } else {
+                    *reinterpret_cast<uint32_t *>(to) = u[0];
+                }
+            } else {
+#pragma unroll
+                for (int s = 0; s < S; s++)
+                    if (i0 + s < E) {
+                        if (XKIND == FP8DL_BF16)
+                            reinterpret_cast<__nv_bfloat16 *>(to)[s] = __float2bfloat16_rn(v[s]);
+                        else
+                            reinterpret_cast<float *>(to)[s] = v[s];
+                    }
+            }
+        }
+        __syncwarp();
+    }
+}
+
+// Lanes of a token and experts of a lane, for n experts: the fewest lanes that hold them one each, 32 lanes
+// from 17 experts on.
+static void route_shape(int n, int &g, int &s) {
+    g = n <= 8 ? 8 : n <= 16 ? 16 : 32;
+    s = 1;
+    while (g * s < n) s *= 2;
+}
+
+// Whether the lanes' S logits are whole aligned words of a row (the rows start on 16 bytes then, or on
+// a word of the lane's size).
+static bool route_vec(int n, int s, int esz) { return n % s == 0 && ((int64_t)n * esz) % (s * esz < 16 ? s * esz : 16) == 0; }
+
+template <int XKIND, int G, int S>
+static fp8dl_status launch_route(RouteArgs a, int tiles, int64_t tile_tokens, cudaStream_t st, bool pdl) {
+    constexpr int THREADS = S >= 16 ? 512 : 1024;
+    const size_t smem = (size_t)(THREADS / G) * a.experts * 4;
+    const bool single = tiles == 1;
+    auto *kernel = single ? route_kernel<XKIND, G, S, THREADS, true> : route_kernel<XKIND, G, S, THREADS, false>;
+    if (smem > 32768) {  // with the static arrays past 48 KB
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return fail(FP8DL_ERR_CUDA, "moe_route: %s", cudaGetErrorString(e));
+    }
+    (void)launch_kernel(kernel, dim3((unsigned)tiles), dim3(THREADS), smem, st, 0, pdl, a);
+    note_launch();
+    FP8DL_TRY(check_launch("moe_route"));
+    if (single) return FP8DL_OK;
+    (void)launch_kernel(route_rows_kernel, dim3((unsigned)(tiles + (a.slope ? 1 : 0))), dim3(1024), 0, st, 0, pdl, a, tiles,
+                        tile_tokens);
+    note_launch();
+    return check_launch("moe_route(rows)");
+}
+
+template <int XKIND, int G, int S>
+static void launch_route_bwd(const RouteArgs &a, const float *dweight, const float *dloss, void *dlogits, int sms,
+                             cudaStream_t st, bool pdl) {
+    const int64_t ctas = (a.tokens + 256 / G - 1) / (256 / G), most = (int64_t)sms * 8;
+    (void)launch_kernel(route_bwd_kernel<XKIND, G, S>, dim3((unsigned)(ctas < most ? ctas : most)), dim3(256), 0, st, 0, pdl, a,
+                        dweight, dloss, dlogits);
+    note_launch();
+}
+
+static fp8dl_status check_route(const void *logits, int32_t dtype, int64_t tokens, int32_t n_experts, int32_t k) {
+    FP8DL_CHECK_ARG(dtype == FP8DL_F32 || dtype == FP8DL_BF16, "dtype must be FP8DL_F32 or FP8DL_BF16");
+    FP8DL_CHECK_ARG(n_experts >= 1 && n_experts <= kMaxGroups, "n_experts must be in [1, %d]", kMaxGroups);
+    FP8DL_CHECK_ARG(k >= 1 && k <= rt::MAX_K && k <= n_experts, "k must be in [1, min(n_experts, %d)]", rt::MAX_K);
+    if (tokens < 0 || tokens >= (int64_t(1) << 31) || tokens * k >= (int64_t(1) << 31))
+        return fail(FP8DL_ERR_SHAPE, "tokens (%lld) must not be negative and tokens * k must be below 2^31", (long long)tokens);
+    FP8DL_CHECK_ARG(tokens == 0 || logits, "logits is NULL");
+    return FP8DL_OK;
+}
+
+}  // namespace fp8dl
+
+using namespace fp8dl;
+
+extern "C" size_t moe_route_workspace_size(int64_t tokens, int32_t n_experts) {
+    if (tokens <= 0 || n_experts < 1 || n_experts > kMaxGroups) return 0;
+    const size_t tiles = tokens < rt::MAX_TILES ? (size_t)tokens : rt::MAX_TILES;
+    return ((tiles * (n_experts + 1) + 3) / 4 * 4 + tiles * n_experts) * 4;
+}
+
+extern "C" fp8dl_status moe_route(const void *logits, int32_t dtype, int64_t tokens, int32_t n_experts, int32_t k,
+                                  const uint8_t *valid, int32_t normalize, int32_t *expert, float *weight,
+                                  int32_t *position, int32_t *token, int32_t *offsets, int32_t *counts, float *slope,
+                                  float *loss, void *workspace, size_t workspace_bytes, fp8dl_stream_t stream) {
+    FP8DL_NVTX("moe_route");
+    FP8DL_TRY(check_route(logits, dtype, tokens, n_experts, k));
+    FP8DL_CHECK_ARG(offsets && (tokens == 0 || (expert && weight && position && token)),
+                    "expert, weight, position, token and offsets must be non-NULL");
+    FP8DL_CHECK_ARG(!slope == !loss, "slope and loss come together");
+    if (!aligned16(logits)) return fail(FP8DL_ERR_ALIGN, "logits must be 16-byte aligned");
+    if (!aligned4(expert) || !aligned4(weight) || !aligned4(position) || !aligned4(token) || !aligned4(offsets) ||
+        !aligned4(counts) || !aligned4(slope) || !aligned4(loss))
+        return fail(FP8DL_ERR_ALIGN, "expert, weight, position, token, offsets, counts, slope and loss must be 4-byte aligned");
+    if (tokens > 0) {
+        if (!workspace || workspace_bytes < moe_route_workspace_size(tokens, n_experts))
+            return fail(FP8DL_ERR_WORKSPACE, "moe_route needs a workspace of %zu bytes (got %zu)",
+                        moe_route_workspace_size(tokens, n_experts), workspace ? workspace_bytes : (size_t)0);
+        if (!aligned16(workspace)) return fail(FP8DL_ERR_ALIGN, "workspace must be 16-byte aligned");
+    }
+    int sms = 0;
+    FP8DL_TRY(current_device(nullptr, &sms));
+    cudaStream_t st = (cudaStream_t)stream;
+    if (tokens == 0) {
+        if (cudaMemsetAsync(offsets, 0, (size_t)(n_experts + 1) * 4, st) != cudaSuccess ||
+            (counts && cudaMemsetAsync(counts, 0, (size_t)n_experts * 4, st) != cudaSuccess) ||
+            (slope && cudaMemsetAsync(slope, 0, (size_t)n_experts * 4, st) != cudaSuccess) ||
+            (loss && cudaMemsetAsync(loss, 0, 4, st) != cudaSuccess))
+            return check_launch("moe_route(empty)");
+        return FP8DL_OK;
+    }
+    int g, s;
+    route_shape(n_experts, g, s);
+    const int esz = dtype == FP8DL_BF16 ? 2 : 4, runs = (s >= 16 ? 512 : 1024) / g;
+    const int64_t most = sms < rt::MAX_TILES ? sms : rt::MAX_TILES;
+    RouteArgs a = {};
+    a.logits = logits;
+    a.tokens = tokens;
+    a.experts = n_experts;
+    a.k = k;
+    a.normalize = normalize != 0;
+    a.vec = route_vec(n_experts, s, esz);
+    a.valid = valid;
+    a.expert = expert, a.position = position, a.token = token, a.offsets = offsets, a.counts = counts;
+    a.weight = weight, a.slope = slope, a.loss = loss;
+    a.per = (tokens + most * runs - 1) / (most * runs);
+    const int64_t tile_tokens = a.per * runs;
+    const int tiles = (int)((tokens + tile_tokens - 1) / tile_tokens);
+    a.hist = static_cast<int32_t *>(workspace);
+    a.psum = slope ? reinterpret_cast<float *>(a.hist + ((int64_t)tiles * (n_experts + 1) + 3) / 4 * 4) : nullptr;
+    const bool pdl = short_call_bytes((double)tokens * n_experts * esz);
+    fp8dl_status r = FP8DL_OK;
+#define FP8DL_ROUTE(g_, s_)                                                                          \
+    r = dtype == FP8DL_BF16 ? launch_route<FP8DL_BF16, g_, s_>(a, tiles, tile_tokens, st, pdl)       \
+                            : launch_route<FP8DL_F32, g_, s_>(a, tiles, tile_tokens, st, pdl)
+    if (g == 8) FP8DL_ROUTE(8, 1);
+    else if (g == 16) FP8DL_ROUTE(16, 1);
+    else if (s == 1) FP8DL_ROUTE(32, 1);
+    else if (s == 2) FP8DL_ROUTE(32, 2);
+    else if (s == 4) FP8DL_ROUTE(32, 4);
+    else if (s == 8) FP8DL_ROUTE(32, 8);
+    else if (s == 16) FP8DL_ROUTE(32, 16);
+    else FP8DL_ROUTE(32, 32);
+#undef FP8DL_ROUTE
+    return r;
+}
+
+extern "C" fp8dl_status moe_route_bwd(const void *logits, int32_t dtype, int64_t tokens, int32_t n_experts, int32_t k,
+                                      int32_t normalize, const int32_t *expert, const float *weight,
+                                      const float *dweight, const float *slope, const float *dloss, void *dlogits,
+                                      fp8dl_stream_t stream) {
+    FP8DL_NVTX("moe_route_bwd");
+    FP8DL_TRY(check_route(logits, dtype, tokens, n_experts, k));
+    FP8DL_CHECK_ARG(tokens == 0 || (expert && weight && dlogits), "expert, weight and dlogits must be non-NULL");
+    FP8DL_CHECK_ARG(tokens == 0 || !dloss || slope, "dloss without slope");
+    if (!aligned16(logits) || !aligned16(dlogits)) return fail(FP8DL_ERR_ALIGN, "logits and dlogits must be 16-byte aligned");
+    if (!aligned4(expert) || !aligned4(weight) || !aligned4(dweight) || !aligned4(slope) || !aligned4(dloss))
+        return fail(FP8DL_ERR_ALIGN, "expert, weight, dweight, slope and dloss must be 4-byte aligned");
+    int sms = 0;
+    FP8DL_TRY(current_device(nullptr, &sms));
+    if (tokens == 0) return FP8DL_OK;
+    int g, s;
+    route_shape(n_experts, g, s);
+    RouteArgs a = {};
+    a.logits = logits;
+    a.tokens = tokens;
+    a.experts = n_experts;
+    a.k = k;
+    a.normalize = normalize != 0;
+    a.vec = route_vec(n_experts, s, dtype == FP8DL_BF16 ? 2 : 4);
+    a.expert = const_cast<int32_t *>(expert);
+    a.weight = const_cast<float *>(weight);
+    a.slope = const_cast<float *>(slope);
+    cudaStream_t st = (cudaStream_t)stream;
+    const bool pdl = short_call_bytes((double)tokens * n_experts * (dtype == FP8DL_BF16 ? 4.0 : 8.0));
+#define FP8DL_ROUTE(g_, s_)                                                                             \
+    dtype == FP8DL_BF16 ? launch_route_bwd<FP8DL_BF16, g_, s_>(a, dweight, dloss, dlogits, sms, st, pdl) \
+                        : launch_route_bwd<FP8DL_F32, g_, s_>(a, dweight, dloss, dlogits, sms, st, pdl)
+    if (g == 8) FP8DL_ROUTE(8, 1);
+    else if (g == 16) FP8DL_ROUTE(16, 1);
+    else if (s == 1) FP8DL_ROUTE(32, 1);
+    else if (s == 2) FP8DL_ROUTE(32, 2);
+    else if (s == 4) FP8DL_ROUTE(32, 4);
+    else if (s == 8) FP8DL_ROUTE(32, 8);
+    else if (s == 16) FP8DL_ROUTE(32, 16);
+    else FP8DL_ROUTE(32, 32);
+#undef FP8DL_ROUTE
+    return check_launch("moe_route_bwd");
+}

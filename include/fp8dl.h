@@ -435,6 +435,144 @@ fp8dl_status fp8_block_gemm_grouped_wgrad(const uint8_t *A, int32_t a_dtype, con
                                           int32_t d_dtype, int32_t *dev_status, fp8dl_stream_t stream);
 
 /* ----------------------------------------------------------------------------
+ * Expert routing: which experts each token goes to, with which weight and into
+ * which row of the grouped products above, and how evenly the experts are used.
+ *
+ * Token counts may be 0; n_experts is in [1, 1024], any number; k in
+ * [1, min(n_experts, 32)]; tokens * k < 2^31.  Logits are bf16 or fp32, all
+ * arithmetic is fp32, sums run in a fixed order: repeated calls give the same
+ * bits. */
+
+/* Route `tokens` tokens, logits l [tokens x n_experts]:
+ *   p[t,e]   = exp(l[t,e] - max l[t,:]) / sum_e exp(..)         (softmax)
+ *   expert   [tokens x k] int32: the experts of the k largest logits, largest
+ *            first, equal ones by the lower expert
+ *   weight   [tokens x k] fp32: p of those experts, with `normalize` divided
+ *            by their sum over the token's k
+ *   offsets  [n_experts + 1] int32: the first row of each expert's group, as the
+ *            grouped calls read them; counts [n_experts] int32: their lengths, or NULL
+ *   position [tokens x k] int32: the row of the token's copy for that expert;
+ *            an expert's rows are in the order of their tokens
+ *   token    [tokens * k] int32: the token of each row.  Entries behind the
+ *            last row (offsets[n_experts]) keep their values.
+ * A logit of -infinity or NaN is never chosen.  A token with fewer than k
+ * others, or with valid[t] = 0 (padding; valid [tokens] bytes, or NULL), has
+ * expert and position -1 and weight 0 in the places that are left.  A NaN
+ * among the logits of a valid token makes its weights NaN (as softmax does).
+ * Balance loss (both or neither of slope and loss NULL), over the N tokens that
+ * have an expert and C = offsets[n_experts] choices:
+ *   slope [n_experts] fp32 = n_experts * counts[e] / (C * N)    (0 if N = 0)
+ *   loss  [1] fp32 = sum_e slope[e] * sum_t p[t,e]
+ * i.e. n_experts * sum_e (share of choices) * (mean probability): 1 when both
+ * are even.  slope is the gradient of loss by each p[t,e] of those tokens
+ * (counts do not carry a gradient).
+ * workspace: moe_route_workspace_size(tokens, n_experts) bytes, 16-byte aligned. */
+size_t moe_route_workspace_size(int64_t tokens, int32_t n_experts);
+
+fp8dl_status moe_route(const void *logits, int32_t dtype, int64_t tokens, int32_t n_experts, int32_t k,
+                       const uint8_t *valid, int32_t normalize, int32_t *expert, float *weight,
+                       int32_t *position, int32_t *token, int32_t *offsets, int32_t *counts, float *slope,
+                       float *loss, void *workspace, size_t workspace_bytes, fp8dl_stream_t stream);
+
+/* Gradient of moe_route's weights and loss by the logits:
+ *   dp[t,e] = dloss * slope[e]
+ *             + (e chosen at j: dweight[t,j], with `normalize`
+ *                (dweight[t,j] - sum_i dweight[t,i] * weight[t,i]) / (sum of the chosen p))
+ *   dlogits[t,e] = p[t,e] * (dp[t,e] - sum_e p[t,e] * dp[t,e])        (of `dtype`)
+ * expert, weight and slope as moe_route wrote them; dweight [tokens x k] fp32 or
+ * NULL (zeros); dloss a device float, or NULL (0; slope may then be NULL).  The row
+ * of a token without experts is zeros. */
+fp8dl_status moe_route_bwd(const void *logits, int32_t dtype, int64_t tokens, int32_t n_experts, int32_t k,
+                           int32_t normalize, const int32_t *expert, const float *weight,
+                           const float *dweight, const float *slope, const float *dloss, void *dlogits,
+                           fp8dl_stream_t stream);
+
+/* Quantise tokens x [tokens x cols] (bf16 or fp32) in blocks of 128 along each row,
+ * once, and put the codes and factors of token t into row position[t,j] of every
+ * j: row_q [rows x cols], row_s [ceil(cols/128) x rows], the A operand of
+ * the experts' product.  q [tokens x cols] and s [ceil(cols/128) x tokens] receive
+ * them in token order too (the checkpoint that fp8_block_recode reads), or NULL.
+ * A position outside [0, rows) is skipped; rows without a token keep their
+ * values; a row that two positions name holds one of the two tokens or a mixture.
+ * 1 <= k <= 32; cols a positive multiple of 16. */
+fp8dl_status fp8_block_dispatch(const void *x, int32_t x_dtype, int64_t tokens, int64_t cols, int32_t out_dtype,
+                                const int32_t *position, int32_t k, int64_t rows, uint8_t *row_q,
+                                float *row_s, uint8_t *q, float *s, fp8dl_stream_t stream);
+
+/* The experts' results back in token order:
+ *   out[t,:] = round( sum_j weight[t,j] * y[position[t,j],:] )
+ * (fp32, j ascending; fused multiply-adds), over the positions inside [0, rows);
+ * zeros for a token without any.  y [rows x cols] and out [tokens x cols] of
+ * `dtype` (bf16 or fp32); weight NULL: 1 (the gradient of fp8_block_dispatch's
+ * input).  1 <= k <= 32; cols a positive multiple of 16. */
+fp8dl_status moe_combine(const void *y, int32_t dtype, int64_t rows, int64_t cols, const int32_t *position,
+                         const float *weight, int64_t tokens, int32_t k, void *out, fp8dl_stream_t stream);
+
+/* Gradients of moe_combine, dout [tokens x cols]:
+ *   dy[position[t,j],:] = round( weight[t,j] * dout[t,:] )        (of `dtype`)
+ *   dweight[t,j] = sum_c dout[t,c] * y[position[t,j],c]           (fp32, a fixed order)
+ * dweight is 0 where the position is outside [0, rows); rows of dy without a
+ * token keep their values.  dy and dweight may each be NULL (y too without
+ * dweight, weight too without dy). */
+fp8dl_status moe_combine_bwd(const void *dout, const void *y, int32_t dtype, int64_t rows, int64_t cols,
+                             const int32_t *position, const float *weight, int64_t tokens, int32_t k,
+                             void *dy, float *dweight, fp8dl_stream_t stream);
+
+/* ----------------------------------------------------------------------------
+ * Activations kept in 8 bits.  Between two block-scaled products the forward
+ * pass quantises the activation's result straight from fp32 and keeps its argument
+ * h as row-wise codes (half the bytes of bf16); the backward pass decodes those,
+ * and computes from them both the gradient's codes and the activation's transposed
+ * codes, which therefore need not be kept.
+ *   act        FP8DL_ACT_GELU, FP8DL_ACT_SILU: g = act(h), h [rows x cols]
+ *              FP8DL_ACT_GEGLU, FP8DL_ACT_SWIGLU: g = act(a) * u, h = [a | u]
+ *              [rows x 2 cols], GELU or SiLU
+ *   GELU(a) = a * Phi(a) (erf form), SiLU(a) = a / (1 + exp(-a)), in fp32.
+ * Groups, rows of any number, factors' layouts and the rule of a block's scale as
+ * above: offsets/n_groups NULL and 0 for the whole matrix, rows outside the
+ * groups are neither read nor written. */
+typedef enum {
+    FP8DL_ACT_GELU = 0,
+    FP8DL_ACT_SILU = 1,
+    FP8DL_ACT_GEGLU = 2,
+    FP8DL_ACT_SWIGLU = 3
+} fp8dl_activation;
+
+/* Forward: g_q [rows x cols], g_s [ceil(cols/128) x rows] codes of g along the rows;
+ * h_q, h_s (or both NULL) exactly what fp8_block_quantize gives for h along the
+ * rows: h_q [rows x W], h_s [ceil(W/128) x rows], W = cols or 2 cols.  h of
+ * h_dtype, both codes of out_dtype. */
+fp8dl_status fp8_block_act(const void *h, int32_t h_dtype, int32_t act, int64_t rows, int64_t cols,
+                           const int32_t *offsets, int32_t n_groups, int32_t out_dtype, uint8_t *g_q,
+                           float *g_s, uint8_t *h_q, float *h_s, fp8dl_stream_t stream);
+
+/* Backward, h = fl32(code * factor) of h_q, h_s (codes of h_fp8):
+ *   dh = dg * act'(h), or [dg * u * act'(a) | dg * act(a)];  dg [rows x cols] of dg_dtype
+ *   dh_q/dh_s    [rows x W], [ceil(W/128) x rows]: codes of dh along the rows
+ *   dh_qt/dh_st  [W x T], [T/128 x W]: transposed, T = fp8_block_padded_rows(rows, n_groups)
+ *   g_qt/g_st    [cols x T], [T/128 x cols]: transposed codes (of h_fp8) of
+ *                g = act(h) or act(a) * u
+ *   dbias        [W] fp32 column sums of dh (fixed order; not with offsets);
+ *                workspace of fp8_cast_workspace_size(rows, W) bytes
+ * any of them NULL (codes and factors in pairs).  dh's codes are of out_dtype.  Nothing
+ * is rounded between the checkpoint's values and the codes but fp32.  Transposed codes
+ * and padding as fp8_block_quantize writes them. */
+fp8dl_status fp8_block_dact(const void *dg, int32_t dg_dtype, int32_t act, int64_t rows, int64_t cols,
+                            const uint8_t *h_q, int32_t h_fp8, const float *h_s, const int32_t *offsets,
+                            int32_t n_groups, int32_t out_dtype, uint8_t *dh_q, float *dh_s, uint8_t *dh_qt,
+                            float *dh_st, uint8_t *g_qt, float *g_st, float *dbias,
+                            void *workspace, size_t workspace_bytes, fp8dl_stream_t stream);
+
+/* Transposed codes from row-wise ones: the values fl32(code * factor) of
+ * q [src_rows x cols], s [ceil(cols/128) x src_rows] (codes of q_fp8) quantised
+ * in blocks of 128 along the rows into col_q [cols x T], col_s [T/128 x cols] as
+ * fp8_block_quantize does.  index [rows] int32: row r is row index[r] of q, zeros
+ * if that is outside [0, src_rows); NULL: r itself (rows <= src_rows). */
+fp8dl_status fp8_block_recode(const uint8_t *q, int32_t q_fp8, const float *s, int64_t src_rows, int64_t rows,
+                              int64_t cols, const int32_t *index, const int32_t *offsets, int32_t n_groups,
+                              int32_t out_dtype, uint8_t *col_q, float *col_s, fp8dl_stream_t stream);
+
+/* ----------------------------------------------------------------------------
  * LayerNormMLP pieces.  The Transformer Engine tutorial builds its blocks
  * from te.LayerNormMLP (LayerNorm -> fc1 -> GELU -> fc2), mirrored in plain
  * PyTorch by nn.LayerNorm and nn.GELU (erf form).  Under delayed scaling the
