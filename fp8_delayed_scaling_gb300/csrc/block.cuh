@@ -108,4 +108,59 @@ __device__ __forceinline__ void group_of_block(const int32_t *offsets, int n_gro
     count = found[1];
 }
 
+// The padded order's 128-row blocks in shared memory, for kernels that look up many of them: before[g] blocks
+// lie before group g, first[g] and length[g] are its rows.  Built once by a block of THREADS >= 256 threads, which meet
+// at a barrier at its end; sums are limited as in group_of_block.
+struct GroupTable {
+    uint32_t before[kMaxGroups + 1];
+    int32_t first[kMaxGroups], length[kMaxGroups];
+    uint32_t warp_sum[8];
+};
+
+__device__ __forceinline__ void build_group_table(GroupTable &t, const int32_t *offsets, int n_groups, int64_t rows) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = (int)rows;
+    const int per = (n_groups + 255) / 256, g0 = (int)threadIdx.x * per;
+    uint32_t mine = 0;
+    if (warp < 8) {
+        for (int i = 0; i < per && g0 + i < n_groups; i++) {
+            const int32_t f = min(max(offsets[g0 + i], 0), n), l = min(max(offsets[g0 + i + 1], f), n) - f;
+            t.first[g0 + i] = f, t.length[g0 + i] = l;
+            mine += ((uint32_t)l + 127) >> 7;
+        }
+    }
+    uint32_t sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += u;
+    }
+    if (lane == 31 && warp < 8) t.warp_sum[warp] = min(sum, 1u << 28);
+    __syncthreads();
+    if (warp < 8) {
+        uint32_t at = sum - mine;
+        for (int w = 0; w < warp; w++) at += t.warp_sum[w];
+        for (int i = 0; i < per && g0 + i < n_groups; i++) {
+            t.before[g0 + i] = at;
+            at += ((uint32_t)t.length[g0 + i] + 127) >> 7;
+            if (g0 + i == n_groups - 1) t.before[n_groups] = at;
+        }
+    }
+    __syncthreads();
+}
+
+// Block `block` of the table, block < before[n_groups]: its first row and how many.
+__device__ __forceinline__ void find_group(const GroupTable &t, int n_groups, uint32_t block, int64_t &first_row, int &count) {
+    int lo = 0, hi = n_groups;  // before[lo] <= block < before[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t.before[mid] <= block)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const int32_t skip = (int32_t)(block - t.before[lo]) * 128;
+    first_row = (int64_t)t.first[lo] + skip;
+    count = min(t.length[lo] - skip, 128);
+}
+
 }  // namespace fp8dl

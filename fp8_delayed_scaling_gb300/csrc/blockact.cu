@@ -26,9 +26,9 @@ __device__ __forceinline__ float2 decode2(uint32_t two, bool e4m3) {
 }
 
 // act(a) and, with D, its derivative.
-template <bool D>
-__device__ __forceinline__ void activation2(float2 a, bool silu, float2 &y, float2 &d) {
-    if (silu) {
+template <bool SILU, bool D>
+__device__ __forceinline__ void activation2(float2 a, float2 &y, float2 &d) {
+    if (SILU) {
         const float2 t = __fmul2_rn(a, f2(-1.4426950409f));
         const float2 e = __fadd2_rn(make_float2(ex2_approx_ftz(t.x), ex2_approx_ftz(t.y)), f2(1.0f));
         const float2 s = make_float2(rcp_approx_ftz(e.x), rcp_approx_ftz(e.y));
@@ -54,7 +54,7 @@ struct BlockActArgs {
     uint8_t *g_q, *h_q;
     float *g_s, *h_s;
     uint32_t jobs;  // blocks of a row
-    int silu, split;
+    int split;
 };
 
 namespace ba {
@@ -99,7 +99,7 @@ __device__ __forceinline__ void put_block(const float2 (&v)[4], bool ok, bool fi
 // A CTA takes 32 rows of one block column (of a's and of u's where g is gated).  Where u's half does not start
 // on a block (cols not a multiple of 128: `split`) h's blocks do not line up with g's: the codes of h
 // are jobs of their own behind g's.
-template <int XKIND, int FMT, bool GATED>
+template <int XKIND, int FMT, bool GATED, bool SILU>
 __global__ void __launch_bounds__(ba::ACT_THREADS) block_act_kernel(const BlockActArgs a) {
     using namespace ba;
     pdl_wait();
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(ba::ACT_THREADS) block_act_kernel(const BlockA
         float2 y[4], none;
 #pragma unroll
         for (int q = 0; q < 4; q++) {
-            activation2<false>(va[i][q], a.silu, y[q], none);
+            activation2<SILU, false>(va[i][q], y[q], none);
             if (GATED) y[q] = __fmul2_rn(y[q], vu[i][q]);
         }
         put_block<FMT>(y, ok[i], put, a.g_q + r * a.cols + c, a.g_s + (c >> 7) * a.rows + r);
@@ -323,7 +323,7 @@ __device__ __forceinline__ void tile_out(const bt::Matrix &sm, uint8_t *q, int64
 
 struct BlockDactArgs {
     const void *dg;
-    int64_t rows, cols, wide;
+    int64_t rows, cols, wide;  // wide: columns of h
     const uint8_t *h_q;
     const float *h_s;
     const int32_t *offsets;
@@ -331,10 +331,304 @@ struct BlockDactArgs {
     uint8_t *dh_q, *dh_qt, *g_qt;
     float *dh_s, *dh_st, *g_st;
     int64_t col_ld;
-    float *ws;       // column sums of dh per 128-row tile, or NULL
-    uint32_t jobs;   // tiles across
-    int silu, h_e4;  // SiLU, else GELU; the checkpoint's format (and g's): E4M3, else E5M2
+    float *ws;              // column sums of dh per 128-row tile, or NULL
+    uint32_t tiles, across;  // tiles down (of the padded order, at most) and across
+    uint32_t row_first, row_jobs;  // blocks along the rows that block_dact_rows_kernel makes: the first, how many
+    int bf16, h_e4;         // dg's type; the checkpoint's format (and g's): E4M3, else E5M2
 };
+
+// cp.async of N bytes, zeros where !ok (nothing is read then).
+template <int N>
+__device__ __forceinline__ void copy_async(void *smem, const void *global, bool ok) {
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(smem)), n = ok ? N : 0;
+    if (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(global), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(global), "n"(N), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Eight codes -> fp16 pairs.  (volatile: a branch, not both conversions and a select.)
+__device__ __forceinline__ void decode8(uint2 u, bool e4m3, uint32_t (&h)[4]) {
+    if (e4m3) {
+        asm volatile("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;}"
+                     : "=r"(h[0]), "=r"(h[1]) : "r"(u.x));
+        asm volatile("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;}"
+                     : "=r"(h[2]), "=r"(h[3]) : "r"(u.y));
+    } else {  // E5M2 is the upper byte of an fp16
+        h[0] = __byte_perm(u.x, 0, 0x1404), h[1] = __byte_perm(u.x, 0, 0x3424);
+        h[2] = __byte_perm(u.y, 0, 0x1404), h[3] = __byte_perm(u.y, 0, 0x3424);
+    }
+}
+
+// dh (and g) of two elements: every caller rounds in this order, so that the same element has the same
+// bits whichever kernel computes it.
+template <bool GATED, bool SILU>
+__device__ __forceinline__ void gradient2(uint32_t ha, float fa, uint32_t hu, float fu, float2 dg, float2 &da, float2 &du,
+                                          float2 &g) {
+    float2 y, d;
+    activation2<SILU, true>(__fmul2_rn(__half22float2(*reinterpret_cast<const __half2 *>(&ha)), f2(fa)), y, d);
+    if (GATED) {
+        const float2 u = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2 *>(&hu)), f2(fu));
+        g = __fmul2_rn(y, u);
+        da = __fmul2_rn(__fmul2_rn(dg, u), d);
+        du = __fmul2_rn(dg, y);
+    } else {
+        g = y;
+        da = __fmul2_rn(dg, d);
+    }
+}
+
+// The transposed codes, column sums and, where whole blocks line up with the tiles, the codes along the
+// rows: a persistent CTA per SM walks 128 x 128 tiles of g's columns.
+//   Reads    each thread copies what it will itself read of the next tile (dg and codes: 32 values of each)
+//            into its own slots in shared memory, right after it has read this tile's: a tile's loads are
+//            under way while the one before it is computed, without registers or a barrier for them.
+//            The rows' factors (a few hundred floats) are copied by the first warps.
+//   Values   of da, du and g in fp32 (96 registers) from one decoding and one activation.
+//   Work     a tile of 16384 values takes 144 KB of traffic and about 25 instructions a value: HBM and the
+//            issue slots are about even, so what counts is that neither waits.
+// 8192 x 11008 swiglu, bf16, bias gradient: see the end of the file's entry for the figures.
+template <int FMT, bool GATED, bool SILU>
+__global__ void __launch_bounds__(bt::THREADS, 1) block_dact_kernel(const BlockDactArgs a) {
+    using namespace bt;
+    constexpr int NM = GATED ? 3 : 2, NH = NM - 1;  // matrices, those of dh
+    constexpr int NF = GATED ? 3 : 1;  // factors of a row: a's block, u's, and the next where a tile of u spans two
+    extern __shared__ __align__(16) uint8_t dyn[];
+    Matrix *sm = reinterpret_cast<Matrix *>(dyn);                       // da, [du,] g
+    uint4 *in_dg = reinterpret_cast<uint4 *>(sm + NM);                  // [8][THREADS] (bf16: half of it)
+    uint2 *in_h = reinterpret_cast<uint2 *>(in_dg + 8 * THREADS);       // [4 * NH][THREADS]
+    float *fac = reinterpret_cast<float *>(in_h + 4 * NH * THREADS);    // [2][NF][TILE]
+    __shared__ GroupTable table;
+    const int tid = threadIdx.x;
+    pdl_wait();
+    pdl_trigger();
+    uint32_t down = a.tiles;
+    if (a.offsets) {
+        build_group_table(table, a.offsets, a.n_groups, a.rows);
+        down = min(down, table.before[a.n_groups]);
+    }
+    const uint32_t total = down * a.across;
+    Where w;
+    w.rr = tid >> 4, w.cc = tid & 15;
+    int64_t next_r0 = 0;
+    int next_n = 0;
+    const auto place = [&](uint32_t t) {
+        const uint32_t tile = t / a.across;
+        if (a.offsets) {
+            find_group(table, a.n_groups, tile, next_r0, next_n);
+        } else {
+            next_r0 = (int64_t)tile * TILE;
+            next_n = (int)min((int64_t)TILE, a.rows - next_r0);
+        }
+    };
+    const auto fetch_row = [&](int i, int64_t c) {  // row i of the thread's four, columns c ..
+        const bool ok = c < a.cols && 4 * w.rr + i < next_n;
+        const int64_t r = next_r0 + 4 * w.rr + i;
+        if (a.bf16) {
+            copy_async<16>(in_dg + i * THREADS + tid, static_cast<const char *>(a.dg) + (ok ? (r * a.cols + c) * 2 : 0), ok);
+        } else {
+            const char *p = static_cast<const char *>(a.dg) + (ok ? (r * a.cols + c) * 4 : 0);
+            copy_async<16>(in_dg + 2 * i * THREADS + tid, p, ok);
+            copy_async<16>(in_dg + (2 * i + 1) * THREADS + tid, p + 16, ok);
+        }
+        const uint8_t *q = a.h_q + (ok ? r * a.wide + c : 0);
+        copy_async<8>(in_h + i * THREADS + tid, q, ok);
+        if (GATED) copy_async<8>(in_h + (4 + i) * THREADS + tid, q + (ok ? a.cols : 0), ok);
+    };
+    const auto fetch_factors = [&](int slot, int64_t first) {
+        if (tid < NF * TILE) {
+            const int which = tid / TILE, row = tid % TILE;
+            const int64_t block = ((first + (which ? a.cols : 0)) >> 7) + (which == 2);
+            const bool ok = row < next_n && block * 128 < a.wide;
+            copy_async<4>(fac + slot * NF * TILE + tid, a.h_s + (ok ? block * a.rows + next_r0 + row : 0), ok);
+        }
+    };
+    uint32_t t = blockIdx.x;
+    if (t < total) {
+        place(t);
+        const int64_t first = (int64_t)(t % a.across) * TILE;
+#pragma unroll
+        for (int i = 0; i < 4; i++) fetch_row(i, first + 8 * w.cc);
+        fetch_factors(0, first);
+    }
+    for (int slot = 0; t < total; t += gridDim.x, slot ^= 1) {
+        const uint32_t tile = t / a.across;
+        const int64_t first = (int64_t)(t - tile * a.across) * TILE;
+        w.r0 = next_r0, w.nrows = next_n;
+        w.c0 = first + 8 * w.cc;
+        w.col_ok = w.c0 < a.cols;
+        const uint32_t u = t + gridDim.x;
+        const bool more = u < total;
+        const int64_t ufirst = more ? (int64_t)(u % a.across) * TILE : 0;
+        copy_wait_all();
+        __syncthreads();  // the factors have come, the last tile's codes have gone
+        if (more) {
+            place(u);
+            fetch_factors(slot ^ 1, ufirst);
+        }
+        const float *fa_of = fac + slot * NF * TILE + 4 * w.rr;
+        const float *fu_of = fa_of + (((w.c0 + a.cols) >> 7) != ((first + a.cols) >> 7) ? 2 : 1) * TILE;
+        Values v[NM];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            float2 dg[4];
+            if (a.bf16) {
+                const uint4 x = in_dg[i * THREADS + tid];
+                dg[0] = make_float2(bf16_lo(x.x), bf16_hi(x.x)), dg[1] = make_float2(bf16_lo(x.y), bf16_hi(x.y));
+                dg[2] = make_float2(bf16_lo(x.z), bf16_hi(x.z)), dg[3] = make_float2(bf16_lo(x.w), bf16_hi(x.w));
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const uint4 x = in_dg[(2 * i + h) * THREADS + tid];
+                    dg[2 * h] = make_float2(__uint_as_float(x.x), __uint_as_float(x.y));
+                    dg[2 * h + 1] = make_float2(__uint_as_float(x.z), __uint_as_float(x.w));
+                }
+            }
+            uint32_t ha[4], hu[4];
+            decode8(in_h[i * THREADS + tid], a.h_e4, ha);
+            if (GATED) decode8(in_h[(4 + i) * THREADS + tid], a.h_e4, hu);
+            const float fa = fa_of[i], fu = GATED ? fu_of[i] : 0.0f;
+            if (more) fetch_row(i, ufirst + 8 * w.cc);
+#pragma unroll
+            for (int p = 0; p < 4; p++)
+                gradient2<GATED, SILU>(ha[p], fa, GATED ? hu[p] : 0u, fu, dg[p], v[0][i][p], v[NH - 1][i][p], v[NM - 1][i][p]);
+        }
+        if (a.dh_q && first < (int64_t)a.row_first * TILE) {
+            tile_rows<FMT>(v[0], w, a.dh_q, a.dh_s, a.wide, a.rows);
+            if (GATED && a.row_jobs == 0) {  // u's blocks line up too
+                Where wu = w;
+                wu.c0 += a.cols;
+                tile_rows<FMT>(v[NH - 1], wu, a.dh_q, a.dh_s, a.wide, a.rows);
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < NM; m++) {
+            if (m < NH ? !a.dh_qt : !a.g_qt) continue;
+            tile_maxima(v[m], w, sm[m]);
+        }
+        if (a.ws) {
+#pragma unroll
+            for (int m = 0; m < NH; m++) tile_sums(v[m], w, sm[m]);
+        }
+        __syncthreads();
+        if (tid < NM * TILE) {
+            const int m = tid / TILE, c = tid % TILE;
+            if (first + c < a.cols) {
+                if (m < NH) {
+                    const int64_t at = (int64_t)tile * a.wide + first + c + (m ? a.cols : 0);
+                    tile_scale<FMT>(sm[m], c, a.dh_qt ? a.dh_st + at : nullptr, a.ws ? a.ws + at : nullptr);
+                } else if (a.g_qt) {
+                    float *to = a.g_st + (int64_t)tile * a.cols + first + c;
+                    if (a.h_e4)
+                        tile_scale<FP8DL_E4M3>(sm[m], c, to, nullptr);
+                    else
+                        tile_scale<FP8DL_E5M2>(sm[m], c, to, nullptr);
+                }
+            }
+        }
+        __syncthreads();
+        if (a.dh_qt) {
+#pragma unroll
+            for (int m = 0; m < NH; m++) tile_stage<FMT>(v[m], w, sm[m]);
+        }
+        if (a.g_qt) {
+            if (a.h_e4)
+                tile_stage<FP8DL_E4M3>(v[NM - 1], w, sm[NM - 1]);
+            else
+                tile_stage<FP8DL_E5M2>(v[NM - 1], w, sm[NM - 1]);
+        }
+        __syncthreads();
+        const int left = (int)min((int64_t)TILE, a.cols - first);
+#pragma unroll
+        for (int m = 0; m < NM; m++) {
+            uint8_t *q = m < NH ? a.dh_qt : a.g_qt;
+            if (q) tile_out(sm[m], q + (first + (GATED && m == 1 ? a.cols : 0)) * a.col_ld + (int64_t)tile * TILE, a.col_ld, left);
+        }
+    }
+}
+
+// Blocks of dh along the rows, a.row_jobs of a row from a.row_first on: all of them where nothing else is
+// wanted; those of u's half (and the one that holds the border) where cols is not a multiple of 128 and
+// the tiles above do not hold whole blocks.  16 lanes a block, two rows of each in flight.
+template <int FMT, bool GATED, bool SILU>
+__global__ void __launch_bounds__(ba::ACT_THREADS) block_dact_rows_kernel(const BlockDactArgs a) {
+    using namespace ba;
+    pdl_wait();
+    pdl_trigger();
+    const uint32_t tile = blockIdx.x / a.row_jobs, job = a.row_first + blockIdx.x % a.row_jobs;
+    int64_t first = 0, end = a.rows;
+    if (a.offsets) {
+        group_rows(a.offsets, 0, a.rows, first, end);
+        end = min(max((int64_t)a.offsets[a.n_groups], first), a.rows);
+    }
+    const int64_t r0 = first + (int64_t)tile * ACT_ROWS + (threadIdx.x >> 4);
+    if (r0 - (threadIdx.x >> 4) >= end) return;
+    const bool lead = (threadIdx.x & 15) == 0;
+    const int64_t at = (int64_t)job * 128 + 8 * (threadIdx.x & 15);  // of dh
+    const bool right = GATED && at >= a.cols;
+    const int64_t c = right ? at - a.cols : at;
+    float2 dg[2][4];
+    uint2 qa[2], qu[2];
+    float fa[2], fu[2];
+    bool ok[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const int64_t r = r0 + 16 * i;
+        ok[i] = r < end && at < a.wide;
+        qa[i] = qu[i] = make_uint2(0u, 0u);
+        fa[i] = fu[i] = 0.0f;
+        if (a.bf16)
+            load8<FP8DL_BF16>(a.dg, r * a.cols + c, ok[i], dg[i]);
+        else
+            load8<FP8DL_F32>(a.dg, r * a.cols + c, ok[i], dg[i]);
+        if (ok[i]) {
+            qa[i] = *reinterpret_cast<const uint2 *>(a.h_q + r * a.wide + c);
+            fa[i] = a.h_s[(c >> 7) * a.rows + r];
+            if (GATED && !right) {
+                qu[i] = *reinterpret_cast<const uint2 *>(a.h_q + r * a.wide + c + a.cols);
+                fu[i] = a.h_s[((c + a.cols) >> 7) * a.rows + r];
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const int64_t r = r0 + 16 * i;
+        uint32_t ha[4], hu[4];
+        decode8(qa[i], a.h_e4, ha);
+        if (GATED) decode8(qu[i], a.h_e4, hu);
+        float2 v[4], du, g;
+#pragma unroll
+        for (int p = 0; p < 4; p++) {
+            gradient2<GATED, SILU>(ha[p], fa[i], GATED ? hu[p] : 0u, fu[i], dg[i][p], v[p], du, g);
+            if (GATED && right) v[p] = du;
+        }
+        put_block<FMT>(v, ok[i], lead && r < end, a.dh_q + r * a.wide + at, a.dh_s + (at >> 7) * a.rows + r);
+    }
+}
+
+template <int FMT, bool GATED, bool SILU>
+static fp8dl_status launch_dact(const BlockDactArgs &a, bool tiles, int sms, cudaStream_t st, bool pdl) {
+    using namespace bt;
+    if (tiles) {
+        constexpr int NM = GATED ? 3 : 2;
+        constexpr size_t smem = NM * sizeof(Matrix) + 8 * THREADS * 16 + 4 * (NM - 1) * THREADS * 8 + 2 * (GATED ? 3 : 1) * TILE * 4;
+        auto *kernel = block_dact_kernel<FMT, GATED, SILU>;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return fail(FP8DL_ERR_CUDA, "fp8_block_dact: %s", cudaGetErrorString(e));
+        const int64_t most = (int64_t)a.tiles * a.across;
+        (void)launch_kernel(kernel, dim3((unsigned)(most < sms ? most : sms)), dim3(THREADS), smem, st, 0, pdl, a);
+        note_launch();
+        FP8DL_TRY(check_launch("fp8_block_dact"));
+    }
+    if (a.dh_q && a.row_jobs) {
+        const int64_t ctas = (a.rows + ba::ACT_ROWS - 1) / ba::ACT_ROWS * a.row_jobs;
+        (void)launch_kernel(block_dact_rows_kernel<FMT, GATED, SILU>, dim3((unsigned)ctas), dim3(ba::ACT_THREADS), 0, st, 0, pdl, a);
+        note_launch();
+        FP8DL_TRY(check_launch("fp8_block_dact(rows)"));
+    }
+    return FP8DL_OK;
+}
 
 // The rows of tile `tile` of the padded order; false where there are none.
 __device__ __forceinline__ bool tile_place(const int32_t *offsets, int n_groups, int64_t rows, uint32_t tile, Where &w) {
@@ -344,87 +638,6 @@ __device__ __forceinline__ bool tile_place(const int32_t *offsets, int n_groups,
     w.nrows = (int)min((int64_t)bt::TILE, rows - w.r0);
     if (offsets) group_of_block(offsets, n_groups, rows, tile, w.r0, w.nrows);
     return w.nrows > 0;
-}
-
-// Eight values of the checkpoint from column c on (of the whole row), row r.
-__device__ __forceinline__ void load_kept(const BlockDactArgs &a, int64_t r, int64_t c, bool ok, float2 (&v)[4]) {
-    uint2 u = make_uint2(0u, 0u);
-    float f = 0.0f;
-    if (ok) {
-        u = *reinterpret_cast<const uint2 *>(a.h_q + r * a.wide + c);
-        f = a.h_s[(c >> 7) * a.rows + r];
-    }
-    v[0] = __fmul2_rn(decode2(u.x, a.h_e4), f2(f)), v[1] = __fmul2_rn(decode2(u.x >> 16, a.h_e4), f2(f));
-    v[2] = __fmul2_rn(decode2(u.y, a.h_e4), f2(f)), v[3] = __fmul2_rn(decode2(u.y >> 16, a.h_e4), f2(f));
-}
-
-// One 128 x 128 tile of one matrix: of dh (its columns 0 .. wide), then of g (0 .. cols).  Right for every
-// width: where u's half does not start on a block, a tile may hold columns of both halves (a
-// thread's eight are always of one: cols is a multiple of 16).
-template <int XKIND, int FMT, bool GATED>
-__global__ void __launch_bounds__(bt::THREADS) block_dact_kernel(const BlockDactArgs a) {
-    using namespace bt;
-    __shared__ __align__(16) Matrix sm;
-    pdl_wait();
-    pdl_trigger();
-    const uint32_t tile = blockIdx.x / a.jobs, job = blockIdx.x % a.jobs, dh_jobs = (uint32_t)((a.wide + 127) / 128);
-    Where w;
-    if (!tile_place(a.offsets, a.n_groups, a.rows, tile, w)) return;
-    const bool is_g = job >= dh_jobs;
-    const int64_t first = (int64_t)(is_g ? job - dh_jobs : job) * TILE, width = is_g ? a.cols : a.wide;
-    w.c0 = first + 8 * w.cc;
-    w.col_ok = w.c0 < width;
-    const bool right = GATED && !is_g && w.c0 >= a.cols;  // of du
-    const int64_t c = right ? w.c0 - a.cols : w.c0;
-    Values v;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int64_t r = w.r0 + 4 * w.rr + i;
-        const bool ok = w.col_ok && 4 * w.rr + i < w.nrows;
-        float2 va[4], vu[4], vd[4];
-        load_kept(a, r, c, ok, va);
-        if (GATED && !right) load_kept(a, r, c + a.cols, ok, vu);
-        if (!is_g) load8<XKIND>(a.dg, r * a.cols + c, ok, vd);
-#pragma unroll
-        for (int p = 0; p < 4; p++) {
-            float2 y, d;
-            activation2<true>(va[p], a.silu, y, d);
-            if (is_g)
-                v[i][p] = GATED ? __fmul2_rn(y, vu[p]) : y;
-            else if (right)
-                v[i][p] = __fmul2_rn(vd[p], y);
-            else
-                v[i][p] = __fmul2_rn(GATED ? __fmul2_rn(vd[p], vu[p]) : vd[p], d);
-        }
-    }
-    if (!is_g && a.dh_q) tile_rows<FMT>(v, w, a.dh_q, a.dh_s, a.wide, a.rows);
-    uint8_t *qt = is_g ? a.g_qt : a.dh_qt;
-    float *st = is_g ? a.g_st : a.dh_st;
-    const bool sums = !is_g && a.ws;
-    if (!qt && !sums) return;
-    tile_maxima(v, w, sm);
-    if (sums) tile_sums(v, w, sm);
-    __syncthreads();
-    if (threadIdx.x < TILE && first + threadIdx.x < width) {
-        float *to = qt ? st + (int64_t)tile * width + first + threadIdx.x : nullptr;
-        float *sum = sums ? a.ws + (int64_t)tile * width + first + threadIdx.x : nullptr;
-        if (is_g && !a.h_e4)
-            tile_scale<FP8DL_E5M2>(sm, threadIdx.x, to, sum);
-        else if (is_g)
-            tile_scale<FP8DL_E4M3>(sm, threadIdx.x, to, sum);
-        else
-            tile_scale<FMT>(sm, threadIdx.x, to, sum);
-    }
-    if (!qt) return;
-    __syncthreads();
-    if (is_g && !a.h_e4)
-        tile_stage<FP8DL_E5M2>(v, w, sm);
-    else if (is_g)
-        tile_stage<FP8DL_E4M3>(v, w, sm);
-    else
-        tile_stage<FMT>(v, w, sm);
-    __syncthreads();
-    tile_out(sm, qt + first * a.col_ld + (int64_t)tile * TILE, a.col_ld, (int)min((int64_t)TILE, width - first));
 }
 
 struct BlockRecodeArgs {
@@ -527,7 +740,6 @@ extern "C" fp8dl_status fp8_block_act(const void *h, int32_t h_dtype, int32_t ac
     a.offsets = offsets;
     a.n_groups = n_groups;
     a.g_q = g_q, a.h_q = h_q, a.g_s = g_s, a.h_s = h_s;
-    a.silu = act_silu(act);
     a.split = gated && cols % 128 != 0;
     a.jobs = (uint32_t)((cols + 127) / 128 + (a.split && h_q ? (a.wide + 127) / 128 : 0));
     const int64_t ctas = (rows + ba::ACT_ROWS - 1) / ba::ACT_ROWS * a.jobs;
@@ -535,8 +747,10 @@ extern "C" fp8dl_status fp8_block_act(const void *h, int32_t h_dtype, int32_t ac
     FP8DL_TRY(current_device(nullptr, nullptr));
     if (rows == 0) return FP8DL_OK;
     const bool pdl = short_call_bytes((double)rows * a.wide * ((h_dtype == FP8DL_BF16 ? 2.0 : 4.0) + (h_q ? 1.0 : 0.0)) + (double)rows * cols);
-    auto *kernel = &block_act_kernel<FP8DL_BF16, FP8DL_E4M3, false>;
-#define FP8DL_ACT(X, F) kernel = gated ? block_act_kernel<X, F, true> : block_act_kernel<X, F, false>
+    auto *kernel = &block_act_kernel<FP8DL_BF16, FP8DL_E4M3, false, false>;
+#define FP8DL_ACT(X, F)                                                                                      \
+    kernel = gated ? (act_silu(act) ? block_act_kernel<X, F, true, true> : block_act_kernel<X, F, true, false>) \
+                   : (act_silu(act) ? block_act_kernel<X, F, false, true> : block_act_kernel<X, F, false, false>)
     if (h_dtype == FP8DL_BF16 && out_dtype == FP8DL_E4M3) FP8DL_ACT(FP8DL_BF16, FP8DL_E4M3);
     else if (h_dtype == FP8DL_BF16) FP8DL_ACT(FP8DL_BF16, FP8DL_E5M2);
     else if (out_dtype == FP8DL_E4M3) FP8DL_ACT(FP8DL_F32, FP8DL_E4M3);
@@ -582,12 +796,18 @@ extern "C" fp8dl_status fp8_block_dact(const void *dg, int32_t dg_dtype, int32_t
     a.dh_q = dh_q, a.dh_qt = dh_qt, a.g_qt = g_qt, a.dh_s = dh_s, a.dh_st = dh_st, a.g_st = g_st;
     a.col_ld = fp8_block_padded_rows(rows, n_groups);
     a.ws = dbias ? static_cast<float *>(workspace) : nullptr;
-    a.silu = act_silu(act);
+    a.bf16 = dg_dtype == FP8DL_BF16;
     a.h_e4 = h_fp8 == FP8DL_E4M3;
-    a.jobs = (uint32_t)((wide + 127) / 128 + (g_qt ? (cols + 127) / 128 : 0));
-    const int64_t ctas = a.col_ld / 128 * a.jobs;
-    FP8DL_TRY(check_tiles(ctas, rows, wide));
-    FP8DL_TRY(current_device(nullptr, nullptr));
+    a.tiles = (uint32_t)(a.col_ld / 128);
+    a.across = (uint32_t)((cols + 127) / 128);
+    const bool tiles = dh_qt || g_qt || dbias, split = gated && cols % 128 != 0;
+    // codes along the rows: by the tiles, but for what does not line up with them or where there are none
+    a.row_first = !tiles ? 0 : split ? (uint32_t)(cols / 128) : a.across;
+    a.row_jobs = tiles && !split ? 0 : (uint32_t)((wide + 127) / 128) - a.row_first;
+    FP8DL_TRY(check_tiles((rows + ba::ACT_ROWS - 1) / ba::ACT_ROWS * a.row_jobs, rows, wide));
+    FP8DL_TRY(check_tiles(a.col_ld / 128 * a.across, rows, wide));
+    int sms = 0;
+    FP8DL_TRY(current_device(nullptr, &sms));
     cudaStream_t st = (cudaStream_t)stream;
     if (rows == 0) {
         if (dbias && cudaMemsetAsync(dbias, 0, (size_t)wide * sizeof(float), st) != cudaSuccess)
@@ -595,16 +815,14 @@ extern "C" fp8dl_status fp8_block_dact(const void *dg, int32_t dg_dtype, int32_t
         return FP8DL_OK;
     }
     const bool pdl = short_call_bytes((double)rows * ((double)cols * (dg_dtype == FP8DL_BF16 ? 3.0 : 5.0) + 3.0 * wide));
-    auto *kernel = &block_dact_kernel<FP8DL_BF16, FP8DL_E4M3, false>;
-#define FP8DL_DACT(X, F) kernel = gated ? block_dact_kernel<X, F, true> : block_dact_kernel<X, F, false>
-    if (dg_dtype == FP8DL_BF16 && out_dtype == FP8DL_E4M3) FP8DL_DACT(FP8DL_BF16, FP8DL_E4M3);
-    else if (dg_dtype == FP8DL_BF16) FP8DL_DACT(FP8DL_BF16, FP8DL_E5M2);
-    else if (out_dtype == FP8DL_E4M3) FP8DL_DACT(FP8DL_F32, FP8DL_E4M3);
-    else FP8DL_DACT(FP8DL_F32, FP8DL_E5M2);
+    auto *launch = &launch_dact<FP8DL_E4M3, false, false>;
+#define FP8DL_DACT(F)                                                                          \
+    launch = gated ? (act_silu(act) ? launch_dact<F, true, true> : launch_dact<F, true, false>) \
+                   : (act_silu(act) ? launch_dact<F, false, true> : launch_dact<F, false, false>)
+    if (out_dtype == FP8DL_E4M3) FP8DL_DACT(FP8DL_E4M3);
+    else FP8DL_DACT(FP8DL_E5M2);
 #undef FP8DL_DACT
-    (void)launch_kernel(kernel, dim3((unsigned)ctas), dim3(bt::THREADS), 0, st, 0, pdl, a);
-    note_launch();
-    FP8DL_TRY(check_launch("fp8_block_dact"));
+    FP8DL_TRY(launch(a, tiles, sms, st, pdl));
     if (dbias) {
         colsum_reduce(a.ws, (rows + 127) / 128, wide, dbias, st, pdl);
         return check_launch("fp8_block_dact(dbias reduce)");
