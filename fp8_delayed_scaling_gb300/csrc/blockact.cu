@@ -15,25 +15,27 @@
 
 namespace fp8dl {
 
-// Codes -> values, two at a time: FP8 is exact in fp16, fp16 in fp32.
-__device__ __forceinline__ float2 decode2(uint32_t two, bool e4m3) {
-    uint32_t h;
-    if (e4m3)
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
+// Four fp32 values -> four codes, v0 in byte 0, the halves joined by the conversions themselves.
+template <int FMT>
+__device__ __forceinline__ uint32_t codes4(float v0, float v1, float v2, float v3) {
+    uint32_t r;
+    if (FMT == FP8DL_E4M3)
+        asm("{.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};}"
+            : "=r"(r) : "f"(v0), "f"(v1), "f"(v2), "f"(v3));
     else
-        asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
-    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+        asm("{.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e5m2x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e5m2x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};}"
+            : "=r"(r) : "f"(v0), "f"(v1), "f"(v2), "f"(v3));
+    return r;
 }
 
 // act(a) and, with D, its derivative.
 template <bool SILU, bool D>
 __device__ __forceinline__ void activation2(float2 a, float2 &y, float2 &d) {
-    if (SILU) {
-        const float2 t = __fmul2_rn(a, f2(-1.4426950409f));
-        const float2 e = __fadd2_rn(make_float2(ex2_approx_ftz(t.x), ex2_approx_ftz(t.y)), f2(1.0f));
-        const float2 s = make_float2(rcp_approx_ftz(e.x), rcp_approx_ftz(e.y));
-        y = __fmul2_rn(a, s);
-        if (D) d = __fmul2_rn(s, __ffma2_rn(a, __fadd2_rn(f2(1.0f), make_float2(-s.x, -s.y)), f2(1.0f)));
+    if (SILU) {  // constants in scalar instructions, which hold them (a packed one wants them in registers)
+        const float2 e = make_float2(ex2_approx_ftz(a.x * -1.4426950409f), ex2_approx_ftz(a.y * -1.4426950409f));
+        const float2 s = make_float2(rcp_approx_ftz(e.x + 1.0f), rcp_approx_ftz(e.y + 1.0f));
+        y = make_float2(a.x * s.x, a.y * s.y);
+        if (D) d = make_float2(fmaf(-y.x, s.x, s.x + y.x), fmaf(-y.y, s.y, s.y + y.y));  // s (1 + a (1 - s)) = s + y - y s
     } else {
         const NormalTail2 n = normal_tail2(a, make_float2(fabsf(a.x), fabsf(a.y)));
         const float2 up = __fadd2_rn(f2(1.0f), n.ntail);
@@ -92,7 +94,7 @@ __device__ __forceinline__ void put_block(const float2 (&v)[4], bool ok, bool fi
     for (int i = 0; i < 4; i++) y[i] = __fmul2_rn(v[i], f2(sc.x));
     if (ok)
         *reinterpret_cast<uint2 *>(q) =
-            make_uint2(pack4<FMT>(y[0].x, y[0].y, y[1].x, y[1].y), pack4<FMT>(y[2].x, y[2].y, y[3].x, y[3].y));
+            make_uint2(codes4<FMT>(y[0].x, y[0].y, y[1].x, y[1].y), codes4<FMT>(y[2].x, y[2].y, y[3].x, y[3].y));
     if (first) *s = sc.y;
 }
 
@@ -175,68 +177,97 @@ struct Matrix {            // shared memory of one of a tile's matrices
 typedef float2 Values[4][4];  // rows, pairs of columns
 }
 
-struct Where {  // a thread's place in its tile
-    int64_t r0, c0;  // the tile's first row, the thread's first column
-    int nrows;       // of the tile
-    int rr, cc;
-    bool col_ok;
-};
+// The largest of |a|, |b| and |c| (NaN does not count): one instruction.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float m;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
 
-// Codes of a tile's matrix along the rows; q, s: of the tensor, ld columns, `rows` factors in a row of s.
-template <int FMT>
-__device__ __forceinline__ void tile_rows(const bt::Values &v, const Where &w, uint8_t *q, float *s, int64_t ld, int64_t rows) {
-    float m[4];
+// Largest magnitude of a thread's row i and column pair p (x, y), over the finite ones where an infinity shows up.
+__device__ __forceinline__ float row_top(const bt::Values &v, int i) {
+    return max3(max3(max3(v[i][0].x, v[i][0].y, v[i][1].x), v[i][1].y, v[i][2].x), max3(v[i][2].y, v[i][3].x, v[i][3].y), 0.0f);
+}
+__device__ __forceinline__ float row_top_finite(const bt::Values &v, int i) {
+    float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        m[i] = 0.0f;
+    for (int p = 0; p < 4; p++) m = fmaxf(m, fmaxf(finite_abs(v[i][p].x), finite_abs(v[i][p].y)));
+    return m;
+}
+
+// Codes of N (one or two) matrices of a tile along the rows.  q: the thread's first value's code, rows ld
+// apart; s: the factor of the thread's first row; the thread has `rows` (0 to 4) rows, and columns if `cols`.  A
+// matrix whose q is NULL is left out.
+//   One scale is worked out by each lane: of row (cc >> 2), of matrix (cc & 1) where there are two.
+template <int FMT, int N>
+__device__ __forceinline__ void tile_rows(const bt::Values *v, uint8_t *q0, uint8_t *q1, int64_t ld, float *s0, float *s1, int rows,
+                                          bool cols) {
+    const int lane = threadIdx.x & 31, cc = lane & 15;
+    float top[N];
 #pragma unroll
-        for (int p = 0; p < 4; p++) m[i] = fmaxf(m[i], fmaxf(fabsf(v[i][p].x), fabsf(v[i][p].y)));
+    for (int n = 0; n < N; n++) {
+        float m[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) m[i] = row_top(v[n], i);
+        if (max3(max3(m[0], m[1], m[2]), m[3], 0.0f) > 3.402823466e38f) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) m[i] = row_top_finite(v[n], i);
+        }
+        const bool up8 = lane & 8, up4 = lane & 4;
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const float send = up8 ? m[i] : m[i + 2], keep = up8 ? m[i + 2] : m[i];
+            m[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, 8));
+        }
+        top[n] = fmaxf(up4 ? m[1] : m[0], __shfl_xor_sync(0xffffffffu, up4 ? m[0] : m[1], 4));
     }
-    if (fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) > 3.402823466e38f) {  // an infinity: over the finite values
+    const bool odd = N == 2 && (lane & 1);
+    float mine = odd ? top[N - 1] : top[0];
+    mine = fmaxf(mine, __shfl_xor_sync(0xffffffffu, N == 2 && !odd ? top[N - 1] : top[0], 1));
+    mine = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, 2));
+    const float2 sc = block_scale<FMT>(mine);
+    float *s = odd ? s1 : s0;
+    if ((cc & 3) < N && (cc >> 2) < rows && (odd ? q1 : q0)) s[cc >> 2] = sc.y;
+#pragma unroll
+    for (int n = 0; n < N; n++) {
+        uint8_t *q = n ? q1 : q0;
+        if (!q) continue;
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            m[i] = 0.0f;
+            const float2 s2 = f2(__shfl_sync(0xffffffffu, sc.x, (lane & 16) + 4 * i + n));
+            float2 y[4];
 #pragma unroll
-            for (int p = 0; p < 4; p++) m[i] = fmaxf(m[i], fmaxf(finite_abs(v[i][p].x), finite_abs(v[i][p].y)));
+            for (int p = 0; p < 4; p++) y[p] = __fmul2_rn(v[n][i][p], s2);
+            if (cols && i < rows)
+                *reinterpret_cast<uint2 *>(q + i * ld) = make_uint2(
+                    codes4<FMT>(y[0].x, y[0].y, y[1].x, y[1].y), codes4<FMT>(y[2].x, y[2].y, y[3].x, y[3].y));
         }
-    }
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-        const bool up = lane & 8;
-        const float send = up ? m[i] : m[i + 2], keep = up ? m[i + 2] : m[i];
-        m[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, 8));
-    }
-    const bool up = lane & 4;
-    float top = fmaxf(up ? m[1] : m[0], __shfl_xor_sync(0xffffffffu, up ? m[0] : m[1], 4));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    const float2 sc = block_scale<FMT>(top);  // of row (cc >> 2) of the thread's four
-    const int row = 4 * w.rr + (w.cc >> 2);
-    if ((w.cc & 3) == 0 && row < w.nrows) s[(w.c0 >> 7) * rows + w.r0 + row] = sc.y;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const float2 s2 = f2(__shfl_sync(0xffffffffu, sc.x, (lane & 16) + 4 * i));
-        float2 y[4];
-#pragma unroll
-        for (int p = 0; p < 4; p++) y[p] = __fmul2_rn(v[i][p], s2);
-        if (w.col_ok && 4 * w.rr + i < w.nrows)
-            *reinterpret_cast<uint2 *>(q + (w.r0 + 4 * w.rr + i) * ld + w.c0) = make_uint2(
-                pack4<FMT>(y[0].x, y[0].y, y[1].x, y[1].y), pack4<FMT>(y[2].x, y[2].y, y[3].x, y[3].y));
     }
 }
 
+// Eight columns' figures, halved over the warp's two row groups and written to a row of 128 per warp.
+template <bool MAX>
+__device__ __forceinline__ void put_columns(float (&m)[8], float *to) {
+    const bool up = threadIdx.x & 16;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const float send = up ? m[j] : m[j + 4], keep = up ? m[j + 4] : m[j];
+        const float other = __shfl_xor_sync(0xffffffffu, send, 16);
+        m[j] = MAX ? fmaxf(keep, other) : keep + other;
+    }
+    *reinterpret_cast<float4 *>(to + (threadIdx.x >> 5) * bt::TILE + 8 * (threadIdx.x & 15) + (up ? 4 : 0)) =
+        make_float4(m[0], m[1], m[2], m[3]);
+}
+
 // The warp's column maxima into shared memory.
-__device__ __forceinline__ void tile_maxima(const bt::Values &v, const Where &w, bt::Matrix &sm) {
-    const int lane = threadIdx.x & 31;
-    float m[8], top = 0.0f;
+__device__ __forceinline__ void tile_maxima(const bt::Values &v, bt::Matrix &sm) {
+    float m[8];
 #pragma unroll
     for (int p = 0; p < 4; p++) {
-        m[2 * p] = fmaxf(fmaxf(fabsf(v[0][p].x), fabsf(v[1][p].x)), fmaxf(fabsf(v[2][p].x), fabsf(v[3][p].x)));
-        m[2 * p + 1] = fmaxf(fmaxf(fabsf(v[0][p].y), fabsf(v[1][p].y)), fmaxf(fabsf(v[2][p].y), fabsf(v[3][p].y)));
-        top = fmaxf(top, fmaxf(m[2 * p], m[2 * p + 1]));
+        m[2 * p] = max3(max3(v[0][p].x, v[1][p].x, v[2][p].x), v[3][p].x, 0.0f);
+        m[2 * p + 1] = max3(max3(v[0][p].y, v[1][p].y, v[2][p].y), v[3][p].y, 0.0f);
     }
-    if (top > 3.402823466e38f) {
+    if (max3(max3(m[0], m[1], m[2]), max3(m[3], m[4], m[5]), max3(m[6], m[7], 0.0f)) > 3.402823466e38f) {
 #pragma unroll
         for (int p = 0; p < 4; p++) {
             m[2 * p] = m[2 * p + 1] = 0.0f;
@@ -247,78 +278,154 @@ __device__ __forceinline__ void tile_maxima(const bt::Values &v, const Where &w,
             }
         }
     }
-    const bool up = lane & 16;
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-        const float send = up ? m[j] : m[j + 4], keep = up ? m[j + 4] : m[j];
-        m[j] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, 16));
-    }
-    *reinterpret_cast<float4 *>(&sm.part[threadIdx.x >> 5][8 * w.cc + (up ? 4 : 0)]) = make_float4(m[0], m[1], m[2], m[3]);
+    put_columns<true>(m, &sm.part[0][0]);
 }
 
 // The warp's column sums (rows in a fixed order) into shared memory, where the codes will be.
-__device__ __forceinline__ void tile_sums(const bt::Values &v, const Where &w, bt::Matrix &sm) {
-    const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void tile_sums(const bt::Values &v, bt::Matrix &sm) {
     float m[8];
 #pragma unroll
     for (int p = 0; p < 4; p++) {
         const float2 t = __fadd2_rn(__fadd2_rn(v[0][p], v[1][p]), __fadd2_rn(v[2][p], v[3][p]));
         m[2 * p] = t.x, m[2 * p + 1] = t.y;
     }
-    const bool up = lane & 16;
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-        const float send = up ? m[j] : m[j + 4], keep = up ? m[j + 4] : m[j];
-        m[j] = keep + __shfl_xor_sync(0xffffffffu, send, 16);
-    }
-    float *to = reinterpret_cast<float *>(sm.code) + (threadIdx.x >> 5) * bt::TILE + 8 * w.cc + (up ? 4 : 0);
-    *reinterpret_cast<float4 *>(to) = make_float4(m[0], m[1], m[2], m[3]);
+    put_columns<false>(m, reinterpret_cast<float *>(sm.code));
 }
 
-// Scale and factor of column c of the tile; its sum, if `sums` is not NULL.  After a barrier.
+// Scale and factor of column c of the tile.  After a barrier.
 template <int FMT>
-__device__ __forceinline__ void tile_scale(bt::Matrix &sm, int c, float *s, float *sums) {
+__device__ __forceinline__ void tile_scale(bt::Matrix &sm, int c, float *s) {
     float m = sm.part[0][c];
 #pragma unroll
-    for (int w = 1; w < bt::WARPS; w++) m = fmaxf(m, sm.part[w][c]);
+    for (int w = 1; w < bt::WARPS; w += 2) m = max3(m, sm.part[w][c], w + 1 < bt::WARPS ? sm.part[w + 1][c] : 0.0f);
     const float2 sc = block_scale<FMT>(m);
     sm.scale[c] = sc.x;
-    if (s) *s = sc.y;
-    if (sums) {
-        const float *from = reinterpret_cast<const float *>(sm.code);
-        float t = from[c];
+    *s = sc.y;
+}
+__device__ __forceinline__ float tile_sum(const bt::Matrix &sm, int c) {
+    const float *from = reinterpret_cast<const float *>(sm.code) + c;
+    float t = from[0];
 #pragma unroll
-        for (int w = 1; w < bt::WARPS; w++) t += from[w * bt::TILE + c];
-        *sums = t;
-    }
+    for (int w = 1; w < bt::WARPS; w++) t += from[w * bt::TILE];
+    return t;
 }
 
 // Transposed codes into shared memory.  After a barrier.
 template <int FMT>
-__device__ __forceinline__ void tile_stage(const bt::Values &v, const Where &w, bt::Matrix &sm) {
-    uint32_t *words = reinterpret_cast<uint32_t *>(sm.code) + (w.rr ^ (2 * w.cc));
+__device__ __forceinline__ void tile_stage(const bt::Values &v, bt::Matrix &sm) {
+    const int rr = threadIdx.x >> 4, cc = threadIdx.x & 15;
+    uint32_t *words = reinterpret_cast<uint32_t *>(sm.code) + 256 * cc + (rr ^ (2 * cc));
+    const float4 *scale = reinterpret_cast<const float4 *>(&sm.scale[8 * cc]);
 #pragma unroll
-    for (int p = 0; p < 4; p++) {  // columns 8cc + 2p and the next
-        const float2 sc = *reinterpret_cast<const float2 *>(&sm.scale[8 * w.cc + 2 * p]);
-        float2 y[4];
+    for (int h = 0; h < 2; h++) {
+        const float4 sc = scale[h];
 #pragma unroll
-        for (int i = 0; i < 4; i++) y[i] = __fmul2_rn(v[i][p], sc);
-        words[(8 * w.cc + 2 * p) * 32] = pack4<FMT>(y[0].x, y[1].x, y[2].x, y[3].x);
-        words[(8 * w.cc + 2 * p + 1) * 32] = pack4<FMT>(y[0].y, y[1].y, y[2].y, y[3].y);
+        for (int g = 0; g < 2; g++) {  // columns 8cc + 2p and the next
+            const int p = 2 * h + g;
+            float2 y[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) y[i] = __fmul2_rn(v[i][p], g ? make_float2(sc.z, sc.w) : make_float2(sc.x, sc.y));
+            words[2 * p * 32] = codes4<FMT>(y[0].x, y[1].x, y[2].x, y[3].x);
+            words[(2 * p + 1) * 32] = codes4<FMT>(y[0].y, y[1].y, y[2].y, y[3].y);
+        }
+    }
+}
+// Rows that are not there: zero codes.
+__device__ __forceinline__ void tile_stage_zero(bt::Matrix &sm) {
+    const int rr = threadIdx.x >> 4, cc = threadIdx.x & 15;
+    uint32_t *words = reinterpret_cast<uint32_t *>(sm.code) + 256 * cc + (rr ^ (2 * cc));
+#pragma unroll
+    for (int c = 0; c < 8; c++) words[c * 32] = 0u;
+}
+
+// The staged codes to their columns.  q: of column (tid >> 3) of the tile, 16-byte chunk (tid & 7); far: 64 columns
+// on; `cols` of the tile's columns exist.  After a barrier.
+__device__ __forceinline__ void tile_out(const bt::Matrix &sm, uint8_t *q, int64_t far, int cols) {
+    const int c0 = threadIdx.x >> 3, ch = threadIdx.x & 7;
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+        const int c = c0 + 64 * k, g = c >> 3;
+        uint4 u = *reinterpret_cast<const uint4 *>(sm.code + c * bt::TILE + ((ch ^ (g >> 1)) << 4));
+        if (g & 1) u = make_uint4(u.z, u.w, u.x, u.y);
+        if (c < cols) *reinterpret_cast<uint4 *>(q + k * far) = u;
     }
 }
 
-// The staged codes to their columns: q at the tile's first column, ld its row length, `cols` of the
-// tile's columns exist.  After a barrier.
-__device__ __forceinline__ void tile_out(const bt::Matrix &sm, uint8_t *q, int64_t ld, int cols) {
-    const int ch = threadIdx.x & 7;
-#pragma unroll
-    for (int k = 0; k < 2; k++) {
-        const int c = (threadIdx.x >> 3) + 64 * k, g = c >> 3;
-        uint4 u = *reinterpret_cast<const uint4 *>(sm.code + c * bt::TILE + ((ch ^ (g >> 1)) << 4));
-        if (g & 1) u = make_uint4(u.z, u.w, u.x, u.y);
-        if (c < cols) *reinterpret_cast<uint4 *>(q + c * ld + 16 * ch) = u;
+// cp.async of N bytes; none and zeros where !ok.
+template <int N>
+__device__ __forceinline__ void copy_async(void *smem, const void *global, bool ok) {
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(smem)), n = ok ? N : 0;
+    if (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(global), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(global), "n"(N), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Eight codes -> fp16 pairs (FP8 is exact in fp16).  volatile: a branch, not both conversions and a select.
+__device__ __forceinline__ void decode8(uint2 u, bool e4m3, uint32_t (&h)[4]) {
+    if (e4m3) {
+        asm volatile("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;}"
+                     : "=r"(h[0]), "=r"(h[1]) : "r"(u.x));
+        asm volatile("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;}"
+                     : "=r"(h[2]), "=r"(h[3]) : "r"(u.y));
+    } else {  // E5M2 is the upper byte of an fp16
+        h[0] = __byte_perm(u.x, 0, 0x1404), h[1] = __byte_perm(u.x, 0, 0x3424);
+        h[2] = __byte_perm(u.y, 0, 0x1404), h[3] = __byte_perm(u.y, 0, 0x3424);
     }
+}
+__device__ __forceinline__ float2 half_pair(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2 *>(&h)); }
+
+// The thread's index, read again: what is derived from it is worked out where it is used and not kept in registers
+// across a tile, which the values fill.
+__device__ __forceinline__ int thread_again() {
+    int t;
+    asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
+    return t;
+}
+
+// A persistent CTA's walk over tiles, `across` of a tile row side by side, CTAs one tile apart.  One thread walks,
+// two tiles ahead of the work, and leaves what it finds in shared memory, where every phase reads what it
+// needs: the values fill the registers.
+struct Step {
+    int64_t r0;          // the tile's first row
+    uint32_t tile, col;  // the tile row of the padded order, the tile in it
+    int n;               // rows; 0 behind the last tile
+};
+struct Walk {
+    Step step[3];
+    uint32_t down;
+    int group;
+};
+__device__ __forceinline__ void walk_place(Walk &w, const GroupTable &table, bool grouped, int64_t rows, uint32_t tile, uint32_t col,
+                                           int at) {
+    Step s = {0, tile, col, 0};
+    if (tile < w.down) {
+        if (grouped) {
+            int g = w.group;
+            find_group(table, tile, g, s.r0, s.n);
+            w.group = g;
+        } else {
+            s.r0 = (int64_t)tile * bt::TILE;
+            s.n = (int)min((int64_t)bt::TILE, rows - s.r0);
+        }
+    }
+    w.step[at] = s;
+}
+__device__ __forceinline__ void walk_on(Walk &w, const GroupTable &table, bool grouped, int64_t rows, uint32_t across, int from, int to) {
+    const uint32_t t = gridDim.x / across;
+    uint32_t tile = w.step[from].tile + t, col = w.step[from].col + gridDim.x - t * across;
+    if (col >= across) col -= across, tile++;
+    if (w.step[from].n) walk_place(w, table, grouped, rows, tile, col, to);
+    else w.step[to].n = 0;
+}
+// The first two steps.  The caller's next barrier shows them.
+__device__ __forceinline__ void walk_start(Walk &w, const GroupTable &table, bool grouped, int n_groups, int64_t rows, uint32_t tiles,
+                                           uint32_t across) {
+    w.down = grouped ? min(tiles, table.before[n_groups]) : tiles;
+    w.group = 0;
+    walk_place(w, table, grouped, rows, blockIdx.x / across, blockIdx.x % across, 0);
+    walk_on(w, table, grouped, rows, across, 0, 1);
 }
 
 struct BlockDactArgs {
@@ -337,214 +444,246 @@ struct BlockDactArgs {
     int bf16, h_e4;         // dg's type; the checkpoint's format (and g's): E4M3, else E5M2
 };
 
-// cp.async of N bytes, zeros where !ok (nothing is read then).
-template <int N>
-__device__ __forceinline__ void copy_async(void *smem, const void *global, bool ok) {
-    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(smem)), n = ok ? N : 0;
-    if (N == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(global), "r"(n) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(global), "n"(N), "r"(n) : "memory");
-}
-__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
-// Eight codes -> fp16 pairs.  (volatile: a branch, not both conversions and a select.)
-__device__ __forceinline__ void decode8(uint2 u, bool e4m3, uint32_t (&h)[4]) {
-    if (e4m3) {
-        asm volatile("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;}"
-                     : "=r"(h[0]), "=r"(h[1]) : "r"(u.x));
-        asm volatile("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;}"
-                     : "=r"(h[2]), "=r"(h[3]) : "r"(u.y));
-    } else {  // E5M2 is the upper byte of an fp16
-        h[0] = __byte_perm(u.x, 0, 0x1404), h[1] = __byte_perm(u.x, 0, 0x3424);
-        h[2] = __byte_perm(u.y, 0, 0x1404), h[3] = __byte_perm(u.y, 0, 0x3424);
-    }
-}
-
 // dh (and g) of two elements: every caller rounds in this order, so that the same element has the same
 // bits whichever kernel computes it.
 template <bool GATED, bool SILU>
 __device__ __forceinline__ void gradient2(uint32_t ha, float fa, uint32_t hu, float fu, float2 dg, float2 &da, float2 &du,
                                           float2 &g) {
+    const float2 p = half_pair(ha), q = half_pair(hu);
     float2 y, d;
-    activation2<SILU, true>(__fmul2_rn(__half22float2(*reinterpret_cast<const __half2 *>(&ha)), f2(fa)), y, d);
+    activation2<SILU, true>(make_float2(__fmul_rn(p.x, fa), __fmul_rn(p.y, fa)), y, d);
     if (GATED) {
-        const float2 u = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2 *>(&hu)), f2(fu));
-        g = __fmul2_rn(y, u);
-        da = __fmul2_rn(__fmul2_rn(dg, u), d);
-        du = __fmul2_rn(dg, y);
+        const float2 u = make_float2(__fmul_rn(q.x, fu), __fmul_rn(q.y, fu));
+        g = make_float2(__fmul_rn(y.x, u.x), __fmul_rn(y.y, u.y));
+        da = make_float2(__fmul_rn(__fmul_rn(dg.x, u.x), d.x), __fmul_rn(__fmul_rn(dg.y, u.y), d.y));
+        du = make_float2(__fmul_rn(dg.x, y.x), __fmul_rn(dg.y, y.y));
     } else {
         g = y;
-        da = __fmul2_rn(dg, d);
+        da = make_float2(__fmul_rn(dg.x, d.x), __fmul_rn(dg.y, d.y));
     }
 }
 
+// 32 x 32 -> 64 bits in one instruction: every extent fits 32 bits, no tensor's size does.
+__device__ __forceinline__ uint64_t wide_mul(uint32_t a, uint32_t b) { return (uint64_t)a * b; }
+
+
+// Codes of N (one or two) matrices along the rows: two rows of eight values a thread, 16 lanes a row.  q, s: the first
+// matrix's code and factor of the thread's first row; the second's lie q1, s1 further on, and are left out unless
+// `both`.  Each lane works out one scale: of row (lane >> 3 & 1), of matrix (lane >> 2 & 1) where there are two.
+template <int FMT, int N>
+__device__ __forceinline__ void put_rows(const float2 (&v)[N][2][4], uint8_t *q, uint32_t q1, uint32_t ld, float *s, uint64_t s1, int rows,
+                                         bool cols, bool both) {
+    const int lane = threadIdx.x & 31;
+    float m[N][2];
+#pragma unroll
+    for (int n = 0; n < N; n++)
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const float2(&w)[4] = v[n][i];
+            m[n][i] = max3(max3(max3(w[0].x, w[0].y, w[1].x), w[1].y, w[2].x), max3(w[2].y, w[3].x, w[3].y), 0.0f);
+        }
+    if (max3(max3(m[0][0], m[0][1], 0.0f), m[N - 1][0], m[N - 1][1]) > 3.402823466e38f) {  // an infinity: over the finite values
+#pragma unroll
+        for (int n = 0; n < N; n++)
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                m[n][i] = 0.0f;
+#pragma unroll
+                for (int p = 0; p < 4; p++) m[n][i] = fmaxf(m[n][i], fmaxf(finite_abs(v[n][i][p].x), finite_abs(v[n][i][p].y)));
+            }
+    }
+    const bool up8 = lane & 8, up4 = lane & 4;
+    float top[N];
+#pragma unroll
+    for (int n = 0; n < N; n++) top[n] = fmaxf(up8 ? m[n][1] : m[n][0], __shfl_xor_sync(0xffffffffu, up8 ? m[n][0] : m[n][1], 8));
+    float mine = N == 2 && up4 ? top[N - 1] : top[0];
+    mine = fmaxf(mine, __shfl_xor_sync(0xffffffffu, N == 2 && !up4 ? top[N - 1] : top[0], 4));
+    mine = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, 2));
+    mine = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, 1));
+    const float2 sc = block_scale_fast<FMT>(mine);
+    if ((lane & 3) == 0 && (lane >> 3 & 1) < rows && (up4 ? N == 2 && both : true)) s[(lane >> 3 & 1) + (up4 ? s1 : 0)] = sc.y;
+#pragma unroll
+    for (int n = 0; n < N; n++) {
+        if (n && !both) continue;
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const float k = __shfl_sync(0xffffffffu, sc.x, (lane & 16) + 8 * i + 4 * n);
+            const float2(&w)[4] = v[n][i];
+            const uint2 u = make_uint2(codes4<FMT>(w[0].x * k, w[0].y * k, w[1].x * k, w[1].y * k),
+                                       codes4<FMT>(w[2].x * k, w[2].y * k, w[3].x * k, w[3].y * k));
+            if (cols && i < rows) *reinterpret_cast<uint2 *>(q + (n ? q1 : 0) + (i ? ld : 0)) = u;
+        }
+    }
+}
+
+// Codes of a column's sixteen values (row pairs), its factor, and its sum where one is wanted; a column's eight lanes
+// are neighbours.
+template <int FMT>
+__device__ __forceinline__ uint4 put_column(const float2 (&v)[8], float &factor) {
+    float t = max3(v[0].x, v[0].y, v[1].x);
+    t = max3(t, v[1].y, v[2].x);
+#pragma unroll
+    for (int k = 2; k < 7; k++) t = max3(t, v[k].y, v[k + 1].x);
+    t = max3(t, v[7].y, 0.0f);
+    if (t > 3.402823466e38f) {  // an infinity: over the finite values
+        t = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; k++) t = fmaxf(t, fmaxf(finite_abs(v[k].x), finite_abs(v[k].y)));
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+    const float2 sc = block_scale_fast<FMT>(t);
+    factor = sc.y;
+    uint32_t u[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const float2 a = __fmul2_rn(v[2 * k], f2(sc.x)), b = __fmul2_rn(v[2 * k + 1], f2(sc.x));
+        u[k] = codes4<FMT>(a.x, a.y, b.x, b.y);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
 // The transposed codes, column sums and, where whole blocks line up with the tiles, the codes along the
-// rows: a persistent CTA per SM walks 128 x 128 tiles of g's columns.
-//   Reads    each thread copies what it will itself read of the next tile (dg and codes: 32 values of each)
-//            into its own slots in shared memory, right after it has read this tile's: a tile's loads are
-//            under way while the one before it is computed, without registers or a barrier for them.
-//            The rows' factors (a few hundred floats) are copied by the first warps.
-//   Values   of da, du and g in fp32 (96 registers) from one decoding and one activation.
-//   Work     a tile of 16384 values takes 144 KB of traffic and about 25 instructions a value: HBM and the
-//            issue slots are about even, so what counts is that neither waits.
-// 8192 x 11008 swiglu, bf16, bias gradient: see the end of the file's entry for the figures.
-template <int FMT, bool GATED, bool SILU>
-__global__ void __launch_bounds__(bt::THREADS, 1) block_dact_kernel(const BlockDactArgs a) {
-    using namespace bt;
+// rows: a persistent CTA of 1024 threads per SM walks 128 x 128 tiles of g's columns, in two phases.
+//   Rows     thread (rr, cc) of 64 x 16 computes rows 2rr, 2rr+1 and columns 8cc .. 8cc+7 of da, du and g in fp32 from
+//            one decoding and one activation, leaves all three in shared memory in fp32, and writes da's
+//            and du's codes along the rows (maxima by shuffle over the 16 lanes of a row).
+//   Columns  thread (c, k) of 128 x 8 takes column c, rows 16k .. 16k+15 of each: maxima and sums over its
+//            values, then over the 8 lanes of a column, one scale, 16 codes, one 16-byte store (8 lanes: a
+//            whole 128-byte line).  The next tile's values are loaded into registers meanwhile.
+// Shared memory holds pairs of rows, so that the column phase reads two values at once; 16-byte units are XORed by
+// unit / 8 and by row / 16: both phases hit 32 banks.
+// Bound: the issue slots.
+namespace bd {
+constexpr int THREADS = 1024, TILE = 128;
+}
+
+template <int XKIND, int FMT, bool GATED, bool SILU>
+__global__ void __launch_bounds__(bd::THREADS, 1) block_dact_kernel(const BlockDactArgs a) {
+    using namespace bd;
     constexpr int NM = GATED ? 3 : 2, NH = NM - 1;  // matrices, those of dh
-    constexpr int NF = GATED ? 3 : 1;  // factors of a row: a's block, u's, and the next where a tile of u spans two
-    extern __shared__ __align__(16) uint8_t dyn[];
-    Matrix *sm = reinterpret_cast<Matrix *>(dyn);                       // da, [du,] g
-    uint4 *in_dg = reinterpret_cast<uint4 *>(sm + NM);                  // [8][THREADS] (bf16: half of it)
-    uint2 *in_h = reinterpret_cast<uint2 *>(in_dg + 8 * THREADS);       // [4 * NH][THREADS]
-    float *fac = reinterpret_cast<float *>(in_h + 4 * NH * THREADS);    // [2][NF][TILE]
-    __shared__ GroupTable table;
-    const int tid = threadIdx.x;
+    extern __shared__ __align__(16) float2 val[];   // [NM][TILE / 2][TILE] pairs of rows
+    const GroupTable table = group_table(val + NM * TILE * TILE / 2, a.n_groups);  // only with offsets
+    __shared__ Walk walk;
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const int rr = tid >> 4, cc = tid & 15;        // rows
+    const int col = tid >> 3, chunk = tid & 7;     // columns
+    const uint32_t cols = (uint32_t)a.cols, wide = (uint32_t)a.wide, rows = (uint32_t)a.rows, ld = (uint32_t)a.col_ld;
     pdl_wait();
     pdl_trigger();
-    uint32_t down = a.tiles;
-    if (a.offsets) {
-        build_group_table(table, a.offsets, a.n_groups, a.rows);
-        down = min(down, table.before[a.n_groups]);
-    }
-    const uint32_t total = down * a.across;
-    Where w;
-    w.rr = tid >> 4, w.cc = tid & 15;
-    int64_t next_r0 = 0;
-    int next_n = 0;
-    const auto place = [&](uint32_t t) {
-        const uint32_t tile = t / a.across;
-        if (a.offsets) {
-            find_group(table, a.n_groups, tile, next_r0, next_n);
-        } else {
-            next_r0 = (int64_t)tile * TILE;
-            next_n = (int)min((int64_t)TILE, a.rows - next_r0);
-        }
-    };
-    const auto fetch_row = [&](int i, int64_t c) {  // row i of the thread's four, columns c ..
-        const bool ok = c < a.cols && 4 * w.rr + i < next_n;
-        const int64_t r = next_r0 + 4 * w.rr + i;
-        if (a.bf16) {
-            copy_async<16>(in_dg + i * THREADS + tid, static_cast<const char *>(a.dg) + (ok ? (r * a.cols + c) * 2 : 0), ok);
-        } else {
-            const char *p = static_cast<const char *>(a.dg) + (ok ? (r * a.cols + c) * 4 : 0);
-            copy_async<16>(in_dg + 2 * i * THREADS + tid, p, ok);
-            copy_async<16>(in_dg + (2 * i + 1) * THREADS + tid, p + 16, ok);
-        }
-        const uint8_t *q = a.h_q + (ok ? r * a.wide + c : 0);
-        copy_async<8>(in_h + i * THREADS + tid, q, ok);
-        if (GATED) copy_async<8>(in_h + (4 + i) * THREADS + tid, q + (ok ? a.cols : 0), ok);
-    };
-    const auto fetch_factors = [&](int slot, int64_t first) {
-        if (tid < NF * TILE) {
-            const int which = tid / TILE, row = tid % TILE;
-            const int64_t block = ((first + (which ? a.cols : 0)) >> 7) + (which == 2);
-            const bool ok = row < next_n && block * 128 < a.wide;
-            copy_async<4>(fac + slot * NF * TILE + tid, a.h_s + (ok ? block * a.rows + next_r0 + row : 0), ok);
-        }
-    };
-    uint32_t t = blockIdx.x;
-    if (t < total) {
-        place(t);
-        const int64_t first = (int64_t)(t % a.across) * TILE;
+    if (a.offsets) build_group_table(table, a.offsets, a.n_groups, a.rows);
+    if (tid == 0) walk_start(walk, table, a.offsets, a.n_groups, a.rows, a.tiles, a.across);
+    __syncthreads();
+    uint4 x[2][XKIND == FP8DL_BF16 ? 1 : 2];  // as loaded: dg, the codes of a and u, their factors
+    uint2 qa[2], qu[2];
+    float fa[2], fu[2];
+    const auto load = [&](const Step &s) {
+        const uint32_t c = s.col * TILE + 8 * cc, r = (uint32_t)s.r0 + 2 * rr;
+        const int have = c < cols ? s.n - 2 * rr : 0;
+        const char *p = static_cast<const char *>(a.dg) + (wide_mul(r, cols) + c) * (XKIND == FP8DL_BF16 ? 2 : 4);
+        const uint8_t *q = a.h_q + wide_mul(r, wide) + c;
+        const float *f = a.h_s + wide_mul(c >> 7, rows) + r, *g = a.h_s + wide_mul((c + cols) >> 7, rows) + r;
 #pragma unroll
-        for (int i = 0; i < 4; i++) fetch_row(i, first + 8 * w.cc);
-        fetch_factors(0, first);
-    }
-    for (int slot = 0; t < total; t += gridDim.x, slot ^= 1) {
-        const uint32_t tile = t / a.across;
-        const int64_t first = (int64_t)(t - tile * a.across) * TILE;
-        w.r0 = next_r0, w.nrows = next_n;
-        w.c0 = first + 8 * w.cc;
-        w.col_ok = w.c0 < a.cols;
-        const uint32_t u = t + gridDim.x;
-        const bool more = u < total;
-        const int64_t ufirst = more ? (int64_t)(u % a.across) * TILE : 0;
-        copy_wait_all();
-        __syncthreads();  // the factors have come, the last tile's codes have gone
-        if (more) {
-            place(u);
-            fetch_factors(slot ^ 1, ufirst);
-        }
-        const float *fa_of = fac + slot * NF * TILE + 4 * w.rr;
-        const float *fu_of = fa_of + (((w.c0 + a.cols) >> 7) != ((first + a.cols) >> 7) ? 2 : 1) * TILE;
-        Values v[NM];
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            float2 dg[4];
-            if (a.bf16) {
-                const uint4 x = in_dg[i * THREADS + tid];
-                dg[0] = make_float2(bf16_lo(x.x), bf16_hi(x.x)), dg[1] = make_float2(bf16_lo(x.y), bf16_hi(x.y));
-                dg[2] = make_float2(bf16_lo(x.z), bf16_hi(x.z)), dg[3] = make_float2(bf16_lo(x.w), bf16_hi(x.w));
-            } else {
-#pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    const uint4 x = in_dg[(2 * i + h) * THREADS + tid];
-                    dg[2 * h] = make_float2(__uint_as_float(x.x), __uint_as_float(x.y));
-                    dg[2 * h + 1] = make_float2(__uint_as_float(x.z), __uint_as_float(x.w));
+        for (int i = 0; i < 2; i++) {
+            x[i][0] = make_uint4(0u, 0u, 0u, 0u);
+            if (XKIND == FP8DL_F32) x[i][XKIND == FP8DL_F32] = make_uint4(0u, 0u, 0u, 0u);
+            qa[i] = qu[i] = make_uint2(0u, 0u);
+            fa[i] = fu[i] = 0.0f;
+            if (i < have) {
+                x[i][0] = ldg_stream(p);
+                if (XKIND == FP8DL_F32) x[i][XKIND == FP8DL_F32] = ldg_stream(p + 16);
+                qa[i] = __ldg(reinterpret_cast<const uint2 *>(q));
+                fa[i] = __ldg(f + i);
+                if (GATED) {
+                    qu[i] = __ldg(reinterpret_cast<const uint2 *>(q + cols));
+                    fu[i] = __ldg(g + i);
                 }
             }
-            uint32_t ha[4], hu[4];
-            decode8(in_h[i * THREADS + tid], a.h_e4, ha);
-            if (GATED) decode8(in_h[(4 + i) * THREADS + tid], a.h_e4, hu);
-            const float fa = fa_of[i], fu = GATED ? fu_of[i] : 0.0f;
-            if (more) fetch_row(i, ufirst + 8 * w.cc);
-#pragma unroll
-            for (int p = 0; p < 4; p++)
-                gradient2<GATED, SILU>(ha[p], fa, GATED ? hu[p] : 0u, fu, dg[p], v[0][i][p], v[NH - 1][i][p], v[NM - 1][i][p]);
+            p += (int64_t)cols * (XKIND == FP8DL_BF16 ? 2 : 4), q += wide;
         }
-        if (a.dh_q && first < (int64_t)a.row_first * TILE) {
-            tile_rows<FMT>(v[0], w, a.dh_q, a.dh_s, a.wide, a.rows);
-            if (GATED && a.row_jobs == 0) {  // u's blocks line up too
-                Where wu = w;
-                wu.c0 += a.cols;
-                tile_rows<FMT>(v[NH - 1], wu, a.dh_q, a.dh_s, a.wide, a.rows);
+    };
+    load(walk.step[0]);
+    for (int cur = 0; walk.step[cur].n;) {
+        const int next = cur == 2 ? 0 : cur + 1, after = next == 2 ? 0 : next + 1, n = walk.step[cur].n;
+        if (4 * warp < ((n + 15) & ~15)) {  // rows up to the last sixteen: those that are not there are zeros
+            float2 v[NH][2][4];
+            uint32_t ha[2][4], hu[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                decode8(qa[i], a.h_e4, ha[i]);
+                if (GATED) decode8(qu[i], a.h_e4, hu[i]);
             }
-        }
+            float4 *to = reinterpret_cast<float4 *>(val + rr * TILE);
 #pragma unroll
-        for (int m = 0; m < NM; m++) {
-            if (m < NH ? !a.dh_qt : !a.g_qt) continue;
-            tile_maxima(v[m], w, sm[m]);
-        }
-        if (a.ws) {
+            for (int p = 0; p < 4; p++) {
+                float2 g[2];
 #pragma unroll
-            for (int m = 0; m < NH; m++) tile_sums(v[m], w, sm[m]);
-        }
-        __syncthreads();
-        if (tid < NM * TILE) {
-            const int m = tid / TILE, c = tid % TILE;
-            if (first + c < a.cols) {
-                if (m < NH) {
-                    const int64_t at = (int64_t)tile * a.wide + first + c + (m ? a.cols : 0);
-                    tile_scale<FMT>(sm[m], c, a.dh_qt ? a.dh_st + at : nullptr, a.ws ? a.ws + at : nullptr);
-                } else if (a.g_qt) {
-                    float *to = a.g_st + (int64_t)tile * a.cols + first + c;
-                    if (a.h_e4)
-                        tile_scale<FP8DL_E4M3>(sm[m], c, to, nullptr);
-                    else
-                        tile_scale<FP8DL_E5M2>(sm[m], c, to, nullptr);
+                for (int i = 0; i < 2; i++) {
+                    float2 dg;
+                    if (XKIND == FP8DL_BF16) {
+                        const uint32_t w = p == 0 ? x[i][0].x : p == 1 ? x[i][0].y : p == 2 ? x[i][0].z : x[i][0].w;
+                        dg = make_float2(bf16_lo(w), bf16_hi(w));
+                    } else {
+                        const uint4 &w = x[i][XKIND == FP8DL_F32 ? p >> 1 : 0];
+                        dg = p & 1 ? make_float2(__uint_as_float(w.z), __uint_as_float(w.w)) : make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+                    }
+                    gradient2<GATED, SILU>(ha[i][p], fa[i], GATED ? hu[i][p] : 0u, fu[i], dg, v[0][i][p], v[NH - 1][i][p], g[i]);
                 }
+                const int unit = 4 * cc + p, at = unit ^ (unit >> 3 & 7) ^ (rr >> 3);
+#pragma unroll
+                for (int m = 0; m < NH; m++) to[m * (TILE * TILE / 4) + at] = make_float4(v[m][0][p].x, v[m][1][p].x, v[m][0][p].y, v[m][1][p].y);
+                to[NH * (TILE * TILE / 4) + at] = make_float4(g[0].x, g[1].x, g[0].y, g[1].y);
+            }
+            const Step &s = walk.step[cur];
+            if (a.dh_q && s.col < a.row_first) {
+                const uint32_t c = s.col * TILE + 8 * cc, r = (uint32_t)s.r0 + 2 * rr;
+                const bool both = GATED && a.row_jobs == 0;  // u's blocks line up too; otherwise they are the other kernel's
+                put_rows<FMT, NH>(v, a.dh_q + wide_mul(r, wide) + c, cols, wide, a.dh_s + wide_mul(s.col, rows) + r,
+                                  wide_mul(cols >> 7, rows), n - 2 * rr, c < cols, both);
             }
         }
+        if (tid == THREADS - 1) walk_on(walk, table, a.offsets, a.rows, a.across, next, after);
         __syncthreads();
-        if (a.dh_qt) {
-#pragma unroll
-            for (int m = 0; m < NH; m++) tile_stage<FMT>(v[m], w, sm[m]);
-        }
-        if (a.g_qt) {
-            if (a.h_e4)
-                tile_stage<FP8DL_E4M3>(v[NM - 1], w, sm[NM - 1]);
-            else
-                tile_stage<FP8DL_E5M2>(v[NM - 1], w, sm[NM - 1]);
-        }
-        __syncthreads();
-        const int left = (int)min((int64_t)TILE, a.cols - first);
+        load(walk.step[next]);  // zeros behind the last tile
+        const uint32_t first = walk.step[cur].col * TILE + col, tile = walk.step[cur].tile;
+        const bool has = 16 * chunk < n, there = first < cols;
+        const int unit = col >> 1;
+        const float2 *from = val + 8 * chunk * TILE + 2 * (unit ^ (unit >> 3 & 7) ^ chunk) + (col & 1);
+        const uint64_t code = wide_mul(first, ld) + tile * TILE + 16 * chunk, factor = wide_mul(tile, wide) + first;
 #pragma unroll
         for (int m = 0; m < NM; m++) {
             uint8_t *q = m < NH ? a.dh_qt : a.g_qt;
-            if (q) tile_out(sm[m], q + (first + (GATED && m == 1 ? a.cols : 0)) * a.col_ld + (int64_t)tile * TILE, a.col_ld, left);
+            const bool sum = m < NH && a.ws, right = GATED && m == 1;
+            if (!q && !sum) continue;
+            asm volatile("" ::: "memory");  // one matrix after the other: the registers hold one's values
+            float2 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; k++) v[k] = has ? from[m * (TILE * TILE / 2) + k * TILE] : f2(0.0f);
+            if (sum) {  // over the rows, in a fixed order
+                float2 t2 = v[0];
+#pragma unroll
+                for (int k = 1; k < 8; k++) t2 = __fadd2_rn(t2, v[k]);
+                float t = t2.x + t2.y;
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+                if (chunk == 0 && there) a.ws[factor + (right ? cols : 0)] = t;
+            }
+            if (!q) continue;
+            float f;
+            uint4 u;
+            if (m < NH)
+                u = put_column<FMT>(v, f);
+            else if (a.h_e4)
+                u = put_column<FP8DL_E4M3>(v, f);
+            else
+                u = put_column<FP8DL_E5M2>(v, f);
+            if (there) {
+                *reinterpret_cast<uint4 *>(q + code + (right ? wide_mul(cols, ld) : 0)) = u;
+                if (chunk == 0) (m < NH ? a.dh_st + factor : a.g_st + wide_mul(tile, cols) + first)[right ? cols : 0] = f;
+            }
         }
+        __syncthreads();
+        cur = next;
     }
 }
 
@@ -609,15 +748,13 @@ __global__ void __launch_bounds__(ba::ACT_THREADS) block_dact_rows_kernel(const 
 
 template <int FMT, bool GATED, bool SILU>
 static fp8dl_status launch_dact(const BlockDactArgs &a, bool tiles, int sms, cudaStream_t st, bool pdl) {
-    using namespace bt;
     if (tiles) {
-        constexpr int NM = GATED ? 3 : 2;
-        constexpr size_t smem = NM * sizeof(Matrix) + 8 * THREADS * 16 + 4 * (NM - 1) * THREADS * 8 + 2 * (GATED ? 3 : 1) * TILE * 4;
-        auto *kernel = block_dact_kernel<FMT, GATED, SILU>;
+        const size_t smem = (GATED ? 3 : 2) * bd::TILE * bd::TILE * sizeof(float) + group_table_bytes(a.n_groups);
+        auto *kernel = a.bf16 ? block_dact_kernel<FP8DL_BF16, FMT, GATED, SILU> : block_dact_kernel<FP8DL_F32, FMT, GATED, SILU>;
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return fail(FP8DL_ERR_CUDA, "fp8_block_dact: %s", cudaGetErrorString(e));
         const int64_t most = (int64_t)a.tiles * a.across;
-        (void)launch_kernel(kernel, dim3((unsigned)(most < sms ? most : sms)), dim3(THREADS), smem, st, 0, pdl, a);
+        (void)launch_kernel(kernel, dim3((unsigned)(most < sms ? most : sms)), dim3(bd::THREADS), smem, st, 0, pdl, a);
         note_launch();
         FP8DL_TRY(check_launch("fp8_block_dact"));
     }
@@ -630,16 +767,6 @@ static fp8dl_status launch_dact(const BlockDactArgs &a, bool tiles, int sms, cud
     return FP8DL_OK;
 }
 
-// The rows of tile `tile` of the padded order; false where there are none.
-__device__ __forceinline__ bool tile_place(const int32_t *offsets, int n_groups, int64_t rows, uint32_t tile, Where &w) {
-    w.rr = threadIdx.x >> 4;
-    w.cc = threadIdx.x & 15;
-    w.r0 = (int64_t)tile * bt::TILE;
-    w.nrows = (int)min((int64_t)bt::TILE, rows - w.r0);
-    if (offsets) group_of_block(offsets, n_groups, rows, tile, w.r0, w.nrows);
-    return w.nrows > 0;
-}
-
 struct BlockRecodeArgs {
     const uint8_t *q;
     const float *s;
@@ -649,51 +776,93 @@ struct BlockRecodeArgs {
     uint8_t *col_q;
     float *col_s;
     int64_t col_ld;
-    uint32_t jobs;
+    uint32_t tiles, across;
     int e4;
 };
 
+// Row-wise codes to transposed ones: the walk and the tiles of block_dact_kernel with one matrix, two CTAs per SM.  The
+// rows' indices are read a tile ahead of the loads that they point to.
 template <int FMT>
-__global__ void __launch_bounds__(bt::THREADS) block_recode_kernel(const BlockRecodeArgs a) {
+__global__ void __launch_bounds__(bt::THREADS, 2) block_recode_kernel(const BlockRecodeArgs a) {
     using namespace bt;
     __shared__ __align__(16) Matrix sm;
+    __shared__ __align__(16) uint2 in_q[4][THREADS];
+    __shared__ float fac[2][TILE];
+    extern __shared__ __align__(16) uint8_t dyn[];
+    const GroupTable table = group_table(dyn, a.n_groups);  // only with offsets
+    __shared__ Walk walk;
+    const int tid = threadIdx.x, rr = tid >> 4, cc = tid & 15;
     pdl_wait();
     pdl_trigger();
-    const uint32_t tile = blockIdx.x / a.jobs;
-    Where w;
-    if (!tile_place(a.offsets, a.n_groups, a.rows, tile, w)) return;
-    const int64_t first = (int64_t)(blockIdx.x % a.jobs) * TILE;
-    w.c0 = first + 8 * w.cc;
-    w.col_ok = w.c0 < a.cols;
-    Values v;
-    uint2 u[4];
-    float f[4];
+    if (a.offsets) build_group_table(table, a.offsets, a.n_groups, a.rows);
+    if (tid == 0) walk_start(walk, table, a.offsets, a.n_groups, a.rows, a.tiles, a.across);
+    __syncthreads();
+    int32_t src[4];  // source rows of the thread's four of the tile whose loads come next, -1: zeros
+    const auto look = [&](const Step &s) {
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        u[i] = make_uint2(0u, 0u);
-        f[i] = 0.0f;
-        if (w.col_ok && 4 * w.rr + i < w.nrows) {
-            int64_t r = w.r0 + 4 * w.rr + i;
-            if (a.index) r = a.index[r];
-            if (r >= 0 && r < a.src_rows) {
-                u[i] = *reinterpret_cast<const uint2 *>(a.q + r * a.cols + w.c0);
-                f[i] = a.s[(w.c0 >> 7) * a.src_rows + r];
-            }
+        for (int i = 0; i < 4; i++) {
+            const int64_t r = s.r0 + 4 * rr + i;
+            src[i] = -1;
+            if (4 * rr + i < s.n) src[i] = a.index ? a.index[r] : (int32_t)r;
         }
-    }
+    };
+    const auto fetch = [&](const Step &s, int slot) {
+        const int64_t c = (int64_t)s.col * TILE + 8 * cc;
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        v[i][0] = __fmul2_rn(decode2(u[i].x, a.e4), f2(f[i])), v[i][1] = __fmul2_rn(decode2(u[i].x >> 16, a.e4), f2(f[i]));
-        v[i][2] = __fmul2_rn(decode2(u[i].y, a.e4), f2(f[i])), v[i][3] = __fmul2_rn(decode2(u[i].y >> 16, a.e4), f2(f[i]));
+        for (int i = 0; i < 4; i++) {
+            const bool row = src[i] >= 0 && src[i] < a.src_rows, ok = row && c < a.cols;
+            copy_async<8>(&in_q[i][tid], a.q + (ok ? src[i] * a.cols + c : 0), ok);
+            if (cc == i) copy_async<4>(&fac[slot][4 * rr + i], a.s + (row ? s.col * a.src_rows + src[i] : 0), row);
+        }
+    };
+    look(walk.step[0]);
+    fetch(walk.step[0], 0);
+    look(walk.step[1]);
+    for (int slot = 0, cur = 0; walk.step[cur].n; slot ^= 1) {
+        const int next = cur == 2 ? 0 : cur + 1, after = next == 2 ? 0 : next + 1;
+        copy_wait_all();
+        __syncthreads();  // the codes and factors have come, the last tile's codes have gone
+        const bool busy = (tid >> 5) * 8 < walk.step[cur].n;
+        uint2 u[4];
+        float f[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) u[i] = in_q[i][tid], f[i] = fac[slot][4 * rr + i];
+        if (walk.step[next].n) fetch(walk.step[next], slot ^ 1);
+        Values v;
+        if (busy) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                uint32_t h[4];
+                decode8(u[i], a.e4, h);
+#pragma unroll
+                for (int p = 0; p < 4; p++) v[i][p] = __fmul2_rn(half_pair(h[p]), f2(f[i]));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+#pragma unroll
+                for (int p = 0; p < 4; p++) v[i][p] = f2(0.0f);
+        }
+        tile_maxima(v, sm);
+        __syncthreads();
+        if (tid < TILE) {
+            const int64_t c = (int64_t)walk.step[cur].col * TILE + tid;
+            if (c < a.cols) tile_scale<FMT>(sm, tid, a.col_s + (int64_t)walk.step[cur].tile * a.cols + c);
+        } else if (tid == TILE) {
+            walk_on(walk, table, a.offsets, a.rows, a.across, next, after);
+        }
+        __syncthreads();
+        look(walk.step[after]);  // under way until the next tile's loads are made
+        if (busy)
+            tile_stage<FMT>(v, sm);
+        else
+            tile_stage_zero(sm);
+        __syncthreads();
+        const int64_t first = (int64_t)walk.step[cur].col * TILE;
+        tile_out(sm, a.col_q + (first + (tid >> 3)) * a.col_ld + (int64_t)walk.step[cur].tile * TILE + 16 * (tid & 7), 64 * a.col_ld,
+                 (int)min((int64_t)TILE, a.cols - first));
+        cur = next;
     }
-    tile_maxima(v, w, sm);
-    __syncthreads();
-    if (threadIdx.x < TILE && first + threadIdx.x < a.cols)
-        tile_scale<FMT>(sm, threadIdx.x, a.col_s + (int64_t)tile * a.cols + first + threadIdx.x, nullptr);
-    __syncthreads();
-    tile_stage<FMT>(v, w, sm);
-    __syncthreads();
-    tile_out(sm, a.col_q + first * a.col_ld + (int64_t)tile * TILE, a.col_ld, (int)min((int64_t)TILE, a.cols - first));
 }
 
 static fp8dl_status check_tiles(int64_t tiles, int64_t rows, int64_t cols) {
@@ -854,15 +1023,23 @@ extern "C" fp8dl_status fp8_block_recode(const uint8_t *q, int32_t q_fp8, const 
     a.n_groups = n_groups;
     a.col_q = col_q, a.col_s = col_s;
     a.col_ld = fp8_block_padded_rows(rows, n_groups);
-    a.jobs = (uint32_t)((cols + 127) / 128);
+    a.tiles = (uint32_t)(a.col_ld / 128);
+    a.across = (uint32_t)((cols + 127) / 128);
     a.e4 = q_fp8 == FP8DL_E4M3;
-    const int64_t ctas = a.col_ld / 128 * a.jobs;
-    FP8DL_TRY(check_tiles(ctas, rows, cols));
-    FP8DL_TRY(current_device(nullptr, nullptr));
+    const int64_t most = a.col_ld / 128 * a.across;
+    FP8DL_TRY(check_tiles(most, rows, cols));
+    int sms = 0;
+    FP8DL_TRY(current_device(nullptr, &sms));
     if (rows == 0) return FP8DL_OK;
     const bool pdl = short_call_bytes(2.0 * (double)rows * (double)cols);
-    (void)launch_kernel(out_dtype == FP8DL_E4M3 ? block_recode_kernel<FP8DL_E4M3> : block_recode_kernel<FP8DL_E5M2>,
-                        dim3((unsigned)ctas), dim3(bt::THREADS), 0, (cudaStream_t)stream, 0, pdl, a);
+    auto *kernel = out_dtype == FP8DL_E4M3 ? block_recode_kernel<FP8DL_E4M3> : block_recode_kernel<FP8DL_E5M2>;
+    if (offsets) {  // past 48 KB with the groups' table
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)group_table_bytes(n_groups));
+        if (e != cudaSuccess) return fail(FP8DL_ERR_CUDA, "fp8_block_recode: %s", cudaGetErrorString(e));
+    }
+    (void)launch_kernel(kernel,
+                        dim3((unsigned)(most < 2 * sms ? most : 2 * sms)), dim3(bt::THREADS), group_table_bytes(n_groups),
+                        (cudaStream_t)stream, 0, pdl, a);
     note_launch();
     return check_launch("fp8_block_recode");
 }
