@@ -577,32 +577,29 @@ __global__ void __launch_bounds__(bd::THREADS, 1) block_dact_kernel(const BlockD
     uint4 x[2][XKIND == FP8DL_BF16 ? 1 : 2];  // as loaded: dg, the codes of a and u, their factors
     uint2 qa[2], qu[2];
     float fa[2], fu[2];
-    const auto load = [&](const Step &s) {
-        const uint32_t c = s.col * TILE + 8 * cc, r = (uint32_t)s.r0 + 2 * rr;
+    const auto load = [&](const Step &s, int i) {  // row i of the thread's two
+        const uint32_t c = s.col * TILE + 8 * cc, r = (uint32_t)s.r0 + 2 * rr + i;
         const int have = c < cols ? s.n - 2 * rr : 0;
         const char *p = static_cast<const char *>(a.dg) + (wide_mul(r, cols) + c) * (XKIND == FP8DL_BF16 ? 2 : 4);
         const uint8_t *q = a.h_q + wide_mul(r, wide) + c;
         const float *f = a.h_s + wide_mul(c >> 7, rows) + r, *g = a.h_s + wide_mul((c + cols) >> 7, rows) + r;
-#pragma unroll
-        for (int i = 0; i < 2; i++) {
-            x[i][0] = make_uint4(0u, 0u, 0u, 0u);
-            if (XKIND == FP8DL_F32) x[i][XKIND == FP8DL_F32] = make_uint4(0u, 0u, 0u, 0u);
-            qa[i] = qu[i] = make_uint2(0u, 0u);
-            fa[i] = fu[i] = 0.0f;
-            if (i < have) {
-                x[i][0] = ldg_stream(p);
-                if (XKIND == FP8DL_F32) x[i][XKIND == FP8DL_F32] = ldg_stream(p + 16);
-                qa[i] = __ldg(reinterpret_cast<const uint2 *>(q));
-                fa[i] = __ldg(f + i);
-                if (GATED) {
-                    qu[i] = __ldg(reinterpret_cast<const uint2 *>(q + cols));
-                    fu[i] = __ldg(g + i);
-                }
+        x[i][0] = make_uint4(0u, 0u, 0u, 0u);
+        if (XKIND == FP8DL_F32) x[i][XKIND == FP8DL_F32] = make_uint4(0u, 0u, 0u, 0u);
+        qa[i] = qu[i] = make_uint2(0u, 0u);
+        fa[i] = fu[i] = 0.0f;
+        if (i < have) {
+            x[i][0] = ldg_stream(p);
+            if (XKIND == FP8DL_F32) x[i][XKIND == FP8DL_F32] = ldg_stream(p + 16);
+            qa[i] = __ldg(reinterpret_cast<const uint2 *>(q));
+            fa[i] = __ldg(f);
+            if (GATED) {
+                qu[i] = __ldg(reinterpret_cast<const uint2 *>(q + cols));
+                fu[i] = __ldg(g);
             }
-            p += (int64_t)cols * (XKIND == FP8DL_BF16 ? 2 : 4), q += wide;
         }
     };
-    load(walk.step[0]);
+    load(walk.step[0], 0);
+    load(walk.step[0], 1);
     for (int cur = 0; walk.step[cur].n;) {
         const int next = cur == 2 ? 0 : cur + 1, after = next == 2 ? 0 : next + 1, n = walk.step[cur].n;
         if (4 * warp < ((n + 15) & ~15)) {  // rows up to the last sixteen: those that are not there are zeros
@@ -634,6 +631,7 @@ __global__ void __launch_bounds__(bd::THREADS, 1) block_dact_kernel(const BlockD
                 for (int m = 0; m < NH; m++) to[m * (TILE * TILE / 4) + at] = make_float4(v[m][0][p].x, v[m][1][p].x, v[m][0][p].y, v[m][1][p].y);
                 to[NH * (TILE * TILE / 4) + at] = make_float4(g[0].x, g[1].x, g[0].y, g[1].y);
             }
+            load(walk.step[next], 0);  // zeros behind the last tile
             const Step &s = walk.step[cur];
             if (a.dh_q && s.col < a.row_first) {
                 const uint32_t c = s.col * TILE + 8 * cc, r = (uint32_t)s.r0 + 2 * rr;
@@ -642,9 +640,9 @@ __global__ void __launch_bounds__(bd::THREADS, 1) block_dact_kernel(const BlockD
                                   wide_mul(cols >> 7, rows), n - 2 * rr, c < cols, both);
             }
         }
+        else load(walk.step[next], 0);
         if (tid == THREADS - 1) walk_on(walk, table, a.offsets, a.rows, a.across, next, after);
         __syncthreads();
-        load(walk.step[next]);  // zeros behind the last tile
         const uint32_t first = walk.step[cur].col * TILE + col, tile = walk.step[cur].tile;
         const bool has = 16 * chunk < n, there = first < cols;
         const int unit = col >> 1;
@@ -654,6 +652,7 @@ __global__ void __launch_bounds__(bd::THREADS, 1) block_dact_kernel(const BlockD
         for (int m = 0; m < NM; m++) {
             uint8_t *q = m < NH ? a.dh_qt : a.g_qt;
             const bool sum = m < NH && a.ws, right = GATED && m == 1;
+            if (m == NM - 2) load(walk.step[next], 1);
             if (!q && !sum) continue;
             asm volatile("" ::: "memory");  // one matrix after the other: the registers hold one's values
             float2 v[8];
