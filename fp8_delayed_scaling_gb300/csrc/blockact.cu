@@ -28,6 +28,16 @@ __device__ __forceinline__ uint32_t codes4(float v0, float v1, float v2, float v
     return r;
 }
 
+// The largest of |a|, |b| and |c| (NaN does not count): one instruction.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float m;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
+
+// 32 x 32 -> 64 bits in one instruction: every extent fits 32 bits, no tensor's size does.
+__device__ __forceinline__ uint64_t wide_mul(uint32_t a, uint32_t b) { return (uint64_t)a * b; }
+
 // act(a) and, with D, its derivative.
 template <bool SILU, bool D>
 __device__ __forceinline__ void activation2(float2 a, float2 &y, float2 &d) {
@@ -80,78 +90,121 @@ __device__ __forceinline__ void load8(const void *base, int64_t at, bool ok, flo
     }
 }
 
-// Codes and factor of one block held by 16 lanes, eight values each.
-template <int FMT>
-__device__ __forceinline__ void put_block(const float2 (&v)[4], bool ok, bool first, uint8_t *q, float *s) {
-    float m = 0.0f;
+// The blocks along the rows that 16 lanes hold together, eight values each: NA matrices, two rows of each.  Their maxima
+// are joined by a halving exchange (8 shuffles for six blocks instead of 24), after which each lane works out
+// one block's scale and the others fetch it.  q: a matrix's code of the thread's first value in the first row; the second
+// row lies `ld` further on.  Returns the factor of the lane's block, (lane & 15) / S of [row][matrix], S lanes each.
+template <int FMT, int NA>
+__device__ __forceinline__ float put_blocks(const float2 (&v)[2][NA][4], uint8_t *const (&q)[NA], const uint32_t (&ld)[NA], bool ok0, bool ok1) {
+    constexpr int N = 2 * NA, P = N <= 2 ? 2 : N <= 4 ? 4 : 8, S = 16 / P;
+    const int lane = threadIdx.x & 31;
+    float m[P];
 #pragma unroll
-    for (int i = 0; i < 4; i++) m = fmaxf(m, fmaxf(finite_abs(v[i].x), finite_abs(v[i].y)));
+    for (int n = 0; n < P; n++) {
+        m[n] = 0.0f;
+        if (n >= N) continue;
+        const float2(&w)[4] = v[n / NA][n % NA];
+        m[n] = max3(max3(max3(w[0].x, w[0].y, w[1].x), w[1].y, w[2].x), max3(w[2].y, w[3].x, w[3].y), 0.0f);
+    }
+    float top = m[0];
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float2 sc = block_scale<FMT>(m);
-    float2 y[4];
+    for (int n = 1; n < N; n++) top = fmaxf(top, m[n]);
+    if (top > 3.402823466e38f) {  // an infinity: over the finite values
 #pragma unroll
-    for (int i = 0; i < 4; i++) y[i] = __fmul2_rn(v[i], f2(sc.x));
-    if (ok)
-        *reinterpret_cast<uint2 *>(q) =
-            make_uint2(codes4<FMT>(y[0].x, y[0].y, y[1].x, y[1].y), codes4<FMT>(y[2].x, y[2].y, y[3].x, y[3].y));
-    if (first) *s = sc.y;
+        for (int n = 0; n < N; n++) {
+            m[n] = 0.0f;
+#pragma unroll
+            for (int p = 0; p < 4; p++)
+                m[n] = fmaxf(m[n], fmaxf(finite_abs(v[n / NA][n % NA][p].x), finite_abs(v[n / NA][n % NA][p].y)));
+        }
+    }
+    int o = 8;
+#pragma unroll
+    for (int h = P / 2; h > 0; h /= 2, o /= 2) {
+#pragma unroll
+        for (int k = 0; k < h; k++) {
+            const bool up = lane & o;
+            const float send = up ? m[k] : m[k + h], keep = up ? m[k + h] : m[k];
+            m[k] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, o));
+        }
+    }
+#pragma unroll
+    for (; o > 0; o /= 2) m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+    const float2 sc = block_scale_fast<FMT>(m[0]);
+#pragma unroll
+    for (int n = 0; n < N; n++) {
+        const float k = __shfl_sync(0xffffffffu, sc.x, (lane & 16) + n * S);
+        const float2(&w)[4] = v[n / NA][n % NA];
+        const uint2 u = make_uint2(codes4<FMT>(w[0].x * k, w[0].y * k, w[1].x * k, w[1].y * k),
+                                   codes4<FMT>(w[2].x * k, w[2].y * k, w[3].x * k, w[3].y * k));
+        if (q[n % NA] && (n < NA ? ok0 : ok1)) *reinterpret_cast<uint2 *>(q[n % NA] + (n < NA ? 0 : ld[n % NA])) = u;
+    }
+    return sc.y;
 }
 
-// A CTA takes 32 rows of one block column (of a's and of u's where g is gated).  Where u's half does not start
-// on a block (cols not a multiple of 128: `split`) h's blocks do not line up with g's: the codes of h
-// are jobs of their own behind g's.
-template <int XKIND, int FMT, bool GATED, bool SILU>
+// A CTA takes 32 rows of one block column (of a's and of u's where g is gated), two neighbouring rows for 16 lanes.
+// Where u's half does not start on a block (cols not a multiple of 128: `split`) h's blocks do not line up with
+// g's: the codes of h are jobs of their own behind g's.  KEEP: with the codes of h.
+// Bound: HBM.
+template <int XKIND, int FMT, bool GATED, bool SILU, bool KEEP>
 __global__ void __launch_bounds__(ba::ACT_THREADS) block_act_kernel(const BlockActArgs a) {
     using namespace ba;
+    constexpr int NA = KEEP ? (GATED ? 3 : 2) : 1;
     pdl_wait();
     pdl_trigger();
     const uint32_t tile = blockIdx.x / a.jobs, job = blockIdx.x % a.jobs, g_jobs = (uint32_t)((a.cols + 127) / 128);
+    const uint32_t cols = (uint32_t)a.cols, wide = (uint32_t)a.wide, rows = (uint32_t)a.rows;
     int64_t first = 0, end = a.rows;
     if (a.offsets) {  // blocks along the rows do not see the groups' borders
         group_rows(a.offsets, 0, a.rows, first, end);
         end = min(max((int64_t)a.offsets[a.n_groups], first), a.rows);
     }
-    const int64_t r0 = first + (int64_t)tile * ACT_ROWS + (threadIdx.x >> 4);
-    if (r0 - (threadIdx.x >> 4) >= end) return;
-    const bool lead = (threadIdx.x & 15) == 0;
-    const int64_t c = (int64_t)(job < g_jobs ? job : job - g_jobs) * 128 + 8 * (threadIdx.x & 15);
+    if (first + (int64_t)tile * ACT_ROWS >= end) return;
+    const uint32_t r = (uint32_t)first + tile * ACT_ROWS + 2 * (threadIdx.x >> 4);  // below 2^31 + 32
+    const bool row0 = r < (uint32_t)end, row1 = r + 1 < (uint32_t)end;
+    const uint32_t c = (job < g_jobs ? job : job - g_jobs) * 128 + 8 * (threadIdx.x & 15);
     if (job >= g_jobs) {  // h alone
-#pragma unroll
-        for (int i = 0; i < 2; i++) {
-            const int64_t r = r0 + 16 * i;
-            const bool ok = r < end && c < a.wide;
-            float2 v[4];
-            load8<XKIND>(a.h, r * a.wide + c, ok, v);
-            put_block<FMT>(v, ok, lead && r < end, a.h_q + r * a.wide + c, a.h_s + (c >> 7) * a.rows + r);
-        }
+        float2 v[2][1][4];
+        const bool there = c < wide;
+        load8<XKIND>(a.h, wide_mul(r, wide) + c, row0 && there, v[0][0]);
+        load8<XKIND>(a.h, wide_mul(r + 1, wide) + c, row1 && there, v[1][0]);
+        uint8_t *const q[1] = {a.h_q + wide_mul(r, wide) + c};
+        const uint32_t ld[1] = {wide};
+        const float f = put_blocks<FMT, 1>(v, q, ld, row0 && there, row1 && there);
+        if ((threadIdx.x & 7) == 0 && (threadIdx.x & 8 ? row1 : row0)) a.h_s[wide_mul(c >> 7, rows) + r + (threadIdx.x >> 3 & 1)] = f;
         return;
     }
-    float2 va[2][4], vu[2][4];
-    bool ok[2];
+    float2 h[2][2][4], v[2][NA][4];
+    const bool there = c < cols, ok0 = row0 && there, ok1 = row1 && there;
+    const uint64_t at = wide_mul(r, wide) + c;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-        const int64_t at = (r0 + 16 * i) * a.wide + c;
-        ok[i] = r0 + 16 * i < end && c < a.cols;
-        load8<XKIND>(a.h, at, ok[i], va[i]);
-        if (GATED) load8<XKIND>(a.h, at + a.cols, ok[i], vu[i]);
+        load8<XKIND>(a.h, at + (i ? wide : 0), i ? ok1 : ok0, h[i][0]);
+        if (GATED) load8<XKIND>(a.h, at + (i ? wide : 0) + cols, i ? ok1 : ok0, h[i][1]);
     }
-    const bool keep = a.h_q && !a.split;
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
-        const int64_t r = r0 + 16 * i, at = r * a.wide + c;
-        const bool put = lead && r < end;
-        float2 y[4], none;
+    for (int i = 0; i < 2; i++)
 #pragma unroll
-        for (int q = 0; q < 4; q++) {
-            activation2<SILU, false>(va[i][q], y[q], none);
-            if (GATED) y[q] = __fmul2_rn(y[q], vu[i][q]);
+        for (int p = 0; p < 4; p++) {
+            float2 none;
+            activation2<SILU, false>(h[i][0][p], v[i][0][p], none);
+            if (GATED) v[i][0][p] = make_float2(v[i][0][p].x * h[i][1][p].x, v[i][0][p].y * h[i][1][p].y);
+            if (NA > 1) v[i][NA > 1 ? 1 : 0][p] = h[i][0][p];
+            if (NA > 2) v[i][NA > 2 ? 2 : 0][p] = h[i][1][p];
         }
-        put_block<FMT>(y, ok[i], put, a.g_q + r * a.cols + c, a.g_s + (c >> 7) * a.rows + r);
-        if (keep) {
-            put_block<FMT>(va[i], ok[i], put, a.h_q + at, a.h_s + (c >> 7) * a.rows + r);
-            if (GATED) put_block<FMT>(vu[i], ok[i], put, a.h_q + at + a.cols, a.h_s + ((c + a.cols) >> 7) * a.rows + r);
-        }
+    uint8_t *q[NA];
+    uint32_t ld[NA];
+    q[0] = a.g_q + wide_mul(r, cols) + c, ld[0] = cols;
+    if (NA > 1) q[NA > 1 ? 1 : 0] = a.h_q + at, ld[NA > 1 ? 1 : 0] = wide;
+    if (NA > 2) q[NA > 2 ? 2 : 0] = a.h_q + at + cols, ld[NA > 2 ? 2 : 0] = wide;
+    uint8_t *const(&qc)[NA] = reinterpret_cast<uint8_t *const(&)[NA]>(q);
+    // a block's factor is written even by a lane that has none of its columns (the last block may be short)
+    const float f = put_blocks<FMT, NA>(v, qc, ld, ok0, ok1);
+    constexpr int N = 2 * NA, P = N <= 2 ? 2 : N <= 4 ? 4 : 8, S = 16 / P;
+    const int mine = (threadIdx.x & 15) / S, i = mine >= NA, n = mine - i * NA;
+    if ((threadIdx.x & (S - 1)) == 0 && mine < N && (i ? row1 : row0)) {
+        float *s = n == 0 ? a.g_s : a.h_s;
+        s[wide_mul((c + (n == 2 ? cols : 0)) >> 7, rows) + r + i] = f;
     }
 }
 
@@ -175,13 +228,6 @@ struct Matrix {            // shared memory of one of a tile's matrices
     float scale[TILE];
 };
 typedef float2 Values[4][4];  // rows, pairs of columns
-}
-
-// The largest of |a|, |b| and |c| (NaN does not count): one instruction.
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float m;
-    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
-    return m;
 }
 
 // Largest magnitude of a thread's row i and column pair p (x, y), over the finite ones where an infinity shows up.
@@ -463,9 +509,6 @@ __device__ __forceinline__ void gradient2(uint32_t ha, float fa, uint32_t hu, fl
     }
 }
 
-// 32 x 32 -> 64 bits in one instruction: every extent fits 32 bits, no tensor's size does.
-__device__ __forceinline__ uint64_t wide_mul(uint32_t a, uint32_t b) { return (uint64_t)a * b; }
-
 
 // Codes of N (one or two) matrices along the rows: two rows of eight values a thread, 16 lanes a row.  q, s: the first
 // matrix's code and factor of the thread's first row; the second's lie q1, s1 further on, and are left out unless
@@ -700,49 +743,51 @@ __global__ void __launch_bounds__(ba::ACT_THREADS) block_dact_rows_kernel(const 
         group_rows(a.offsets, 0, a.rows, first, end);
         end = min(max((int64_t)a.offsets[a.n_groups], first), a.rows);
     }
-    const int64_t r0 = first + (int64_t)tile * ACT_ROWS + (threadIdx.x >> 4);
-    if (r0 - (threadIdx.x >> 4) >= end) return;
-    const bool lead = (threadIdx.x & 15) == 0;
-    const int64_t at = (int64_t)job * 128 + 8 * (threadIdx.x & 15);  // of dh
-    const bool right = GATED && at >= a.cols;
-    const int64_t c = right ? at - a.cols : at;
-    float2 dg[2][4];
+    if (first + (int64_t)tile * ACT_ROWS >= end) return;
+    const uint32_t cols = (uint32_t)a.cols, wide = (uint32_t)a.wide, rows = (uint32_t)a.rows;
+    const uint32_t r = (uint32_t)first + tile * ACT_ROWS + 2 * (threadIdx.x >> 4);
+    const uint32_t at = job * 128 + 8 * (threadIdx.x & 15);  // of dh
+    const bool right = GATED && at >= cols;
+    const uint32_t c = right ? at - cols : at;
+    const bool row[2] = {r < (uint32_t)end, r + 1 < (uint32_t)end};
+    float2 dg[2][4], v[2][1][4];
     uint2 qa[2], qu[2];
     float fa[2], fu[2];
-    bool ok[2];
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-        const int64_t r = r0 + 16 * i;
-        ok[i] = r < end && at < a.wide;
+        const bool ok = row[i] && at < wide;
         qa[i] = qu[i] = make_uint2(0u, 0u);
         fa[i] = fu[i] = 0.0f;
         if (a.bf16)
-            load8<FP8DL_BF16>(a.dg, r * a.cols + c, ok[i], dg[i]);
+            load8<FP8DL_BF16>(a.dg, wide_mul(r + i, cols) + c, ok, dg[i]);
         else
-            load8<FP8DL_F32>(a.dg, r * a.cols + c, ok[i], dg[i]);
-        if (ok[i]) {
-            qa[i] = *reinterpret_cast<const uint2 *>(a.h_q + r * a.wide + c);
-            fa[i] = a.h_s[(c >> 7) * a.rows + r];
+            load8<FP8DL_F32>(a.dg, wide_mul(r + i, cols) + c, ok, dg[i]);
+        if (ok) {
+            const uint8_t *q = a.h_q + wide_mul(r + i, wide) + c;
+            qa[i] = __ldg(reinterpret_cast<const uint2 *>(q));
+            fa[i] = __ldg(a.h_s + wide_mul(c >> 7, rows) + r + i);
             if (GATED && !right) {
-                qu[i] = *reinterpret_cast<const uint2 *>(a.h_q + r * a.wide + c + a.cols);
-                fu[i] = a.h_s[((c + a.cols) >> 7) * a.rows + r];
+                qu[i] = __ldg(reinterpret_cast<const uint2 *>(q + cols));
+                fu[i] = __ldg(a.h_s + wide_mul((c + cols) >> 7, rows) + r + i);
             }
         }
     }
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-        const int64_t r = r0 + 16 * i;
         uint32_t ha[4], hu[4];
         decode8(qa[i], a.h_e4, ha);
         if (GATED) decode8(qu[i], a.h_e4, hu);
-        float2 v[4], du, g;
+        float2 du, g;
 #pragma unroll
         for (int p = 0; p < 4; p++) {
-            gradient2<GATED, SILU>(ha[p], fa[i], GATED ? hu[p] : 0u, fu[i], dg[i][p], v[p], du, g);
-            if (GATED && right) v[p] = du;
+            gradient2<GATED, SILU>(ha[p], fa[i], GATED ? hu[p] : 0u, fu[i], dg[i][p], v[i][0][p], du, g);
+            if (GATED && right) v[i][0][p] = du;
         }
-        put_block<FMT>(v, ok[i], lead && r < end, a.dh_q + r * a.wide + at, a.dh_s + (at >> 7) * a.rows + r);
     }
+    uint8_t *const q[1] = {a.dh_q + wide_mul(r, wide) + at};
+    const uint32_t ld[1] = {wide};
+    const float f = put_blocks<FMT, 1>(v, q, ld, row[0] && at < wide, row[1] && at < wide);
+    if ((threadIdx.x & 7) == 0 && row[threadIdx.x >> 3 & 1]) a.dh_s[wide_mul(at >> 7, rows) + r + (threadIdx.x >> 3 & 1)] = f;
 }
 
 template <int FMT, bool GATED, bool SILU>
@@ -915,15 +960,18 @@ extern "C" fp8dl_status fp8_block_act(const void *h, int32_t h_dtype, int32_t ac
     FP8DL_TRY(current_device(nullptr, nullptr));
     if (rows == 0) return FP8DL_OK;
     const bool pdl = short_call_bytes((double)rows * a.wide * ((h_dtype == FP8DL_BF16 ? 2.0 : 4.0) + (h_q ? 1.0 : 0.0)) + (double)rows * cols);
-    auto *kernel = &block_act_kernel<FP8DL_BF16, FP8DL_E4M3, false, false>;
-#define FP8DL_ACT(X, F)                                                                                      \
-    kernel = gated ? (act_silu(act) ? block_act_kernel<X, F, true, true> : block_act_kernel<X, F, true, false>) \
-                   : (act_silu(act) ? block_act_kernel<X, F, false, true> : block_act_kernel<X, F, false, false>)
+    const bool keep = h_q && !a.split;
+    auto *kernel = &block_act_kernel<FP8DL_BF16, FP8DL_E4M3, false, false, false>;
+#define FP8DL_ACT_KEEP(X, F, G, S) (keep ? block_act_kernel<X, F, G, S, true> : block_act_kernel<X, F, G, S, false>)
+#define FP8DL_ACT(X, F)                                                                                           \
+    kernel = gated ? (act_silu(act) ? FP8DL_ACT_KEEP(X, F, true, true) : FP8DL_ACT_KEEP(X, F, true, false))         \
+                   : (act_silu(act) ? FP8DL_ACT_KEEP(X, F, false, true) : FP8DL_ACT_KEEP(X, F, false, false))
     if (h_dtype == FP8DL_BF16 && out_dtype == FP8DL_E4M3) FP8DL_ACT(FP8DL_BF16, FP8DL_E4M3);
     else if (h_dtype == FP8DL_BF16) FP8DL_ACT(FP8DL_BF16, FP8DL_E5M2);
     else if (out_dtype == FP8DL_E4M3) FP8DL_ACT(FP8DL_F32, FP8DL_E4M3);
     else FP8DL_ACT(FP8DL_F32, FP8DL_E5M2);
 #undef FP8DL_ACT
+#undef FP8DL_ACT_KEEP
     (void)launch_kernel(kernel, dim3((unsigned)ctas), dim3(ba::ACT_THREADS), 0, (cudaStream_t)stream, 0, pdl, a);
     note_launch();
     return check_launch("fp8_block_act");
