@@ -210,204 +210,7 @@ __global__ void __launch_bounds__(ba::ACT_THREADS) block_act_kernel(const BlockA
 
 // ---------------------------------------------------------------------------
 // 128 x 128 tiles with blocks along the rows and along the columns (dact, recode).
-//   Threads  32 x 16, thread (rr, cc) holds rows 4rr .. 4rr+3 and columns 8cc .. 8cc+7 of each of
-//            the tile's up to three matrices, in fp32 from the first computation to the codes.
-//   Row      maxima over the 16 lanes that share a row by a halving exchange.
-//   blocks
-//   Column   maxima over 4 rows in the thread, halved over two row groups by shuffle, 16 warps
-//   blocks   through shared memory.
-//   Codes    transposed codes are packed along the rows (four from four registers), staged in
-//            shared memory word by word, XOR-swizzled by column group (32 lanes hit 32 banks both
-//            ways), and leave as whole 128-byte lines.
 // ---------------------------------------------------------------------------
-namespace bt {
-constexpr int THREADS = 512, TILE = 128, WARPS = 16;
-struct Matrix {            // shared memory of one of a tile's matrices
-    uint8_t code[TILE * TILE];
-    float part[WARPS][TILE];
-    float scale[TILE];
-};
-typedef float2 Values[4][4];  // rows, pairs of columns
-}
-
-// Largest magnitude of a thread's row i and column pair p (x, y), over the finite ones where an infinity shows up.
-__device__ __forceinline__ float row_top(const bt::Values &v, int i) {
-    return max3(max3(max3(v[i][0].x, v[i][0].y, v[i][1].x), v[i][1].y, v[i][2].x), max3(v[i][2].y, v[i][3].x, v[i][3].y), 0.0f);
-}
-__device__ __forceinline__ float row_top_finite(const bt::Values &v, int i) {
-    float m = 0.0f;
-#pragma unroll
-    for (int p = 0; p < 4; p++) m = fmaxf(m, fmaxf(finite_abs(v[i][p].x), finite_abs(v[i][p].y)));
-    return m;
-}
-
-// Codes of N (one or two) matrices of a tile along the rows.  q: the thread's first value's code, rows ld
-// apart; s: the factor of the thread's first row; the thread has `rows` (0 to 4) rows, and columns if `cols`.  A
-// matrix whose q is NULL is left out.
-//   One scale is worked out by each lane: of row (cc >> 2), of matrix (cc & 1) where there are two.
-template <int FMT, int N>
-__device__ __forceinline__ void tile_rows(const bt::Values *v, uint8_t *q0, uint8_t *q1, int64_t ld, float *s0, float *s1, int rows,
-                                          bool cols) {
-    const int lane = threadIdx.x & 31, cc = lane & 15;
-    float top[N];
-#pragma unroll
-    for (int n = 0; n < N; n++) {
-        float m[4];
-#pragma unroll
-        for (int i = 0; i < 4; i++) m[i] = row_top(v[n], i);
-        if (max3(max3(m[0], m[1], m[2]), m[3], 0.0f) > 3.402823466e38f) {
-#pragma unroll
-            for (int i = 0; i < 4; i++) m[i] = row_top_finite(v[n], i);
-        }
-        const bool up8 = lane & 8, up4 = lane & 4;
-#pragma unroll
-        for (int i = 0; i < 2; i++) {
-            const float send = up8 ? m[i] : m[i + 2], keep = up8 ? m[i + 2] : m[i];
-            m[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, 8));
-        }
-        top[n] = fmaxf(up4 ? m[1] : m[0], __shfl_xor_sync(0xffffffffu, up4 ? m[0] : m[1], 4));
-    }
-    const bool odd = N == 2 && (lane & 1);
-    float mine = odd ? top[N - 1] : top[0];
-    mine = fmaxf(mine, __shfl_xor_sync(0xffffffffu, N == 2 && !odd ? top[N - 1] : top[0], 1));
-    mine = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, 2));
-    const float2 sc = block_scale<FMT>(mine);
-    float *s = odd ? s1 : s0;
-    if ((cc & 3) < N && (cc >> 2) < rows && (odd ? q1 : q0)) s[cc >> 2] = sc.y;
-#pragma unroll
-    for (int n = 0; n < N; n++) {
-        uint8_t *q = n ? q1 : q0;
-        if (!q) continue;
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const float2 s2 = f2(__shfl_sync(0xffffffffu, sc.x, (lane & 16) + 4 * i + n));
-            float2 y[4];
-#pragma unroll
-            for (int p = 0; p < 4; p++) y[p] = __fmul2_rn(v[n][i][p], s2);
-            if (cols && i < rows)
-                *reinterpret_cast<uint2 *>(q + i * ld) = make_uint2(
-                    codes4<FMT>(y[0].x, y[0].y, y[1].x, y[1].y), codes4<FMT>(y[2].x, y[2].y, y[3].x, y[3].y));
-        }
-    }
-}
-
-// Eight columns' figures, halved over the warp's two row groups and written to a row of 128 per warp.
-template <bool MAX>
-__device__ __forceinline__ void put_columns(float (&m)[8], float *to) {
-    const bool up = threadIdx.x & 16;
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-        const float send = up ? m[j] : m[j + 4], keep = up ? m[j + 4] : m[j];
-        const float other = __shfl_xor_sync(0xffffffffu, send, 16);
-        m[j] = MAX ? fmaxf(keep, other) : keep + other;
-    }
-    *reinterpret_cast<float4 *>(to + (threadIdx.x >> 5) * bt::TILE + 8 * (threadIdx.x & 15) + (up ? 4 : 0)) =
-        make_float4(m[0], m[1], m[2], m[3]);
-}
-
-// The warp's column maxima into shared memory.
-__device__ __forceinline__ void tile_maxima(const bt::Values &v, bt::Matrix &sm) {
-    float m[8];
-#pragma unroll
-    for (int p = 0; p < 4; p++) {
-        m[2 * p] = max3(max3(v[0][p].x, v[1][p].x, v[2][p].x), v[3][p].x, 0.0f);
-        m[2 * p + 1] = max3(max3(v[0][p].y, v[1][p].y, v[2][p].y), v[3][p].y, 0.0f);
-    }
-    if (max3(max3(m[0], m[1], m[2]), max3(m[3], m[4], m[5]), max3(m[6], m[7], 0.0f)) > 3.402823466e38f) {
-#pragma unroll
-        for (int p = 0; p < 4; p++) {
-            m[2 * p] = m[2 * p + 1] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                m[2 * p] = fmaxf(m[2 * p], finite_abs(v[i][p].x));
-                m[2 * p + 1] = fmaxf(m[2 * p + 1], finite_abs(v[i][p].y));
-            }
-        }
-    }
-    put_columns<true>(m, &sm.part[0][0]);
-}
-
-// The warp's column sums (rows in a fixed order) into shared memory, where the codes will be.
-__device__ __forceinline__ void tile_sums(const bt::Values &v, bt::Matrix &sm) {
-    float m[8];
-#pragma unroll
-    for (int p = 0; p < 4; p++) {
-        const float2 t = __fadd2_rn(__fadd2_rn(v[0][p], v[1][p]), __fadd2_rn(v[2][p], v[3][p]));
-        m[2 * p] = t.x, m[2 * p + 1] = t.y;
-    }
-    put_columns<false>(m, reinterpret_cast<float *>(sm.code));
-}
-
-// Scale and factor of column c of the tile.  After a barrier.
-template <int FMT>
-__device__ __forceinline__ void tile_scale(bt::Matrix &sm, int c, float *s) {
-    float m = sm.part[0][c];
-#pragma unroll
-    for (int w = 1; w < bt::WARPS; w += 2) m = max3(m, sm.part[w][c], w + 1 < bt::WARPS ? sm.part[w + 1][c] : 0.0f);
-    const float2 sc = block_scale<FMT>(m);
-    sm.scale[c] = sc.x;
-    *s = sc.y;
-}
-__device__ __forceinline__ float tile_sum(const bt::Matrix &sm, int c) {
-    const float *from = reinterpret_cast<const float *>(sm.code) + c;
-    float t = from[0];
-#pragma unroll
-    for (int w = 1; w < bt::WARPS; w++) t += from[w * bt::TILE];
-    return t;
-}
-
-// Transposed codes into shared memory.  After a barrier.
-template <int FMT>
-__device__ __forceinline__ void tile_stage(const bt::Values &v, bt::Matrix &sm) {
-    const int rr = threadIdx.x >> 4, cc = threadIdx.x & 15;
-    uint32_t *words = reinterpret_cast<uint32_t *>(sm.code) + 256 * cc + (rr ^ (2 * cc));
-    const float4 *scale = reinterpret_cast<const float4 *>(&sm.scale[8 * cc]);
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-        const float4 sc = scale[h];
-#pragma unroll
-        for (int g = 0; g < 2; g++) {  // columns 8cc + 2p and the next
-            const int p = 2 * h + g;
-            float2 y[4];
-#pragma unroll
-            for (int i = 0; i < 4; i++) y[i] = __fmul2_rn(v[i][p], g ? make_float2(sc.z, sc.w) : make_float2(sc.x, sc.y));
-            words[2 * p * 32] = codes4<FMT>(y[0].x, y[1].x, y[2].x, y[3].x);
-            words[(2 * p + 1) * 32] = codes4<FMT>(y[0].y, y[1].y, y[2].y, y[3].y);
-        }
-    }
-}
-// Rows that are not there: zero codes.
-__device__ __forceinline__ void tile_stage_zero(bt::Matrix &sm) {
-    const int rr = threadIdx.x >> 4, cc = threadIdx.x & 15;
-    uint32_t *words = reinterpret_cast<uint32_t *>(sm.code) + 256 * cc + (rr ^ (2 * cc));
-#pragma unroll
-    for (int c = 0; c < 8; c++) words[c * 32] = 0u;
-}
-
-// The staged codes to their columns.  q: of column (tid >> 3) of the tile, 16-byte chunk (tid & 7); far: 64 columns
-// on; `cols` of the tile's columns exist.  After a barrier.
-__device__ __forceinline__ void tile_out(const bt::Matrix &sm, uint8_t *q, int64_t far, int cols) {
-    const int c0 = threadIdx.x >> 3, ch = threadIdx.x & 7;
-#pragma unroll
-    for (int k = 0; k < 2; k++) {
-        const int c = c0 + 64 * k, g = c >> 3;
-        uint4 u = *reinterpret_cast<const uint4 *>(sm.code + c * bt::TILE + ((ch ^ (g >> 1)) << 4));
-        if (g & 1) u = make_uint4(u.z, u.w, u.x, u.y);
-        if (c < cols) *reinterpret_cast<uint4 *>(q + k * far) = u;
-    }
-}
-
-// cp.async of N bytes; none and zeros where !ok.
-template <int N>
-__device__ __forceinline__ void copy_async(void *smem, const void *global, bool ok) {
-    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(smem)), n = ok ? N : 0;
-    if (N == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(global), "r"(n) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(global), "n"(N), "r"(n) : "memory");
-}
-__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
 // Eight codes -> fp16 pairs (FP8 is exact in fp16).  volatile: a branch, not both conversions and a select.
 __device__ __forceinline__ void decode8(uint2 u, bool e4m3, uint32_t (&h)[4]) {
     if (e4m3) {
@@ -421,14 +224,6 @@ __device__ __forceinline__ void decode8(uint2 u, bool e4m3, uint32_t (&h)[4]) {
     }
 }
 __device__ __forceinline__ float2 half_pair(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2 *>(&h)); }
-
-// The thread's index, read again: what is derived from it is worked out where it is used and not kept in registers
-// across a tile, which the values fill.
-__device__ __forceinline__ int thread_again() {
-    int t;
-    asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
-    return t;
-}
 
 // A persistent CTA's walk over tiles, `across` of a tile row side by side, CTAs one tile apart.  One thread walks,
 // two tiles ahead of the work, and leaves what it finds in shared memory, where every phase reads what it
@@ -452,8 +247,8 @@ __device__ __forceinline__ void walk_place(Walk &w, const GroupTable &table, boo
             find_group(table, tile, g, s.r0, s.n);
             w.group = g;
         } else {
-            s.r0 = (int64_t)tile * bt::TILE;
-            s.n = (int)min((int64_t)bt::TILE, rows - s.r0);
+            s.r0 = (int64_t)tile * 128;
+            s.n = (int)min((int64_t)128, rows - s.r0);
         }
     }
     w.step[at] = s;
@@ -820,92 +615,125 @@ struct BlockRecodeArgs {
     uint8_t *col_q;
     float *col_s;
     int64_t col_ld;
-    uint32_t tiles, across;
-    int e4;
+    uint32_t across;
 };
 
-// Row-wise codes to transposed ones: the walk and the tiles of block_dact_kernel with one matrix, two CTAs per SM.  The
-// rows' indices are read a tile ahead of the loads that they point to.
-template <int FMT>
-__global__ void __launch_bounds__(bt::THREADS, 2) block_recode_kernel(const BlockRecodeArgs a) {
-    using namespace bt;
-    __shared__ __align__(16) Matrix sm;
-    __shared__ __align__(16) uint2 in_q[4][THREADS];
-    __shared__ float fac[2][TILE];
-    extern __shared__ __align__(16) uint8_t dyn[];
-    const GroupTable table = group_table(dyn, a.n_groups);  // only with offsets
-    __shared__ Walk walk;
-    const int tid = threadIdx.x, rr = tid >> 4, cc = tid & 15;
+// Two codes (the lower or upper half of a word) -> their values times f.
+template <bool E4>
+__device__ __forceinline__ float2 value2(uint32_t word, bool upper, float f) {
+    uint32_t h;
+    if (E4)
+        asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;}" : "=r"(h) : "r"(upper ? word >> 16 : word));
+    else
+        h = __byte_perm(word, 0, upper ? 0x3424 : 0x1404);  // E5M2 is the upper byte of an fp16
+    return __fmul2_rn(half_pair(h), f2(f));
+}
+
+// Row-wise codes to transposed ones, one CTA a 128 x 128 tile: thread (rr, cc) of 16 x 16 holds the codes of rows 8rr ..
+// 8rr+7, columns 8cc .. 8cc+7 and decodes them twice, for the column maxima (8 rows in the thread, two row groups by
+// shuffle, eight warps through shared memory) and for the new codes: kept as fp32 they would take 64
+// registers and leave two CTAs an SM instead of four (51 us against ... at 16384 x 4096).  The codes go through shared
+// memory in 8-byte pieces XORed by column group and leave as whole 128-byte lines.
+namespace br {
+constexpr int THREADS = 256, TILE = 128;
+}
+template <int FMT, bool E4>
+__global__ void __launch_bounds__(br::THREADS, 4) block_recode_kernel(const BlockRecodeArgs a) {
+    using namespace br;
+    __shared__ __align__(16) uint8_t code[TILE * TILE];
+    __shared__ __align__(16) float part[8][TILE];
+    __shared__ __align__(16) float scale[TILE];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rr = tid >> 4, cc = tid & 15;
     pdl_wait();
     pdl_trigger();
-    if (a.offsets) build_group_table(table, a.offsets, a.n_groups, a.rows);
-    if (tid == 0) walk_start(walk, table, a.offsets, a.n_groups, a.rows, a.tiles, a.across);
-    __syncthreads();
-    int32_t src[4];  // source rows of the thread's four of the tile whose loads come next, -1: zeros
-    const auto look = [&](const Step &s) {
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int64_t r = s.r0 + 4 * rr + i;
-            src[i] = -1;
-            if (4 * rr + i < s.n) src[i] = a.index ? a.index[r] : (int32_t)r;
+    const uint32_t tile = blockIdx.x / a.across, first = (blockIdx.x - tile * a.across) * TILE, cols = (uint32_t)a.cols;
+    int64_t r0 = (int64_t)tile * TILE;
+    int n = (int)min((int64_t)TILE, a.rows - r0);
+    if (a.offsets) group_of_block(a.offsets, a.n_groups, a.rows, tile, r0, n);
+    if (n <= 0) return;  // behind the last group
+    const bool busy = 16 * warp < n;  // the warp has rows
+    uint2 u[8];
+    float f = 0.0f;  // lane i of each 16: the factor of row 8rr + i
+    if (busy) {
+        int32_t src = -1;  // its source, -1: zeros
+        if ((lane & 15) < 8 && 8 * rr + (lane & 7) < n) {
+            src = (int32_t)r0 + 8 * rr + (lane & 7);
+            if (a.index) src = __ldg(a.index + src);
+            if (src < 0 || src >= a.src_rows)
+                src = -1;
+            else
+                f = __ldg(a.s + wide_mul(first >> 7, (uint32_t)a.src_rows) + (uint32_t)src);
         }
-    };
-    const auto fetch = [&](const Step &s, int slot) {
-        const int64_t c = (int64_t)s.col * TILE + 8 * cc;
+        const uint32_t c = first + 8 * cc;
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const bool row = src[i] >= 0 && src[i] < a.src_rows, ok = row && c < a.cols;
-            copy_async<8>(&in_q[i][tid], a.q + (ok ? src[i] * a.cols + c : 0), ok);
-            if (cc == i) copy_async<4>(&fac[slot][4 * rr + i], a.s + (row ? s.col * a.src_rows + src[i] : 0), row);
+        for (int i = 0; i < 8; i++) {
+            const int32_t r = __shfl_sync(0xffffffffu, src, (lane & 16) + i);
+            u[i] = make_uint2(0u, 0u);
+            if (r >= 0 && c < cols) u[i] = __ldg(reinterpret_cast<const uint2 *>(a.q + wide_mul(r, cols) + c));
         }
-    };
-    look(walk.step[0]);
-    fetch(walk.step[0], 0);
-    look(walk.step[1]);
-    for (int slot = 0, cur = 0; walk.step[cur].n; slot ^= 1) {
-        const int next = cur == 2 ? 0 : cur + 1, after = next == 2 ? 0 : next + 1;
-        copy_wait_all();
-        __syncthreads();  // the codes and factors have come, the last tile's codes have gone
-        const bool busy = (tid >> 5) * 8 < walk.step[cur].n;
-        uint2 u[4];
-        float f[4];
+    }
+    float m[8];
 #pragma unroll
-        for (int i = 0; i < 4; i++) u[i] = in_q[i][tid], f[i] = fac[slot][4 * rr + i];
-        if (walk.step[next].n) fetch(walk.step[next], slot ^ 1);
-        Values v;
-        if (busy) {
+    for (int j = 0; j < 8; j++) m[j] = 0.0f;
+    if (busy) {
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                uint32_t h[4];
-                decode8(u[i], a.e4, h);
+        for (int i = 0; i < 8; i += 2) {
+            const float k0 = __shfl_sync(0xffffffffu, f, (lane & 16) + i), k1 = __shfl_sync(0xffffffffu, f, (lane & 16) + i + 1);
 #pragma unroll
-                for (int p = 0; p < 4; p++) v[i][p] = __fmul2_rn(half_pair(h[p]), f2(f[i]));
+            for (int p = 0; p < 4; p++) {
+                float2 x = value2<E4>(p < 2 ? u[i].x : u[i].y, p & 1, k0), y = value2<E4>(p < 2 ? u[i + 1].x : u[i + 1].y, p & 1, k1);
+                x = __ffma2_rn(x, f2(0.0f), x), y = __ffma2_rn(y, f2(0.0f), y);  // an infinity turns into NaN, which does not count
+                m[2 * p] = max3(m[2 * p], x.x, y.x), m[2 * p + 1] = max3(m[2 * p + 1], x.y, y.y);
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-#pragma unroll
-                for (int p = 0; p < 4; p++) v[i][p] = f2(0.0f);
         }
-        tile_maxima(v, sm);
-        __syncthreads();
-        if (tid < TILE) {
-            const int64_t c = (int64_t)walk.step[cur].col * TILE + tid;
-            if (c < a.cols) tile_scale<FMT>(sm, tid, a.col_s + (int64_t)walk.step[cur].tile * a.cols + c);
-        } else if (tid == TILE) {
-            walk_on(walk, table, a.offsets, a.rows, a.across, next, after);
+        const bool up = lane & 16;
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const float send = up ? m[j] : m[j + 4], keep = up ? m[j + 4] : m[j];
+            m[j] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, 16));
         }
-        __syncthreads();
-        look(walk.step[after]);  // under way until the next tile's loads are made
-        if (busy)
-            tile_stage<FMT>(v, sm);
-        else
-            tile_stage_zero(sm);
-        __syncthreads();
-        const int64_t first = (int64_t)walk.step[cur].col * TILE;
-        tile_out(sm, a.col_q + (first + (tid >> 3)) * a.col_ld + (int64_t)walk.step[cur].tile * TILE + 16 * (tid & 7), 64 * a.col_ld,
-                 (int)min((int64_t)TILE, a.cols - first));
-        cur = next;
+    }
+    *reinterpret_cast<float4 *>(&part[warp][8 * cc + (lane & 16 ? 4 : 0)]) = make_float4(m[0], m[1], m[2], m[3]);
+    __syncthreads();
+    if (tid < TILE) {
+        float t = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; w += 2) t = max3(t, part[w][tid], part[w + 1][tid]);
+        const float2 sc = block_scale_fast<FMT>(t);
+        scale[tid] = sc.x;
+        if (first + tid < cols) a.col_s[wide_mul(tile, cols) + first + tid] = sc.y;
+    }
+    __syncthreads();
+    uint8_t *at = code + 8 * cc * TILE + ((rr ^ cc) << 3);
+    if (busy) {
+        float k[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) k[i] = __shfl_sync(0xffffffffu, f, (lane & 16) + i);
+#pragma unroll
+        for (int p = 0; p < 4; p++) {  // columns 8cc + 2p and the next
+#pragma unroll
+            for (int i = 0; i < 8; i++) asm volatile("" : "+r"(u[i].x), "+r"(u[i].y)::"memory");  // decoded again, a pair at a time
+            const float2 sc = *reinterpret_cast<const float2 *>(&scale[8 * cc + 2 * p]);
+            float2 y[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) y[i] = __fmul2_rn(value2<E4>(p < 2 ? u[i].x : u[i].y, p & 1, k[i]), sc);
+            *reinterpret_cast<uint2 *>(at + 2 * p * TILE) =
+                make_uint2(codes4<FMT>(y[0].x, y[1].x, y[2].x, y[3].x), codes4<FMT>(y[4].x, y[5].x, y[6].x, y[7].x));
+            *reinterpret_cast<uint2 *>(at + (2 * p + 1) * TILE) =
+                make_uint2(codes4<FMT>(y[0].y, y[1].y, y[2].y, y[3].y), codes4<FMT>(y[4].y, y[5].y, y[6].y, y[7].y));
+        }
+    }
+    __syncthreads();
+    const int ch = tid & 7;
+    const uint32_t ld = (uint32_t)a.col_ld, left = min((uint32_t)TILE, cols - first);
+    uint8_t *to = a.col_q + wide_mul(first + (tid >> 3), ld) + tile * TILE + 16 * ch;
+#pragma unroll
+    for (int k = 0; k < 4; k++, to += wide_mul(32, ld)) {
+        const uint32_t c = (tid >> 3) + 32 * k, g = c >> 3;
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (16 * ch < n) w = *reinterpret_cast<const uint4 *>(code + c * TILE + (((2 * ch) ^ (g & 14)) << 3));
+        if (g & 1) w = make_uint4(w.z, w.w, w.x, w.y);
+        if (c < left) *reinterpret_cast<uint4 *>(to) = w;
     }
 }
 
@@ -1070,23 +898,15 @@ extern "C" fp8dl_status fp8_block_recode(const uint8_t *q, int32_t q_fp8, const 
     a.n_groups = n_groups;
     a.col_q = col_q, a.col_s = col_s;
     a.col_ld = fp8_block_padded_rows(rows, n_groups);
-    a.tiles = (uint32_t)(a.col_ld / 128);
     a.across = (uint32_t)((cols + 127) / 128);
-    a.e4 = q_fp8 == FP8DL_E4M3;
-    const int64_t most = a.col_ld / 128 * a.across;
-    FP8DL_TRY(check_tiles(most, rows, cols));
-    int sms = 0;
-    FP8DL_TRY(current_device(nullptr, &sms));
+    const int64_t ctas = a.col_ld / 128 * a.across;
+    FP8DL_TRY(check_tiles(ctas, rows, cols));
+    FP8DL_TRY(current_device(nullptr, nullptr));
     if (rows == 0) return FP8DL_OK;
-    const bool pdl = short_call_bytes(2.0 * (double)rows * (double)cols);
-    auto *kernel = out_dtype == FP8DL_E4M3 ? block_recode_kernel<FP8DL_E4M3> : block_recode_kernel<FP8DL_E5M2>;
-    if (offsets) {  // past 48 KB with the groups' table
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)group_table_bytes(n_groups));
-        if (e != cudaSuccess) return fail(FP8DL_ERR_CUDA, "fp8_block_recode: %s", cudaGetErrorString(e));
-    }
-    (void)launch_kernel(kernel,
-                        dim3((unsigned)(most < 2 * sms ? most : 2 * sms)), dim3(bt::THREADS), group_table_bytes(n_groups),
-                        (cudaStream_t)stream, 0, pdl, a);
+    const bool pdl = short_call_bytes(2.0 * (double)rows * (double)cols), e4 = q_fp8 == FP8DL_E4M3;
+    auto *kernel = out_dtype == FP8DL_E4M3 ? (e4 ? block_recode_kernel<FP8DL_E4M3, true> : block_recode_kernel<FP8DL_E4M3, false>)
+                                           : (e4 ? block_recode_kernel<FP8DL_E5M2, true> : block_recode_kernel<FP8DL_E5M2, false>);
+    (void)launch_kernel(kernel, dim3((unsigned)ctas), dim3(br::THREADS), 0, (cudaStream_t)stream, 0, pdl, a);
     note_launch();
     return check_launch("fp8_block_recode");
 }
