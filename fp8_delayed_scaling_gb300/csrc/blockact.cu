@@ -615,25 +615,42 @@ struct BlockRecodeArgs {
     uint8_t *col_q;
     float *col_s;
     int64_t col_ld;
-    uint32_t across;
+    uint32_t tiles, across;
 };
 
 // Two codes (the lower or upper half of a word) -> their values times f.
-template <bool E4>
-__device__ __forceinline__ float2 value2(uint32_t word, bool upper, float f) {
+template <bool E4, bool UPPER>
+__device__ __forceinline__ float2 value2(uint32_t word, float f) {
     uint32_t h;
-    if (E4)
-        asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;}" : "=r"(h) : "r"(upper ? word >> 16 : word));
+    if (E4 && UPPER)
+        asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, b;}" : "=r"(h) : "r"(word));
+    else if (E4)
+        asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;}" : "=r"(h) : "r"(word));
     else
-        h = __byte_perm(word, 0, upper ? 0x3424 : 0x1404);  // E5M2 is the upper byte of an fp16
-    return __fmul2_rn(half_pair(h), f2(f));
+        h = __byte_perm(word, 0, UPPER ? 0x3424 : 0x1404);  // E5M2 is the upper byte of an fp16
+    const float2 x = half_pair(h);
+    return make_float2(x.x * f, x.y * f);
+}
+// The same of pair p of eight codes.
+template <bool E4>
+__device__ __forceinline__ float2 pair_of(uint2 u, int p, float f) {
+    return p == 0 ? value2<E4, false>(u.x, f) : p == 1 ? value2<E4, true>(u.x, f) : p == 2 ? value2<E4, false>(u.y, f) : value2<E4, true>(u.y, f);
 }
 
-// Row-wise codes to transposed ones, one CTA a 128 x 128 tile: thread (rr, cc) of 16 x 16 holds the codes of rows 8rr ..
-// 8rr+7, columns 8cc .. 8cc+7 and decodes them twice, for the column maxima (8 rows in the thread, two row groups by
-// shuffle, eight warps through shared memory) and for the new codes: kept as fp32 they would take 64
-// registers and leave two CTAs an SM instead of four (51 us against ... at 16384 x 4096).  The codes go through shared
-// memory in 8-byte pieces XORed by column group and leave as whole 128-byte lines.
+// cp.async of N bytes; none and zeros where !ok.
+template <int N>
+__device__ __forceinline__ void copy_async(void *smem, const void *global, bool ok) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(smem))), "l"(global), "n"(N), "r"(ok ? N : 0) : "memory");
+}
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Row-wise codes to transposed ones: persistent CTAs, four per SM, walk 128 x 128 tiles.  Thread (rr, cc) of 16 x 16 holds
+// the codes of rows 8rr .. 8rr+7, columns 8cc .. 8cc+7 and decodes them twice, for the column maxima (8 rows in the
+// thread, two row groups by shuffle, eight warps through shared memory) and for the new codes: kept as fp32 they
+// would take 64 registers and leave two CTAs an SM.  The new codes go through shared memory in 8-byte pieces XORed by
+// column group and leave as whole 128-byte lines.  Each thread copies the next tile's codes into its own slots of
+// shared memory meanwhile (no barrier, no registers), and reads the indices of the one after it.
+// Bound: the issue slots (about 13 instructions a value).
 namespace br {
 constexpr int THREADS = 256, TILE = 128;
 }
@@ -641,48 +658,65 @@ template <int FMT, bool E4>
 __global__ void __launch_bounds__(br::THREADS, 4) block_recode_kernel(const BlockRecodeArgs a) {
     using namespace br;
     __shared__ __align__(16) uint8_t code[TILE * TILE];
+    __shared__ __align__(16) uint2 in[8][THREADS];
     __shared__ __align__(16) float part[8][TILE];
     __shared__ __align__(16) float scale[TILE];
+    __shared__ __align__(16) float fac[2][TILE];  // the rows' factors, of every other tile
+    __shared__ Walk walk;
+    extern __shared__ __align__(16) uint8_t dyn[];
+    const GroupTable table = group_table(dyn, a.n_groups);  // only with offsets
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rr = tid >> 4, cc = tid & 15;
+    const uint32_t cols = (uint32_t)a.cols, src_rows = (uint32_t)a.src_rows;
     pdl_wait();
     pdl_trigger();
-    const uint32_t tile = blockIdx.x / a.across, first = (blockIdx.x - tile * a.across) * TILE, cols = (uint32_t)a.cols;
-    int64_t r0 = (int64_t)tile * TILE;
-    int n = (int)min((int64_t)TILE, a.rows - r0);
-    if (a.offsets) group_of_block(a.offsets, a.n_groups, a.rows, tile, r0, n);
-    if (n <= 0) return;  // behind the last group
-    const bool busy = 16 * warp < n;  // the warp has rows
-    uint2 u[8];
-    float f = 0.0f;  // lane i of each 16: the factor of row 8rr + i
-    if (busy) {
-        int32_t src = -1;  // its source, -1: zeros
-        if ((lane & 15) < 8 && 8 * rr + (lane & 7) < n) {
-            src = (int32_t)r0 + 8 * rr + (lane & 7);
+    if (a.offsets) build_group_table(table, a.offsets, a.n_groups, a.rows);
+    if (tid == 0) walk_start(walk, table, a.offsets, a.n_groups, a.rows, a.tiles, a.across);
+    __syncthreads();
+    int32_t src;  // lane i of each 16: the source of row 8rr + i of the tile whose codes come next, -1: zeros
+    const auto look = [&](const Step &s) {
+        src = -1;
+        if ((lane & 15) < 8 && 8 * rr + (lane & 7) < s.n) {
+            src = (int32_t)s.r0 + 8 * rr + (lane & 7);
             if (a.index) src = __ldg(a.index + src);
-            if (src < 0 || src >= a.src_rows)
-                src = -1;
-            else
-                f = __ldg(a.s + wide_mul(first >> 7, (uint32_t)a.src_rows) + (uint32_t)src);
         }
-        const uint32_t c = first + 8 * cc;
+    };
+    const auto fetch = [&](const Step &s, int slot) {
+        if (src >= 0 && (uint32_t)src >= src_rows) src = -1;
+        if ((lane & 15) < 8)
+            copy_async<4>(&fac[slot][8 * rr + (lane & 7)], a.s + (src >= 0 ? wide_mul(s.col, src_rows) + (uint32_t)src : 0), src >= 0);
+        const uint32_t c = s.col * TILE + 8 * cc;
 #pragma unroll
         for (int i = 0; i < 8; i++) {
             const int32_t r = __shfl_sync(0xffffffffu, src, (lane & 16) + i);
-            u[i] = make_uint2(0u, 0u);
-            if (r >= 0 && c < cols) u[i] = __ldg(reinterpret_cast<const uint2 *>(a.q + wide_mul(r, cols) + c));
+            const bool ok = r >= 0 && c < cols;
+            copy_async<8>(&in[i][tid], a.q + (ok ? wide_mul(r, cols) + c : 0), ok);
         }
-    }
+    };
+    look(walk.step[0]);
+    fetch(walk.step[0], 0);
+    look(walk.step[1]);
+    for (int cur = 0, slot = 0; walk.step[cur].n; slot ^= 1) {
+    const int next = cur == 2 ? 0 : cur + 1, after = next == 2 ? 0 : next + 1, n = walk.step[cur].n;
+    const bool busy = 16 * warp < n;  // the warp has rows
+    copy_wait_all();
+    __syncwarp();  // a row's factor is another lane's copy
+    uint2 u[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) u[i] = in[i][tid];
+    if (walk.step[next].n) fetch(walk.step[next], slot ^ 1);
+    const float *f = &fac[slot][8 * rr];
     float m[8];
 #pragma unroll
     for (int j = 0; j < 8; j++) m[j] = 0.0f;
     if (busy) {
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-            const float k0 = __shfl_sync(0xffffffffu, f, (lane & 16) + i), k1 = __shfl_sync(0xffffffffu, f, (lane & 16) + i + 1);
+            const float2 k = *reinterpret_cast<const float2 *>(f + i);
 #pragma unroll
             for (int p = 0; p < 4; p++) {
-                float2 x = value2<E4>(p < 2 ? u[i].x : u[i].y, p & 1, k0), y = value2<E4>(p < 2 ? u[i + 1].x : u[i + 1].y, p & 1, k1);
-                x = __ffma2_rn(x, f2(0.0f), x), y = __ffma2_rn(y, f2(0.0f), y);  // an infinity turns into NaN, which does not count
+                float2 x = pair_of<E4>(u[i], p, k.x), y = pair_of<E4>(u[i + 1], p, k.y);
+                // an infinity turns into NaN, which does not count
+                x = __ffma2_rn(x, f2(0.0f), x), y = __ffma2_rn(y, f2(0.0f), y);
                 m[2 * p] = max3(m[2 * p], x.x, y.x), m[2 * p + 1] = max3(m[2 * p + 1], x.y, y.y);
             }
         }
@@ -701,32 +735,39 @@ __global__ void __launch_bounds__(br::THREADS, 4) block_recode_kernel(const Bloc
         for (int w = 0; w < 8; w += 2) t = max3(t, part[w][tid], part[w + 1][tid]);
         const float2 sc = block_scale_fast<FMT>(t);
         scale[tid] = sc.x;
-        if (first + tid < cols) a.col_s[wide_mul(tile, cols) + first + tid] = sc.y;
+        const uint32_t c = walk.step[cur].col * TILE + tid;
+        if (c < cols) a.col_s[wide_mul(walk.step[cur].tile, cols) + c] = sc.y;
+    } else if (tid == TILE) {
+        walk_on(walk, table, a.offsets, a.rows, a.across, next, after);
     }
     __syncthreads();
+    look(walk.step[after]);
     uint8_t *at = code + 8 * cc * TILE + ((rr ^ cc) << 3);
     if (busy) {
-        float k[8];
 #pragma unroll
-        for (int i = 0; i < 8; i++) k[i] = __shfl_sync(0xffffffffu, f, (lane & 16) + i);
-#pragma unroll
-        for (int p = 0; p < 4; p++) {  // columns 8cc + 2p and the next
-#pragma unroll
-            for (int i = 0; i < 8; i++) asm volatile("" : "+r"(u[i].x), "+r"(u[i].y)::"memory");  // decoded again, a pair at a time
+        for (int p = 0; p < 4; p++) {  // columns 8cc + 2p and the next, four rows at a time
             const float2 sc = *reinterpret_cast<const float2 *>(&scale[8 * cc + 2 * p]);
-            float2 y[8];
+            uint32_t w[2][2];
 #pragma unroll
-            for (int i = 0; i < 8; i++) y[i] = __fmul2_rn(value2<E4>(p < 2 ? u[i].x : u[i].y, p & 1, k[i]), sc);
-            *reinterpret_cast<uint2 *>(at + 2 * p * TILE) =
-                make_uint2(codes4<FMT>(y[0].x, y[1].x, y[2].x, y[3].x), codes4<FMT>(y[4].x, y[5].x, y[6].x, y[7].x));
-            *reinterpret_cast<uint2 *>(at + (2 * p + 1) * TILE) =
-                make_uint2(codes4<FMT>(y[0].y, y[1].y, y[2].y, y[3].y), codes4<FMT>(y[4].y, y[5].y, y[6].y, y[7].y));
+            for (int h = 0; h < 2; h++) {
+                const float4 k = *reinterpret_cast<const float4 *>(f + 4 * h);
+                float2 y[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    asm volatile("" : "+r"(u[4 * h + i].x), "+r"(u[4 * h + i].y)::"memory");  // decoded again, not kept
+                    const float2 x = pair_of<E4>(u[4 * h + i], p, i == 0 ? k.x : i == 1 ? k.y : i == 2 ? k.z : k.w);
+                    y[i] = make_float2(x.x * sc.x, x.y * sc.y);
+                }
+                w[0][h] = codes4<FMT>(y[0].x, y[1].x, y[2].x, y[3].x), w[1][h] = codes4<FMT>(y[0].y, y[1].y, y[2].y, y[3].y);
+            }
+            *reinterpret_cast<uint2 *>(at + 2 * p * TILE) = make_uint2(w[0][0], w[0][1]);
+            *reinterpret_cast<uint2 *>(at + (2 * p + 1) * TILE) = make_uint2(w[1][0], w[1][1]);
         }
     }
     __syncthreads();
     const int ch = tid & 7;
-    const uint32_t ld = (uint32_t)a.col_ld, left = min((uint32_t)TILE, cols - first);
-    uint8_t *to = a.col_q + wide_mul(first + (tid >> 3), ld) + tile * TILE + 16 * ch;
+    const uint32_t first = walk.step[cur].col * TILE, ld = (uint32_t)a.col_ld, left = min((uint32_t)TILE, cols - first);
+    uint8_t *to = a.col_q + wide_mul(first + (tid >> 3), ld) + walk.step[cur].tile * TILE + 16 * ch;
 #pragma unroll
     for (int k = 0; k < 4; k++, to += wide_mul(32, ld)) {
         const uint32_t c = (tid >> 3) + 32 * k, g = c >> 3;
@@ -734,6 +775,8 @@ __global__ void __launch_bounds__(br::THREADS, 4) block_recode_kernel(const Bloc
         if (16 * ch < n) w = *reinterpret_cast<const uint4 *>(code + c * TILE + (((2 * ch) ^ (g & 14)) << 3));
         if (g & 1) w = make_uint4(w.z, w.w, w.x, w.y);
         if (c < left) *reinterpret_cast<uint4 *>(to) = w;
+    }
+    cur = next;
     }
 }
 
@@ -899,14 +942,21 @@ extern "C" fp8dl_status fp8_block_recode(const uint8_t *q, int32_t q_fp8, const 
     a.col_q = col_q, a.col_s = col_s;
     a.col_ld = fp8_block_padded_rows(rows, n_groups);
     a.across = (uint32_t)((cols + 127) / 128);
-    const int64_t ctas = a.col_ld / 128 * a.across;
-    FP8DL_TRY(check_tiles(ctas, rows, cols));
-    FP8DL_TRY(current_device(nullptr, nullptr));
+    a.tiles = (uint32_t)(a.col_ld / 128);
+    const int64_t most = a.col_ld / 128 * a.across;
+    FP8DL_TRY(check_tiles(most, rows, cols));
+    int sms = 0;
+    FP8DL_TRY(current_device(nullptr, &sms));
     if (rows == 0) return FP8DL_OK;
     const bool pdl = short_call_bytes(2.0 * (double)rows * (double)cols), e4 = q_fp8 == FP8DL_E4M3;
     auto *kernel = out_dtype == FP8DL_E4M3 ? (e4 ? block_recode_kernel<FP8DL_E4M3, true> : block_recode_kernel<FP8DL_E4M3, false>)
                                            : (e4 ? block_recode_kernel<FP8DL_E5M2, true> : block_recode_kernel<FP8DL_E5M2, false>);
-    (void)launch_kernel(kernel, dim3((unsigned)ctas), dim3(br::THREADS), 0, (cudaStream_t)stream, 0, pdl, a);
+    if (offsets) {  // past 48 KB with the groups' table
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)group_table_bytes(n_groups));
+        if (e != cudaSuccess) return fail(FP8DL_ERR_CUDA, "fp8_block_recode: %s", cudaGetErrorString(e));
+    }
+    (void)launch_kernel(kernel, dim3((unsigned)(most < 4 * sms ? most : 4 * sms)), dim3(br::THREADS), group_table_bytes(n_groups),
+                        (cudaStream_t)stream, 0, pdl, a);
     note_launch();
     return check_launch("fp8_block_recode");
 }
