@@ -684,12 +684,14 @@ __global__ void __launch_bounds__(br::THREADS, 4) block_recode_kernel(const Bloc
         if (src >= 0 && (uint32_t)src >= src_rows) src = -1;
         if ((lane & 15) < 8)
             copy_async<4>(&fac[slot][8 * rr + (lane & 7)], a.s + (src >= 0 ? wide_mul(s.col, src_rows) + (uint32_t)src : 0), src >= 0);
+        // rows and columns that are not there: none is copied, and the address stays on the tensor
         const uint32_t c = s.col * TILE + 8 * cc;
+        const uint8_t *q = a.q + min(c, cols - 8);
+        const int32_t least = c < cols ? 0 : 0x7fffffff;
 #pragma unroll
         for (int i = 0; i < 8; i++) {
             const int32_t r = __shfl_sync(0xffffffffu, src, (lane & 16) + i);
-            const bool ok = r >= 0 && c < cols;
-            copy_async<8>(&in[i][tid], a.q + (ok ? wide_mul(r, cols) + c : 0), ok);
+            copy_async<8>(&in[i][tid], q + wide_mul(max(r, 0), cols), r >= least);
         }
     };
     look(walk.step[0]);
@@ -763,18 +765,22 @@ __global__ void __launch_bounds__(br::THREADS, 4) block_recode_kernel(const Bloc
             *reinterpret_cast<uint2 *>(at + 2 * p * TILE) = make_uint2(w[0][0], w[0][1]);
             *reinterpret_cast<uint2 *>(at + (2 * p + 1) * TILE) = make_uint2(w[1][0], w[1][1]);
         }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++) *reinterpret_cast<uint2 *>(at + j * TILE) = make_uint2(0u, 0u);
     }
     __syncthreads();
     const int ch = tid & 7;
     const uint32_t first = walk.step[cur].col * TILE, ld = (uint32_t)a.col_ld, left = min((uint32_t)TILE, cols - first);
     uint8_t *to = a.col_q + wide_mul(first + (tid >> 3), ld) + walk.step[cur].tile * TILE + 16 * ch;
+    const uint8_t *from = code + (tid >> 3) * TILE;
 #pragma unroll
-    for (int k = 0; k < 4; k++, to += wide_mul(32, ld)) {
+    for (int k = 0; k < 4; k++) {  // two pieces of 8 bytes, each where the XOR put it
         const uint32_t c = (tid >> 3) + 32 * k, g = c >> 3;
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (16 * ch < n) w = *reinterpret_cast<const uint4 *>(code + c * TILE + (((2 * ch) ^ (g & 14)) << 3));
-        if (g & 1) w = make_uint4(w.z, w.w, w.x, w.y);
-        if (c < left) *reinterpret_cast<uint4 *>(to) = w;
+        const uint2 x = *reinterpret_cast<const uint2 *>(from + 32 * k * TILE + (((2 * ch) ^ g) << 3));
+        const uint2 y = *reinterpret_cast<const uint2 *>(from + 32 * k * TILE + (((2 * ch + 1) ^ g) << 3));
+        if (c < left) *reinterpret_cast<uint4 *>(to) = make_uint4(x.x, x.y, y.x, y.y);
+        to += wide_mul(32, ld);
     }
     cur = next;
     }
