@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(256) block_dispatch_kernel(const DispatchArgs 
         for (int q = 0; q < 4; q++) m = fmaxf(m, fmaxf(finite_abs(v[i].pair(q).x), finite_abs(v[i].pair(q).y)));
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float2 sc = block_scale<FMT>(m);
+        const float2 sc = block_scale_fast<FMT>(m);
         inv[i] = sc.y;
         float2 y[4];
 #pragma unroll
@@ -124,87 +124,131 @@ struct CombineArgs {
     float *dweight;
 };
 
-// A thread sums eight columns of a token, four rows of y under way at once.
-template <int XKIND>
+// A warp sums 256 CH columns of a token, the CH loads of up to J rows of y under way at once.  A lane holds a choice's row
+// and weight; the others fetch them.
+template <int XKIND, int J, int CH>
 __global__ void __launch_bounds__(256) moe_combine_kernel(const CombineArgs a) {
-    constexpr int U = 4;
-    pdl_wait();
-    pdl_trigger();
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, per = a.cols / 8, t = i / per;
-    if (t >= a.tokens) return;
-    const int64_t c = (i - t * per) * 8;
-    float2 sum[4];
-#pragma unroll
-    for (int q = 0; q < 4; q++) sum[q] = f2(0.0f);
-    for (int j0 = 0; j0 < a.k; j0 += U) {
-        Eight<XKIND> v[U];
-        float w[U];
-        bool has[U];
-#pragma unroll
-        for (int j = 0; j < U; j++) {
-            const int64_t row = j0 + j < a.k ? a.position[t * a.k + j0 + j] : -1;
-            has[j] = row >= 0 && row < a.rows;
-            w[j] = !has[j] ? 0.0f : a.weight ? a.weight[t * a.k + j0 + j] : 1.0f;
-            v[j].zero();
-            if (has[j]) v[j].load(a.y, row * a.cols + c);
-        }
-#pragma unroll
-        for (int j = 0; j < U; j++)
-            if (has[j]) {
-#pragma unroll
-                for (int q = 0; q < 4; q++) sum[q] = __ffma2_rn(v[j].pair(q), f2(w[j]), sum[q]);
-            }
-    }
-    Eight<XKIND>::store(a.out, t * a.cols + c, sum);
-}
-
-// A warp walks a token's row, 256 columns a step, J choices at once (more: again, dout from L1).  The sums
-// run over a lane's columns in order, then over the lanes in a fixed tree.
-template <int XKIND, int J>
-__global__ void __launch_bounds__(256) moe_combine_bwd_kernel(const CombineArgs a) {
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const uint32_t per = (uint32_t)((a.cols + 256 * CH - 1) / (256 * CH)), warp = blockIdx.x * 8 + (threadIdx.x >> 5), t = warp / per;
     if (t >= a.tokens) return;
+    const int64_t c = (int64_t)(warp - t * per) * (256 * CH) + 8 * lane;
+    int32_t row = -1;
+    float w = 0.0f;
+    if (lane < a.k) {
+        row = a.position[(int64_t)t * a.k + lane];
+        w = a.weight ? a.weight[(int64_t)t * a.k + lane] : 1.0f;
+        if (row >= a.rows) row = -1;
+    }
+    float2 sum[CH][4];
+#pragma unroll
+    for (int h = 0; h < CH; h++)
+#pragma unroll
+        for (int q = 0; q < 4; q++) sum[h][q] = f2(0.0f);
     for (int j0 = 0; j0 < a.k; j0 += J) {
-        int64_t row[J];
-        float w[J], sum[J];
+        Eight<XKIND> v[J][CH];
 #pragma unroll
         for (int j = 0; j < J; j++) {
-            row[j] = j0 + j < a.k ? a.position[t * a.k + j0 + j] : -1;
-            if (row[j] >= a.rows) row[j] = -1;
-            w[j] = a.dy && row[j] >= 0 ? a.weight[t * a.k + j0 + j] : 0.0f;
+            const int32_t r = __shfl_sync(0xffffffffu, row, (j0 + j) & 31);
+#pragma unroll
+            for (int h = 0; h < CH; h++) {
+                v[j][h].zero();
+                if (j0 + j < a.k && r >= 0 && c + 256 * h < a.cols) v[j][h].load(a.y, r * a.cols + c + 256 * h);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < J; j++) {
+            const int32_t r = __shfl_sync(0xffffffffu, row, (j0 + j) & 31);
+            const float k = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
+            if (j0 + j >= a.k || r < 0) continue;
+#pragma unroll
+            for (int h = 0; h < CH; h++)
+#pragma unroll
+                for (int q = 0; q < 4; q++) sum[h][q] = __ffma2_rn(v[j][h].pair(q), f2(k), sum[h][q]);
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < CH; h++)
+        if (c + 256 * h < a.cols) Eight<XKIND>::store(a.out, t * a.cols + c + 256 * h, sum[h]);
+}
+
+// W warps walk a token's row, 256 columns a step each, two steps' loads of J choices under way at once (more choices: again, dout
+// from L1).  The sums run over a lane's columns in order, then over the lanes in a fixed tree, then over the warps.
+template <int XKIND, int J>
+__global__ void __launch_bounds__(256) moe_combine_bwd_kernel(const CombineArgs a, int wlog) {
+    __shared__ float part[8][J];
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = 1 << wlog, mine = warp & (W - 1);
+    const int64_t t = (int64_t)blockIdx.x * (8 >> wlog) + (warp >> wlog);
+    const bool here = t < a.tokens;
+    int32_t row = -1;
+    float w = 0.0f;
+    if (here && lane < a.k) {
+        row = a.position[t * a.k + lane];
+        if (row >= a.rows) row = -1;
+        if (a.dy && row >= 0) w = a.weight[t * a.k + lane];
+    }
+    for (int j0 = 0; j0 < a.k; j0 += J) {
+        int32_t r[J];
+        float k[J], sum[J];
+#pragma unroll
+        for (int j = 0; j < J; j++) {
+            r[j] = __shfl_sync(0xffffffffu, row, (j0 + j) & 31);
+            if (j0 + j >= a.k) r[j] = -1;
+            k[j] = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
             sum[j] = 0.0f;
         }
-        for (int64_t c = 8 * lane; c < a.cols; c += 256) {
-            Eight<XKIND> d, v[J];
-            d.load(a.dout, t * a.cols + c);
+        if (here) {
+            const auto add = [&](const Eight<XKIND> &d, const Eight<XKIND> (&v)[J], int64_t c) {
 #pragma unroll
-            for (int j = 0; j < J; j++) {
-                v[j].zero();
-                if (a.dweight && row[j] >= 0) v[j].load(a.y, row[j] * a.cols + c);
-            }
+                for (int j = 0; j < J; j++) {
+                    if (r[j] < 0) continue;
+                    float2 s[4], p = f2(0.0f);
 #pragma unroll
-            for (int j = 0; j < J; j++) {
-                if (row[j] < 0) continue;
-                float2 s[4], part = f2(0.0f);
-#pragma unroll
-                for (int q = 0; q < 4; q++) {
-                    s[q] = __fmul2_rn(d.pair(q), f2(w[j]));
-                    part = __ffma2_rn(d.pair(q), v[j].pair(q), part);
+                    for (int q = 0; q < 4; q++) {
+                        s[q] = __fmul2_rn(d.pair(q), f2(k[j]));
+                        p = __ffma2_rn(d.pair(q), v[j].pair(q), p);
+                    }
+                    if (a.dy) Eight<XKIND>::store(a.dy, r[j] * a.cols + c, s);
+                    sum[j] += p.x + p.y;
                 }
-                if (a.dy) Eight<XKIND>::store(a.dy, row[j] * a.cols + c, s);
-                sum[j] += part.x + part.y;
+            };
+            const auto load = [&](Eight<XKIND> &d, Eight<XKIND> (&v)[J], int64_t c) {
+                d.load(a.dout, t * a.cols + c);
+#pragma unroll
+                for (int j = 0; j < J; j++) {
+                    v[j].zero();
+                    if (a.dweight && r[j] >= 0) v[j].load(a.y, r[j] * a.cols + c);
+                }
+            };
+            const int64_t step = 256 * W;
+            for (int64_t c = 256 * mine + 8 * lane; c < a.cols; c += 2 * step) {
+                Eight<XKIND> d0, d1, v0[J], v1[J];
+                const bool two = c + step < a.cols;
+                load(d0, v0, c);
+                if (two) load(d1, v1, c + step);
+                add(d0, v0, c);
+                if (two) add(d1, v1, c + step);
             }
         }
+        if (!a.dweight) continue;
 #pragma unroll
         for (int j = 0; j < J; j++) {
-            if (!a.dweight || j0 + j >= a.k) break;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
-            if (lane == 0) a.dweight[t * a.k + j0 + j] = row[j] >= 0 ? sum[j] : 0.0f;
+            if (lane == 0) part[warp][j] = sum[j];
         }
+        if (W > 1) __syncthreads();
+        else __syncwarp();
+        if (here && mine == 0 && lane < J && j0 + lane < a.k) {
+            float s = part[warp][lane];
+            for (int o = 1; o < W; o++) s += part[warp + o][lane];
+            a.dweight[t * a.k + j0 + lane] = s;  // zero where there is no row
+        }
+        if (W > 1) __syncthreads();
+        else __syncwarp();
     }
 }
 
@@ -263,14 +307,20 @@ extern "C" fp8dl_status moe_combine(const void *y, int32_t dtype, int64_t rows, 
     FP8DL_CHECK_ARG(tokens == 0 || (out && (y || rows == 0)), "y and out must be non-NULL");
     if (!aligned16(y) || !aligned16(out) || !aligned4(weight))
         return fail(FP8DL_ERR_ALIGN, "y and out must be 16-byte aligned, weight 4-byte");
-    FP8DL_TRY(current_device(nullptr, nullptr));
+    int sms = 0;
+    FP8DL_TRY(current_device(nullptr, &sms));
     if (tokens == 0) return FP8DL_OK;
     CombineArgs a = {y, nullptr, rows, cols, tokens, position, weight, k, out, nullptr, nullptr};
-    const int64_t ctas = (tokens * (cols / 8) + 255) / 256;
-    FP8DL_TRY(exchange_grid(ctas));
+    // 512 columns a warp, 256 where the warps would be few
+    const bool two = tokens * ((cols + 511) / 512) >= 16 * (int64_t)sms;
+    const int64_t per = (cols + (two ? 511 : 255)) / (two ? 512 : 256), ctas = (tokens * per + 7) / 8;
+    FP8DL_TRY(exchange_grid(8 * ctas));
     const bool pdl = short_call_bytes((double)tokens * (double)cols * (dtype == FP8DL_BF16 ? 2.0 : 4.0) * (k + 1));
-    (void)launch_kernel(dtype == FP8DL_BF16 ? moe_combine_kernel<FP8DL_BF16> : moe_combine_kernel<FP8DL_F32>,
-                        dim3((unsigned)ctas), dim3(256), 0, (cudaStream_t)stream, 0, pdl, a);
+#define FP8DL_COMBINE(X) \
+    (k <= 2 ? (two ? moe_combine_kernel<X, 2, 2> : moe_combine_kernel<X, 2, 1>) : (two ? moe_combine_kernel<X, 4, 2> : moe_combine_kernel<X, 4, 1>))
+    (void)launch_kernel(dtype == FP8DL_BF16 ? FP8DL_COMBINE(FP8DL_BF16) : FP8DL_COMBINE(FP8DL_F32), dim3((unsigned)ctas), dim3(256), 0,
+                        (cudaStream_t)stream, 0, pdl, a);
+#undef FP8DL_COMBINE
     note_launch();
     return check_launch("moe_combine");
 }
@@ -285,15 +335,18 @@ extern "C" fp8dl_status moe_combine_bwd(const void *dout, const void *y, int32_t
     FP8DL_CHECK_ARG(tokens == 0 || rows == 0 || ((!dy || weight) && (!dweight || y)), "dy needs weight, dweight needs y");
     if (!aligned16(dout) || !aligned16(y) || !aligned16(dy) || !aligned4(weight) || !aligned4(dweight))
         return fail(FP8DL_ERR_ALIGN, "dout, y and dy must be 16-byte aligned, weight and dweight 4-byte");
-    FP8DL_TRY(current_device(nullptr, nullptr));
+    int sms = 0;
+    FP8DL_TRY(current_device(nullptr, &sms));
     if (tokens == 0) return FP8DL_OK;
     CombineArgs a = {y, dout, rows, cols, tokens, position, weight, k, nullptr, dy, dweight};
-    const int64_t ctas = (tokens + 7) / 8;
+    int wlog = 0;  // warps a token: more where tokens are few
+    while (wlog < 3 && (tokens << wlog) < 16 * (int64_t)sms && (int64_t(256) << wlog) < cols) wlog++;
+    const int64_t ctas = ((tokens << wlog) + 7) / 8;
     const bool pdl = short_call_bytes((double)tokens * (double)cols * (dtype == FP8DL_BF16 ? 2.0 : 4.0) * (2 * k + 1));
     auto *kernel = dtype == FP8DL_BF16
                        ? (k <= 2 ? moe_combine_bwd_kernel<FP8DL_BF16, 2> : moe_combine_bwd_kernel<FP8DL_BF16, 4>)
                        : (k <= 2 ? moe_combine_bwd_kernel<FP8DL_F32, 2> : moe_combine_bwd_kernel<FP8DL_F32, 4>);
-    (void)launch_kernel(kernel, dim3((unsigned)ctas), dim3(256), 0, (cudaStream_t)stream, 0, pdl, a);
+    (void)launch_kernel(kernel, dim3((unsigned)ctas), dim3(256), 0, (cudaStream_t)stream, 0, pdl, a, wlog);
     note_launch();
     return check_launch("moe_combine_bwd");
 }
