@@ -15,29 +15,6 @@
 
 namespace fp8dl {
 
-// Four fp32 values -> four codes, v0 in byte 0, the halves joined by the conversions themselves.
-template <int FMT>
-__device__ __forceinline__ uint32_t codes4(float v0, float v1, float v2, float v3) {
-    uint32_t r;
-    if (FMT == FP8DL_E4M3)
-        asm("{.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};}"
-            : "=r"(r) : "f"(v0), "f"(v1), "f"(v2), "f"(v3));
-    else
-        asm("{.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e5m2x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e5m2x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};}"
-            : "=r"(r) : "f"(v0), "f"(v1), "f"(v2), "f"(v3));
-    return r;
-}
-
-// The largest of |a|, |b| and |c| (NaN does not count): one instruction.
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float m;
-    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
-    return m;
-}
-
-// 32 x 32 -> 64 bits in one instruction: every extent fits 32 bits, no tensor's size does.
-__device__ __forceinline__ uint64_t wide_mul(uint32_t a, uint32_t b) { return (uint64_t)a * b; }
-
 // act(a) and, with D, its derivative.
 template <bool SILU, bool D>
 __device__ __forceinline__ void activation2(float2 a, float2 &y, float2 &d) {

@@ -74,43 +74,56 @@ __global__ void __launch_bounds__(256) block_dispatch_kernel(const DispatchArgs 
     const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), t = w / a.chunks;
     if (t >= a.tokens) return;
     const int64_t c0 = (w - t * a.chunks) * 1024 + 8 * lane;
-    const int64_t at = lane < a.k ? a.position[t * a.k + lane] : -1;  // lane j: where copy j goes
+    const int32_t at = lane < a.k ? a.position[t * a.k + lane] : -1;  // lane j: where copy j goes
     Eight<XKIND> v[U];
 #pragma unroll
     for (int i = 0; i < U; i++) {
         v[i].zero();
         if (c0 + 256 * i < a.cols) v[i].load(a.x, t * a.cols + c0 + 256 * i);
     }
-    uint2 code[U];
-    float inv[U];
+    // maxima of the four blocks by a halving exchange: each lane ends up with that of block (lane >> 2 & 3) of its 16 lanes
+    float m[U];
 #pragma unroll
     for (int i = 0; i < U; i++) {
-        float m = 0.0f;
-#pragma unroll
-        for (int q = 0; q < 4; q++) m = fmaxf(m, fmaxf(finite_abs(v[i].pair(q).x), finite_abs(v[i].pair(q).y)));
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float2 sc = block_scale_fast<FMT>(m);
-        inv[i] = sc.y;
-        float2 y[4];
-#pragma unroll
-        for (int q = 0; q < 4; q++) y[q] = __fmul2_rn(v[i].pair(q), f2(sc.x));
-        code[i] = make_uint2(pack4<FMT>(y[0].x, y[0].y, y[1].x, y[1].y), pack4<FMT>(y[2].x, y[2].y, y[3].x, y[3].y));
+        const float2 x = v[i].pair(0), y = v[i].pair(1), z = v[i].pair(2), w4 = v[i].pair(3);
+        m[i] = max3(max3(max3(x.x, x.y, y.x), y.y, z.x), max3(z.y, w4.x, w4.y), 0.0f);
     }
+    if (max3(max3(m[0], m[1], m[2]), m[3], 0.0f) > 3.402823466e38f) {  // an infinity: over the finite values
+#pragma unroll
+        for (int i = 0; i < U; i++) {
+            m[i] = 0.0f;
+#pragma unroll
+            for (int q = 0; q < 4; q++) m[i] = fmaxf(m[i], fmaxf(finite_abs(v[i].pair(q).x), finite_abs(v[i].pair(q).y)));
+        }
+    }
+    const bool up8 = lane & 8, up4 = lane & 4;
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+        m[i] = fmaxf(up8 ? m[i + 2] : m[i], __shfl_xor_sync(0xffffffffu, up8 ? m[i] : m[i + 2], 8));
+    m[0] = fmaxf(up4 ? m[1] : m[0], __shfl_xor_sync(0xffffffffu, up4 ? m[0] : m[1], 4));
+    m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], 2));
+    m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], 1));
+    const float2 sc = block_scale_fast<FMT>(m[0]);
+    uint2 code[U];
+#pragma unroll
+    for (int i = 0; i < U; i++) {
+        const float k = __shfl_sync(0xffffffffu, sc.x, (lane & 16) + 4 * i);
+        const float2 x = v[i].pair(0), y = v[i].pair(1), z = v[i].pair(2), w4 = v[i].pair(3);
+        code[i] = make_uint2(codes4<FMT>(x.x * k, x.y * k, y.x * k, y.y * k), codes4<FMT>(z.x * k, z.y * k, w4.x * k, w4.y * k));
+    }
+    // the lane that writes a block's factor: the first of four, of the block that it holds
+    const int64_t cs = c0 - 8 * (lane & 15) + 256 * (lane >> 2 & 3);
+    const bool lead = (lane & 3) == 0 && cs < a.cols;
     for (int j = a.q ? -1 : 0; j < a.k; j++) {
         int64_t row = t;
         if (j >= 0) row = __shfl_sync(0xffffffffu, at, j);
         if (j >= 0 && (row < 0 || row >= a.rows)) continue;
-        uint8_t *q = j < 0 ? a.q : a.row_q;
-        float *s = j < 0 ? a.s : a.row_s;
-        const int64_t ld = j < 0 ? a.tokens : a.rows;
+        uint8_t *q = (j < 0 ? a.q : a.row_q) + row * a.cols + c0;
+        float *s = (j < 0 ? a.s : a.row_s) + row;
 #pragma unroll
-        for (int i = 0; i < U; i++) {
-            const int64_t c = c0 + 256 * i;
-            if (c >= a.cols) continue;
-            *reinterpret_cast<uint2 *>(q + row * a.cols + c) = code[i];
-            if ((lane & 15) == 0) s[(c >> 7) * ld + row] = inv[i];
-        }
+        for (int i = 0; i < U; i++)
+            if (c0 + 256 * i < a.cols) *reinterpret_cast<uint2 *>(q + 256 * i) = code[i];
+        if (lead) s[(cs >> 7) * (j < 0 ? a.tokens : a.rows)] = sc.y;
     }
 }
 
