@@ -42,6 +42,36 @@ __device__ __forceinline__ uint32_t route_key(float v) {
 __device__ __forceinline__ float route_value(uint32_t key) {
     return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
+// A bf16's key in the upper half (its lower half is zeros, or ones where the sign is set) and the expert's place from
+// the end below it: no two are alike, and the largest is the largest logit of the lowest expert.
+__device__ __forceinline__ uint32_t route_key16(float v, int i) {
+    const uint32_t k = route_key(v);
+    return k ? (k & 0xffff0000u) | (uint32_t)(0xffff - i) : 0u;
+}
+__device__ __forceinline__ float route_value16(uint32_t key) {
+    return __uint_as_float(key & 0x80000000u ? (key & 0xffff0000u) ^ 0x80000000u : ~key & 0xffff0000u);
+}
+// exp(v - m) from the hardware's 2^x: v - m first, so that the error goes by that difference (2 units of 2^-24 for each
+// 1 of it, and 4 of 2^x) whatever the logits' size.
+__device__ __forceinline__ float route_exp(float v, float m) { return ex2_approx_ftz((v - m) * 1.4426950409f); }
+
+// S (1, 2, 4 or 8) keys into descending order: Batcher's odd-even merge exchange (19 exchanges for eight).
+__device__ __forceinline__ void exchange_down(uint32_t &a, uint32_t &b) {
+    const uint32_t hi = max(a, b), lo = min(a, b);
+    a = hi, b = lo;
+}
+template <int S>
+__device__ __forceinline__ void sort_down(uint32_t (&k)[S]) {
+#pragma unroll
+    for (int p = 1; p < S; p *= 2)
+#pragma unroll
+        for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+            for (int j = q % p; j + q < S; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; i++)
+                    if (i + j + q < S && (i + j) / (2 * p) == (i + j + q) / (2 * p)) exchange_down(k[i + j], k[i + j + q]);
+}
 
 // S consecutive logits of a row from element i0 on (lane-contiguous, so that the lowest lane
 // among equal maxima holds the lowest expert); -infinity behind the row's end.
@@ -164,58 +194,89 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
 #pragma unroll
     for (int s = 0; s < S; s++) ps[s] = 0.0f;
     int n_counted = 0;
-    for (int64_t i = 0; i < a.per; i++) {
+    float v[S], v_next[S];
+    const auto load = [&](int64_t i) {  // of token i of the run: -infinity where there is none
         const int64_t t = t0 + i;
-        const bool here = t < a.tokens, live = here && (!a.valid || a.valid[t]);
-        float v[S];
-        uint32_t key[S], best = 0;
-        if (live) {
-            route_load<XKIND, S>(a.logits, t, E, l * S, a.vec, v);
+        if (i < a.per && t < a.tokens && (!a.valid || a.valid[t])) {
+            route_load<XKIND, S>(a.logits, t, E, l * S, a.vec, v_next);
         } else {
 #pragma unroll
-            for (int s = 0; s < S; s++) v[s] = rt::NEG_INF;
+            for (int s = 0; s < S; s++) v_next[s] = rt::NEG_INF;
         }
+    };
+    load(0);
+    for (int64_t i = 0; i < a.per; i++) {
+        const int64_t t = t0 + i;
+        const bool here = t < a.tokens;
+        uint32_t key[S], best = 0, choice = 0;  // choice: lane j's, the key of choice j
+        int32_t pick = -1;                      // and its expert
+        int slot = 0;
 #pragma unroll
         for (int s = 0; s < S; s++) {
-            key[s] = route_key(v[s]);
-            best = max(best, key[s]);
+            v[s] = v_next[s];
+            key[s] = XKIND == FP8DL_BF16 ? route_key16(v[s], l * S + s) : route_key(v[s]);
         }
-        uint32_t choice = 0;  // lane j: the key and the expert of choice j
-        int32_t pick = -1;
-        for (int j = 0; j < k; j++) {
-            const uint32_t top = __reduce_max_sync(gmask, best);
-            const int winner = __ffs(__ballot_sync(0xffffffffu, best == top) & gmask) - 1;
-            int slot = 0;
+        if (S < 16) load(i + 1);  // under way while this token's experts are chosen
+        if (XKIND == FP8DL_BF16 && S <= 8) {  // the lane's keys in order once; the lane that had the largest moves up
+            sort_down(key);
+            for (int j = 0; j < k; j++) {
+                const uint32_t top = __reduce_max_sync(gmask, key[0]);
+                if (l == j) choice = top;
+                const bool mine = key[0] == top;
+#pragma unroll
+                for (int s = 0; s < S; s++) key[s] = mine ? (s + 1 < S ? key[s + 1 < S ? s + 1 : s] : 0u) : key[s];
+            }
+        } else if (XKIND == FP8DL_BF16) {
+#pragma unroll
+            for (int s = 0; s < S; s++) best = max(best, key[s]);
+            for (int j = 0; j < k; j++) {
+                const uint32_t top = __reduce_max_sync(gmask, best);
+                if (l == j) choice = top;
+                if (best == top) {  // one lane: the largest below it, which wrap around when it is taken off
+                    uint32_t under = 0;
+#pragma unroll
+                    for (int s = 0; s < S; s++) under = max(under, key[s] - top);
+                    best = (int32_t)under < 0 ? under + top : 0;
+                }
+            }
+        } else {
 #pragma unroll
             for (int s = S - 1; s >= 0; s--)
-                if (key[s] == top) slot = s;
-            slot = __shfl_sync(0xffffffffu, slot, winner);
-            if (l == j && top != 0) {
-                choice = top;
-                pick = (winner & (G - 1)) * S + slot;
-            }
-            if (lane == winner) {
-                best = 0;
+                if (key[s] >= best) best = key[s], slot = s;
+            for (int j = 0; j < k; j++) {
+                const uint32_t top = __reduce_max_sync(gmask, best);
+                const int winner = __ffs(__ballot_sync(0xffffffffu, best == top) & gmask) - 1;
+                const int where = __shfl_sync(0xffffffffu, slot, winner);
+                if (l == j && top != 0) {
+                    choice = top;
+                    pick = (winner & (G - 1)) * S + where;
+                }
+                if (lane == winner) {
+                    best = 0;
 #pragma unroll
-                for (int s = 0; s < S; s++) {
-                    if (s == slot) key[s] = 0;
-                    best = max(best, key[s]);
+                    for (int s = S - 1; s >= 0; s--) {
+                        if (s == where) key[s] = 0;
+                        if (key[s] >= best) best = key[s], slot = s;
+                    }
                 }
             }
         }
+        if (XKIND == FP8DL_BF16 && choice) pick = 0xffff - (int)(choice & 0xffff);
+        if (S >= 16) load(i + 1);
         const uint32_t top = __shfl_sync(0xffffffffu, choice, lane & ~(G - 1));
-        const float m = top ? route_value(top) : 0.0f;
+        const auto value = [](uint32_t c) { return XKIND == FP8DL_BF16 ? route_value16(c) : route_value(c); };
+        const float m = top ? value(top) : 0.0f;
         float z = 0.0f;
 #pragma unroll
         for (int s = 0; s < S; s++) {
-            v[s] = top ? expf(v[s] - m) : v[s] == v[s] ? 0.0f : v[s];  // nothing to choose: 0, or NaN
+            v[s] = top ? route_exp(v[s], m) : v[s] == v[s] ? 0.0f : v[s];  // nothing to choose: 0, or NaN
             z += v[s];
         }
         z = group_sum<G>(z);
         const float inv = top ? __frcp_rn(z) : 1.0f;
 #pragma unroll
         for (int s = 0; s < S; s++) ps[s] = fmaf(v[s], inv, ps[s]);
-        const float e = pick >= 0 ? expf(route_value(choice) - m) : 0.0f;
+        const float e = pick >= 0 ? route_exp(value(choice), m) : 0.0f;
         const float chosen = group_sum<G>(e);
         if (l == 0 && top) n_counted++;
         if (here && l < k) {
@@ -256,14 +317,22 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
         }
     }
     if (l < k) {
-        for (int64_t i = 0; i < a.per; i++) {
-            const int64_t t = t0 + i;
-            if (t >= a.tokens) break;
-            const int32_t e = a.expert[t * k + l];
-            if (e < 0) continue;
-            const int32_t at = a.position[t * k + l] + mine[e] + (SINGLE ? first[e] : 0);
-            a.position[t * k + l] = at;
-            if (SINGLE) a.token[at] = (int32_t)t;
+        constexpr int U = 8;  // tokens read at once
+        for (int64_t i0 = 0; i0 < a.per && t0 + i0 < a.tokens; i0 += U) {
+            int32_t e[U], at[U];
+#pragma unroll
+            for (int i = 0; i < U; i++) {
+                const bool ok = i0 + i < a.per && t0 + i0 + i < a.tokens;
+                e[i] = ok ? a.expert[(t0 + i0 + i) * k + l] : -1;
+                at[i] = ok ? a.position[(t0 + i0 + i) * k + l] : -1;
+            }
+#pragma unroll
+            for (int i = 0; i < U; i++) {
+                if (e[i] < 0) continue;
+                at[i] += mine[e[i]] + (SINGLE ? first[e[i]] : 0);
+                a.position[(t0 + i0 + i) * k + l] = at[i];
+                if (SINGLE) a.token[at[i]] = (int32_t)(t0 + i0 + i);
+            }
         }
     }
     if (!(SINGLE ? (void *)a.slope : (void *)a.psum)) return;
@@ -346,12 +415,23 @@ __global__ void __launch_bounds__(1024) route_rows_kernel(const RouteArgs a, int
     if (tid < E) before[tid] += first[tid];
     __syncthreads();
     const int64_t lo = tile * tile_tokens * a.k, hi = min((tile + 1) * tile_tokens, a.tokens) * a.k;
-    for (int64_t i = lo + tid; i < hi; i += 1024) {
-        const int32_t x = a.expert[i];
-        if (x < 0) continue;
-        const int32_t at = a.position[i] + before[x];
-        a.position[i] = at;
-        a.token[at] = (int32_t)((uint32_t)i / (uint32_t)a.k);
+    constexpr int U = 2;
+    for (int64_t i0 = lo + tid; i0 < hi; i0 += 1024 * U) {
+        int32_t x[U], at[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int64_t i = i0 + 1024 * u;
+            x[u] = i < hi ? a.expert[i] : -1;
+            at[u] = i < hi ? a.position[i] : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int64_t i = i0 + 1024 * u;
+            if (x[u] < 0) continue;
+            at[u] += before[x[u]];
+            a.position[i] = at[u];
+            a.token[at[u]] = (int32_t)((uint32_t)i / (uint32_t)a.k);
+        }
     }
 }
 
@@ -374,41 +454,53 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteArgs a, const
     for (int s = 0; s < S; s++) even[s] = dloss && i0 + s < E ? dl * a.slope[i0 + s] : 0.0f;
     __syncwarp();
     const int64_t step = (int64_t)gridDim.x * NG, rounds = (a.tokens + step - 1) / step;
+    int32_t pick_next;
+    float w_next, dw_next, v_next[S];
+    const auto load = [&](int64_t r) {  // of the group's token in round r
+        const int64_t t = r * step + (int64_t)blockIdx.x * NG + run;
+        const bool here = r < rounds && t < a.tokens;
+        pick_next = -1;
+        w_next = dw_next = 0.0f;
+        if (here && l < k) {
+            pick_next = a.expert[t * k + l];
+            w_next = a.weight[t * k + l];
+            if (dweight) dw_next = dweight[t * k + l];
+        }
+        if (here) {
+            route_load<XKIND, S>(a.logits, t, E, i0, a.vec, v_next);
+        } else {
+#pragma unroll
+            for (int s = 0; s < S; s++) v_next[s] = rt::NEG_INF;
+        }
+    };
+    load(0);
     for (int64_t r = 0; r < rounds; r++) {
         const int64_t t = r * step + (int64_t)blockIdx.x * NG + run;
         const bool here = t < a.tokens;
-        int32_t pick = -1;
-        float w = 0.0f, dw = 0.0f, vj = 0.0f;
-        if (here && l < k) {
-            pick = a.expert[t * k + l];
-            pick = pick < E ? pick : -1;
-            if (pick >= 0) {
-                w = a.weight[t * k + l];
-                dw = dweight ? dweight[t * k + l] : 0.0f;
-                vj = XKIND == FP8DL_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(a.logits)[t * E + pick])
-                                         : static_cast<const float *>(a.logits)[t * E + pick];
-            }
-        }
-        const bool some = __shfl_sync(0xffffffffu, pick, lane & ~(G - 1)) >= 0;
-        const float m = __shfl_sync(0xffffffffu, vj, lane & ~(G - 1));
-        float v[S], z = 0.0f;
-        if (some) {
-            route_load<XKIND, S>(a.logits, t, E, i0, a.vec, v);
-        } else {
-#pragma unroll
-            for (int s = 0; s < S; s++) v[s] = rt::NEG_INF;
-        }
+        const int32_t pick = pick_next < E ? pick_next : -1;
+        const float w = pick >= 0 ? w_next : 0.0f, dw = pick >= 0 ? dw_next : 0.0f;
+        float v[S], z = 0.0f, m = rt::NEG_INF;
 #pragma unroll
         for (int s = 0; s < S; s++) {
-            v[s] = expf(v[s] - m);
+            v[s] = v_next[s];
+            m = fmaxf(m, v[s]);  // NaN does not count, as in the choice
+        }
+        if (S < 16) load(r + 1);  // under way meanwhile
+        const bool some = __shfl_sync(0xffffffffu, pick, lane & ~(G - 1)) >= 0;
+#pragma unroll
+        for (int o = G / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (!some) m = 0.0f;
+#pragma unroll
+        for (int s = 0; s < S; s++) {
+            v[s] = route_exp(v[s], m);
             z += v[s];
         }
         z = group_sum<G>(z);
         const float inv = some ? __frcp_rn(z) : 0.0f;
         float d = dw;
-        if (a.normalize) {
-            const float chosen = group_sum<G>(pick >= 0 ? expf(vj - m) : 0.0f), dot = group_sum<G>(dw * w);
-            d = (dw - dot) * __fdiv_rn(z, chosen);
+        if (a.normalize) {  // the first choice's weight is 1 / (sum of the chosen exponentials)
+            const float dot = group_sum<G>(dw * w), first = __shfl_sync(0xffffffffu, w, lane & ~(G - 1));
+            d = (dw - dot) * (z * first);
         }
         if (pick >= 0) mine[pick] = d;
         __syncwarp();
@@ -459,6 +551,7 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteArgs a, const
             }
         }
         __syncwarp();
+        if (S >= 16) load(r + 1);
     }
 }
 
@@ -567,7 +660,8 @@ extern "C" fp8dl_status moe_route(const void *logits, int32_t dtype, int64_t tok
     a.valid = valid;
     a.expert = expert, a.position = position, a.token = token, a.offsets = offsets, a.counts = counts;
     a.weight = weight, a.slope = slope, a.loss = loss;
-    a.per = (tokens + most * runs - 1) / (most * runs);
+    // few tokens: one CTA and one launch, up to four tokens a run
+    a.per = tokens <= 4 * runs ? (tokens + runs - 1) / runs : (tokens + most * runs - 1) / (most * runs);
     const int64_t tile_tokens = a.per * runs;
     const int tiles = (int)((tokens + tile_tokens - 1) / tile_tokens);
     a.hist = static_cast<int32_t *>(workspace);
