@@ -29,8 +29,9 @@ struct RouteArgs {
     const uint8_t *valid;
     int32_t *expert, *position, *token, *offsets, *counts;
     float *weight, *slope, *loss;
-    int32_t *hist;  // [tiles][experts + 1]: the tile's choices of each expert, its tokens with a choice
-    float *psum;    // [tiles][experts]: the tile's sums of p, or NULL
+    int32_t *hist;     // [tiles][experts]: the tile's choices of each expert
+    int32_t *counted;  // [tiles]: its tokens with a choice
+    float *psum;       // [tiles][experts]: its sums of p, or NULL
     int64_t per;    // tokens of a run
 };
 
@@ -305,9 +306,9 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
         if (SINGLE)
             total[e] = sum;
         else
-            a.hist[(int64_t)blockIdx.x * (E + 1) + e] = sum;
+            a.hist[(int)blockIdx.x * E + e] = sum;
     }
-    if (!SINGLE && tid == 0) a.hist[(int64_t)blockIdx.x * (E + 1) + E] = counted;
+    if (!SINGLE && tid == 0) a.counted[blockIdx.x] = counted;
     __syncthreads();
     if (SINGLE) {
         scan_experts<THREADS>(total, first, E, warps);
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
         if (SINGLE)
             pf[e] = sum;  // (run 0's own entry, read by this thread alone)
         else
-            a.psum[(int64_t)blockIdx.x * E + e] = sum;
+            a.psum[(int)blockIdx.x * E + e] = sum;
     }
     if (SINGLE) {
         __syncthreads();
@@ -359,44 +360,62 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
 // The rows of every tile: CTA i adds up the counts of the tiles before its own and of all tiles, and the
 // experts' first rows; its tokens' ranks become rows.  The CTA behind the last tile makes the loss.
 __global__ void __launch_bounds__(1024) route_rows_kernel(const RouteArgs a, int tiles, int64_t tile_tokens) {
+    __shared__ int4 part_b[1024], part_n[1024];
     __shared__ int32_t before[1024], total[1024], first[1025], warps[32];
     __shared__ float sums[1024];
     pdl_wait();
     pdl_trigger();
     const int E = a.experts, tid = threadIdx.x, tile = blockIdx.x;
-    int wide = 32;  // threads across the experts; the rest share out the tiles
-    while (wide < E) wide *= 2;
-    const int parts = 1024 / wide, part = tid / wide, e = tid % wide;
-    int32_t b = 0, n = 0;
-    float p = 0.0f;
-    if (e < E) {
-#pragma unroll 8
+    int wide = 8;  // threads across the experts, four each; the rest share out the tiles
+    while (4 * wide < E) wide *= 2;
+    const int parts = min(1024 / wide, 32), part = tid / wide, e = 4 * (tid % wide);
+    int4 b = make_int4(0, 0, 0, 0), n = b;
+    float4 p = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const bool vec = E % 4 == 0;
+    const auto four = [&](const int32_t *at) {  // four experts' figures, zeros behind the last
+        if (vec) return *reinterpret_cast<const int4 *>(at);
+        return make_int4(at[0], e + 1 < E ? at[1] : 0, e + 2 < E ? at[2] : 0, e + 3 < E ? at[3] : 0);
+    };
+    if (e < E && part < parts) {
+#pragma unroll 10
         for (int i = part; i < tiles; i += parts) {
-            const int32_t c = a.hist[(int64_t)i * (E + 1) + e];
-            n += c;
-            b += i < tile ? c : 0;
+            const int4 c = four(a.hist + i * E + e);
+            n.x += c.x, n.y += c.y, n.z += c.z, n.w += c.w;
+            if (i < tile) b.x += c.x, b.y += c.y, b.z += c.z, b.w += c.w;
         }
         if (tile == tiles) {
-#pragma unroll 8
-            for (int i = part; i < tiles; i += parts) p += a.psum[(int64_t)i * E + e];
+#pragma unroll 10
+            for (int i = part; i < tiles; i += parts) {
+                const int4 c = four(reinterpret_cast<const int32_t *>(a.psum) + i * E + e);
+                p.x += __int_as_float(c.x), p.y += __int_as_float(c.y), p.z += __int_as_float(c.z), p.w += __int_as_float(c.w);
+            }
         }
     }
-    before[tid] = b, total[tid] = n, sums[tid] = p;
+    // [part][expert], so that a thread per expert reads one line of banks
+    part_b[tid] = b, part_n[tid] = n;
     __syncthreads();
     if (tid < E) {
-        for (int q = 1; q < parts; q++) {
-            b += before[q * wide + tid];
-            n += total[q * wide + tid];
-            p += sums[q * wide + tid];
+        const int32_t *pb = reinterpret_cast<const int32_t *>(part_b) + tid, *pn = reinterpret_cast<const int32_t *>(part_n) + tid;
+        int32_t sb = 0, sn = 0;
+        for (int q = 0; q < parts; q++) sb += pb[4 * wide * q], sn += pn[4 * wide * q];
+        before[tid] = sb, total[tid] = sn;
+    }
+    if (tile == tiles) {
+        __syncthreads();
+        reinterpret_cast<float4 *>(part_b)[tid] = p;
+        __syncthreads();
+        if (tid < E) {
+            const float *pp = reinterpret_cast<const float *>(part_b) + tid;
+            float s = 0.0f;
+            for (int q = 0; q < parts; q++) s += pp[4 * wide * q];
+            sums[tid] = s;
         }
     }
-    __syncthreads();
-    if (tid < E) before[tid] = b, total[tid] = n, sums[tid] = p;
     __syncthreads();
     scan_experts<1024>(total, first, E, warps);
     if (tile == tiles) {
         int32_t c = 0;
-        for (int i = tid; i < tiles; i += 1024) c += a.hist[(int64_t)i * (E + 1) + E];  // at most one each
+        for (int i = tid; i < tiles; i += 1024) c += a.counted[i];  // at most one each
         __shared__ int32_t counted;
         if (tid == 0) counted = 0;
         __syncthreads();
@@ -613,7 +632,7 @@ using namespace fp8dl;
 extern "C" size_t moe_route_workspace_size(int64_t tokens, int32_t n_experts) {
     if (tokens <= 0 || n_experts < 1 || n_experts > kMaxGroups) return 0;
     const size_t tiles = tokens < rt::MAX_TILES ? (size_t)tokens : rt::MAX_TILES;
-    return ((tiles * (n_experts + 1) + 3) / 4 * 4 + tiles * n_experts) * 4;
+    return (tiles * n_experts + 3) / 4 * 16 + (tiles + 3) / 4 * 16 + tiles * n_experts * 4;
 }
 
 extern "C" fp8dl_status moe_route(const void *logits, int32_t dtype, int64_t tokens, int32_t n_experts, int32_t k,
@@ -665,7 +684,8 @@ extern "C" fp8dl_status moe_route(const void *logits, int32_t dtype, int64_t tok
     const int64_t tile_tokens = a.per * runs;
     const int tiles = (int)((tokens + tile_tokens - 1) / tile_tokens);
     a.hist = static_cast<int32_t *>(workspace);
-    a.psum = slope ? reinterpret_cast<float *>(a.hist + ((int64_t)tiles * (n_experts + 1) + 3) / 4 * 4) : nullptr;
+    a.counted = a.hist + (tiles * n_experts + 3) / 4 * 4;
+    a.psum = slope ? reinterpret_cast<float *>(a.counted + (tiles + 3) / 4 * 4) : nullptr;
     const bool pdl = short_call_bytes((double)tokens * n_experts * esz);
     fp8dl_status r = FP8DL_OK;
 #define FP8DL_ROUTE(g_, s_)                                                                          \
