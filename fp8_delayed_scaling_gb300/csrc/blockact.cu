@@ -605,8 +605,7 @@ __device__ __forceinline__ float2 value2(uint32_t word, float f) {
         asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;}" : "=r"(h) : "r"(word));
     else
         h = __byte_perm(word, 0, UPPER ? 0x3424 : 0x1404);  // E5M2 is the upper byte of an fp16
-    const float2 x = half_pair(h);
-    return make_float2(x.x * f, x.y * f);
+    return __fmul2_rn(half_pair(h), f2(f));
 }
 // The same of pair p of eight codes.
 template <bool E4>
@@ -735,7 +734,7 @@ __global__ void __launch_bounds__(br::THREADS, 4) block_recode_kernel(const Bloc
                 for (int i = 0; i < 4; i++) {
                     asm volatile("" : "+r"(u[4 * h + i].x), "+r"(u[4 * h + i].y)::"memory");  // decoded again, not kept
                     const float2 x = pair_of<E4>(u[4 * h + i], p, i == 0 ? k.x : i == 1 ? k.y : i == 2 ? k.z : k.w);
-                    y[i] = make_float2(x.x * sc.x, x.y * sc.y);
+                    y[i] = __fmul2_rn(x, sc);
                 }
                 w[0][h] = codes4<FMT>(y[0].x, y[1].x, y[2].x, y[3].x), w[1][h] = codes4<FMT>(y[0].y, y[1].y, y[2].y, y[3].y);
             }
