@@ -406,7 +406,7 @@ def _tensor(t, dtype, shape, dev: int, name: str):
 
 def _launch(dev: int, stream):
     """The stream to launch on; the tensors must be on the current CUDA device, where the kernels run."""
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         raise ValueError("the tensors must be on the current CUDA device, got %s" % ("cuda:%d" % dev if dev >= 0 else "CPU tensors"))
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 

@@ -122,11 +122,14 @@ class BlockMoE:
         T, k, H, F, W = self.m, self.k, self.H, self.F, self.W
         if tuple(dy.shape) != (T, H) or dy.dtype is not torch.bfloat16:
             raise ValueError("dy is %s %s, the forward pass had %d tokens of %d: bfloat16 is wanted" % (dy.dtype, tuple(dy.shape), T, H))
-        self.m = -1  # the row results' buffer is used again below
+        if dloss is not None and (dloss.dtype is not torch.float32 or dloss.shape != (1,) or dloss.device != dy.device):
+            raise ValueError("dloss must be a float32 tensor of shape (1,) on the device of dy, got %s %s on %s" % (
+                dloss.dtype, tuple(dloss.shape), dloss.device))
         R, gf = T * k, self.grad_dtype
         P = fp8_block_padded_rows(R, self.E)
         ye, dye, dweight = self._ye[:R * H].view(R, H), self._dye[:R * H].view(R, H), self._dweight[:R].view(T, k)
         moe_combine_bwd(dy, ye, self.position, self.weight, dy=dye, dweight=dweight, stream=stream)
+        self.m = -1  # the row results' buffer is used again below
         self.dye8.quantize(dye, gf, offsets=self.offsets, stream=stream)
         dg = self._h[:R * F].view(R, F)
         fp8_block_gemm_grouped(self.dye8.row_q, gf, self.dye8.row_s, self.w2_8.q_t, E4M3, self.w2_8.s_t, self.offsets, dg, stream=stream)

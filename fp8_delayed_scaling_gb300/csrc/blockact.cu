@@ -562,18 +562,24 @@ __global__ void __launch_bounds__(ba::ACT_THREADS) block_dact_rows_kernel(const 
     if ((threadIdx.x & 7) == 0 && row[threadIdx.x >> 3 & 1]) a.dh_s[wide_mul(at >> 7, rows) + r + (threadIdx.x >> 3 & 1)] = f;
 }
 
+template <int XKIND, int FMT, bool GATED, bool SILU>
+static fp8dl_status launch_dact_tiles(const BlockDactArgs &a, int dev, int sms, cudaStream_t st, bool pdl) {
+    static std::atomic<uint64_t> done{0};
+    constexpr size_t values = (GATED ? 3 : 2) * bd::TILE * bd::TILE * sizeof(float);
+    auto *kernel = block_dact_kernel<XKIND, FMT, GATED, SILU>;
+    FP8DL_TRY(allow_smem(kernel, values + group_table_bytes(kMaxGroups), dev, done, "fp8_block_dact"));
+    const int64_t most = (int64_t)a.tiles * a.across;
+    (void)launch_kernel(kernel, dim3((unsigned)(most < sms ? most : sms)), dim3(bd::THREADS), values + group_table_bytes(a.n_groups), st, 0,
+                        pdl, a);
+    note_launch();
+    return check_launch("fp8_block_dact");
+}
+
 template <int FMT, bool GATED, bool SILU>
-static fp8dl_status launch_dact(const BlockDactArgs &a, bool tiles, int sms, cudaStream_t st, bool pdl) {
-    if (tiles) {
-        const size_t smem = (GATED ? 3 : 2) * bd::TILE * bd::TILE * sizeof(float) + group_table_bytes(a.n_groups);
-        auto *kernel = a.bf16 ? block_dact_kernel<FP8DL_BF16, FMT, GATED, SILU> : block_dact_kernel<FP8DL_F32, FMT, GATED, SILU>;
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return fail(FP8DL_ERR_CUDA, "fp8_block_dact: %s", cudaGetErrorString(e));
-        const int64_t most = (int64_t)a.tiles * a.across;
-        (void)launch_kernel(kernel, dim3((unsigned)(most < sms ? most : sms)), dim3(bd::THREADS), smem, st, 0, pdl, a);
-        note_launch();
-        FP8DL_TRY(check_launch("fp8_block_dact"));
-    }
+static fp8dl_status launch_dact(const BlockDactArgs &a, bool tiles, int dev, int sms, cudaStream_t st, bool pdl) {
+    if (tiles)
+        FP8DL_TRY((a.bf16 ? launch_dact_tiles<FP8DL_BF16, FMT, GATED, SILU>(a, dev, sms, st, pdl)
+                          : launch_dact_tiles<FP8DL_F32, FMT, GATED, SILU>(a, dev, sms, st, pdl)));
     if (a.dh_q && a.row_jobs) {
         const int64_t ctas = (a.rows + ba::ACT_ROWS - 1) / ba::ACT_ROWS * a.row_jobs;
         (void)launch_kernel(block_dact_rows_kernel<FMT, GATED, SILU>, dim3((unsigned)ctas), dim3(ba::ACT_THREADS), 0, st, 0, pdl, a);
@@ -875,8 +881,8 @@ extern "C" fp8dl_status fp8_block_dact(const void *dg, int32_t dg_dtype, int32_t
     a.row_jobs = tiles && !split ? 0 : (uint32_t)((wide + 127) / 128) - a.row_first;
     FP8DL_TRY(check_tiles((rows + ba::ACT_ROWS - 1) / ba::ACT_ROWS * a.row_jobs, rows, wide));
     FP8DL_TRY(check_tiles(a.col_ld / 128 * a.across, rows, wide));
-    int sms = 0;
-    FP8DL_TRY(current_device(nullptr, &sms));
+    int dev = 0, sms = 0;
+    FP8DL_TRY(current_device(&dev, &sms));
     cudaStream_t st = (cudaStream_t)stream;
     if (rows == 0) {
         if (dbias && cudaMemsetAsync(dbias, 0, (size_t)wide * sizeof(float), st) != cudaSuccess)
@@ -891,7 +897,7 @@ extern "C" fp8dl_status fp8_block_dact(const void *dg, int32_t dg_dtype, int32_t
     if (out_dtype == FP8DL_E4M3) FP8DL_DACT(FP8DL_E4M3);
     else FP8DL_DACT(FP8DL_E5M2);
 #undef FP8DL_DACT
-    FP8DL_TRY(launch(a, tiles, sms, st, pdl));
+    FP8DL_TRY(launch(a, tiles, dev, sms, st, pdl));
     if (dbias) {
         colsum_reduce(a.ws, (rows + 127) / 128, wide, dbias, st, pdl);
         return check_launch("fp8_block_dact(dbias reduce)");
@@ -915,7 +921,7 @@ extern "C" fp8dl_status fp8_block_recode(const uint8_t *q, int32_t q_fp8, const 
     if (!aligned16(q) || !aligned16(s) || !aligned16(col_q) || !aligned16(col_s) || !aligned4(index))
         return fail(FP8DL_ERR_ALIGN, "q, s, col_q and col_s must be 16-byte aligned, index 4-byte");
     BlockRecodeArgs a = {};
-    a.q = q, a.s = s;
+    a.q = src_rows ? q : col_q, a.s = src_rows ? s : col_s;  // without source rows nothing is read
     a.src_rows = src_rows;
     a.rows = rows;
     a.cols = cols;
@@ -927,16 +933,14 @@ extern "C" fp8dl_status fp8_block_recode(const uint8_t *q, int32_t q_fp8, const 
     a.tiles = (uint32_t)(a.col_ld / 128);
     const int64_t most = a.col_ld / 128 * a.across;
     FP8DL_TRY(check_tiles(most, rows, cols));
-    int sms = 0;
-    FP8DL_TRY(current_device(nullptr, &sms));
+    int dev = 0, sms = 0;
+    FP8DL_TRY(current_device(&dev, &sms));
     if (rows == 0) return FP8DL_OK;
     const bool pdl = short_call_bytes(2.0 * (double)rows * (double)cols), e4 = q_fp8 == FP8DL_E4M3;
     auto *kernel = out_dtype == FP8DL_E4M3 ? (e4 ? block_recode_kernel<FP8DL_E4M3, true> : block_recode_kernel<FP8DL_E4M3, false>)
                                            : (e4 ? block_recode_kernel<FP8DL_E5M2, true> : block_recode_kernel<FP8DL_E5M2, false>);
-    if (offsets) {  // past 48 KB with the groups' table
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)group_table_bytes(n_groups));
-        if (e != cudaSuccess) return fail(FP8DL_ERR_CUDA, "fp8_block_recode: %s", cudaGetErrorString(e));
-    }
+    static std::atomic<uint64_t> done[4];  // past 48 KB with the groups' table
+    FP8DL_TRY(allow_smem(kernel, group_table_bytes(kMaxGroups), dev, done[2 * (out_dtype == FP8DL_E4M3) + e4], "fp8_block_recode"));
     (void)launch_kernel(kernel, dim3((unsigned)(most < 4 * sms ? most : 4 * sms)), dim3(br::THREADS), group_table_bytes(n_groups),
                         (cudaStream_t)stream, 0, pdl, a);
     note_launch();

@@ -587,15 +587,15 @@ static void route_shape(int n, int &g, int &s) {
 static bool route_vec(int n, int s, int esz) { return n % s == 0 && ((int64_t)n * esz) % (s * esz < 16 ? s * esz : 16) == 0; }
 
 template <int XKIND, int G, int S>
-static fp8dl_status launch_route(RouteArgs a, int tiles, int64_t tile_tokens, cudaStream_t st, bool pdl) {
+static fp8dl_status launch_route(const RouteArgs &a, int tiles, int64_t tile_tokens, int dev, cudaStream_t st, bool pdl) {
     constexpr int THREADS = S >= 16 ? 512 : 1024;
     const size_t smem = (size_t)(THREADS / G) * a.experts * 4;
     const bool single = tiles == 1;
     auto *kernel = single ? route_kernel<XKIND, G, S, THREADS, true> : route_kernel<XKIND, G, S, THREADS, false>;
-    if (smem > 32768) {  // with the static arrays past 48 KB
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return fail(FP8DL_ERR_CUDA, "moe_route: %s", cudaGetErrorString(e));
-    }
+    constexpr size_t most = (size_t)THREADS * S * 4;
+    static std::atomic<uint64_t> done[2];
+    if (most > 32768)  // with the static arrays past 48 KB
+        FP8DL_TRY(allow_smem(kernel, most, dev, done[single], "moe_route"));
     (void)launch_kernel(kernel, dim3((unsigned)tiles), dim3(THREADS), smem, st, 0, pdl, a);
     note_launch();
     FP8DL_TRY(check_launch("moe_route"));
@@ -654,8 +654,8 @@ extern "C" fp8dl_status moe_route(const void *logits, int32_t dtype, int64_t tok
                         moe_route_workspace_size(tokens, n_experts), workspace ? workspace_bytes : (size_t)0);
         if (!aligned16(workspace)) return fail(FP8DL_ERR_ALIGN, "workspace must be 16-byte aligned");
     }
-    int sms = 0;
-    FP8DL_TRY(current_device(nullptr, &sms));
+    int dev = 0, sms = 0;
+    FP8DL_TRY(current_device(&dev, &sms));
     cudaStream_t st = (cudaStream_t)stream;
     if (tokens == 0) {
         if (cudaMemsetAsync(offsets, 0, (size_t)(n_experts + 1) * 4, st) != cudaSuccess ||
@@ -689,8 +689,8 @@ extern "C" fp8dl_status moe_route(const void *logits, int32_t dtype, int64_t tok
     const bool pdl = short_call_bytes((double)tokens * n_experts * esz);
     fp8dl_status r = FP8DL_OK;
 #define FP8DL_ROUTE(g_, s_)                                                                          \
-    r = dtype == FP8DL_BF16 ? launch_route<FP8DL_BF16, g_, s_>(a, tiles, tile_tokens, st, pdl)       \
-                            : launch_route<FP8DL_F32, g_, s_>(a, tiles, tile_tokens, st, pdl)
+    r = dtype == FP8DL_BF16 ? launch_route<FP8DL_BF16, g_, s_>(a, tiles, tile_tokens, dev, st, pdl)       \
+                            : launch_route<FP8DL_F32, g_, s_>(a, tiles, tile_tokens, dev, st, pdl)
     if (g == 8) FP8DL_ROUTE(8, 1);
     else if (g == 16) FP8DL_ROUTE(16, 1);
     else if (s == 1) FP8DL_ROUTE(32, 1);
