@@ -579,8 +579,9 @@ def moe_combine_bwd(dout: torch.Tensor, y, position: torch.Tensor, weight, dy=No
     """dy[position[t, j]] = weight[t, j] * dout[t] (dy [R x C]) and dweight[t, j] = <dout[t], y[position[t, j]]>."""
     _need(dout.dim() == 2 and dout.is_contiguous() and position.dim() == 2, "dout [T x C] and position [T x k] must be matrices")
     _need(dy is not None or dweight is not None, "dy and dweight are both None")
-    (T, C), k, dev = dout.shape, position.shape[1], dout.get_device()
-    R = (y if dy is None else dy).shape[0]
+    rows = y if dy is None else dy
+    _need(rows is not None, "dweight needs y")
+    (T, C), k, dev, R = dout.shape, position.shape[1], dout.get_device(), rows.shape[0]
     args = (dout.data_ptr(), _tensor(y, dout.dtype, (R, C), dev, "y"), _hp(dout), R, C,
             _tensor(position, torch.int32, (T, k), dev, "position"), _tensor(weight, torch.float32, (T, k), dev, "weight"), T, k,
             _tensor(dy, dout.dtype, (R, C), dev, "dy"), _tensor(dweight, torch.float32, (T, k), dev, "dweight"))

@@ -233,11 +233,10 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
             for (int j = 0; j < k; j++) {
                 const uint32_t top = __reduce_max_sync(gmask, best);
                 if (l == j) choice = top;
-                if (best == top) {  // one lane: the largest below it, which wrap around when it is taken off
-                    uint32_t under = 0;
+                if (best == top) {  // one lane: the largest of its keys below it
+                    best = 0;
 #pragma unroll
-                    for (int s = 0; s < S; s++) under = max(under, key[s] - top);
-                    best = (int32_t)under < 0 ? under + top : 0;
+                    for (int s = 0; s < S; s++) best = max(best, key[s] < top ? key[s] : 0u);
                 }
             }
         } else {

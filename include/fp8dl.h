@@ -458,7 +458,8 @@ fp8dl_status fp8_block_gemm_grouped_wgrad(const uint8_t *A, int32_t a_dtype, con
  * A logit of -infinity or NaN is never chosen.  A token with fewer than k
  * others, or with valid[t] = 0 (padding; valid [tokens] bytes, or NULL), has
  * expert and position -1 and weight 0 in the places that are left.  A NaN
- * among the logits of a valid token makes its weights NaN (as softmax does).
+ * or +infinity among the logits of a valid token makes its weights NaN, and the
+ * loss (as softmax does).
  * Balance loss (both or neither of slope and loss NULL), over the N tokens that
  * have an expert and C = offsets[n_experts] choices:
  *   slope [n_experts] fp32 = n_experts * counts[e] / (C * N)    (0 if N = 0)
@@ -512,7 +513,8 @@ fp8dl_status moe_combine(const void *y, int32_t dtype, int64_t rows, int64_t col
  *   dy[position[t,j],:] = round( weight[t,j] * dout[t,:] )        (of `dtype`)
  *   dweight[t,j] = sum_c dout[t,c] * y[position[t,j],c]           (fp32, a fixed order)
  * dweight is 0 where the position is outside [0, rows); rows of dy without a
- * token keep their values.  dy and dweight may each be NULL (y too without
+ * token keep their values, a row that two positions name holds either's or a
+ * mixture.  dy and dweight may each be NULL (y too without
  * dweight, weight too without dy). */
 fp8dl_status moe_combine_bwd(const void *dout, const void *y, int32_t dtype, int64_t rows, int64_t cols,
                              const int32_t *position, const float *weight, int64_t tokens, int32_t k,
