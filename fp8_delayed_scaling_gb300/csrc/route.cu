@@ -43,11 +43,16 @@ __device__ __forceinline__ uint32_t route_key(float v) {
 __device__ __forceinline__ float route_value(uint32_t key) {
     return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
-// A bf16's key in the upper half (its lower half is zeros, or ones where the sign is set) and the expert's place from
-// the end below it: no two are alike, and the largest is the largest logit of the lowest expert.
-__device__ __forceinline__ uint32_t route_key16(float v, int i) {
-    const uint32_t k = route_key(v);
-    return k ? (k & 0xffff0000u) | (uint32_t)(0xffff - i) : 0u;
+// The same of two bf16 values at once: a 16-bit key in the upper half of each, and the expert's place from the end below
+// it: no two are alike, and the largest is the largest logit of the lowest expert.  -infinity's key (NaN's too) is below
+// NONE16, every other one above it.
+constexpr uint32_t NONE16 = 0x00800000u;
+__device__ __forceinline__ void route_keys16(uint32_t pair, int i, uint32_t &lo, uint32_t &hi) {
+    uint32_t y, sign;
+    asm("{.reg .b32 a;\n\tadd.rn.bf16x2 a, %1, %2;\n\tmax.bf16x2 %0, a, %3;}" : "=r"(y) : "r"(pair), "r"(0u), "r"(0xff80ff80u));
+    asm("prmt.b32 %0, %1, 0, 0xbb99;" : "=r"(sign) : "r"(y));  // all ones in the halves below zero
+    y ^= sign | 0x80008000u;
+    lo = __byte_perm(y, 0xffffu - i, 0x1054), hi = (y & 0xffff0000u) | (0xfffeu - i);
 }
 __device__ __forceinline__ float route_value16(uint32_t key) {
     return __uint_as_float(key & 0x80000000u ? (key & 0xffff0000u) ^ 0x80000000u : ~key & 0xffff0000u);
@@ -74,17 +79,21 @@ __device__ __forceinline__ void sort_down(uint32_t (&k)[S]) {
                     if (i + j + q < S && (i + j) / (2 * p) == (i + j + q) / (2 * p)) exchange_down(k[i + j], k[i + j + q]);
 }
 
-// S consecutive logits of a row from element i0 on (lane-contiguous, so that the lowest lane
+// S consecutive logits of a row from element i0 on, as they lie in memory (lane-contiguous, so that the lowest lane
 // among equal maxima holds the lowest expert); -infinity behind the row's end.
 template <int XKIND, int S>
-__device__ __forceinline__ void route_load(const void *base, int64_t row, int E, int i0, bool vec, float (&v)[S]) {
-    constexpr int ESZ = XKIND == FP8DL_BF16 ? 2 : 4, BYTES = S * ESZ;
-    const char *p = static_cast<const char *>(base) + (row * E + i0) * ESZ;
+struct Logits {
+    static constexpr int ESZ = XKIND == FP8DL_BF16 ? 2 : 4, BYTES = S * ESZ, WORDS = (BYTES + 3) / 4, PAIRS = (S + 1) / 2;
+    uint32_t w[WORDS];
+    __device__ __forceinline__ void none() {
 #pragma unroll
-    for (int s = 0; s < S; s++) v[s] = rt::NEG_INF;
-    if (vec && BYTES >= 4) {
-        if (i0 < E) {  // E is a multiple of S: all of the lane's or none
-            uint32_t w[BYTES >= 4 ? BYTES / 4 : 1];
+        for (int q = 0; q < WORDS; q++) w[q] = XKIND == FP8DL_BF16 ? 0xff80ff80u : 0xff800000u;
+    }
+    __device__ __forceinline__ void load(const void *base, int64_t row, int E, int i0, bool vec) {
+        const char *p = static_cast<const char *>(base) + (row * E + i0) * ESZ;
+        none();
+        if (vec && BYTES >= 4) {
+            if (i0 >= E) return;  // E is a multiple of S: all of the lane's or none
             if constexpr (BYTES >= 16) {
 #pragma unroll
                 for (int q = 0; q < BYTES / 16; q++) {
@@ -97,17 +106,32 @@ __device__ __forceinline__ void route_load(const void *base, int64_t row, int E,
             } else if constexpr (BYTES == 4) {
                 w[0] = *reinterpret_cast<const uint32_t *>(p);
             }
+        } else {
 #pragma unroll
-            for (int s = 0; s < S; s++)
-                v[s] = XKIND == FP8DL_BF16 ? ((s & 1) ? bf16_hi(w[s / 2]) : bf16_lo(w[s / 2])) : __uint_as_float(w[s]);
+            for (int s = 0; s < S; s++) {
+                if (i0 + s >= E) continue;
+                if (XKIND == FP8DL_F32) w[s < WORDS ? s : 0] = reinterpret_cast<const uint32_t *>(p)[s];
+                else w[s / 2] = __byte_perm(w[s / 2], reinterpret_cast<const uint16_t *>(p)[s], s & 1 ? 0x5410 : 0x3254);
+            }
         }
-    } else {
-#pragma unroll
-        for (int s = 0; s < S; s++)
-            if (i0 + s < E)
-                v[s] = XKIND == FP8DL_BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p)[s])
-                                           : reinterpret_cast<const float *>(p)[s];
     }
+    __device__ __forceinline__ float2 pair(int p) const {
+        if (XKIND == FP8DL_BF16) return make_float2(bf16_lo(w[p]), bf16_hi(w[p]));
+        return make_float2(__uint_as_float(w[2 * p < WORDS ? 2 * p : 0]), S > 1 ? __uint_as_float(w[2 * p + 1 < WORDS ? 2 * p + 1 : 0]) : rt::NEG_INF);
+    }
+};
+
+// exp(v - m) of a pair, by the same steps as route_exp.
+__device__ __forceinline__ float2 route_exp2(float2 v, float m) {
+    const float2 x = __fmul2_rn(__fadd2_rn(v, f2(-m)), f2(1.4426950409f));
+    return make_float2(ex2_approx_ftz(x.x), ex2_approx_ftz(x.y));
+}
+
+// The largest of a group's values, the same in all of its lanes; NaN does not count.
+__device__ __forceinline__ float group_max(float v, uint32_t mask) {
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, %2;" : "=f"(m) : "f"(v), "r"(mask));
+    return m;
 }
 
 // Sum over the G lanes of a group, the same in all of them.
@@ -191,19 +215,16 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
     __syncthreads();
     const int64_t t0 = ((int64_t)blockIdx.x * NG + run) * a.per;
     int32_t *mine = cnt + run * E;
-    float ps[S];
+    constexpr int PAIRS = Logits<XKIND, S>::PAIRS;
+    float2 ps[PAIRS];
 #pragma unroll
-    for (int s = 0; s < S; s++) ps[s] = 0.0f;
+    for (int p = 0; p < PAIRS; p++) ps[p] = f2(0.0f);
     int n_counted = 0;
-    float v[S], v_next[S];
+    Logits<XKIND, S> x, x_next;
     const auto load = [&](int64_t i) {  // of token i of the run: -infinity where there is none
         const int64_t t = t0 + i;
-        if (i < a.per && t < a.tokens && (!a.valid || a.valid[t])) {
-            route_load<XKIND, S>(a.logits, t, E, l * S, a.vec, v_next);
-        } else {
-#pragma unroll
-            for (int s = 0; s < S; s++) v_next[s] = rt::NEG_INF;
-        }
+        if (i < a.per && t < a.tokens && (!a.valid || a.valid[t])) x_next.load(a.logits, t, E, l * S, a.vec);
+        else x_next.none();
     };
     load(0);
     for (int64_t i = 0; i < a.per; i++) {
@@ -212,10 +233,14 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
         uint32_t key[S], best = 0, choice = 0;  // choice: lane j's, the key of choice j
         int32_t pick = -1;                      // and its expert
         int slot = 0;
+        x = x_next;
 #pragma unroll
-        for (int s = 0; s < S; s++) {
-            v[s] = v_next[s];
-            key[s] = XKIND == FP8DL_BF16 ? route_key16(v[s], l * S + s) : route_key(v[s]);
+        for (int p = 0; p < PAIRS; p++) {
+            uint32_t lo, hi;
+            if (XKIND == FP8DL_BF16) route_keys16(x.w[p < Logits<XKIND, S>::WORDS ? p : 0], l * S + 2 * p, lo, hi);
+            else lo = route_key(x.pair(p).x), hi = route_key(x.pair(p).y);
+            key[2 * p] = lo;
+            if (2 * p + 1 < S) key[2 * p + 1 < S ? 2 * p + 1 : 0] = hi;
         }
         if (S < 16) load(i + 1);  // under way while this token's experts are chosen
         if (XKIND == FP8DL_BF16 && S <= 8) {  // the lane's keys in order once; the lane that had the largest moves up
@@ -261,24 +286,26 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
                 }
             }
         }
-        if (XKIND == FP8DL_BF16 && choice) pick = 0xffff - (int)(choice & 0xffff);
-        if (S >= 16) load(i + 1);
+        if (XKIND == FP8DL_BF16) {
+            if (choice < NONE16) choice = 0;
+            else pick = 0xffff - (int)(choice & 0xffff);
+        }
         const uint32_t top = __shfl_sync(0xffffffffu, choice, lane & ~(G - 1));
         const auto value = [](uint32_t c) { return XKIND == FP8DL_BF16 ? route_value16(c) : route_value(c); };
-        const float m = top ? value(top) : 0.0f;
-        float z = 0.0f;
+        const float m = top ? value(top) : 0.0f;  // nothing to choose: all -infinity or NaN, whose exponentials are 0 or NaN
+        float2 v[PAIRS], z2 = f2(0.0f);
 #pragma unroll
-        for (int s = 0; s < S; s++) {
-            v[s] = top ? route_exp(v[s], m) : v[s] == v[s] ? 0.0f : v[s];  // nothing to choose: 0, or NaN
-            z += v[s];
+        for (int p = 0; p < PAIRS; p++) {
+            v[p] = route_exp2(x.pair(p), m);
+            z2 = __fadd2_rn(z2, v[p]);
         }
-        z = group_sum<G>(z);
-        const float inv = top ? __frcp_rn(z) : 1.0f;
+        const float z = group_sum<G>(z2.x + z2.y), inv = top ? __frcp_rn(z) : 1.0f;
 #pragma unroll
-        for (int s = 0; s < S; s++) ps[s] = fmaf(v[s], inv, ps[s]);
+        for (int p = 0; p < PAIRS; p++) ps[p] = __ffma2_rn(v[p], f2(inv), ps[p]);
         const float e = pick >= 0 ? route_exp(value(choice), m) : 0.0f;
         const float chosen = group_sum<G>(e);
         if (l == 0 && top) n_counted++;
+        if (S >= 16) load(i + 1);
         if (here && l < k) {
             float w = 0.0f;
             int32_t rank = -1;
@@ -340,7 +367,7 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
     float *pf = reinterpret_cast<float *>(cnt);
 #pragma unroll
     for (int s = 0; s < S; s++)
-        if (l * S + s < E) pf[run * E + l * S + s] = ps[s];
+        if (l * S + s < E) pf[run * E + l * S + s] = s & 1 ? ps[s / 2].y : ps[s / 2].x;
     __syncthreads();
     for (int e = tid; e < E; e += THREADS) {
         float sum = 0.0f;
@@ -375,6 +402,18 @@ __global__ void __launch_bounds__(1024) route_rows_kernel(const RouteArgs a, int
         if (vec) return *reinterpret_cast<const int4 *>(at);
         return make_int4(at[0], e + 1 < E ? at[1] : 0, e + 2 < E ? at[2] : 0, e + 3 < E ? at[3] : 0);
     };
+    const int64_t lo = tile * tile_tokens * a.k, hi = min((tile + 1) * tile_tokens, a.tokens) * a.k;
+    constexpr int U = 2;
+    int32_t x[U], at[U];
+    const auto load = [&](int64_t i0) {  // U choices a thread and the ranks in their tile
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int64_t i = i0 + 1024 * u;
+            x[u] = i < hi ? a.expert[i] : -1;
+            at[u] = i < hi ? a.position[i] : -1;
+        }
+    };
+    load(lo + tid);  // the first ones while the tiles' counts add up
     if (e < E && part < parts) {
 #pragma unroll 10
         for (int i = part; i < tiles; i += parts) {
@@ -432,16 +471,7 @@ __global__ void __launch_bounds__(1024) route_rows_kernel(const RouteArgs a, int
     }
     if (tid < E) before[tid] += first[tid];
     __syncthreads();
-    const int64_t lo = tile * tile_tokens * a.k, hi = min((tile + 1) * tile_tokens, a.tokens) * a.k;
-    constexpr int U = 2;
     for (int64_t i0 = lo + tid; i0 < hi; i0 += 1024 * U) {
-        int32_t x[U], at[U];
-#pragma unroll
-        for (int u = 0; u < U; u++) {
-            const int64_t i = i0 + 1024 * u;
-            x[u] = i < hi ? a.expert[i] : -1;
-            at[u] = i < hi ? a.position[i] : -1;
-        }
 #pragma unroll
         for (int u = 0; u < U; u++) {
             const int64_t i = i0 + 1024 * u;
@@ -450,6 +480,7 @@ __global__ void __launch_bounds__(1024) route_rows_kernel(const RouteArgs a, int
             a.position[i] = at[u];
             a.token[at[u]] = (int32_t)((uint32_t)i / (uint32_t)a.k);
         }
+        load(i0 + 1024 * U);
     }
 }
 
@@ -459,7 +490,7 @@ template <int XKIND, int G, int S>
 __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteArgs a, const float *dweight, const float *dloss,
                                                         void *dlogits) {
     constexpr int NG = 256 / G, ESZ = XKIND == FP8DL_BF16 ? 2 : 4;
-    __shared__ float extra[NG][G * S];
+    __shared__ __align__(8) float extra[NG][G * S];
     const int E = a.experts, k = a.k, lane = threadIdx.x & 31, run = threadIdx.x / G, l = threadIdx.x % G, i0 = l * S;
     float *mine = extra[run];
 #pragma unroll
@@ -467,13 +498,18 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteArgs a, const
     pdl_wait();
     pdl_trigger();
     const float dl = dloss ? *dloss : 0.0f;
-    float even[S];
+    constexpr int PAIRS = Logits<XKIND, S>::PAIRS;
+    float2 even[PAIRS];
 #pragma unroll
-    for (int s = 0; s < S; s++) even[s] = dloss && i0 + s < E ? dl * a.slope[i0 + s] : 0.0f;
+    for (int p = 0; p < PAIRS; p++)
+        even[p] = make_float2(dloss && i0 + 2 * p < E ? dl * a.slope[i0 + 2 * p] : 0.0f,
+                              dloss && 2 * p + 1 < S && i0 + 2 * p + 1 < E ? dl * a.slope[i0 + 2 * p + 1] : 0.0f);
     __syncwarp();
+    const uint32_t gmask = G == 32 ? 0xffffffffu : ((1u << (G & 31)) - 1u) << (lane & ~(G - 1));
     const int64_t step = (int64_t)gridDim.x * NG, rounds = (a.tokens + step - 1) / step;
     int32_t pick_next;
-    float w_next, dw_next, v_next[S];
+    float w_next, dw_next;
+    Logits<XKIND, S> x_next;
     const auto load = [&](int64_t r) {  // of the group's token in round r
         const int64_t t = r * step + (int64_t)blockIdx.x * NG + run;
         const bool here = r < rounds && t < a.tokens;
@@ -484,12 +520,8 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteArgs a, const
             w_next = a.weight[t * k + l];
             if (dweight) dw_next = dweight[t * k + l];
         }
-        if (here) {
-            route_load<XKIND, S>(a.logits, t, E, i0, a.vec, v_next);
-        } else {
-#pragma unroll
-            for (int s = 0; s < S; s++) v_next[s] = rt::NEG_INF;
-        }
+        if (here) x_next.load(a.logits, t, E, i0, a.vec);
+        else x_next.none();
     };
     load(0);
     for (int64_t r = 0; r < rounds; r++) {
@@ -497,56 +529,59 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteArgs a, const
         const bool here = t < a.tokens;
         const int32_t pick = pick_next < E ? pick_next : -1;
         const float w = pick >= 0 ? w_next : 0.0f, dw = pick >= 0 ? dw_next : 0.0f;
-        float v[S], z = 0.0f, m = rt::NEG_INF;
-#pragma unroll
-        for (int s = 0; s < S; s++) {
-            v[s] = v_next[s];
-            m = fmaxf(m, v[s]);  // NaN does not count, as in the choice
-        }
+        const Logits<XKIND, S> x = x_next;
         if (S < 16) load(r + 1);  // under way meanwhile
         const bool some = __shfl_sync(0xffffffffu, pick, lane & ~(G - 1)) >= 0;
+        float m = rt::NEG_INF;
 #pragma unroll
-        for (int o = G / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int p = 0; p < PAIRS; p++) m = fmaxf(m, fmaxf(x.pair(p).x, x.pair(p).y));  // NaN does not count, as in the choice
+        m = group_max(m, gmask);
         if (!some) m = 0.0f;
+        float2 v[PAIRS], z2 = f2(0.0f), even2 = f2(0.0f);
 #pragma unroll
-        for (int s = 0; s < S; s++) {
-            v[s] = route_exp(v[s], m);
-            z += v[s];
+        for (int p = 0; p < PAIRS; p++) {
+            v[p] = route_exp2(x.pair(p), m);
+            z2 = __fadd2_rn(z2, v[p]);
+            even2 = __ffma2_rn(v[p], even[p], even2);
         }
-        z = group_sum<G>(z);
+        // three sums at once: of the exponentials, of theirs times the loss's slopes, and <dw, w>
+        float z = z2.x + z2.y, loss = even2.x + even2.y, dot = dw * w;
+#pragma unroll
+        for (int o = G / 2; o > 0; o >>= 1) {
+            z += __shfl_xor_sync(0xffffffffu, z, o);
+            loss += __shfl_xor_sync(0xffffffffu, loss, o);
+            dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        }
         const float inv = some ? __frcp_rn(z) : 0.0f;
+        // the chosen experts' part of <p, dp> is <dw, w>, and with `normalize` nothing: their weights add up to 1.  The first
+        // choice's weight is then 1 / (sum of the chosen exponentials)
         float d = dw;
-        if (a.normalize) {  // the first choice's weight is 1 / (sum of the chosen exponentials)
-            const float dot = group_sum<G>(dw * w), first = __shfl_sync(0xffffffffu, w, lane & ~(G - 1));
-            d = (dw - dot) * (z * first);
-        }
+        if (a.normalize) d = (dw - dot) * (z * __shfl_sync(0xffffffffu, w, lane & ~(G - 1)));
+        const float all = fmaf(dot, a.normalize ? 0.0f : 1.0f, loss * inv);
         if (pick >= 0) mine[pick] = d;
         __syncwarp();
-        float dp[S], dot = 0.0f;
 #pragma unroll
-        for (int s = 0; s < S; s++) {
-            dp[s] = even[s] + mine[i0 + s];
-            v[s] *= inv;
-            dot = fmaf(v[s], dp[s], dot);
+        for (int p = 0; p < PAIRS; p++) {
+            const float2 extra2 = S > 1 ? *reinterpret_cast<const float2 *>(mine + i0 + 2 * p) : make_float2(mine[i0], 0.0f);
+            v[p] = __fmul2_rn(__fmul2_rn(v[p], f2(inv)), __fadd2_rn(__fadd2_rn(even[p], extra2), f2(-all)));
+            if (!some) v[p] = f2(0.0f);
         }
-        dot = group_sum<G>(dot);
         __syncwarp();
         if (pick >= 0) mine[pick] = 0.0f;
         if (here && i0 < E) {
-#pragma unroll
-            for (int s = 0; s < S; s++) v[s] = some ? v[s] * (dp[s] - dot) : 0.0f;
             char *to = static_cast<char *>(dlogits) + (t * E + i0) * ESZ;
             if (a.vec && S * ESZ >= 4) {
-                uint32_t u[S * ESZ >= 4 ? S * ESZ / 4 : 1];
-                if constexpr (XKIND == FP8DL_BF16) {
+                constexpr int WORDS = Logits<XKIND, S>::WORDS;
+                uint32_t u[WORDS];
 #pragma unroll
-                    for (int s = 0; s + 1 < S; s += 2) {
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(v[s], v[s + 1]);
-                        u[s / 2] = *reinterpret_cast<const uint32_t *>(&h);
+                for (int p = 0; p < PAIRS; p++) {
+                    if (XKIND == FP8DL_BF16) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(v[p].x, v[p].y);
+                        u[p < WORDS ? p : 0] = *reinterpret_cast<const uint32_t *>(&h);
+                    } else {
+                        u[2 * p < WORDS ? 2 * p : 0] = __float_as_uint(v[p].x);
+                        if (S > 1) u[2 * p + 1 < WORDS ? 2 * p + 1 : 0] = __float_as_uint(v[p].y);
                     }
-                } else {
-#pragma unroll
-                    for (int s = 0; s < S; s++) u[s] = __float_as_uint(v[s]);
                 }
                 if constexpr (S * ESZ >= 16) {
 #pragma unroll
@@ -559,13 +594,12 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteArgs a, const
                 }
             } else {
 #pragma unroll
-                for (int s = 0; s < S; s++)
-                    if (i0 + s < E) {
-                        if (XKIND == FP8DL_BF16)
-                            reinterpret_cast<__nv_bfloat16 *>(to)[s] = __float2bfloat16_rn(v[s]);
-                        else
-                            reinterpret_cast<float *>(to)[s] = v[s];
-                    }
+                for (int s = 0; s < S; s++) {
+                    const float y = s & 1 ? v[s / 2].y : v[s / 2].x;
+                    if (i0 + s >= E) continue;
+                    if (XKIND == FP8DL_BF16) reinterpret_cast<__nv_bfloat16 *>(to)[s] = __float2bfloat16_rn(y);
+                    else reinterpret_cast<float *>(to)[s] = y;
+                }
             }
         }
         __syncwarp();

@@ -259,3 +259,25 @@ def test_first_calls_from_several_threads_and_streams():
     env["PYTHONPATH"] = ROOT + os.pathsep + env.get("PYTHONPATH", "")
     r = subprocess.run([sys.executable, "-c", SCRIPT], cwd=ROOT, env=env, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "threads ok" in r.stdout, r.stdout[-2000:] + r.stderr[-4000:]
+
+
+@pytest.mark.parametrize("E", [1, 6, 16, 24, 50, 64, 100, 200, 256, 400, 1024])
+def test_choices_among_all_bf16_values(E):
+    """Every bit pattern of bf16, subnormal ones, both zeros, infinities and NaN among them: the choices are those of the
+    values' order, equal ones by the lower expert."""
+    import fp8_delayed_scaling_gb300 as fd
+    dev = gpu()
+    k = min(E, 16)
+    T = max(200, 65536 // E + 1)
+    n = T * E
+    bits = torch.randperm(n, generator=wl.generator(436, "p%d" % E)) % 65536
+    bits[::5] = torch.tensor([0, 0x8000, 1, 0x8001, 0xff80, 0x7f80, 0x7fc0, 0xffc0])[torch.arange(bits[::5].numel()) % 8]
+    l = (bits - 65536 * (bits >= 32768)).to(torch.int16).view(torch.bfloat16).view(T, E)
+    with np.errstate(invalid="ignore"):
+        r = mr.route(l.double().numpy(), k)
+    b = Buffers(fd, T, E, k, dev)
+    b.run(fd, l.to(dev))
+    for name in ("expert", "position", "offsets", "counts"):
+        assert np.array_equal(getattr(b, name).cpu().numpy(), r[name]), name
+    nan = np.isnan(l.double().numpy()).any(1) | (l.double().numpy() == np.inf).any(1)
+    assert np.array_equal(np.isnan(host(b.weight))[:, 0], nan & r["has"][:, 0])
