@@ -486,8 +486,9 @@ __global__ void __launch_bounds__(1024) route_rows_kernel(const RouteArgs a, int
 
 // G lanes a token; the chosen experts' extra gradient reaches its lanes through shared memory, a row
 // of zeros per group of lanes that is cleared again.
+constexpr int bwd_ctas(int S) { return S <= 2 ? 5 : S == 4 ? 4 : S <= 16 ? 3 : 2; }  // of an SM: as many as its registers hold
 template <int XKIND, int G, int S>
-__global__ void __launch_bounds__(256) route_bwd_kernel(const RouteArgs a, const float *dweight, const float *dloss,
+__global__ void __launch_bounds__(256, bwd_ctas(S)) route_bwd_kernel(const RouteArgs a, const float *dweight, const float *dloss,
                                                         void *dlogits) {
     constexpr int NG = 256 / G, ESZ = XKIND == FP8DL_BF16 ? 2 : 4;
     __shared__ __align__(8) float extra[NG][G * S];
@@ -642,7 +643,7 @@ static fp8dl_status launch_route(const RouteArgs &a, int tiles, int64_t tile_tok
 template <int XKIND, int G, int S>
 static void launch_route_bwd(const RouteArgs &a, const float *dweight, const float *dloss, void *dlogits, int sms,
                              cudaStream_t st, bool pdl) {
-    const int64_t ctas = (a.tokens + 256 / G - 1) / (256 / G), most = (int64_t)sms * 8;
+    const int64_t ctas = (a.tokens + 256 / G - 1) / (256 / G), most = (int64_t)sms * bwd_ctas(S);
     (void)launch_kernel(route_bwd_kernel<XKIND, G, S>, dim3((unsigned)(ctas < most ? ctas : most)), dim3(256), 0, st, 0, pdl, a,
                         dweight, dloss, dlogits);
     note_launch();
@@ -750,8 +751,10 @@ extern "C" fp8dl_status moe_route_bwd(const void *logits, int32_t dtype, int64_t
     int sms = 0;
     FP8DL_TRY(current_device(nullptr, &sms));
     if (tokens == 0) return FP8DL_OK;
-    int g, s;
-    route_shape(n_experts, g, s);
+    // lanes of a token (a choice each) and experts of a lane: the fewest lanes that hold them eight each
+    const int g = n_experts <= 64 && k <= 8 ? 8 : n_experts <= 128 && k <= 16 ? 16 : 32;
+    int s = 1;
+    while (g * s < n_experts) s *= 2;
     RouteArgs a = {};
     a.logits = logits;
     a.tokens = tokens;
@@ -767,14 +770,21 @@ extern "C" fp8dl_status moe_route_bwd(const void *logits, int32_t dtype, int64_t
 #define FP8DL_ROUTE(g_, s_)                                                                             \
     dtype == FP8DL_BF16 ? launch_route_bwd<FP8DL_BF16, g_, s_>(a, dweight, dloss, dlogits, sms, st, pdl) \
                         : launch_route_bwd<FP8DL_F32, g_, s_>(a, dweight, dloss, dlogits, sms, st, pdl)
-    if (g == 8) FP8DL_ROUTE(8, 1);
-    else if (g == 16) FP8DL_ROUTE(16, 1);
-    else if (s == 1) FP8DL_ROUTE(32, 1);
-    else if (s == 2) FP8DL_ROUTE(32, 2);
-    else if (s == 4) FP8DL_ROUTE(32, 4);
-    else if (s == 8) FP8DL_ROUTE(32, 8);
-    else if (s == 16) FP8DL_ROUTE(32, 16);
-    else FP8DL_ROUTE(32, 32);
+#define FP8DL_LANES(g_)                 \
+    if (s == 1) FP8DL_ROUTE(g_, 1);      \
+    else if (s == 2) FP8DL_ROUTE(g_, 2); \
+    else if (s == 4) FP8DL_ROUTE(g_, 4); \
+    else if (s == 8) FP8DL_ROUTE(g_, 8)
+    if (g == 8) {
+        FP8DL_LANES(8);
+    } else if (g == 16) {
+        FP8DL_LANES(16);
+    } else {
+        FP8DL_LANES(32);
+        else if (s == 16) FP8DL_ROUTE(32, 16);
+        else FP8DL_ROUTE(32, 32);
+    }
+#undef FP8DL_LANES
 #undef FP8DL_ROUTE
     return check_launch("moe_route_bwd");
 }
