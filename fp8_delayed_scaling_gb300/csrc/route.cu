@@ -89,8 +89,7 @@ struct Logits {
 #pragma unroll
         for (int q = 0; q < WORDS; q++) w[q] = XKIND == FP8DL_BF16 ? 0xff80ff80u : 0xff800000u;
     }
-    __device__ __forceinline__ void load(const void *base, int64_t row, int E, int i0, bool vec) {
-        const char *p = static_cast<const char *>(base) + (row * E + i0) * ESZ;
+    __device__ __forceinline__ void load(const char *p, int E, int i0, bool vec) {  // p: logit i0 of a row of E
         none();
         if (vec && BYTES >= 4) {
             if (i0 >= E) return;  // E is a multiple of S: all of the lane's or none
@@ -221,15 +220,20 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
     for (int p = 0; p < PAIRS; p++) ps[p] = f2(0.0f);
     int n_counted = 0;
     Logits<XKIND, S> x, x_next;
-    const auto load = [&](int64_t i) {  // of token i of the run: -infinity where there is none
-        const int64_t t = t0 + i;
-        if (i < a.per && t < a.tokens && (!a.valid || a.valid[t])) x_next.load(a.logits, t, E, l * S, a.vec);
+    // tokens * k is below 2^31: so are the tokens of a run, and the places of their choices
+    const int per = (int)a.per, n_here = (int)min(max(a.tokens - t0, (int64_t)0), a.per);
+    const int row = E * Logits<XKIND, S>::ESZ;
+    const char *at_logits = static_cast<const char *>(a.logits) + t0 * row + l * S * Logits<XKIND, S>::ESZ;
+    const uint8_t *at_valid = a.valid ? a.valid + t0 : nullptr;
+    const auto load = [&](int i) {  // of token i of the run, one after the other: -infinity where there is none
+        if (i < n_here && (!at_valid || at_valid[i])) x_next.load(at_logits, E, l * S, a.vec);
         else x_next.none();
+        at_logits += row;
     };
     load(0);
-    for (int64_t i = 0; i < a.per; i++) {
-        const int64_t t = t0 + i;
-        const bool here = t < a.tokens;
+    uint32_t place = (uint32_t)(t0 * k) + l;
+    for (int i = 0; i < per; i++, place += k) {
+        const bool here = i < n_here;
         uint32_t key[S], best = 0, choice = 0;  // choice: lane j's, the key of choice j
         int32_t pick = -1;                      // and its expert
         int slot = 0;
@@ -245,12 +249,24 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
         if (S < 16) load(i + 1);  // under way while this token's experts are chosen
         if (XKIND == FP8DL_BF16 && S <= 8) {  // the lane's keys in order once; the lane that had the largest moves up
             sort_down(key);
-            for (int j = 0; j < k; j++) {
-                const uint32_t top = __reduce_max_sync(gmask, key[0]);
-                if (l == j) choice = top;
-                const bool mine = key[0] == top;
+            if (k <= S) {  // S - j keys of a lane still matter at choice j
 #pragma unroll
-                for (int s = 0; s < S; s++) key[s] = mine ? (s + 1 < S ? key[s + 1 < S ? s + 1 : s] : 0u) : key[s];
+                for (int j = 0; j < S; j++) {
+                    if (j >= k) break;
+                    const uint32_t top = __reduce_max_sync(gmask, key[0]);
+                    if (l == j) choice = top;
+                    const bool taken = key[0] == top;
+#pragma unroll
+                    for (int s = 0; s + 1 < S - j; s++) key[s] = taken ? key[s + 1] : key[s];
+                }
+            } else {
+                for (int j = 0; j < k; j++) {
+                    const uint32_t top = __reduce_max_sync(gmask, key[0]);
+                    if (l == j) choice = top;
+                    const bool taken = key[0] == top;
+#pragma unroll
+                    for (int s = 0; s < S; s++) key[s] = taken ? (s + 1 < S ? key[s + 1 < S ? s + 1 : s] : 0u) : key[s];
+                }
             }
         } else if (XKIND == FP8DL_BF16) {
 #pragma unroll
@@ -310,13 +326,13 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
             float w = 0.0f;
             int32_t rank = -1;
             if (pick >= 0) {
-                w = z == z ? (a.normalize ? __fdiv_rn(e, chosen) : e * inv) : z;
+                w = z == z ? e * (a.normalize ? __frcp_rn(chosen) : inv) : z;
                 rank = mine[pick];
                 mine[pick] = rank + 1;
             }
-            a.expert[t * k + l] = pick;
-            a.weight[t * k + l] = w;
-            a.position[t * k + l] = rank;
+            a.expert[place] = pick;
+            a.weight[place] = w;
+            a.position[place] = rank;
         }
         __syncwarp();
     }
@@ -345,19 +361,20 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
     }
     if (l < k) {
         constexpr int U = 8;  // tokens read at once
-        for (int64_t i0 = 0; i0 < a.per && t0 + i0 < a.tokens; i0 += U) {
+        place = (uint32_t)(t0 * k) + l;
+        for (int i0 = 0; i0 < n_here; i0 += U, place += U * k) {
             int32_t e[U], at[U];
 #pragma unroll
             for (int i = 0; i < U; i++) {
-                const bool ok = i0 + i < a.per && t0 + i0 + i < a.tokens;
-                e[i] = ok ? a.expert[(t0 + i0 + i) * k + l] : -1;
-                at[i] = ok ? a.position[(t0 + i0 + i) * k + l] : -1;
+                const bool ok = i0 + i < n_here;
+                e[i] = ok ? a.expert[place + i * k] : -1;
+                at[i] = ok ? a.position[place + i * k] : -1;
             }
 #pragma unroll
             for (int i = 0; i < U; i++) {
                 if (e[i] < 0) continue;
                 at[i] += mine[e[i]] + (SINGLE ? first[e[i]] : 0);
-                a.position[(t0 + i0 + i) * k + l] = at[i];
+                a.position[place + i * k] = at[i];
                 if (SINGLE) a.token[at[i]] = (int32_t)(t0 + i0 + i);
             }
         }
@@ -521,7 +538,7 @@ __global__ void __launch_bounds__(256, bwd_ctas(S)) route_bwd_kernel(const Route
             w_next = a.weight[t * k + l];
             if (dweight) dw_next = dweight[t * k + l];
         }
-        if (here) x_next.load(a.logits, t, E, i0, a.vec);
+        if (here) x_next.load(static_cast<const char *>(a.logits) + (t * E + i0) * ESZ, E, i0, a.vec);
         else x_next.none();
     };
     load(0);
