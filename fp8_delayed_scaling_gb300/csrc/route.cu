@@ -62,12 +62,13 @@ __device__ __forceinline__ float route_value16(uint32_t key) {
 __device__ __forceinline__ float route_exp(float v, float m) { return ex2_approx_ftz((v - m) * 1.4426950409f); }
 
 // S (1, 2, 4 or 8) keys into descending order: Batcher's odd-even merge exchange (19 exchanges for eight).
-__device__ __forceinline__ void exchange_down(uint32_t &a, uint32_t &b) {
-    const uint32_t hi = max(a, b), lo = min(a, b);
+template <typename T>
+__device__ __forceinline__ void exchange_down(T &a, T &b) {
+    const T hi = a > b ? a : b, lo = a > b ? b : a;
     a = hi, b = lo;
 }
-template <int S>
-__device__ __forceinline__ void sort_down(uint32_t (&k)[S]) {
+template <typename T, int S>
+__device__ __forceinline__ void sort_down(T (&k)[S]) {
 #pragma unroll
     for (int p = 1; p < S; p *= 2)
 #pragma unroll
@@ -161,8 +162,7 @@ __device__ __forceinline__ void scan_experts(const int32_t *total, int32_t *firs
     }
     if (lane == 31) warps[warp] = run;
     __syncthreads();
-    int32_t before = run - sum;
-    for (int w = 0; w < warp; w++) before += warps[w];
+    int32_t before = run - sum + __reduce_add_sync(0xffffffffu, lane < warp ? warps[lane] : 0);
 #pragma unroll
     for (int i = 0; i < PER; i++) {
         if (i0 + i < n) first[i0 + i] = before;
@@ -278,6 +278,36 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
                     best = 0;
 #pragma unroll
                     for (int s = 0; s < S; s++) best = max(best, key[s] < top ? key[s] : 0u);
+                }
+            }
+        } else if (S <= 8) {  // the same with the expert's place beside an fp32's key; of lanes with the largest the lowest moves up
+            uint64_t list[S];
+#pragma unroll
+            for (int s = 0; s < S; s++) list[s] = (uint64_t)key[s] << 32 | (uint32_t)(0xffff - (l * S + s));
+            sort_down(list);
+            const auto take = [&](int j) {
+                const uint32_t own = (uint32_t)(list[0] >> 32), top = __reduce_max_sync(gmask, own);
+                const int winner = __ffs(__ballot_sync(0xffffffffu, own == top) & gmask) - 1;
+                const uint32_t place_of = __shfl_sync(0xffffffffu, (uint32_t)list[0], winner);
+                if (l == j && top != 0) {
+                    choice = top;
+                    pick = 0xffff - (int)place_of;
+                }
+                return lane == winner;
+            };
+            if (k <= S) {
+#pragma unroll
+                for (int j = 0; j < S; j++) {
+                    if (j >= k) break;
+                    const bool taken = take(j);
+#pragma unroll
+                    for (int s = 0; s + 1 < S - j; s++) list[s] = taken ? list[s + 1] : list[s];
+                }
+            } else {
+                for (int j = 0; j < k; j++) {
+                    const bool taken = take(j);
+#pragma unroll
+                    for (int s = 0; s < S; s++) list[s] = taken ? (s + 1 < S ? list[s + 1 < S ? s + 1 : s] : 0u) : list[s];
                 }
             }
         } else {
