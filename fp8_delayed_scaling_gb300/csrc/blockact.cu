@@ -32,6 +32,17 @@ __device__ __forceinline__ void activation2(float2 a, float2 &y, float2 &d) {
     }
 }
 
+// cp.async of N bytes; none and zeros where !ok.
+template <int N, bool PAST_L1 = false>
+__device__ __forceinline__ void copy_async(void *smem, const void *global, bool ok) {
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+    if (PAST_L1)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(global), "r"(ok ? 16 : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(global), "n"(N), "r"(ok ? N : 0) : "memory");
+}
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // ---------------------------------------------------------------------------
 // act: blocks along the rows only, 16 lanes a block.
 // ---------------------------------------------------------------------------
@@ -48,23 +59,30 @@ struct BlockActArgs {
 
 namespace ba {
 constexpr int ACT_THREADS = 256, ACT_ROWS = 32;  // rows of a CTA: two for each 16 lanes
+constexpr int ACT_CTAS = 3;                       // CTAs an SM holds
 }
 
-// Eight columns of a row in fp32; zeros where there are none.
-template <int XKIND>
-__device__ __forceinline__ void load8(const void *base, int64_t at, bool ok, float2 (&v)[4]) {
+// Eight columns of a row in fp32, of UNITS 16-byte units as they lie in memory.
+template <int XKIND, typename Unit>
+__device__ __forceinline__ void widen8(const Unit &unit, float2 (&v)[4]) {
     if (XKIND == FP8DL_BF16) {
-        const uint4 u = ok ? ldg_stream(static_cast<const char *>(base) + at * 2) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 u = unit(0);
         v[0] = make_float2(bf16_lo(u.x), bf16_hi(u.x)), v[1] = make_float2(bf16_lo(u.y), bf16_hi(u.y));
         v[2] = make_float2(bf16_lo(u.z), bf16_hi(u.z)), v[3] = make_float2(bf16_lo(u.w), bf16_hi(u.w));
     } else {
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            const uint4 u = ok ? ldg_stream(static_cast<const char *>(base) + at * 4 + 16 * h) : make_uint4(0u, 0u, 0u, 0u);
+            const uint4 u = unit(h);
             v[2 * h] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
             v[2 * h + 1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
         }
     }
+}
+// The same from memory; zeros where there are none.
+template <int XKIND>
+__device__ __forceinline__ void load8(const void *base, int64_t at, bool ok, float2 (&v)[4]) {
+    const char *p = static_cast<const char *>(base) + at * (XKIND == FP8DL_BF16 ? 2 : 4);
+    widen8<XKIND>([&](int h) { return ok ? ldg_stream(p + 16 * h) : make_uint4(0u, 0u, 0u, 0u); }, v);
 }
 
 // The blocks along the rows that 16 lanes hold together, eight values each: NA matrices, two rows of each.  Their maxima
@@ -119,69 +137,96 @@ __device__ __forceinline__ float put_blocks(const float2 (&v)[2][NA][4], uint8_t
     return sc.y;
 }
 
-// A CTA takes 32 rows of one block column (of a's and of u's where g is gated), two neighbouring rows for 16 lanes.
+// Persistent CTAs, a job of 32 rows of one block column (of a's and of u's where g is gated) after the other, two
+// neighbouring rows for 16 lanes.  Each thread copies its values of the next job into its own slots of shared memory
+// while it works on this one's (no barrier, no registers).
 // Where u's half does not start on a block (cols not a multiple of 128: `split`) h's blocks do not line up with
 // g's: the codes of h are jobs of their own behind g's.  KEEP: with the codes of h.
-// Bound: HBM.
 template <int XKIND, int FMT, bool GATED, bool SILU, bool KEEP>
-__global__ void __launch_bounds__(ba::ACT_THREADS) block_act_kernel(const BlockActArgs a) {
+__global__ void __launch_bounds__(ba::ACT_THREADS, ba::ACT_CTAS) block_act_kernel(const BlockActArgs a) {
     using namespace ba;
-    constexpr int NA = KEEP ? (GATED ? 3 : 2) : 1;
+    constexpr int NA = KEEP ? (GATED ? 3 : 2) : 1, NH = GATED ? 2 : 1, UNITS = XKIND == FP8DL_BF16 ? 1 : 2, ESZ = XKIND == FP8DL_BF16 ? 2 : 4;
+    __shared__ uint4 in[2 * NH * UNITS][ACT_THREADS];  // [row][a, u][unit]
     pdl_wait();
     pdl_trigger();
-    const uint32_t tile = blockIdx.x / a.jobs, job = blockIdx.x % a.jobs, g_jobs = (uint32_t)((a.cols + 127) / 128);
-    const uint32_t cols = (uint32_t)a.cols, wide = (uint32_t)a.wide, rows = (uint32_t)a.rows;
+    const int tid = threadIdx.x;
+    const uint32_t g_jobs = (uint32_t)((a.cols + 127) / 128), cols = (uint32_t)a.cols, wide = (uint32_t)a.wide, rows = (uint32_t)a.rows;
     int64_t first = 0, end = a.rows;
     if (a.offsets) {  // blocks along the rows do not see the groups' borders
         group_rows(a.offsets, 0, a.rows, first, end);
         end = min(max((int64_t)a.offsets[a.n_groups], first), a.rows);
     }
-    if (first + (int64_t)tile * ACT_ROWS >= end) return;
-    const uint32_t r = (uint32_t)first + tile * ACT_ROWS + 2 * (threadIdx.x >> 4);  // below 2^31 + 32
-    const bool row0 = r < (uint32_t)end, row1 = r + 1 < (uint32_t)end;
-    const uint32_t c = (job < g_jobs ? job : job - g_jobs) * 128 + 8 * (threadIdx.x & 15);
-    if (job >= g_jobs) {  // h alone
-        float2 v[2][1][4];
-        const bool there = c < wide;
-        load8<XKIND>(a.h, wide_mul(r, wide) + c, row0 && there, v[0][0]);
-        load8<XKIND>(a.h, wide_mul(r + 1, wide) + c, row1 && there, v[1][0]);
-        uint8_t *const q[1] = {a.h_q + wide_mul(r, wide) + c};
-        const uint32_t ld[1] = {wide};
-        const float f = put_blocks<FMT, 1>(v, q, ld, row0 && there, row1 && there);
-        if ((threadIdx.x & 7) == 0 && (threadIdx.x & 8 ? row1 : row0)) a.h_s[wide_mul(c >> 7, rows) + r + (threadIdx.x >> 3 & 1)] = f;
-        return;
-    }
-    float2 h[2][2][4], v[2][NA][4];
-    const bool there = c < cols, ok0 = row0 && there, ok1 = row1 && there;
-    const uint64_t at = wide_mul(r, wide) + c;
+    const uint32_t last = (uint32_t)end, tiles = (uint32_t)((end - first + ACT_ROWS - 1) / ACT_ROWS), jobs = a.jobs;
+    const auto row_of = [&](uint32_t tile) { return (uint32_t)first + tile * ACT_ROWS + 2 * (tid >> 4); };  // below 2^31 + 32
+    const auto col_of = [&](uint32_t job) { return (job < g_jobs ? job : job - g_jobs) * 128 + 8 * (tid & 15); };
+    const auto fetch = [&](uint32_t tile, uint32_t job) {
+        const uint32_t r = row_of(tile), c = col_of(job);
+        const bool there = c < (job < g_jobs ? cols : wide);
+        const char *p = static_cast<const char *>(a.h) + (wide_mul(r, wide) + c) * ESZ;
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
-        load8<XKIND>(a.h, at + (i ? wide : 0), i ? ok1 : ok0, h[i][0]);
-        if (GATED) load8<XKIND>(a.h, at + (i ? wide : 0) + cols, i ? ok1 : ok0, h[i][1]);
-    }
+        for (int i = 0; i < 2; i++)
 #pragma unroll
-    for (int i = 0; i < 2; i++)
+            for (int n = 0; n < NH; n++) {
+                if (n && job >= g_jobs) continue;
+                const bool ok = r + i < last && there;
 #pragma unroll
-        for (int p = 0; p < 4; p++) {
-            float2 none;
-            activation2<SILU, false>(h[i][0][p], v[i][0][p], none);
-            if (GATED) v[i][0][p] = make_float2(v[i][0][p].x * h[i][1][p].x, v[i][0][p].y * h[i][1][p].y);
-            if (NA > 1) v[i][NA > 1 ? 1 : 0][p] = h[i][0][p];
-            if (NA > 2) v[i][NA > 2 ? 2 : 0][p] = h[i][1][p];
+                for (int u = 0; u < UNITS; u++)
+                    copy_async<16, UNITS == 1>(&in[(i * NH + n) * UNITS + u][tid], ok ? p + ((i ? wide : 0) + (uint64_t)(n ? cols : 0)) * ESZ + 16 * u : a.h, ok);
+            }
+    };
+    uint32_t tile = blockIdx.x / jobs, job = blockIdx.x - tile * jobs;
+    const uint32_t tile_step = gridDim.x / jobs, job_step = gridDim.x - tile_step * jobs;
+    if (tile < tiles) fetch(tile, job);
+    while (tile < tiles) {
+        const uint32_t r = row_of(tile), c = col_of(job);
+        const bool row0 = r < last, row1 = r + 1 < last, alone = job >= g_jobs;
+        copy_wait_all();
+        float2 h[2][NH][4];
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int n = 0; n < NH; n++) widen8<XKIND>([&](int u) { return in[(i * NH + n) * UNITS + u][tid]; }, h[i][n]);
+        tile += tile_step, job += job_step;
+        if (job >= jobs) job -= jobs, tile++;
+        if (tile < tiles) fetch(tile, job);
+        if (alone) {  // h alone
+            float2 v[2][1][4];
+#pragma unroll
+            for (int p = 0; p < 4; p++) v[0][0][p] = h[0][0][p], v[1][0][p] = h[1][0][p];
+            const bool there = c < wide;
+            uint8_t *const q[1] = {a.h_q + wide_mul(r, wide) + c};
+            const uint32_t ld[1] = {wide};
+            const float f = put_blocks<FMT, 1>(v, q, ld, row0 && there, row1 && there);
+            if ((tid & 7) == 0 && (tid & 8 ? row1 : row0)) a.h_s[wide_mul(c >> 7, rows) + r + (tid >> 3 & 1)] = f;
+            continue;
         }
-    uint8_t *q[NA];
-    uint32_t ld[NA];
-    q[0] = a.g_q + wide_mul(r, cols) + c, ld[0] = cols;
-    if (NA > 1) q[NA > 1 ? 1 : 0] = a.h_q + at, ld[NA > 1 ? 1 : 0] = wide;
-    if (NA > 2) q[NA > 2 ? 2 : 0] = a.h_q + at + cols, ld[NA > 2 ? 2 : 0] = wide;
-    uint8_t *const(&qc)[NA] = reinterpret_cast<uint8_t *const(&)[NA]>(q);
-    // a block's factor is written even by a lane that has none of its columns (the last block may be short)
-    const float f = put_blocks<FMT, NA>(v, qc, ld, ok0, ok1);
-    constexpr int N = 2 * NA, P = N <= 2 ? 2 : N <= 4 ? 4 : 8, S = 16 / P;
-    const int mine = (threadIdx.x & 15) / S, i = mine >= NA, n = mine - i * NA;
-    if ((threadIdx.x & (S - 1)) == 0 && mine < N && (i ? row1 : row0)) {
-        float *s = n == 0 ? a.g_s : a.h_s;
-        s[wide_mul((c + (n == 2 ? cols : 0)) >> 7, rows) + r + i] = f;
+        float2 v[2][NA][4];
+        const bool there = c < cols, ok0 = row0 && there, ok1 = row1 && there;
+        const uint64_t at = wide_mul(r, wide) + c;
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int p = 0; p < 4; p++) {
+                float2 none;
+                activation2<SILU, false>(h[i][0][p], v[i][0][p], none);
+                if (GATED) v[i][0][p] = make_float2(v[i][0][p].x * h[i][NH - 1][p].x, v[i][0][p].y * h[i][NH - 1][p].y);
+                if (NA > 1) v[i][NA > 1 ? 1 : 0][p] = h[i][0][p];
+                if (NA > 2) v[i][NA > 2 ? 2 : 0][p] = h[i][NH - 1][p];
+            }
+        uint8_t *q[NA];
+        uint32_t ld[NA];
+        q[0] = a.g_q + wide_mul(r, cols) + c, ld[0] = cols;
+        if (NA > 1) q[NA > 1 ? 1 : 0] = a.h_q + at, ld[NA > 1 ? 1 : 0] = wide;
+        if (NA > 2) q[NA > 2 ? 2 : 0] = a.h_q + at + cols, ld[NA > 2 ? 2 : 0] = wide;
+        uint8_t *const(&qc)[NA] = reinterpret_cast<uint8_t *const(&)[NA]>(q);
+        // a block's factor is written even by a lane that has none of its columns (the last block may be short)
+        const float f = put_blocks<FMT, NA>(v, qc, ld, ok0, ok1);
+        constexpr int N = 2 * NA, P = N <= 2 ? 2 : N <= 4 ? 4 : 8, S = 16 / P;
+        const int mine = (tid & 15) / S, i = mine >= NA, n = mine - i * NA;
+        if ((tid & (S - 1)) == 0 && mine < N && (i ? row1 : row0)) {
+            float *s = n == 0 ? a.g_s : a.h_s;
+            s[wide_mul((c + (n == 2 ? cols : 0)) >> 7, rows) + r + i] = f;
+        }
     }
 }
 
@@ -619,13 +664,6 @@ __device__ __forceinline__ float2 pair_of(uint2 u, int p, float f) {
     return p == 0 ? value2<E4, false>(u.x, f) : p == 1 ? value2<E4, true>(u.x, f) : p == 2 ? value2<E4, false>(u.y, f) : value2<E4, true>(u.y, f);
 }
 
-// cp.async of N bytes; none and zeros where !ok.
-template <int N>
-__device__ __forceinline__ void copy_async(void *smem, const void *global, bool ok) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(smem))), "l"(global), "n"(N), "r"(ok ? N : 0) : "memory");
-}
-__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
 // Row-wise codes to transposed ones: persistent CTAs, four per SM, walk 128 x 128 tiles.  Thread (rr, cc) of 16 x 16 holds
 // the codes of rows 8rr .. 8rr+7, columns 8cc .. 8cc+7 and decodes them twice, for the column maxima (8 rows in the
 // thread, two row groups by shuffle, eight warps through shared memory) and for the new codes: kept as fp32 they
@@ -816,7 +854,9 @@ extern "C" fp8dl_status fp8_block_act(const void *h, int32_t h_dtype, int32_t ac
     a.jobs = (uint32_t)((cols + 127) / 128 + (a.split && h_q ? (a.wide + 127) / 128 : 0));
     const int64_t ctas = (rows + ba::ACT_ROWS - 1) / ba::ACT_ROWS * a.jobs;
     FP8DL_TRY(check_tiles(ctas, rows, cols));
-    FP8DL_TRY(current_device(nullptr, nullptr));
+    int sms = 0;
+    FP8DL_TRY(current_device(nullptr, &sms));
+    const int64_t resident = (int64_t)sms * ba::ACT_CTAS;
     if (rows == 0) return FP8DL_OK;
     const bool pdl = short_call_bytes((double)rows * a.wide * ((h_dtype == FP8DL_BF16 ? 2.0 : 4.0) + (h_q ? 1.0 : 0.0)) + (double)rows * cols);
     const bool keep = h_q && !a.split;
@@ -831,7 +871,7 @@ extern "C" fp8dl_status fp8_block_act(const void *h, int32_t h_dtype, int32_t ac
     else FP8DL_ACT(FP8DL_F32, FP8DL_E5M2);
 #undef FP8DL_ACT
 #undef FP8DL_ACT_KEEP
-    (void)launch_kernel(kernel, dim3((unsigned)ctas), dim3(ba::ACT_THREADS), 0, (cudaStream_t)stream, 0, pdl, a);
+    (void)launch_kernel(kernel, dim3((unsigned)(ctas < resident ? ctas : resident)), dim3(ba::ACT_THREADS), 0, (cudaStream_t)stream, 0, pdl, a);
     note_launch();
     return check_launch("fp8_block_act");
 }
