@@ -209,10 +209,11 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
     const uint32_t gmask = G == 32 ? 0xffffffffu : ((1u << (G & 31)) - 1u) << (lane & ~(G - 1));
     pdl_wait();
     pdl_trigger();
-    for (int i = tid; i < NG * E; i += THREADS) cnt[i] = 0;
+    const int64_t tile0 = (int64_t)blockIdx.x * NG * a.per, t0 = tile0 + run * a.per;
+    const int runs = (int)min((a.tokens - tile0 + a.per - 1) / a.per, (int64_t)NG);  // those that have tokens
+    for (int i = tid; i < runs * E; i += THREADS) cnt[i] = 0;
     if (tid == 0) counted = 0;
     __syncthreads();
-    const int64_t t0 = ((int64_t)blockIdx.x * NG + run) * a.per;
     int32_t *mine = cnt + run * E;
     constexpr int PAIRS = Logits<XKIND, S>::PAIRS;
     float2 ps[PAIRS];
@@ -368,17 +369,35 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
     }
     if (n_counted) atomicAdd(&counted, n_counted);
     __syncthreads();
-    for (int e = tid; e < E; e += THREADS) {  // the runs before each run
-        int32_t sum = 0;
-        for (int g = 0; g < NG; g++) {
-            const int32_t c = cnt[g * E + e];
-            cnt[g * E + e] = sum;
-            sum += c;
+    int32_t *sums = SINGLE ? total : a.hist + (int)blockIdx.x * E;
+    if (G == 32) {  // the runs before each run: 16 or 32 of them, a thread per expert
+        for (int e = tid; e < E; e += THREADS) {
+            int32_t sum = 0;
+#pragma unroll 8
+            for (int g = 0; g < runs; g++) {
+                const int32_t c = cnt[g * E + e];
+                cnt[g * E + e] = sum;
+                sum += c;
+            }
+            sums[e] = sum;
         }
-        if (SINGLE)
-            total[e] = sum;
-        else
-            a.hist[(int)blockIdx.x * E + e] = sum;
+    } else {  // 64 or 128 runs, a warp per expert
+        for (int e = tid >> 5; e < E; e += THREADS / 32) {
+            int32_t sum = 0;
+            for (int g0 = 0; g0 < runs; g0 += 32) {
+                const bool ok = g0 + lane < runs;
+                const int32_t c = ok ? cnt[(g0 + lane) * E + e] : 0;
+                int32_t upto = c;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int32_t u = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += u;
+                }
+                if (ok) cnt[(g0 + lane) * E + e] = sum + upto - c;
+                sum += __shfl_sync(0xffffffffu, upto, 31);
+            }
+            if (lane == 0) sums[e] = sum;
+        }
     }
     if (!SINGLE && tid == 0) a.counted[blockIdx.x] = counted;
     __syncthreads();
@@ -414,19 +433,27 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
     float *pf = reinterpret_cast<float *>(cnt);
 #pragma unroll
     for (int s = 0; s < S; s++)
-        if (l * S + s < E) pf[run * E + l * S + s] = s & 1 ? ps[s / 2].y : ps[s / 2].x;
+        if (l * S + s < E && run < runs) pf[run * E + l * S + s] = s & 1 ? ps[s / 2].y : ps[s / 2].x;
     __syncthreads();
-    for (int e = tid; e < E; e += THREADS) {
-        float sum = 0.0f;
-        for (int g = 0; g < NG; g++) sum += pf[g * E + e];
-        if (SINGLE)
-            pf[e] = sum;  // (run 0's own entry, read by this thread alone)
-        else
-            a.psum[(int)blockIdx.x * E + e] = sum;
+    float *psum = SINGLE ? reinterpret_cast<float *>(first) : a.psum + (int)blockIdx.x * E;  // first's rows are done with
+    if (G == 32) {
+        for (int e = tid; e < E; e += THREADS) {
+            float sum = 0.0f;
+#pragma unroll 8
+            for (int g = 0; g < runs; g++) sum += pf[g * E + e];
+            psum[e] = sum;
+        }
+    } else {
+        for (int e = tid >> 5; e < E; e += THREADS / 32) {
+            float sum = 0.0f;
+            for (int g = lane; g < runs; g += 32) sum += pf[g * E + e];
+            sum = group_sum<32>(sum);
+            if (lane == 0) psum[e] = sum;
+        }
     }
     if (SINGLE) {
         __syncthreads();
-        balance<THREADS>(a, total, pf, counted, first[E], reinterpret_cast<float *>(warps));
+        balance<THREADS>(a, total, psum, counted, first[E], reinterpret_cast<float *>(warps));
     }
 }
 
