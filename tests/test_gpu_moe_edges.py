@@ -281,3 +281,50 @@ def test_choices_among_all_bf16_values(E):
         assert np.array_equal(getattr(b, name).cpu().numpy(), r[name]), name
     nan = np.isnan(l.double().numpy()).any(1) | (l.double().numpy() == np.inf).any(1)
     assert np.array_equal(np.isnan(host(b.weight))[:, 0], nan & r["has"][:, 0])
+
+
+@pytest.mark.parametrize("act", [0, 2])
+def test_gelu_of_blocks_that_hold_small_results_only(act):
+    """Blocks of one value each from -13 to 13: their factors are the results, to a relative error.  In units of 2^-24:
+    the exponent's two roundings and its constant (3 of a^2 / 2), 2^x (4), the ratio (9 and 1/x: 3), products (4) and
+    the factor (4).  The derivative's difference of ratio and phi(0) x is at most 2.2 times smaller than their sum
+    beyond |a| = 1.5."""
+    import math
+
+    import fp8_delayed_scaling_gb300 as fd
+    dev = gpu()
+    R, C = 2601, 16
+    a = torch.linspace(-13, 13, R)
+    q, s = torch.full((R, C), 0x38, dtype=torch.uint8), a.abs().view(1, R)  # the code of 1, -1 where a < 0
+    q[a < 0] = 0xb8
+    gated = act == 2
+    hq = torch.cat([q, torch.full((R, C), 0x38, dtype=torch.uint8)], 1) if gated else q
+    hs = s  # 2 C columns are one block: u = |a| too
+    W = hq.shape[1]
+    groups = 1024
+    v = a.double().numpy()
+    u = np.abs(v) if gated else np.ones(R)
+    e = np.exp(-v * v / 2)
+    cdf = np.array([0.5 * math.erfc(-x / math.sqrt(2)) for x in v])
+    y, d = v * cdf * u, (cdf + v * e / math.sqrt(2 * math.pi)) * u
+    tol = (1.5 * v * v + 30) * mr.EPS
+    h = (torch.cat([a[:, None].expand(R, C), a.abs()[:, None].expand(R, C)], 1) if gated else a[:, None].expand(R, C)).contiguous()
+    gq, gs = torch.zeros((R, C), dtype=torch.uint8, device=dev), torch.zeros((1, R), device=dev)
+    fd.fp8_block_act(h.to(dev), act, 0, gq, gs)
+    small = np.abs(y) > 2.0 ** -99  # a block's scale is that of a maximum of 2^-100 at least: below it the factor says nothing
+    got = host(gs)[0] * 448
+    assert np.all((np.abs(got - np.abs(y)) <= tol * np.abs(y))[small & (v != 0)])
+    # backward: groups of one row, so that a column's block holds one value
+    for lo in range(0, R, groups):
+        n = min(groups, R - lo)
+        off = torch.arange(n + 1, dtype=torch.int32, device=dev)
+        T = fd.fp8_block_padded_rows(n, n)
+        gt, gts = torch.zeros((C, T), dtype=torch.uint8, device=dev), torch.zeros((T // 128, C), device=dev)
+        dt, dts = torch.zeros((W, T), dtype=torch.uint8, device=dev), torch.zeros((T // 128, W), device=dev)
+        fd.fp8_block_dact(torch.ones((n, C), device=dev), hq[lo:lo + n].contiguous().to(dev), 0, hs[:, lo:lo + n].contiguous().to(dev), act, 0,
+                          dh_qt=dt, dh_st=dts, g_qt=gt, g_st=gts, offsets=off)
+        at = slice(lo, lo + n)
+        w = small[at] & (v[at] != 0)
+        assert np.all((np.abs(host(gts)[:n, 0] * 448 - np.abs(y[at])) <= tol[at] * np.abs(y[at]))[w])
+        far = w & (np.abs(v[at]) > 1.5) & (np.abs(d[at]) > 2.0 ** -99)
+        assert np.all((np.abs(host(dts)[:n, 0] * 448 - np.abs(d[at])) <= 2.2 * tol[at] * np.abs(d[at]))[far])
