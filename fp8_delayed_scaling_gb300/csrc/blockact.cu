@@ -161,6 +161,10 @@ __device__ __forceinline__ float put_blocks(const float2 (&v)[2][NA][4], uint8_t
 // while it works on this one's (no barrier, no registers).
 // Where u's half does not start on a block (cols not a multiple of 128: `split`) h's blocks do not line up with
 // g's: the codes of h are jobs of their own behind g's.  KEEP: with the codes of h.
+// Bound: HBM, SwiGLU of 8192 x 11008 in bf16 with the checkpoint: 100 us, 6.4 TB/s, without it 69 us, 6.6 TB/s (a CTA a
+// job, loads into registers: 118 and 79); GELU of 8192 x 16384 127 us, 4.3 TB/s: the issue slots.
+// The 16 bytes of a thread go past L1 where they are whole sectors' worth; two halves of fp32 values go through it (past
+// it every sector is fetched twice: 8192 x 8192 182 us against 112).
 template <int XKIND, int FMT, bool GATED, bool SILU, bool KEEP>
 __global__ void __launch_bounds__(ba::ACT_THREADS, ba::ACT_CTAS) block_act_kernel(const BlockActArgs a) {
     using namespace ba;
@@ -345,7 +349,6 @@ __device__ __forceinline__ void gradient2(uint32_t ha, float fa, uint32_t hu, fl
     }
 }
 
-
 // Codes of N (one or two) matrices along the rows: two rows of eight values a thread, 16 lanes a row.  q, s: the first
 // matrix's code and factor of the thread's first row; the second's lie q1, s1 further on, and are left out unless
 // `both`.  Each lane works out one scale: of row (lane >> 3 & 1), of matrix (lane >> 2 & 1) where there are two.
@@ -432,7 +435,10 @@ __device__ __forceinline__ uint4 put_column(const float2 (&v)[8], float &factor)
 //            whole 128-byte line).  The next tile's values are loaded into registers meanwhile.
 // Shared memory holds pairs of rows, so that the column phase reads two values at once; 16-byte units are XORed by
 // unit / 8 and by row / 16: both phases hit 32 banks.
-// Bound: the issue slots.
+// Bound: the issue slots (71% in use, 60 instructions a value of g).  SwiGLU of 8192 x 11008 in bf16 with dbias: 196 us,
+// 4.2 TB/s; GELU of 8192 x 16384 252 us; 2999 x 1408 in 24 groups, GELU 17 us (three rounds of tiles).  Slower at the
+// first of these: values kept in registers by 512 threads (305 us), CTA pairs that share the rows' maxima over distributed
+// shared memory with two CTAs an SM (421), short tiles with fewer lanes a column (205), packed products (207).
 namespace bd {
 constexpr int THREADS = 1024, TILE = 128;
 }
@@ -567,7 +573,8 @@ __global__ void __launch_bounds__(bd::THREADS, 1) block_dact_kernel(const BlockD
 
 // Blocks of dh along the rows, a.row_jobs of a row from a.row_first on: all of them where nothing else is
 // wanted; those of u's half (and the one that holds the border) where cols is not a multiple of 128 and
-// the tiles above do not hold whole blocks.  16 lanes a block, two rows of each in flight.
+// the tiles above do not hold whole blocks.  16 lanes a block, two rows of each in flight.  (8192 x 11024: 308 us for both
+// kernels, 196 where the blocks line up.)
 template <int FMT, bool GATED, bool SILU>
 __global__ void __launch_bounds__(ba::ACT_THREADS) block_dact_rows_kernel(const BlockDactArgs a) {
     using namespace ba;
@@ -689,7 +696,9 @@ __device__ __forceinline__ float2 pair_of(uint2 u, int p, float f) {
 // would take 64 registers and leave two CTAs an SM.  The new codes go through shared memory in 8-byte pieces XORed by
 // column group and leave as whole 128-byte lines.  Each thread copies the next tile's codes into its own slots of
 // shared memory meanwhile (no barrier, no registers), and reads the indices of the one after it.
-// Bound: the issue slots (about 13 instructions a value).
+// Bound: the issue slots (62% in use, 12 instructions a value) and the three barriers a tile.  32768 x 4096 in 16 groups
+// through an index: 66 us, 3.1 TB/s (64 values a thread without the walk 134, bulk copies of the rows 71, eight-byte
+// factors 69); 3001 x 2048 5.7 us.
 namespace br {
 constexpr int THREADS = 256, TILE = 128;
 }
@@ -737,91 +746,91 @@ __global__ void __launch_bounds__(br::THREADS, 4) block_recode_kernel(const Bloc
     fetch(walk.step[0], 0);
     look(walk.step[1]);
     for (int cur = 0, slot = 0; walk.step[cur].n; slot ^= 1) {
-    const int next = cur == 2 ? 0 : cur + 1, after = next == 2 ? 0 : next + 1, n = walk.step[cur].n;
-    const bool busy = 16 * warp < n;  // the warp has rows
-    copy_wait_all();
-    __syncwarp();  // a row's factor is another lane's copy
-    uint2 u[8];
+        const int next = cur == 2 ? 0 : cur + 1, after = next == 2 ? 0 : next + 1, n = walk.step[cur].n;
+        const bool busy = 16 * warp < n;  // the warp has rows
+        copy_wait_all();
+        __syncwarp();  // a row's factor is another lane's copy
+        uint2 u[8];
 #pragma unroll
-    for (int i = 0; i < 8; i++) u[i] = in[i][tid];
-    if (walk.step[next].n) fetch(walk.step[next], slot ^ 1);
-    const float *f = &fac[slot][8 * rr];
-    float m[8];
+        for (int i = 0; i < 8; i++) u[i] = in[i][tid];
+        if (walk.step[next].n) fetch(walk.step[next], slot ^ 1);
+        const float *f = &fac[slot][8 * rr];
+        float m[8];
 #pragma unroll
-    for (int j = 0; j < 8; j++) m[j] = 0.0f;
-    if (busy) {
+        for (int j = 0; j < 8; j++) m[j] = 0.0f;
+        if (busy) {
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            const float2 k = *reinterpret_cast<const float2 *>(f + i);
+            for (int i = 0; i < 8; i += 2) {
+                const float2 k = *reinterpret_cast<const float2 *>(f + i);
 #pragma unroll
-            for (int p = 0; p < 4; p++) {
-                float2 x = pair_of<E4>(u[i], p, k.x), y = pair_of<E4>(u[i + 1], p, k.y);
-                // an infinity turns into NaN, which does not count
-                x = __ffma2_rn(x, f2(0.0f), x), y = __ffma2_rn(y, f2(0.0f), y);
-                m[2 * p] = max3(m[2 * p], x.x, y.x), m[2 * p + 1] = max3(m[2 * p + 1], x.y, y.y);
-            }
-        }
-        const bool up = lane & 16;
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const float send = up ? m[j] : m[j + 4], keep = up ? m[j + 4] : m[j];
-            m[j] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, 16));
-        }
-    }
-    *reinterpret_cast<float4 *>(&part[warp][8 * cc + (lane & 16 ? 4 : 0)]) = make_float4(m[0], m[1], m[2], m[3]);
-    __syncthreads();
-    if (tid < TILE) {
-        float t = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 8; w += 2) t = max3(t, part[w][tid], part[w + 1][tid]);
-        const float2 sc = block_scale_fast<FMT>(t);
-        scale[tid] = sc.x;
-        const uint32_t c = walk.step[cur].col * TILE + tid;
-        if (c < cols) a.col_s[wide_mul(walk.step[cur].tile, cols) + c] = sc.y;
-    } else if (tid == TILE) {
-        walk_on(walk, table, a.offsets, a.rows, a.across, next, after);
-    }
-    __syncthreads();
-    look(walk.step[after]);
-    uint8_t *at = code + 8 * cc * TILE + ((rr ^ cc) << 3);
-    if (busy) {
-#pragma unroll
-        for (int p = 0; p < 4; p++) {  // columns 8cc + 2p and the next, four rows at a time
-            const float2 sc = *reinterpret_cast<const float2 *>(&scale[8 * cc + 2 * p]);
-            uint32_t w[2][2];
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const float4 k = *reinterpret_cast<const float4 *>(f + 4 * h);
-                float2 y[4];
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    asm volatile("" : "+r"(u[4 * h + i].x), "+r"(u[4 * h + i].y)::"memory");  // decoded again, not kept
-                    const float2 x = pair_of<E4>(u[4 * h + i], p, i == 0 ? k.x : i == 1 ? k.y : i == 2 ? k.z : k.w);
-                    y[i] = __fmul2_rn(x, sc);
+                for (int p = 0; p < 4; p++) {
+                    float2 x = pair_of<E4>(u[i], p, k.x), y = pair_of<E4>(u[i + 1], p, k.y);
+                    // an infinity turns into NaN, which does not count
+                    x = __ffma2_rn(x, f2(0.0f), x), y = __ffma2_rn(y, f2(0.0f), y);
+                    m[2 * p] = max3(m[2 * p], x.x, y.x), m[2 * p + 1] = max3(m[2 * p + 1], x.y, y.y);
                 }
-                w[0][h] = codes4<FMT>(y[0].x, y[1].x, y[2].x, y[3].x), w[1][h] = codes4<FMT>(y[0].y, y[1].y, y[2].y, y[3].y);
             }
-            *reinterpret_cast<uint2 *>(at + 2 * p * TILE) = make_uint2(w[0][0], w[0][1]);
-            *reinterpret_cast<uint2 *>(at + (2 * p + 1) * TILE) = make_uint2(w[1][0], w[1][1]);
+            const bool up = lane & 16;
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const float send = up ? m[j] : m[j + 4], keep = up ? m[j + 4] : m[j];
+                m[j] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, 16));
+            }
         }
-    } else {
+        *reinterpret_cast<float4 *>(&part[warp][8 * cc + (lane & 16 ? 4 : 0)]) = make_float4(m[0], m[1], m[2], m[3]);
+        __syncthreads();
+        if (tid < TILE) {
+            float t = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; j++) *reinterpret_cast<uint2 *>(at + j * TILE) = make_uint2(0u, 0u);
-    }
-    __syncthreads();
-    const int ch = tid & 7;
-    const uint32_t first = walk.step[cur].col * TILE, ld = (uint32_t)a.col_ld, left = min((uint32_t)TILE, cols - first);
-    uint8_t *to = a.col_q + wide_mul(first + (tid >> 3), ld) + walk.step[cur].tile * TILE + 16 * ch;
-    const uint8_t *from = code + (tid >> 3) * TILE;
+            for (int w = 0; w < 8; w += 2) t = max3(t, part[w][tid], part[w + 1][tid]);
+            const float2 sc = block_scale_fast<FMT>(t);
+            scale[tid] = sc.x;
+            const uint32_t c = walk.step[cur].col * TILE + tid;
+            if (c < cols) a.col_s[wide_mul(walk.step[cur].tile, cols) + c] = sc.y;
+        } else if (tid == TILE) {
+            walk_on(walk, table, a.offsets, a.rows, a.across, next, after);
+        }
+        __syncthreads();
+        look(walk.step[after]);
+        uint8_t *at = code + 8 * cc * TILE + ((rr ^ cc) << 3);
+        if (busy) {
 #pragma unroll
-    for (int k = 0; k < 4; k++) {  // two pieces of 8 bytes, each where the XOR put it
-        const uint32_t c = (tid >> 3) + 32 * k, g = c >> 3;
-        const uint2 x = *reinterpret_cast<const uint2 *>(from + 32 * k * TILE + (((2 * ch) ^ g) << 3));
-        const uint2 y = *reinterpret_cast<const uint2 *>(from + 32 * k * TILE + (((2 * ch + 1) ^ g) << 3));
-        if (c < left) *reinterpret_cast<uint4 *>(to) = make_uint4(x.x, x.y, y.x, y.y);
-        to += wide_mul(32, ld);
-    }
-    cur = next;
+            for (int p = 0; p < 4; p++) {  // columns 8cc + 2p and the next, four rows at a time
+                const float2 sc = *reinterpret_cast<const float2 *>(&scale[8 * cc + 2 * p]);
+                uint32_t w[2][2];
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const float4 k = *reinterpret_cast<const float4 *>(f + 4 * h);
+                    float2 y[4];
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        asm volatile("" : "+r"(u[4 * h + i].x), "+r"(u[4 * h + i].y)::"memory");  // decoded again, not kept
+                        const float2 x = pair_of<E4>(u[4 * h + i], p, i == 0 ? k.x : i == 1 ? k.y : i == 2 ? k.z : k.w);
+                        y[i] = __fmul2_rn(x, sc);
+                    }
+                    w[0][h] = codes4<FMT>(y[0].x, y[1].x, y[2].x, y[3].x), w[1][h] = codes4<FMT>(y[0].y, y[1].y, y[2].y, y[3].y);
+                }
+                *reinterpret_cast<uint2 *>(at + 2 * p * TILE) = make_uint2(w[0][0], w[0][1]);
+                *reinterpret_cast<uint2 *>(at + (2 * p + 1) * TILE) = make_uint2(w[1][0], w[1][1]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; j++) *reinterpret_cast<uint2 *>(at + j * TILE) = make_uint2(0u, 0u);
+        }
+        __syncthreads();
+        const int ch = tid & 7;
+        const uint32_t first = walk.step[cur].col * TILE, ld = (uint32_t)a.col_ld, left = min((uint32_t)TILE, cols - first);
+        uint8_t *to = a.col_q + wide_mul(first + (tid >> 3), ld) + walk.step[cur].tile * TILE + 16 * ch;
+        const uint8_t *from = code + (tid >> 3) * TILE;
+#pragma unroll
+        for (int k = 0; k < 4; k++) {  // two pieces of 8 bytes, each where the XOR put it
+            const uint32_t c = (tid >> 3) + 32 * k, g = c >> 3;
+            const uint2 x = *reinterpret_cast<const uint2 *>(from + 32 * k * TILE + (((2 * ch) ^ g) << 3));
+            const uint2 y = *reinterpret_cast<const uint2 *>(from + 32 * k * TILE + (((2 * ch + 1) ^ g) << 3));
+            if (c < left) *reinterpret_cast<uint4 *>(to) = make_uint4(x.x, x.y, y.x, y.y);
+            to += wide_mul(32, ld);
+        }
+        cur = next;
     }
 }
 

@@ -65,6 +65,7 @@ struct DispatchArgs {
 };
 
 // A warp quantises 1024 columns of a token: four loads under way at once, 16 lanes a block of 128.
+// 16384 tokens x 4096 of 2 choices, bf16, with the copy in token order: 54 us, 6.3 TB/s.
 template <int XKIND, int FMT>
 __global__ void __launch_bounds__(256) block_dispatch_kernel(const DispatchArgs a) {
     constexpr int U = 4;
@@ -137,10 +138,12 @@ struct CombineArgs {
     float *dweight;
 };
 
-// A warp sums 256 CH columns of a token, the CH loads of up to J rows of y under way at once.  A lane holds a choice's row
-// and weight; the others fetch them.
-template <int XKIND, int J, int CH>
+// A warp sums 512 columns of a token, the two loads of up to J rows of y under way at once (256 columns a warp: 512 tokens x
+// 2048 of 6 choices 4.0 us against 3.0).  A lane holds a choice's row and weight; the others fetch them.
+// 16384 tokens x 4096 of 2 choices, bf16: 68 us, 5.9 TB/s.
+template <int XKIND, int J>
 __global__ void __launch_bounds__(256) moe_combine_kernel(const CombineArgs a) {
+    constexpr int CH = 2;
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31;
@@ -188,6 +191,7 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const CombineArgs a) {
 
 // W warps walk a token's row, 256 columns a step each, two steps' loads of J choices under way at once (more choices: again, dout
 // from L1).  The sums run over a lane's columns in order, then over the lanes in a fixed tree, then over the warps.
+// 16384 tokens x 4096 of 2 choices, bf16: 103 us, 6.5 TB/s.
 template <int XKIND, int J>
 __global__ void __launch_bounds__(256) moe_combine_bwd_kernel(const CombineArgs a, int wlog) {
     __shared__ float part[8][J];
@@ -320,20 +324,15 @@ extern "C" fp8dl_status moe_combine(const void *y, int32_t dtype, int64_t rows, 
     FP8DL_CHECK_ARG(tokens == 0 || (out && (y || rows == 0)), "y and out must be non-NULL");
     if (!aligned16(y) || !aligned16(out) || !aligned4(weight))
         return fail(FP8DL_ERR_ALIGN, "y and out must be 16-byte aligned, weight 4-byte");
-    int sms = 0;
-    FP8DL_TRY(current_device(nullptr, &sms));
+    FP8DL_TRY(current_device(nullptr, nullptr));
     if (tokens == 0) return FP8DL_OK;
     CombineArgs a = {y, nullptr, rows, cols, tokens, position, weight, k, out, nullptr, nullptr};
-    // 512 columns a warp, 256 where the warps would be few
-    const bool two = tokens * ((cols + 511) / 512) >= 16 * (int64_t)sms;
-    const int64_t per = (cols + (two ? 511 : 255)) / (two ? 512 : 256), ctas = (tokens * per + 7) / 8;
+    const int64_t per = (cols + 511) / 512, ctas = (tokens * per + 7) / 8;
     FP8DL_TRY(exchange_grid(8 * ctas));
     const bool pdl = short_call_bytes((double)tokens * (double)cols * (dtype == FP8DL_BF16 ? 2.0 : 4.0) * (k + 1));
-#define FP8DL_COMBINE(X) \
-    (k <= 2 ? (two ? moe_combine_kernel<X, 2, 2> : moe_combine_kernel<X, 2, 1>) : (two ? moe_combine_kernel<X, 4, 2> : moe_combine_kernel<X, 4, 1>))
-    (void)launch_kernel(dtype == FP8DL_BF16 ? FP8DL_COMBINE(FP8DL_BF16) : FP8DL_COMBINE(FP8DL_F32), dim3((unsigned)ctas), dim3(256), 0,
-                        (cudaStream_t)stream, 0, pdl, a);
-#undef FP8DL_COMBINE
+    auto *kernel = dtype == FP8DL_BF16 ? (k <= 2 ? moe_combine_kernel<FP8DL_BF16, 2> : moe_combine_kernel<FP8DL_BF16, 4>)
+                                       : (k <= 2 ? moe_combine_kernel<FP8DL_F32, 2> : moe_combine_kernel<FP8DL_F32, 4>);
+    (void)launch_kernel(kernel, dim3((unsigned)ctas), dim3(256), 0, (cudaStream_t)stream, 0, pdl, a);
     note_launch();
     return check_launch("moe_combine");
 }
@@ -352,7 +351,9 @@ extern "C" fp8dl_status moe_combine_bwd(const void *dout, const void *y, int32_t
     FP8DL_TRY(current_device(nullptr, &sms));
     if (tokens == 0) return FP8DL_OK;
     CombineArgs a = {y, dout, rows, cols, tokens, position, weight, k, nullptr, dy, dweight};
-    int wlog = 0;  // warps a token: more where tokens are few
+    // warps a token: more where tokens are few (x 4096 of 2 choices: 64 tokens 5.8 us with one warp, 2.2 with eight; 1024
+    // tokens 6.6 and 5.9, 5.2 with four; 4096 tokens 23.0 with one, 25.4 with eight)
+    int wlog = 0;
     while (wlog < 3 && (tokens << wlog) < 16 * (int64_t)sms && (int64_t(256) << wlog) < cols) wlog++;
     const int64_t ctas = ((tokens << wlog) + 7) / 8;
     const bool pdl = short_call_bytes((double)tokens * (double)cols * (dtype == FP8DL_BF16 ? 2.0 : 4.0) * (2 * k + 1));
