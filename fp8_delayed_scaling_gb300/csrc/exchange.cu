@@ -189,8 +189,8 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const CombineArgs a) {
         if (c + 256 * h < a.cols) Eight<XKIND>::store(a.out, t * a.cols + c + 256 * h, sum[h]);
 }
 
-// W warps walk a token's row, 256 columns a step each, two steps' loads of J choices under way at once (more choices: again, dout
-// from L1).  The sums run over a lane's columns in order, then over the lanes in a fixed tree, then over the warps.
+// W warps walk a token's row, 256 columns a step each, two steps' loads of up to four choices under way at once or one step's
+// of eight (4096 tokens x 2048 of 6 choices: 40 us, in two passes of four 46); more choices: again, dout from L1.  The sums run over a lane's columns in order, then over the lanes in a fixed tree, then over the warps.
 // 16384 tokens x 4096 of 2 choices, bf16: 103 us, 6.5 TB/s.
 template <int XKIND, int J>
 __global__ void __launch_bounds__(256) moe_combine_bwd_kernel(const CombineArgs a, int wlog) {
@@ -241,13 +241,21 @@ __global__ void __launch_bounds__(256) moe_combine_bwd_kernel(const CombineArgs 
                 }
             };
             const int64_t step = 256 * W;
-            for (int64_t c = 256 * mine + 8 * lane; c < a.cols; c += 2 * step) {
-                Eight<XKIND> d0, d1, v0[J], v1[J];
-                const bool two = c + step < a.cols;
-                load(d0, v0, c);
-                if (two) load(d1, v1, c + step);
-                add(d0, v0, c);
-                if (two) add(d1, v1, c + step);
+            if (J > 4) {
+                for (int64_t c = 256 * mine + 8 * lane; c < a.cols; c += step) {
+                    Eight<XKIND> d, v[J];
+                    load(d, v, c);
+                    add(d, v, c);
+                }
+            } else {
+                for (int64_t c = 256 * mine + 8 * lane; c < a.cols; c += 2 * step) {
+                    Eight<XKIND> d0, d1, v0[J], v1[J];
+                    const bool two = c + step < a.cols;
+                    load(d0, v0, c);
+                    if (two) load(d1, v1, c + step);
+                    add(d0, v0, c);
+                    if (two) add(d1, v1, c + step);
+                }
             }
         }
         if (!a.dweight) continue;
@@ -352,14 +360,15 @@ extern "C" fp8dl_status moe_combine_bwd(const void *dout, const void *y, int32_t
     if (tokens == 0) return FP8DL_OK;
     CombineArgs a = {y, dout, rows, cols, tokens, position, weight, k, nullptr, dy, dweight};
     // warps a token: more where tokens are few (x 4096 of 2 choices: 64 tokens 5.8 us with one warp, 2.2 with eight; 1024
-    // tokens 6.6 and 5.9, 5.2 with four; 4096 tokens 23.0 with one, 25.4 with eight)
+    // tokens 6.6 and 5.9, 5.2 with four; 4096 tokens 23.0 with one, 25.4 with eight; x 2048 of 6 choices, fewer of whose
+    // warps fit an SM: 512 tokens 7.6, 4.4 with four, 5.4 with eight; 2048 tokens 15.5 with one, 16.9 with two)
     int wlog = 0;
-    while (wlog < 3 && (tokens << wlog) < 16 * (int64_t)sms && (int64_t(256) << wlog) < cols) wlog++;
+    while (wlog < 3 && (tokens << wlog) < (k <= 4 ? 16 : 8) * (int64_t)sms && (int64_t(256) << wlog) < cols) wlog++;
     const int64_t ctas = ((tokens << wlog) + 7) / 8;
     const bool pdl = short_call_bytes((double)tokens * (double)cols * (dtype == FP8DL_BF16 ? 2.0 : 4.0) * (2 * k + 1));
     auto *kernel = dtype == FP8DL_BF16
-                       ? (k <= 2 ? moe_combine_bwd_kernel<FP8DL_BF16, 2> : moe_combine_bwd_kernel<FP8DL_BF16, 4>)
-                       : (k <= 2 ? moe_combine_bwd_kernel<FP8DL_F32, 2> : moe_combine_bwd_kernel<FP8DL_F32, 4>);
+                       ? (k <= 2 ? moe_combine_bwd_kernel<FP8DL_BF16, 2> : k <= 4 ? moe_combine_bwd_kernel<FP8DL_BF16, 4> : moe_combine_bwd_kernel<FP8DL_BF16, 8>)
+                       : (k <= 2 ? moe_combine_bwd_kernel<FP8DL_F32, 2> : k <= 4 ? moe_combine_bwd_kernel<FP8DL_F32, 4> : moe_combine_bwd_kernel<FP8DL_F32, 8>);
     (void)launch_kernel(kernel, dim3((unsigned)ctas), dim3(256), 0, (cudaStream_t)stream, 0, pdl, a, wlog);
     note_launch();
     return check_launch("moe_combine_bwd");
