@@ -9,6 +9,7 @@ import torch
 
 import block_reference as br
 import moe_reference as mr
+import test_gpu_route
 import workloads as wl
 from conftest import ROOT
 from helpers import gpu
@@ -328,3 +329,40 @@ def test_gelu_of_blocks_that_hold_small_results_only(act):
         assert np.all((np.abs(host(gts)[:n, 0] * 448 - np.abs(y[at])) <= tol[at] * np.abs(y[at]))[w])
         far = w & (np.abs(v[at]) > 1.5) & (np.abs(d[at]) > 2.0 ** -99)
         assert np.all((np.abs(host(dts)[:n, 0] * 448 - np.abs(d[at])) <= 2.2 * tol[at] * np.abs(d[at]))[far])
+
+
+@pytest.mark.parametrize("T,E,k", [(40, 20, 12), (33, 30, 9), (65, 50, 10), (50, 64, 16), (70, 128, 16), (70, 127, 17), (5000, 60, 9)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_more_choices_than_a_quarter_of_a_warp_has_lanes(T, E, k, dtype):
+    test_gpu_route.test_route_and_gradient(T, E, k, dtype)
+
+
+@pytest.mark.parametrize("T,k,C", [(3000, 1, 144), (3000, 2, 272), (2600, 4, 144), (2600, 5, 272), (1300, 8, 528), (1300, 9, 144)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_exchange_of_many_tokens(T, k, C, dtype):
+    """One warp a token in the gradient; sums of k products in order, C products over a lane, a tree and a few warps."""
+    import fp8_delayed_scaling_gb300 as fd
+    dev = gpu()
+    g = wl.generator(437, "x%d,%d" % (T, k))
+    R = T * k + 7
+    pos = torch.randperm(R, generator=g)[:T * k].view(T, k).int()
+    pos[torch.rand((T, k), generator=g) < 0.1] = -1
+    y, x = wl.normal((R, C), 1.0, g, dtype), wl.normal((T, C), 1.0, g, dtype)
+    w = torch.rand((T, k), generator=g) + 0.1
+    yd, xd, pd, wd = y.to(dev), x.to(dev), pos.to(dev), w.to(dev)
+    out, dy, dw = torch.empty_like(xd), torch.full_like(yd, 9.0), torch.empty_like(wd)
+    fd.moe_combine(yd, pd, out, weight=wd)
+    fd.moe_combine_bwd(xd, yd, pd, wd, dy=dy, dweight=dw)
+    used = (pos >= 0).numpy()
+    rows = np.where(used, pos.numpy(), 0)
+    yv, xv, wv = y.double().numpy(), x.double().numpy(), np.where(used, w.double().numpy(), 0.0)
+    terms = wv[:, :, None] * yv[rows]
+    half = torch.finfo(dtype).eps / 2
+    want, size = terms.sum(1), np.abs(terms).sum(1)
+    assert np.all(np.abs(host(out) - want) <= half * np.abs(want) * 1.01 + (k + 1) * mr.EPS * size)
+    want_dy = np.full((R, C), 9.0)
+    want_dy[rows[used]] = (wv[:, :, None] * xv[:, None, :])[used]
+    assert np.all(np.abs(host(dy) - want_dy) <= half * np.abs(want_dy) * 1.01 + mr.EPS * np.abs(want_dy))
+    prod = xv[:, None, :] * yv[rows]
+    want_dw, size_dw = np.where(used, prod.sum(2), 0.0), np.abs(prod).sum(2)
+    assert np.all(np.abs(host(dw) - want_dw) <= (C / 32 + 16) * mr.EPS * size_dw)
