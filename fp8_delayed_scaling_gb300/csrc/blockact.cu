@@ -81,7 +81,7 @@ constexpr int ACT_THREADS = 256, ACT_ROWS = 32;  // rows of a CTA: two for each 
 constexpr int ACT_CTAS = 3;                       // CTAs an SM holds
 }
 
-// Eight columns of a row in fp32, of UNITS 16-byte units as they lie in memory.
+// Eight columns of a row in fp32; unit(i): their i-th 16 bytes as they lie in memory.
 template <int XKIND, typename Unit>
 __device__ __forceinline__ void widen8(const Unit &unit, float2 (&v)[4]) {
     if (XKIND == FP8DL_BF16) {
