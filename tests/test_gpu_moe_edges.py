@@ -366,3 +366,49 @@ def test_exchange_of_many_tokens(T, k, C, dtype):
     prod = xv[:, None, :] * yv[rows]
     want_dw, size_dw = np.where(used, prod.sum(2), 0.0), np.abs(prod).sum(2)
     assert np.all(np.abs(host(dw) - want_dw) <= (C / 32 + 16) * mr.EPS * size_dw)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("act", range(4))
+def test_more_jobs_than_there_are_threads_blocks(act, dtype):
+    """Thread blocks that walk several jobs and tiles, with halves of h that do not start on a block: rows, tiles and their
+    sums are, bit by bit, those of calls for 128 rows, and dbias the sum of theirs."""
+    import fp8_delayed_scaling_gb300 as fd
+    dev = gpu()
+    R, C = 3000, 1040
+    W = 2 * C if act >= 2 else C
+    B, D = (C + 127) // 128, (W + 127) // 128
+    g = wl.generator(438, "h%d" % act)
+    h, dg = wl.normal((R, W), 1.5, g, dtype).to(dev), wl.normal((R, C), 1.0, g, dtype).to(dev)
+
+    def run(h, dg):
+        n = h.shape[0]
+        T = (n + 127) // 128 * 128
+        u8, f32 = (lambda *s: torch.full(s, 0xAB, dtype=torch.uint8, device=dev)), (lambda *s: torch.full(s, -7.0, device=dev))
+        b = dict(gq=u8(n, C), gs=f32(B, n), hq=u8(n, W), hs=f32(D, n), dq=u8(n, W), ds=f32(D, n), dt=u8(W, T), dts=f32(T // 128, W),
+                 gt=u8(C, T), gts=f32(T // 128, C), db=f32(W))
+        only = u8(n, C), f32(B, n)
+        fd.fp8_block_act(h, act, 0, *only)
+        fd.fp8_block_act(h, act, 0, b["gq"], b["gs"], h_q=b["hq"], h_s=b["hs"])
+        assert torch.equal(only[0], b["gq"]) and torch.equal(only[1], b["gs"])
+        ws = torch.empty(fd.fp8_cast_workspace_size(n, W), dtype=torch.uint8, device=dev)
+        fd.fp8_block_dact(dg, b["hq"], 0, b["hs"], act, 1, dh_q=b["dq"], dh_s=b["ds"], dh_qt=b["dt"], dh_st=b["dts"], g_qt=b["gt"],
+                          g_st=b["gts"], dbias=b["db"], workspace=ws)
+        return b
+
+    whole = run(h, dg)
+    total, size = torch.zeros(W, dtype=torch.float64, device=dev), torch.zeros(W, dtype=torch.float64, device=dev)
+    for lo in range(0, R, 128):
+        hi = min(lo + 128, R)
+        part = run(h[lo:hi], dg[lo:hi])
+        for name in ("gq", "hq", "dq"):
+            assert torch.equal(whole[name][lo:hi], part[name]), (name, lo)
+        for name in ("gs", "hs", "ds"):
+            assert torch.equal(whole[name][:, lo:hi], part[name]), (name, lo)
+        for name in ("dt", "gt"):
+            assert torch.equal(whole[name][:, lo:lo + 128], part[name]), (name, lo)
+        for name in ("dts", "gts"):
+            assert torch.equal(whole[name][lo // 128:lo // 128 + 1], part[name]), (name, lo)
+        total += part["db"].double()
+        size += part["db"].double().abs()
+    assert torch.all((whole["db"].double() - total).abs() <= (R // 128 + 2) * mr.EPS * size)
