@@ -186,9 +186,9 @@ __device__ __forceinline__ void balance(const RouteArgs &a, const int32_t *total
     sum = group_sum<32>(sum);
     if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = sum;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < THREADS / 32; w++) sum += warps[w];
-        a.loss[0] = sum;
+    if (threadIdx.x < 32) {
+        sum = group_sum<32>(threadIdx.x < THREADS / 32 ? warps[threadIdx.x] : 0.0f);
+        if (threadIdx.x == 0) a.loss[0] = sum;
     }
 }
 
@@ -376,11 +376,15 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
     if (G == 32) {  // the runs before each run: 16 or 32 of them, a thread per expert
         for (int e = tid; e < E; e += THREADS) {
             int32_t sum = 0;
-#pragma unroll 8
-            for (int g = 0; g < runs; g++) {
-                const int32_t c = cnt[g * E + e];
-                cnt[g * E + e] = sum;
-                sum += c;
+            for (int g0 = 0; g0 < runs; g0 += 8) {  // eight reads at once
+                int32_t c[8];
+#pragma unroll
+                for (int i = 0; i < 8; i++) c[i] = g0 + i < runs ? cnt[(g0 + i) * E + e] : 0;
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    if (g0 + i < runs) cnt[(g0 + i) * E + e] = sum;
+                    sum += c[i];
+                }
             }
             sums[e] = sum;
         }
@@ -465,8 +469,7 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
 // Bound: latency (152 tiles' counts of 256 experts, 156 KB from L2 a CTA, then two dependent accesses).
 __global__ void __launch_bounds__(1024) route_rows_kernel(const RouteArgs a, int tiles, int64_t tile_tokens) {
     __shared__ int4 part_b[1024], part_n[1024];
-    __shared__ int32_t before[1024], total[1024], first[1025], warps[32];
-    __shared__ float sums[1024];
+    __shared__ int32_t before[1024], total[1024], first[1025], warps[32], counted;
     pdl_wait();
     pdl_trigger();
     const int E = a.experts, tid = threadIdx.x, tile = blockIdx.x;
@@ -492,52 +495,47 @@ __global__ void __launch_bounds__(1024) route_rows_kernel(const RouteArgs a, int
         }
     };
     load(lo + tid);  // the first ones while the tiles' counts add up
+    const bool loss = tile == tiles;  // all tiles' sums of p in the place of the counts before
+    if (tid == 0) counted = 0;
+    const int32_t own = loss && tid < tiles ? a.counted[tid] : 0;
     if (e < E && part < parts) {
-#pragma unroll 10
-        for (int i = part; i < tiles; i += parts) {
-            const int4 c = four(a.hist + i * E + e);
-            n.x += c.x, n.y += c.y, n.z += c.z, n.w += c.w;
-            if (i < tile) b.x += c.x, b.y += c.y, b.z += c.z, b.w += c.w;
-        }
-        if (tile == tiles) {
+        if (loss) {
+#pragma unroll 5
+            for (int i = part; i < tiles; i += parts) {
+                const int4 c = four(a.hist + i * E + e), d = four(reinterpret_cast<const int32_t *>(a.psum) + i * E + e);
+                n.x += c.x, n.y += c.y, n.z += c.z, n.w += c.w;
+                p.x += __int_as_float(d.x), p.y += __int_as_float(d.y), p.z += __int_as_float(d.z), p.w += __int_as_float(d.w);
+            }
+            b = make_int4(__float_as_int(p.x), __float_as_int(p.y), __float_as_int(p.z), __float_as_int(p.w));
+        } else {
 #pragma unroll 10
             for (int i = part; i < tiles; i += parts) {
-                const int4 c = four(reinterpret_cast<const int32_t *>(a.psum) + i * E + e);
-                p.x += __int_as_float(c.x), p.y += __int_as_float(c.y), p.z += __int_as_float(c.z), p.w += __int_as_float(c.w);
+                const int4 c = four(a.hist + i * E + e);
+                n.x += c.x, n.y += c.y, n.z += c.z, n.w += c.w;
+                if (i < tile) b.x += c.x, b.y += c.y, b.z += c.z, b.w += c.w;
             }
         }
     }
     // [part][expert], so that a thread per expert reads one line of banks
     part_b[tid] = b, part_n[tid] = n;
     __syncthreads();
+    if (own) atomicAdd(&counted, own);
     if (tid < E) {
         const int32_t *pb = reinterpret_cast<const int32_t *>(part_b) + tid, *pn = reinterpret_cast<const int32_t *>(part_n) + tid;
         int32_t sb = 0, sn = 0;
-        for (int q = 0; q < parts; q++) sb += pb[4 * wide * q], sn += pn[4 * wide * q];
-        before[tid] = sb, total[tid] = sn;
-    }
-    if (tile == tiles) {
-        __syncthreads();
-        reinterpret_cast<float4 *>(part_b)[tid] = p;
-        __syncthreads();
-        if (tid < E) {
-            const float *pp = reinterpret_cast<const float *>(part_b) + tid;
-            float s = 0.0f;
-            for (int q = 0; q < parts; q++) s += pp[4 * wide * q];
-            sums[tid] = s;
+        float sp = 0.0f;
+#pragma unroll 4
+        for (int q = 0; q < parts; q++) {
+            sn += pn[4 * wide * q];
+            if (loss) sp += __int_as_float(pb[4 * wide * q]);
+            else sb += pb[4 * wide * q];
         }
+        before[tid] = loss ? __float_as_int(sp) : sb, total[tid] = sn;
     }
     __syncthreads();
     scan_experts<1024>(total, first, E, warps);
-    if (tile == tiles) {
-        int32_t c = 0;
-        for (int i = tid; i < tiles; i += 1024) c += a.counted[i];  // at most one each
-        __shared__ int32_t counted;
-        if (tid == 0) counted = 0;
-        __syncthreads();
-        if (c) atomicAdd(&counted, c);
-        __syncthreads();
-        balance<1024>(a, total, sums, counted, first[E], reinterpret_cast<float *>(warps));
+    if (loss) {
+        balance<1024>(a, total, reinterpret_cast<const float *>(before), counted, first[E], reinterpret_cast<float *>(warps));
         return;
     }
     if (tile == 0) {
