@@ -118,18 +118,6 @@ cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
-// Lets a kernel take up to `bytes` of dynamic shared memory: once per device (`done` holds a bit for each), and always
-// the most that any call of it needs, so that calls of several threads cannot lower it for one another.
-template <typename... KArgs>
-fp8dl_status allow_smem(void (*kernel)(KArgs...), size_t bytes, int dev, std::atomic<uint64_t> &done, const char *what) {
-    const uint64_t bit = uint64_t(1) << (dev & 63);
-    if (done.load(std::memory_order_acquire) & bit) return FP8DL_OK;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e != cudaSuccess) return fail(FP8DL_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-    done.fetch_or(bit, std::memory_order_release);
-    return FP8DL_OK;
-}
-
 // ---------------------------------------------------------------------------
 // Device-side FP8 conversion through the hardware cvt (round to nearest even,
 // saturating to the largest finite value; NaN stays NaN).

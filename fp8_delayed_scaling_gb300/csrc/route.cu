@@ -202,7 +202,7 @@ __device__ __forceinline__ void balance(const RouteArgs &a, const int32_t *total
 // The runs' counters and then the runs' sums of p share one buffer [runs][experts].
 // Bound: the issue slots (about 390 instructions a token of 256 experts and 8 choices, 66% of the slots in use, half of
 // them the one pipe of comparisons and selects); few tokens: the launches.  32768 tokens of 256 experts in bf16, 8 choices,
-// this kernel and the next: 24 us with the balance loss, 21 without (fp32 33); 1 token of 64: 3.3 us.
+// this kernel and the next: 23 us with the balance loss, 21 without (fp32 33); 1 token of 64: 3.3 us.
 template <int XKIND, int G, int S, int THREADS, bool SINGLE>
 __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
     constexpr int NG = THREADS / G;
