@@ -19,6 +19,7 @@ namespace fp8dl {
 namespace rt {
 constexpr int MAX_TILES = 160;  // CTAs of the first kernel (workspace rows); one per SM fits every GB300
 constexpr int MAX_K = 32;       // choices of a token: one per lane
+constexpr int KEPT = 8;         // a run's first tokens, whose choices wait in shared memory for their rows
 constexpr float NEG_INF = -__builtin_huge_valf();
 }
 
@@ -197,7 +198,8 @@ __device__ __forceinline__ void balance(const RouteArgs &a, const int32_t *total
 //   choice   each lane sorts its keys once (up to eight; more: it searches them again); k rounds of a maximum over
 //            the lanes (redux) of the lanes' first keys, and the lane that had it moves up.  Lane j keeps choice j.
 //   row      rank within the run from the CTA's shared counters (a token's experts differ, so its
-//            lanes never meet), plus the runs before it after the last token.
+//            lanes never meet), plus the runs before it after the last token.  The ranks of a run's first
+//            tokens wait in shared memory, further ones in `position`.
 //   SINGLE   the tile is all there is: rows, counts and the loss are finished here, one launch.
 // The runs' counters and then the runs' sums of p share one buffer [runs][experts].
 // Bound: the issue slots (about 390 instructions a token of 256 experts and 8 choices, 66% of the slots in use, half of
@@ -235,6 +237,8 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
         at_logits += row;
     };
     load(0);
+    const int kept_tokens = min(per, rt::KEPT);
+    int32_t *kept = cnt + NG * E;  // [token of the run][run][choice]: the expert and the rank in the run above it, or -1
     uint32_t place = (uint32_t)(t0 * k) + l;
     for (int i = 0; i < per; i++, place += k) {
         const bool here = i < n_here;
@@ -366,7 +370,8 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
             }
             a.expert[place] = pick;
             a.weight[place] = w;
-            a.position[place] = rank;
+            if (i < kept_tokens) kept[(i * NG + run) * k + l] = pick >= 0 ? rank << 10 | pick : -1;
+            else a.position[place] = rank;
         }
         __syncwarp();
     }
@@ -418,7 +423,13 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
     if (l < k) {
         constexpr int U = 8;  // tokens read at once
         place = (uint32_t)(t0 * k) + l;
-        for (int i0 = 0; i0 < n_here; i0 += U, place += U * k) {
+        for (int i = 0; i < min(n_here, kept_tokens); i++, place += k) {
+            const int32_t c = kept[(i * NG + run) * k + l];
+            const int32_t at = c < 0 ? -1 : (c >> 10) + mine[c & 1023] + (SINGLE ? first[c & 1023] : 0);
+            a.position[place] = at;
+            if (SINGLE && c >= 0) a.token[at] = (int32_t)(t0 + i);
+        }
+        for (int i0 = kept_tokens; i0 < n_here; i0 += U, place += U * k) {
             int32_t e[U], at[U];
 #pragma unroll
             for (int i = 0; i < U; i++) {
@@ -701,13 +712,13 @@ static bool route_vec(int n, int s, int esz) { return n % s == 0 && ((int64_t)n 
 template <int XKIND, int G, int S>
 static fp8dl_status launch_route(const RouteArgs &a, int tiles, int64_t tile_tokens, int dev, cudaStream_t st, bool pdl) {
     constexpr int THREADS = S >= 16 ? 512 : 1024;
-    const size_t smem = (size_t)(THREADS / G) * a.experts * 4;
+    constexpr int NG = THREADS / G;
+    const size_t smem = (size_t)NG * (a.experts + (a.per < rt::KEPT ? a.per : rt::KEPT) * a.k) * 4;
     const bool single = tiles == 1;
     auto *kernel = single ? route_kernel<XKIND, G, S, THREADS, true> : route_kernel<XKIND, G, S, THREADS, false>;
-    constexpr size_t most = (size_t)THREADS * S * 4;
+    constexpr size_t most = (size_t)NG * (G * S + rt::KEPT * (G < rt::MAX_K ? G : rt::MAX_K)) * 4;  // with the static arrays past 48 KB
     static std::atomic<uint64_t> done[2];
-    if (most > 32768)  // with the static arrays past 48 KB
-        FP8DL_TRY(allow_smem(kernel, most, dev, done[single], "moe_route"));
+    FP8DL_TRY(allow_smem(kernel, most, dev, done[single], "moe_route"));
     (void)launch_kernel(kernel, dim3((unsigned)tiles), dim3(THREADS), smem, st, 0, pdl, a);
     note_launch();
     FP8DL_TRY(check_launch("moe_route"));
