@@ -204,7 +204,7 @@ __device__ __forceinline__ void balance(const RouteArgs &a, const int32_t *total
 // The runs' counters and then the runs' sums of p share one buffer [runs][experts].
 // Bound: the issue slots (about 390 instructions a token of 256 experts and 8 choices, 66% of the slots in use, half of
 // them the one pipe of comparisons and selects); few tokens: the launches.  32768 tokens of 256 experts in bf16, 8 choices,
-// this kernel and the next: 23 us with the balance loss, 21 without (fp32 33); 1 token of 64: 3.3 us.
+// this kernel and the next: 23 us with the balance loss, 21 without (fp32 33); 1 token of 64: 3.2 us.
 template <int XKIND, int G, int S, int THREADS, bool SINGLE>
 __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
     constexpr int NG = THREADS / G;
@@ -802,8 +802,8 @@ extern "C" fp8dl_status moe_route(const void *logits, int32_t dtype, int64_t tok
     a.valid = valid;
     a.expert = expert, a.position = position, a.token = token, a.offsets = offsets, a.counts = counts;
     a.weight = weight, a.slope = slope, a.loss = loss;
-    // few tokens: one CTA and one launch, up to two tokens a run (64 tokens of 64 experts 5.5 us against 6.4, 256 of 8
-    // 6.2 against 7.1; with four 7.7 against 6.4, 8.9 against 7.2)
+    // few tokens: one CTA and one launch, up to two tokens a run (64 tokens of 64 experts 4.8 us against 5.6, 256 of 8
+    // 5.6 against 6.3; with four 7.2 against 5.7, 8.4 against 6.3)
     a.per = tokens <= 2 * runs ? (tokens + runs - 1) / runs : (tokens + most * runs - 1) / (most * runs);
     const int64_t tile_tokens = a.per * runs;
     const int tiles = (int)((tokens + tile_tokens - 1) / tile_tokens);
