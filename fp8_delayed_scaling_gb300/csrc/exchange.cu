@@ -140,57 +140,71 @@ struct CombineArgs {
 
 // A warp sums 512 columns of a token, the two loads of up to J rows of y under way at once (256 columns a warp: 512 tokens x
 // 2048 of 6 choices 4.0 us against 3.0).  A lane holds a choice's row and weight; the others fetch them.
-// 16384 tokens x 4096 of 2 choices, bf16: 68 us, 5.9 TB/s.
-template <int XKIND, int J>
+// WALK: resident CTAs go on to further tokens, whose rows and weights are looked up meanwhile.  It pays for two bf16 rows only
+// (16384 tokens x 4096: 62.5 us against 68.5, 6.4 TB/s), where the least is under way; with four rows 60 against 50 (8192
+// tokens, 6.7 TB/s), in fp32 153 against 122: the registers for it cost CTAs.
+template <int XKIND, int J, bool WALK>
 __global__ void __launch_bounds__(256) moe_combine_kernel(const CombineArgs a) {
     constexpr int CH = 2;
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31;
-    const uint32_t per = (uint32_t)((a.cols + 256 * CH - 1) / (256 * CH)), warp = blockIdx.x * 8 + (threadIdx.x >> 5), t = warp / per;
-    if (t >= a.tokens) return;
-    const int64_t c = (int64_t)(warp - t * per) * (256 * CH) + 8 * lane;
-    int32_t row = -1;
-    float w = 0.0f;
-    if (lane < a.k) {
-        row = a.position[(int64_t)t * a.k + lane];
-        w = a.weight ? a.weight[(int64_t)t * a.k + lane] : 1.0f;
-        if (row >= a.rows) row = -1;
-    }
-    float2 sum[CH][4];
+    const uint32_t per = (uint32_t)((a.cols + 256 * CH - 1) / (256 * CH)), units = (uint32_t)a.tokens * per, step = gridDim.x * 8;
+    uint32_t unit = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (unit >= units) return;
+    int32_t row_next = -1;
+    float w_next = 0.0f;
+    const auto look = [&](uint32_t u) {
+        const int64_t t = u / per;
+        if (u < units && lane < a.k) {
+            row_next = a.position[t * a.k + lane];
+            w_next = a.weight ? a.weight[t * a.k + lane] : 1.0f;
+        }
+    };
+    look(unit);
+    do {
+        const uint32_t t = unit / per;
+        const int64_t c = (int64_t)(unit - t * per) * (256 * CH) + 8 * lane;
+        const int32_t row = row_next < a.rows ? row_next : -1;
+        const float w = w_next;
+        unit += step;
+        if (WALK) look(unit);
+        float2 sum[CH][4];
 #pragma unroll
-    for (int h = 0; h < CH; h++)
+        for (int h = 0; h < CH; h++)
 #pragma unroll
-        for (int q = 0; q < 4; q++) sum[h][q] = f2(0.0f);
-    for (int j0 = 0; j0 < a.k; j0 += J) {
-        Eight<XKIND> v[J][CH];
+            for (int q = 0; q < 4; q++) sum[h][q] = f2(0.0f);
+        for (int j0 = 0; j0 < a.k; j0 += J) {
+            Eight<XKIND> v[J][CH];
 #pragma unroll
-        for (int j = 0; j < J; j++) {
-            const int32_t r = __shfl_sync(0xffffffffu, row, (j0 + j) & 31);
+            for (int j = 0; j < J; j++) {
+                const int32_t r = __shfl_sync(0xffffffffu, row, (j0 + j) & 31);
 #pragma unroll
-            for (int h = 0; h < CH; h++) {
-                v[j][h].zero();
-                if (j0 + j < a.k && r >= 0 && c + 256 * h < a.cols) v[j][h].load(a.y, r * a.cols + c + 256 * h);
+                for (int h = 0; h < CH; h++) {
+                    v[j][h].zero();
+                    if (j0 + j < a.k && r >= 0 && c + 256 * h < a.cols) v[j][h].load(a.y, r * a.cols + c + 256 * h);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < J; j++) {
+                const int32_t r = __shfl_sync(0xffffffffu, row, (j0 + j) & 31);
+                const float k = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
+                if (j0 + j >= a.k || r < 0) continue;
+#pragma unroll
+                for (int h = 0; h < CH; h++)
+#pragma unroll
+                    for (int q = 0; q < 4; q++) sum[h][q] = __ffma2_rn(v[j][h].pair(q), f2(k), sum[h][q]);
             }
         }
 #pragma unroll
-        for (int j = 0; j < J; j++) {
-            const int32_t r = __shfl_sync(0xffffffffu, row, (j0 + j) & 31);
-            const float k = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
-            if (j0 + j >= a.k || r < 0) continue;
-#pragma unroll
-            for (int h = 0; h < CH; h++)
-#pragma unroll
-                for (int q = 0; q < 4; q++) sum[h][q] = __ffma2_rn(v[j][h].pair(q), f2(k), sum[h][q]);
-        }
-    }
-#pragma unroll
-    for (int h = 0; h < CH; h++)
-        if (c + 256 * h < a.cols) Eight<XKIND>::store(a.out, t * a.cols + c + 256 * h, sum[h]);
+        for (int h = 0; h < CH; h++)
+            if (c + 256 * h < a.cols) Eight<XKIND>::store(a.out, t * a.cols + c + 256 * h, sum[h]);
+    } while (WALK && unit < units);
 }
 
 // W warps walk a token's row, 256 columns a step each, two steps' loads of up to four choices under way at once or one step's
-// of eight (4096 tokens x 2048 of 6 choices: 40 us, in two passes of four 46); more choices: again, dout from L1.  The sums run over a lane's columns in order, then over the lanes in a fixed tree, then over the warps.
+// of eight (4096 tokens x 2048 of 6 choices: 40 us, in two passes of four 46); more choices: again, dout from L1.  The sums
+// run over a lane's columns in order, then over the lanes in a fixed tree, then over the warps.
 // 16384 tokens x 4096 of 2 choices, bf16: 103 us, 6.5 TB/s.
 template <int XKIND, int J>
 __global__ void __launch_bounds__(256) moe_combine_bwd_kernel(const CombineArgs a, int wlog) {
@@ -332,15 +346,19 @@ extern "C" fp8dl_status moe_combine(const void *y, int32_t dtype, int64_t rows, 
     FP8DL_CHECK_ARG(tokens == 0 || (out && (y || rows == 0)), "y and out must be non-NULL");
     if (!aligned16(y) || !aligned16(out) || !aligned4(weight))
         return fail(FP8DL_ERR_ALIGN, "y and out must be 16-byte aligned, weight 4-byte");
-    FP8DL_TRY(current_device(nullptr, nullptr));
+    int sms = 0;
+    FP8DL_TRY(current_device(nullptr, &sms));
     if (tokens == 0) return FP8DL_OK;
     CombineArgs a = {y, nullptr, rows, cols, tokens, position, weight, k, out, nullptr, nullptr};
     const int64_t per = (cols + 511) / 512, ctas = (tokens * per + 7) / 8;
     FP8DL_TRY(exchange_grid(8 * ctas));
     const bool pdl = short_call_bytes((double)tokens * (double)cols * (dtype == FP8DL_BF16 ? 2.0 : 4.0) * (k + 1));
-    auto *kernel = dtype == FP8DL_BF16 ? (k <= 2 ? moe_combine_kernel<FP8DL_BF16, 2> : moe_combine_kernel<FP8DL_BF16, 4>)
-                                       : (k <= 2 ? moe_combine_kernel<FP8DL_F32, 2> : moe_combine_kernel<FP8DL_F32, 4>);
-    (void)launch_kernel(kernel, dim3((unsigned)ctas), dim3(256), 0, (cudaStream_t)stream, 0, pdl, a);
+    const int64_t resident = 4 * (int64_t)sms;
+    const bool walk = dtype == FP8DL_BF16 && k <= 2 && ctas > resident;
+    auto *kernel = walk                  ? moe_combine_kernel<FP8DL_BF16, 2, true>
+                   : dtype == FP8DL_BF16 ? (k <= 2 ? moe_combine_kernel<FP8DL_BF16, 2, false> : moe_combine_kernel<FP8DL_BF16, 4, false>)
+                                         : (k <= 2 ? moe_combine_kernel<FP8DL_F32, 2, false> : moe_combine_kernel<FP8DL_F32, 4, false>);
+    (void)launch_kernel(kernel, dim3((unsigned)(walk ? resident : ctas)), dim3(256), 0, (cudaStream_t)stream, 0, pdl, a);
     note_launch();
     return check_launch("moe_combine");
 }

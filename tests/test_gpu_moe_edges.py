@@ -337,7 +337,8 @@ def test_more_choices_than_a_quarter_of_a_warp_has_lanes(T, E, k, dtype):
     test_gpu_route.test_route_and_gradient(T, E, k, dtype)
 
 
-@pytest.mark.parametrize("T,k,C", [(3000, 1, 144), (3000, 2, 272), (2600, 4, 144), (2600, 5, 272), (1300, 8, 528), (1300, 9, 144)])
+@pytest.mark.parametrize("T,k,C", [(3000, 1, 144), (3000, 2, 272), (2600, 4, 144), (2600, 5, 272), (1300, 8, 528), (1300, 9, 144),
+                                   (11001, 1, 144), (5200, 2, 528)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_exchange_of_many_tokens(T, k, C, dtype):
     """One warp a token in the gradient; sums of k products in order, C products over a lane, a tree and a few warps."""
