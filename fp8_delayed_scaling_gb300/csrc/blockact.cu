@@ -694,11 +694,11 @@ __device__ __forceinline__ float2 pair_of(uint2 u, int p, float f) {
 // the codes of rows 8rr .. 8rr+7, columns 8cc .. 8cc+7 and decodes them twice, for the column maxima (8 rows in the
 // thread, two row groups by shuffle, eight warps through shared memory) and for the new codes: kept as fp32 they
 // would take 64 registers and leave two CTAs an SM.  The new codes go through shared memory in 8-byte pieces XORed by
-// column group and leave as whole 128-byte lines.  Each thread copies the next tile's codes into its own slots of
-// shared memory meanwhile (no barrier, no registers), and reads the indices of the one after it.
-// Bound: the issue slots (62% in use, 12 instructions a value) and the three barriers a tile.  32768 x 4096 in 16 groups
-// through an index: 66 us, 3.1 TB/s (64 values a thread without the walk 134, bulk copies of the rows 71, eight-byte
-// factors 69); 3001 x 2048 5.7 us.
+// column group and leave as whole 128-byte lines.  Neighbours copy the next tile's codes into each other's slots of
+// shared memory meanwhile, 16 bytes at a time (no barrier, no registers), and read the indices of the one after it.
+// Bound: the issue slots (63% in use, 12 instructions a value) and the three barriers a tile.  32768 x 4096 in 16 groups
+// through an index: 62 us, 3.3 TB/s (64 values a thread without the walk 134, bulk copies of the rows 71, eight bytes a
+// copy 66); 3001 x 2048 5.4 us.
 namespace br {
 constexpr int THREADS = 256, TILE = 128;
 }
@@ -733,13 +733,14 @@ __global__ void __launch_bounds__(br::THREADS, 4) block_recode_kernel(const Bloc
         if ((lane & 15) < 8)
             copy_async<4>(&fac[slot][8 * rr + (lane & 7)], a.s + (src >= 0 ? wide_mul(s.col, src_rows) + (uint32_t)src : 0), src >= 0);
         // rows and columns that are not there: none is copied, and the address stays on the tensor
-        const uint32_t c = s.col * TILE + 8 * cc;
-        const uint8_t *q = a.q + min(c, cols - 8);
+        const uint32_t c = s.col * TILE + 8 * (cc & 14);
+        const uint8_t *q = a.q + min(c, cols - 16);
         const int32_t least = c < cols ? 0 : 0x7fffffff;
+        const int half = 4 * (lane & 1);  // of two neighbours one copies the first four rows for both, one the others
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const int32_t r = __shfl_sync(0xffffffffu, src, (lane & 16) + i);
-            copy_async<8>(&in[i][tid], q + wide_mul(max(r, 0), cols), r >= least);
+        for (int i = 0; i < 4; i++) {
+            const int32_t r = __shfl_sync(0xffffffffu, src, (lane & 16) + half + i);
+            copy_async<16, true>(&in[half + i][tid & ~1], q + wide_mul(max(r, 0), cols), r >= least);
         }
     };
     look(walk.step[0]);
@@ -753,6 +754,7 @@ __global__ void __launch_bounds__(br::THREADS, 4) block_recode_kernel(const Bloc
         uint2 u[8];
 #pragma unroll
         for (int i = 0; i < 8; i++) u[i] = in[i][tid];
+        __syncwarp();  // before a neighbour copies over them
         if (walk.step[next].n) fetch(walk.step[next], slot ^ 1);
         const float *f = &fac[slot][8 * rr];
         float m[8];
