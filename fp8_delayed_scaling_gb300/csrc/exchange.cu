@@ -72,9 +72,9 @@ __global__ void __launch_bounds__(256) block_dispatch_kernel(const DispatchArgs 
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), t = w / a.chunks;
+    const uint32_t w = blockIdx.x * 8 + (threadIdx.x >> 5), chunks = (uint32_t)a.chunks, tok = w / chunks;
+    const int64_t t = tok, c0 = (int64_t)(w - tok * chunks) * 1024 + 8 * lane;
     if (t >= a.tokens) return;
-    const int64_t c0 = (w - t * a.chunks) * 1024 + 8 * lane;
     const int32_t at = lane < a.k ? a.position[t * a.k + lane] : -1;  // lane j: where copy j goes
     Eight<XKIND> v[U];
 #pragma unroll
@@ -327,7 +327,7 @@ extern "C" fp8dl_status fp8_block_dispatch(const void *x, int32_t x_dtype, int64
     if (tokens == 0) return FP8DL_OK;
     DispatchArgs a = {x, tokens, cols, rows, (cols + 1023) / 1024, position, k, row_q, q, row_s, s};
     const int64_t ctas = (tokens * a.chunks + 7) / 8;
-    FP8DL_TRY(exchange_grid(ctas));
+    FP8DL_TRY(exchange_grid(8 * ctas));
     const bool pdl = short_call_bytes((double)tokens * (double)cols * ((x_dtype == FP8DL_BF16 ? 2.0 : 4.0) + k));
     auto *kernel = x_dtype == FP8DL_BF16
                        ? (out_dtype == FP8DL_E4M3 ? block_dispatch_kernel<FP8DL_BF16, FP8DL_E4M3>
