@@ -594,6 +594,14 @@ __global__ void __launch_bounds__(256, bwd_ctas(S)) route_bwd_kernel(const Route
     for (int p = 0; p < PAIRS; p++)
         even[p] = make_float2(dloss && i0 + 2 * p < E ? dl * a.slope[i0 + 2 * p] : 0.0f,
                               dloss && 2 * p + 1 < S && i0 + 2 * p + 1 < E ? dl * a.slope[i0 + 2 * p + 1] : 0.0f);
+    // less their mean, which drops out of dp - <p, dp>: with experts used evenly little is left to cancel
+    float2 mean2 = f2(0.0f);
+#pragma unroll
+    for (int p = 0; p < PAIRS; p++) mean2 = __fadd2_rn(mean2, even[p]);
+    const float mean = group_sum<G>(mean2.x + mean2.y) / (float)E;
+#pragma unroll
+    for (int p = 0; p < PAIRS; p++)  // zeros stay behind the last expert, where p is zero
+        even[p] = make_float2(i0 + 2 * p < E ? even[p].x - mean : 0.0f, i0 + 2 * p + 1 < E ? even[p].y - mean : 0.0f);
     __syncwarp();
     const uint32_t gmask = G == 32 ? 0xffffffffu : ((1u << (G & 31)) - 1u) << (lane & ~(G - 1));
     const int64_t step = (int64_t)gridDim.x * NG, rounds = (a.tokens + step - 1) / step;
