@@ -37,7 +37,8 @@ __device__ __forceinline__ void activation2(float2 a, float2 &y, float2 &d) {
         const float2 e = make_float2(ex2_approx_ftz(a.x * -1.4426950409f), ex2_approx_ftz(a.y * -1.4426950409f));
         const float2 s = make_float2(rcp_approx_ftz(e.x + 1.0f), rcp_approx_ftz(e.y + 1.0f));
         y = make_float2(a.x * s.x, a.y * s.y);
-        if (D) d = make_float2(fmaf(-y.x, s.x, s.x + y.x), fmaf(-y.y, s.y, s.y + y.y));  // s (1 + a (1 - s)) = s + y - y s
+        // s + y (1 - s): 1 - s first, which is nothing where s is 1 (s + y - y s loses s beside y from 2^24 on)
+        if (D) d = make_float2(fmaf(y.x, 1.0f - s.x, s.x), fmaf(y.y, 1.0f - s.y, s.y));
     } else {
         // with e = exp(-a^2 / 2), x = |a|: Phi(a) = e R, or 1 - e R; the derivative e (R - phi(0) x), or 1 less that
         const float2 x = make_float2(fabsf(a.x), fabsf(a.y)), q = __fmul2_rn(__fmul2_rn(a, a), f2(-0.7213475204f));

@@ -1,0 +1,96 @@
+"""The activations of fp8_block_act and fp8_block_dact over the whole range of their argument, to a relative error.
+
+A block that holds one value says by its factor what that value was in fp32: factor = fl(1 / fl(MAX / amax)), so that
+factor * MAX is amax to 3 roundings (3 units of 2^-24).  The checkpoint's codes are 1 or -1 and its factors |a|, so that the
+decoded argument is a itself."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import block_reference as br
+from helpers import gpu
+
+pytestmark = pytest.mark.gpu
+
+EPS = 2.0 ** -24
+C = 128  # one block a matrix and row
+GELU, SILU, GEGLU, SWIGLU = range(4)
+
+
+def truth(a, kind):
+    """act(a) and its derivative in 64 bits."""
+    a = np.asarray(a, np.float64)
+    if kind in (GELU, GEGLU):
+        cdf = 0.5 * np.array([math.erfc(-x / math.sqrt(2)) for x in a])
+        return a * cdf, cdf + a * np.exp(-a * a / 2) / math.sqrt(2 * math.pi)
+    z = np.exp(-np.abs(a))
+    s, c = np.where(a >= 0, 1, z) / (1 + z), np.where(a >= 0, z, 1) / (1 + z)  # the sigmoid and 1 less it
+    return a * s, s + a * s * c
+
+
+def forward(fd, dev, a, kind, fmt=0):
+    """The codes and factors of act(a) (u = 1 where gated): a row for each argument."""
+    R = a.numel()
+    h = a[:, None].expand(R, C)
+    if kind >= GEGLU:
+        h = torch.cat([h, torch.ones((R, C))], 1)
+    q, s = torch.empty((R, C), dtype=torch.uint8, device=dev), torch.empty((1, R), device=dev)
+    fd.fp8_block_act(h.contiguous().to(dev), kind, fmt, q, s)
+    return q.cpu(), s.cpu()[0]
+
+
+def backward(fd, dev, a, kind, fmt=0, dg=1.0, offsets=None):
+    """What fp8_block_dact writes for these arguments, u = 1 where gated, and dg everywhere; the column sums only without groups."""
+    R, gated = a.numel(), kind >= GEGLU
+    W = 2 * C if gated else C
+    hq, hs = torch.full((R, W), 0x38, dtype=torch.uint8), torch.ones((W // 128, R))
+    hq[a < 0, :C] = 0xb8
+    hs[0] = a.abs()
+    T = fd.fp8_block_padded_rows(R, 0 if offsets is None else offsets.numel() - 1)
+    u8, f32 = dict(dtype=torch.uint8, device=dev), dict(device=dev)
+    b = dict(dh_q=torch.empty((R, W), **u8), dh_s=torch.empty((W // 128, R), **f32), dh_qt=torch.empty((W, T), **u8),
+             dh_st=torch.empty((T // 128, W), **f32), g_qt=torch.empty((C, T), **u8), g_st=torch.empty((T // 128, C), **f32))
+    if offsets is None:
+        b.update(dbias=torch.empty(W, **f32), workspace=torch.empty(fd.fp8_cast_workspace_size(R, W), **u8))
+    fd.fp8_block_dact(torch.full((R, C), dg, device=dev), hq.to(dev), 0, hs.to(dev), kind, fmt,
+                      offsets=None if offsets is None else offsets.to(dev), **b)
+    return {k: v.cpu() for k, v in b.items()}
+
+
+def alone(n):
+    """Groups of one row each."""
+    return torch.arange(n + 1, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("kind", range(4))
+def test_large_arguments(kind):
+    """act(a) = a and act'(a) = 1 for large a, act(a) = act'(a) = 0 for large -a, however large: along the rows, transposed
+    and in the column sums.  8 units of 2^-24: the reading's three, a sum or a product each in Phi or the sigmoid, and its use."""
+    import fp8_delayed_scaling_gb300 as fd
+    dev = gpu()
+    a = torch.tensor([20.0, 1e3, 2050.0, 1e4, 1e6, 2.0 ** 24 - 1, 2.0 ** 24 + 2, 3e7, 1e9, 1e20, 1e38])
+    v = a.double().numpy()
+    y, d = truth(v, kind)
+
+    def near(got, want, what):
+        assert np.all(np.abs(got.double().numpy() * 448 - want) <= 8 * EPS * want), (what, got * 448)
+
+    q, s = forward(fd, dev, a, kind)
+    assert torch.all(q == 0x7e)
+    near(s, y, "g")
+    b = backward(fd, dev, a, kind)
+    near(b["dh_s"][0], d, "dh along the rows")
+    assert abs(float(b["dbias"][0]) - a.numel()) <= 16 * a.numel() * EPS
+    if kind >= GEGLU:
+        near(b["dh_s"][1], y, "dh of u along the rows")
+    b = backward(fd, dev, a, kind, offsets=alone(a.numel()))
+    near(b["dh_st"][:, 0], d, "dh transposed")
+    near(b["g_st"][:, 0], y, "g transposed")
+    # nothing is left on the other side: blocks of zeros, whose factor is 1
+    a = -a[1:]
+    b = backward(fd, dev, a, kind)
+    assert torch.all(b["dh_s"] == 1) and torch.all(b["dh_q"] & 0x7f == 0) and torch.all(b["dbias"] == 0)
+    q, s = forward(fd, dev, a, kind)
+    assert torch.all(s == 1) and torch.all(q & 0x7f == 0)
