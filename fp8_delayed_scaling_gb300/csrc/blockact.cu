@@ -40,9 +40,11 @@ __device__ __forceinline__ void activation2(float2 a, float2 &y, float2 &d) {
         // s + y (1 - s): 1 - s first, which is nothing where s is 1 (s + y - y s loses s beside y from 2^24 on)
         if (D) d = make_float2(fmaf(y.x, 1.0f - s.x, s.x), fmaf(y.y, 1.0f - s.y, s.y));
     } else {
-        // with e = exp(-a^2 / 2), x = |a|: Phi(a) = e R, or 1 - e R; the derivative e (R - phi(0) x), or 1 less that
-        const float2 x = make_float2(fabsf(a.x), fabsf(a.y)), q = __fmul2_rn(__fmul2_rn(a, a), f2(-0.7213475204f));
-        const float2 e = make_float2(ex2_approx_ftz(q.x), ex2_approx_ftz(q.y)), r = normal_ratio2(x);
+        // with e = exp(-a^2 / 2), x = |a|: Phi(a) = e R, or 1 - e R; the derivative e (R - phi(0) x), or 1 less that.  e is the
+        // square of its root, so that it reaches the subnormal numbers (2^x itself flushes them: a block of nothing but such
+        // results had the factor of a block of zeros)
+        const float2 x = make_float2(fabsf(a.x), fabsf(a.y)), q = __fmul2_rn(__fmul2_rn(a, a), f2(-0.3606737602f));
+        const float2 root = make_float2(ex2_approx_ftz(q.x), ex2_approx_ftz(q.y)), r = normal_ratio2(x), e = __fmul2_rn(root, root);
         const float2 tail = __fmul2_rn(e, r), up = __fadd2_rn(f2(1.0f), tail);
         y = __fmul2_rn(a, make_float2(a.x >= 0.0f ? up.x : -tail.x, a.y >= 0.0f ? up.y : -tail.y));  // infinity stays infinity
         if (D) {

@@ -94,3 +94,51 @@ def test_large_arguments(kind):
     assert torch.all(b["dh_s"] == 1) and torch.all(b["dh_q"] & 0x7f == 0) and torch.all(b["dbias"] == 0)
     q, s = forward(fd, dev, a, kind)
     assert torch.all(s == 1) and torch.all(q & 0x7f == 0)
+
+
+SMALLEST = 2.0 ** -149
+
+
+@pytest.mark.parametrize("kind", range(4))
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_results_too_small_for_a_factor_of_their_own(kind, fmt):
+    """Rows (and groups of one row) whose results are all below 2^-100, GELU's into the subnormal numbers (SiLU's are zero
+    below -87.3, where its sigmoid is subnormal): they have the factor of a maximum of 2^-100, not that of zeros, and E5M2,
+    which reaches 2^-16 / 57344 of that, codes for the results.
+
+    A result is off by what the subnormal factors in it are: a times e R, each to half a step, so (|a| + 1) halves (the
+    derivative's sum, at most 5.6 e: four times that), and 1e-4 relative, far below half a code (2^-4, 2^-3).  Results below
+    that may be zero."""
+    import fp8_delayed_scaling_gb300 as fd
+    dev = gpu()
+    lo, hi = (-14.8, -12.4) if kind in (GELU, GEGLU) else (-87.0, -72.0)
+    a = torch.linspace(lo, hi, 400)
+    v = a.double().numpy()
+    y, d = truth(v, kind)
+    most, half, sub = (448.0, 2.0 ** -4, 2.0 ** -10) if fmt == 0 else (57344.0, 2.0 ** -3, 2.0 ** -17)
+    f8 = torch.float8_e4m3fn if fmt == 0 else torch.float8_e5m2
+    scale = np.float32(most) / np.float32(2.0 ** -100)
+    factor = float(np.float32(1) / scale)
+
+    def check(q, s, want, what, most_of=2):
+        q, s = q.view(f8).double().numpy(), s.double().numpy()
+        err = most_of * (np.abs(v) + 1) * SMALLEST + 1e-4 * np.abs(want)
+        sure = np.abs(want) > err  # not zero in fp32
+        tiny = sure & (np.abs(want) < 2.0 ** -101)
+        assert tiny.sum() > 100 and np.all(s[tiny] == factor), (what, s[tiny])
+        assert np.all((s == factor) | (s == 1) | ~(np.abs(want) < 2.0 ** -101)), what
+        off = np.abs(q * s[:, None] - want[:, None])
+        assert np.all((off <= (half * np.abs(want) + sub * factor + err)[:, None] * 1.001)[s != 1]), what
+        if fmt == 1:
+            seen = sure & (np.abs(want) > 2.0 ** -16 / scale)
+            assert np.all(q[seen] != 0) and (kind in (SILU, SWIGLU) or (seen & (np.abs(want) < 2.0 ** -126)).sum() > 5), what
+
+    check(*forward(fd, dev, a, kind, fmt), y, "g")
+    b = backward(fd, dev, a, kind, fmt)
+    check(b["dh_q"][:, :C], b["dh_s"][0], d, "dh", 4)
+    if kind >= GEGLU:
+        check(b["dh_q"][:, C:], b["dh_s"][1], y, "dh of u")
+    b = backward(fd, dev, a, kind, fmt, offsets=alone(a.numel()))
+    check(b["dh_qt"][:C, ::128].t().contiguous(), b["dh_st"][:, 0], d, "dh transposed", 4)
+    if fmt == 0:  # the activation's transposed codes are of the checkpoint's format
+        check(b["g_qt"][:, ::128].t().contiguous(), b["g_st"][:, 0], y, "g transposed")
