@@ -529,7 +529,10 @@ fp8dl_status moe_combine_bwd(const void *dout, const void *y, int32_t dtype, int
  *   act        FP8DL_ACT_GELU, FP8DL_ACT_SILU: g = act(h), h [rows x cols]
  *              FP8DL_ACT_GEGLU, FP8DL_ACT_SWIGLU: g = act(a) * u, h = [a | u]
  *              [rows x 2 cols], GELU or SiLU
- *   GELU(a) = a * Phi(a) (erf form), SiLU(a) = a / (1 + exp(-a)), in fp32.
+ *   GELU(a) = a * Phi(a) (erf form), SiLU(a) = a / (1 + exp(-a)), in fp32, relative
+ *   errors at most (1.25 a^2 + 23) * 2^-24 (a >= 0: 23) and (1.25 |a| + 9) * 2^-24;
+ *   results below 2^-126 keep what bits subnormal numbers have, but for SiLU of
+ *   a < -87.3, which is 0.
  * Groups, rows of any number, factors' layouts and the rule of a block's scale as
  * above: offsets/n_groups NULL and 0 for the whole matrix, rows outside the
  * groups are neither read nor written. */

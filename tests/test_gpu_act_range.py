@@ -142,3 +142,48 @@ def test_results_too_small_for_a_factor_of_their_own(kind, fmt):
     check(b["dh_qt"][:C, ::128].t().contiguous(), b["dh_st"][:, 0], d, "dh transposed", 4)
     if fmt == 0:  # the activation's transposed codes are of the checkpoint's format
         check(b["g_qt"][:, ::128].t().contiguous(), b["g_st"][:, 0], y, "g transposed")
+
+
+@pytest.mark.parametrize("kind", range(4))
+def test_relative_errors(kind):
+    """act(a) and act'(a) against 64 bits over the range of results that have a factor of their own, in units of 2^-24 with 3 for
+    the reading.  E bounds the relative error of the exponential, R that of the ratio (12).
+
+    GELU: E = 1.25 a^2 + 9.  y: E + R + 2 (the smaller part of 1 - e R for a > 0).  The derivative's small part w = phi |a| - Phi(-|a|)
+    is E + 2 of |w|, R + 1 of Phi(-|a|) and 1 of phi |a| off, the sum and the product with dg 2 of the result.
+    SiLU: the exponential is 1.25 |a| + 4 off, 1 + z one unit, its reciprocal two: the sigmoid s by S = (1.25 |a| + 4) (1 - s) + 3,
+    or z where 1 + z is 1.  1 - s is s S off and half a step of its own; the derivative s + a s (1 - s)."""
+    import fp8_delayed_scaling_gb300 as fd
+    dev = gpu()
+    lo, hi = (-11.3, 11.3) if kind in (GELU, GEGLU) else (-65.0, 40.0)
+    near = torch.linspace(-3, 3, 3001)
+    a = torch.cat([torch.linspace(lo, hi, 3000), near[near != 0], torch.logspace(-20, -1, 200), -torch.logspace(-20, -1, 200)])
+    v = a.double().numpy()
+    y, d = truth(v, kind)
+    m = np.abs(v)
+    if kind in (GELU, GEGLU):
+        tail = 0.5 * np.array([math.erfc(x / math.sqrt(2)) for x in m])
+        phi = m * np.exp(-m * m / 2) / math.sqrt(2 * math.pi)
+        rel = 1.25 * m * m + 23
+        ey = np.abs(y) * (np.where(v < 0, rel, 2 + rel * tail / (1 - tail)) + 3)
+        ed = (1.25 * m * m + 11) * np.abs(phi - tail) + 13 * tail + phi + 5 * np.abs(d)
+    else:
+        z = np.exp(-m)
+        s, c = np.where(v >= 0, 1, z) / (1 + z), np.where(v >= 0, z, 1) / (1 + z)
+        S = np.where((v > 0) & (z < 2.0 ** -25), z / EPS, (1.25 * m + 4) * c + 3)
+        ey = np.abs(y) * (S + 1 + 3)
+        ed = s * S * (1 + m * c) + m * s * (s * S + c) + m * s * c + 5 * np.abs(d)
+    got = forward(fd, dev, a, kind)[1].double().numpy() * 448
+    assert np.all(np.abs(got - np.abs(y)) <= ey * EPS)
+    for fmt, most in ((0, 448), (1, 57344)):
+        got = backward(fd, dev, a, kind, fmt)["dh_s"][0].double().numpy() * most
+        live = np.abs(d) > 2.0 ** -99
+        assert np.all((np.abs(got - np.abs(d)) <= ed * EPS)[live])
+    got = []
+    for i in range(0, a.numel(), 1024):  # groups of one row
+        part = a[i:i + 1024].contiguous()
+        got.append(backward(fd, dev, part, kind, offsets=alone(part.numel())))
+    for name, want, err in (("dh_st", d, ed), ("g_st", y, ey)):
+        t = np.concatenate([b[name][:, 0].double().numpy() for b in got]) * 448
+        live = np.abs(want) > 2.0 ** -99
+        assert np.all((np.abs(t - np.abs(want)) <= err * EPS)[live]), name
