@@ -83,7 +83,7 @@ __device__ __forceinline__ float finite_abs(float v) {
     return a <= 3.402823466e38f ? a : 0.0f;
 }
 
-// Called by all threads of a block of 256 or 512 (the first 256 hold the groups): the rows behind 128-row block `block` of the padded order (every
+// Called by all 256 threads of a block: the rows behind 128-row block `block` of the padded order (every
 // group rounded up to a multiple of 128): first row and how many (0 behind the last group).  A
 // thread takes up to four groups, so every offset is loaded at once and few instructions are issued
 // (a search by every warp for itself cost twice the time with 200 groups).  Offsets in disorder may make
@@ -114,7 +114,7 @@ __device__ __forceinline__ void group_of_block(const int32_t *offsets, int n_gro
         const uint32_t u = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += u;
     }
-    if (lane == 31 && warp < 8) warp_sum[warp] = min(sum, 1u << 28);
+    if (lane == 31) warp_sum[warp] = min(sum, 1u << 28);
     if (threadIdx.x == 0) found[1] = 0;
     __syncthreads();
     uint32_t at = block - (sum - mine);  // within this thread's blocks, if below `mine`

@@ -82,7 +82,6 @@ struct BlockActArgs {
     uint8_t *g_q, *h_q;
     float *g_s, *h_s;
     uint32_t jobs;  // blocks of a row
-    int split;
 };
 
 namespace ba {
@@ -168,7 +167,7 @@ __device__ __forceinline__ float put_blocks(const float2 (&v)[2][NA][4], uint8_t
 // Persistent CTAs, a job of 32 rows of one block column (of a's and of u's where g is gated) after the other, two
 // neighbouring rows for 16 lanes.  Each thread copies its values of the next job into its own slots of shared memory
 // while it works on this one's (no barrier, no registers).
-// Where u's half does not start on a block (cols not a multiple of 128: `split`) h's blocks do not line up with
+// Where u's half does not start on a block (cols not a multiple of 128) h's blocks do not line up with
 // g's: the codes of h are jobs of their own behind g's.  KEEP: with the codes of h.
 // Bound: HBM, SwiGLU of 8192 x 11008 in bf16 with the checkpoint: 100 us, 6.4 TB/s, without it 69 us, 6.6 TB/s (a CTA a
 // job, loads into registers: 118 and 79); GELU of 8192 x 16384 127 us, 4.3 TB/s: the issue slots.
@@ -889,8 +888,8 @@ extern "C" fp8dl_status fp8_block_act(const void *h, int32_t h_dtype, int32_t ac
     a.offsets = offsets;
     a.n_groups = n_groups;
     a.g_q = g_q, a.h_q = h_q, a.g_s = g_s, a.h_s = h_s;
-    a.split = gated && cols % 128 != 0;
-    a.jobs = (uint32_t)((cols + 127) / 128 + (a.split && h_q ? (a.wide + 127) / 128 : 0));
+    const bool split = gated && cols % 128 != 0;
+    a.jobs = (uint32_t)((cols + 127) / 128 + (split && h_q ? (a.wide + 127) / 128 : 0));
     const int64_t ctas = (rows + ba::ACT_ROWS - 1) / ba::ACT_ROWS * a.jobs;
     FP8DL_TRY(check_tiles(ctas, rows, cols));
     int sms = 0;
@@ -898,7 +897,7 @@ extern "C" fp8dl_status fp8_block_act(const void *h, int32_t h_dtype, int32_t ac
     const int64_t resident = (int64_t)sms * ba::ACT_CTAS;
     if (rows == 0) return FP8DL_OK;
     const bool pdl = short_call_bytes((double)rows * a.wide * ((h_dtype == FP8DL_BF16 ? 2.0 : 4.0) + (h_q ? 1.0 : 0.0)) + (double)rows * cols);
-    const bool keep = h_q && !a.split;
+    const bool keep = h_q && !split;
     auto *kernel = &block_act_kernel<FP8DL_BF16, FP8DL_E4M3, false, false, false>;
 #define FP8DL_ACT_KEEP(X, F, G, S) (keep ? block_act_kernel<X, F, G, S, true> : block_act_kernel<X, F, G, S, false>)
 #define FP8DL_ACT(X, F)                                                                                           \
