@@ -15,28 +15,37 @@
 
 namespace fp8dl {
 
-// -R(x) of two values x >= 0, Phi(-x) = exp(-x^2 / 2) R(x): a polynomial of degree 9 in t = 1 / (1 + p x) without constant
-// term, fitted here by weighted least squares until the relative error was even over x in [0, 14.6] (3.2e-8; 4.7e-7 in fp32,
-// of which the rounding of 1 + p x and its reciprocal make most).  Relative, because a block may hold nothing but small
-// results: a column of a group of one row.
+// -R(x) of two values x >= 0, Phi(-x) = exp(-x^2 / 2) R(x): t S(1 - t), t = 1 / (1 + p x), S a polynomial of degree 8 that is
+// 1/2 at x = 0, fitted here by weighted least squares until the relative error was even over x in [0, 14.6] (3.6e-8; 2.5e-7
+// in fp32).  In 1 - t, which is p x t, what the rounding of 1 + p x does to S goes with x; a polynomial in t was 4.7e-7 off near
+// 0, where activations are.  Relative, because a block may hold nothing but small results: a column of a group of one row.
 __device__ __forceinline__ float2 normal_ratio2(float2 x) {
     const float2 d = __ffma2_rn(f2(0.35f), x, f2(1.0f)), t = make_float2(rcp_approx_ftz(d.x), rcp_approx_ftz(d.y));
-    float2 poly = __ffma2_rn(t, f2(0.02915947757340436f), f2(-0.1440388069763008f));
-    poly = __ffma2_rn(t, poly, f2(0.2558556228802927f));
-    poly = __ffma2_rn(t, poly, f2(-0.1593390872971131f));
-    poly = __ffma2_rn(t, poly, f2(0.02322601534805139f));
-    poly = __ffma2_rn(t, poly, f2(-0.1055584323568273f));
-    poly = __ffma2_rn(t, poly, f2(-0.1198197446306157f));
-    poly = __ffma2_rn(t, poly, f2(-0.1398637346849845f));
-    poly = __ffma2_rn(t, poly, f2(-0.1396212938650767f));
+    const float2 u = __fmul2_rn(__fmul2_rn(f2(0.35f), x), t);
+    float2 poly = __ffma2_rn(u, f2(0.02892103901855419f), f2(-0.08838456601291317f));
+    poly = __ffma2_rn(u, poly, f2(0.06279255146641106f));
+    poly = __ffma2_rn(u, poly, f2(0.01707466298726712f));
+    poly = __ffma2_rn(u, poly, f2(0.06372926568268843f));
+    poly = __ffma2_rn(u, poly, f2(-0.102527480416411f));
+    poly = __ffma2_rn(u, poly, f2(-0.2610602466252296f));
+    poly = __ffma2_rn(u, poly, f2(0.639832909834862f));
+    poly = __ffma2_rn(u, poly, f2(-0.5f));
     return __fmul2_rn(poly, t);
+}
+
+// |a|, at most 32, where exp(-a^2 / 2) has long been zero: finite, so that what it is multiplied by stays zero.  NaN stays NaN.
+__device__ __forceinline__ float magnitude(float a) {
+    float x;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(fabsf(a)), "f"(32.0f));
+    return x;
 }
 
 // act(a) and, with D, its derivative.  Relative errors in units of 2^-24, at most: GELU 1.25 a^2 + 23 where a < 0 (the
 // exponent's two roundings and its constant; 8 and 1 for the squared 2^x, 12 for the ratio, 2 products), SiLU 1.25 |a| + 9.
-// Measured: GELU 9 within |a| <= 1, 43 at -7, 121 at -11.5, SiLU 6 within |a| <= 4, 61 at -70.  What an exact exponent would
-// cost (its remainder applied to 2^x): 8192 x 16384 GELU 136 -> 158 us, its gradient 257 -> 273, SiLU's 206 -> 228, for results
-// that are rounded to 3 or 4 significant bits.
+// Measured: GELU 7 within |a| <= 1, 43 at -7, 121 at -11.5, SiLU 6 within |a| <= 4, 61 at -70; fp32 codes of gradients differ
+// from 64 bits as rarely as those of a plain fp32 form (2999 x 1408, E5M2: 27 and 32 of 8 x 4 M).  An exact exponent (its
+// remainder applied to 2^x) would cost 22 us on 140 for GELU of 8192 x 16384, 16 on 263 for its gradient, 22 on 207 for SiLU's,
+// for results that are rounded to 3 or 4 significant bits.
 template <bool SILU, bool D>
 __device__ __forceinline__ void activation2(float2 a, float2 &y, float2 &d) {
     if (SILU) {  // constants in scalar instructions, which hold them (a packed one wants them in registers)
@@ -49,7 +58,7 @@ __device__ __forceinline__ void activation2(float2 a, float2 &y, float2 &d) {
         // with e = exp(-a^2 / 2), x = |a|: Phi(a) = e R, or 1 - e R; the derivative e (R - phi(0) x), or 1 less that.  e is the
         // square of its root, so that it reaches the subnormal numbers (2^x itself flushes them: a block of nothing but such
         // results had the factor of a block of zeros)
-        const float2 x = make_float2(fabsf(a.x), fabsf(a.y)), q = __fmul2_rn(__fmul2_rn(a, a), f2(-0.3606737602f));
+        const float2 x = make_float2(magnitude(a.x), magnitude(a.y)), q = __fmul2_rn(__fmul2_rn(a, a), f2(-0.3606737602f));
         const float2 root = make_float2(ex2_approx_ftz(q.x), ex2_approx_ftz(q.y)), r = normal_ratio2(x), e = __fmul2_rn(root, root);
         const float2 tail = __fmul2_rn(e, r), up = __fadd2_rn(f2(1.0f), tail);
         y = __fmul2_rn(a, make_float2(a.x >= 0.0f ? up.x : -tail.x, a.y >= 0.0f ? up.y : -tail.y));  // infinity stays infinity
@@ -170,7 +179,7 @@ __device__ __forceinline__ float put_blocks(const float2 (&v)[2][NA][4], uint8_t
 // Where u's half does not start on a block (cols not a multiple of 128) h's blocks do not line up with
 // g's: the codes of h are jobs of their own behind g's.  KEEP: with the codes of h.
 // Bound: HBM, SwiGLU of 8192 x 11008 in bf16 with the checkpoint: 100 us, 6.4 TB/s, without it 69 us, 6.6 TB/s (a CTA a
-// job, loads into registers: 118 and 79); GELU of 8192 x 16384 127 us, 4.3 TB/s: the issue slots.
+// job, loads into registers: 118 and 79); GELU of 8192 x 16384 140 us, 3.8 TB/s: the issue slots.
 // The 16 bytes of a thread go past L1 where they are whole sectors' worth; two halves of fp32 values go through it (past
 // it every sector is fetched twice: 8192 x 8192 182 us against 112).
 template <int XKIND, int FMT, bool GATED, bool SILU, bool KEEP>
@@ -444,7 +453,7 @@ __device__ __forceinline__ uint4 put_column(const float2 (&v)[8], float &factor)
 // Shared memory holds pairs of rows, so that the column phase reads two values at once; 16-byte units are XORed by
 // unit / 8 and by row / 16: both phases hit 32 banks.
 // Bound: the issue slots (71% in use, 60 instructions a value of g).  SwiGLU of 8192 x 11008 in bf16 with dbias: 196 us,
-// 4.2 TB/s; GELU of 8192 x 16384 252 us; 2999 x 1408 in 24 groups, GELU 17 us (three rounds of tiles).  Slower at the
+// 4.2 TB/s; GELU of 8192 x 16384 263 us; 2999 x 1408 in 24 groups, GELU 17 us (three rounds of tiles).  Slower at the
 // first of these: values kept in registers by 512 threads (305 us), CTA pairs that share the rows' maxima over distributed
 // shared memory with two CTAs an SM (421), short tiles with fewer lanes a column (205), packed products (207).
 namespace bd {

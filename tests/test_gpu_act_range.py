@@ -144,6 +144,20 @@ def test_results_too_small_for_a_factor_of_their_own(kind, fmt):
         check(b["g_qt"][:, ::128].t().contiguous(), b["g_st"][:, 0], y, "g transposed")
 
 
+@pytest.mark.parametrize("kind", [GELU, GEGLU])
+def test_gelu_of_infinities_in_the_checkpoint(kind):
+    """A factor of infinity in the checkpoint (codes 1 and -1): the derivative has its limits, 1 and 0; NaN stays NaN."""
+    import fp8_delayed_scaling_gb300 as fd
+    dev = gpu()
+    b = backward(fd, dev, torch.tensor([float("inf"), float("-inf"), float("nan"), 2.0]), kind)
+    v = b["dh_q"][:, :C].view(torch.float8_e4m3fn).float()
+    s = b["dh_s"][0]
+    assert torch.all(v[0] == 448) and torch.all(v[1] == 0) and torch.all(torch.isnan(v[2])) and torch.all(v[3] == 448)
+    assert abs(float(s[0]) * 448 - 1) <= 3 * EPS and s[1] == 1 and s[2] == 1
+    g = b["g_qt"][0, :4].view(torch.float8_e4m3fn).float()
+    assert g[0] == 448 and torch.isnan(g[1]) and torch.isnan(g[2]) and g[3] == 448
+
+
 @pytest.mark.parametrize("kind", range(4))
 def test_relative_errors(kind):
     """act(a) and act'(a) against 64 bits over the range of results that have a factor of their own, in units of 2^-24 with 3 for
