@@ -404,6 +404,16 @@ def _tensor(t, dtype, shape, dev: int, name: str):
     return t.data_ptr()
 
 
+def _workspace(t, dev: int):
+    """(address, bytes) of a workspace on device `dev` (or none): contiguous, since a view may have fewer bytes than elements."""
+    if t is None:
+        return None, 0
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the device of the others, got %s%s" % (
+            t.device, "" if t.is_contiguous() else ", strided"))
+    return t.data_ptr(), _nbytes(t)
+
+
 def _launch(dev: int, stream):
     """The stream to launch on; the tensors must be on the current CUDA device, where the kernels run."""
     if dev < 0 or dev != torch._C._cuda_getDevice():
@@ -431,13 +441,12 @@ def fp8_block_quantize(x: torch.Tensor, out_dtype: int, row_q=None, row_s=None, 
     groups = 0 if offsets is None else offsets.numel() - 1
     _need(groups >= 1 or offsets is None, "offsets must hold n_groups + 1 entries")
     dev, T = x.get_device(), (rows + 127 * min(max(groups, 1), rows)) // 128 * 128  # fp8_block_padded_rows
-    _need(workspace is None or workspace.get_device() == dev, "workspace must be on the device of x")
     args = (x.data_ptr(), _hp(x), rows, cols, _tensor(offsets, torch.int32, (groups + 1,), dev, "offsets"), groups,
             out_dtype, _tensor(row_q, torch.uint8, (rows, cols), dev, "row_q"),
             _tensor(row_s, torch.float32, (_blocks(cols), rows), dev, "row_s"),
             _tensor(col_q, torch.uint8, (cols, T), dev, "col_q"),
             _tensor(col_s, torch.float32, (T // 128, cols), dev, "col_s"),
-            _tensor(dbias, torch.float32, (cols,), dev, "dbias"), _p(workspace), _nbytes(workspace))
+            _tensor(dbias, torch.float32, (cols,), dev, "dbias"), *_workspace(workspace, dev))
     _check(_lib.fp8_block_quantize(*args, _launch(dev, stream)), "fp8_block_quantize")
 
 
@@ -530,13 +539,12 @@ def moe_route(logits: torch.Tensor, expert: torch.Tensor, weight: torch.Tensor, 
     moe_route_workspace_size bytes."""
     _need(logits.dim() == 2 and logits.is_contiguous() and expert.dim() == 2, "logits [T x E] and expert [T x k] must be matrices")
     (T, E), k, dev, i32, f32 = logits.shape, expert.shape[1], logits.get_device(), torch.int32, torch.float32
-    _need(workspace is None or workspace.get_device() == dev, "workspace must be on the device of logits")
     args = (logits.data_ptr(), _hp(logits), T, E, k,
             None if valid is None else _tensor(valid, torch.bool if valid.dtype is torch.bool else torch.uint8, (T,), dev, "valid"),
             1 if normalize else 0, _tensor(expert, i32, (T, k), dev, "expert"), _tensor(weight, f32, (T, k), dev, "weight"),
             _tensor(position, i32, (T, k), dev, "position"), _tensor(token, i32, (T * k,), dev, "token"),
             _tensor(offsets, i32, (E + 1,), dev, "offsets"), _tensor(counts, i32, (E,), dev, "counts"),
-            _tensor(slope, f32, (E,), dev, "slope"), _tensor(loss, f32, (1,), dev, "loss"), _p(workspace), _nbytes(workspace))
+            _tensor(slope, f32, (E,), dev, "slope"), _tensor(loss, f32, (1,), dev, "loss"), *_workspace(workspace, dev))
     _check(_lib.moe_route(*args, _launch(dev, stream)), "moe_route")
 
 
@@ -620,13 +628,12 @@ def fp8_block_dact(dg: torch.Tensor, h_q: torch.Tensor, h_fp8: int, h_s: torch.T
     _need(dg.dim() == 2 and dg.is_contiguous(), "dg must be a contiguous matrix")
     (R, C), G, dev, u8, f32 = dg.shape, _groups(offsets), dg.get_device(), torch.uint8, torch.float32
     W, T = 2 * C if act >= ACT_GEGLU else C, (R + 127 * min(max(G, 1), R)) // 128 * 128
-    _need(workspace is None or workspace.get_device() == dev, "workspace must be on the device of dg")
     args = (dg.data_ptr(), _hp(dg), act, R, C, _tensor(h_q, u8, (R, W), dev, "h_q"), h_fp8,
             _tensor(h_s, f32, (_blocks(W), R), dev, "h_s"), _tensor(offsets, torch.int32, (G + 1,), dev, "offsets"), G, out_dtype,
             _tensor(dh_q, u8, (R, W), dev, "dh_q"), _tensor(dh_s, f32, (_blocks(W), R), dev, "dh_s"),
             _tensor(dh_qt, u8, (W, T), dev, "dh_qt"), _tensor(dh_st, f32, (T // 128, W), dev, "dh_st"),
             _tensor(g_qt, u8, (C, T), dev, "g_qt"), _tensor(g_st, f32, (T // 128, C), dev, "g_st"),
-            _tensor(dbias, f32, (W,), dev, "dbias"), _p(workspace), _nbytes(workspace))
+            _tensor(dbias, f32, (W,), dev, "dbias"), *_workspace(workspace, dev))
     _check(_lib.fp8_block_dact(*args, _launch(dev, stream)), "fp8_block_dact")
 
 
