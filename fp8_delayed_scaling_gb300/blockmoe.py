@@ -22,7 +22,8 @@ fp32 scale per 128 values: the just-in-time scaling of "FP8 低精度训练：Tr
 block); the gradient of the logits leaves out that the choice of experts itself may change.
 
 The layer keeps its outputs and codes in buffers made once: an output is valid until the next call.  It
-takes any number of tokens up to `tokens`, down to a single one.  need_backward=False (serving) keeps nothing.
+takes any number of tokens up to `tokens`, down to a single one.  need_backward=False (serving) writes nothing that a
+backward pass reads; the buffers of one are there all the same.
 """
 from __future__ import annotations
 

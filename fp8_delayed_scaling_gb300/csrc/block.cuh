@@ -64,7 +64,8 @@ __device__ __forceinline__ float2 block_scale(float amax) {
 // functions on the IBM RISC System/6000 processor", IBM J. Res. Dev. 34, 1990): a reciprocal refined by one step is
 // the correctly rounded one or next to it, and a quotient corrected by its exact remainder is correctly rounded.
 // No step leaves the normal numbers for maxima of 2^-100 to the largest finite one: dividend and divisor are taken a
-// fourth, so that the divisor's reciprocal stays above 2^-126.  (Compared with the divisions for every fp32 maximum.)
+// fourth, so that the divisor's reciprocal stays above 2^-126.  The tests compare both figures with the divisions for every
+// maximum of six binades, both formats: the hardware's first estimate decides the last bit of a handful of mantissas.
 __device__ __forceinline__ float refined_rcp(float b) {
     const float y = rcp_approx_ftz(b);
     return __fmaf_rn(y, __fmaf_rn(-b, y, 1.0f), y);

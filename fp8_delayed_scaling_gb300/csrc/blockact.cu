@@ -452,8 +452,8 @@ __device__ __forceinline__ uint4 put_column(const float2 (&v)[8], float &factor)
 //            whole 128-byte line).  The next tile's values are loaded into registers meanwhile.
 // Shared memory holds pairs of rows, so that the column phase reads two values at once; 16-byte units are XORed by
 // unit / 8 and by row / 16: both phases hit 32 banks.
-// Bound: the issue slots (71% in use, 60 instructions a value of g).  SwiGLU of 8192 x 11008 in bf16 with dbias: 196 us,
-// 4.2 TB/s; GELU of 8192 x 16384 263 us; 2999 x 1408 in 24 groups, GELU 17 us (three rounds of tiles).  Slower at the
+// Bound: the issue slots (71% in use, 60 instructions a value of g).  SwiGLU of 8192 x 11008 in bf16 with dbias: 199 us,
+// 4.2 TB/s; GELU of 8192 x 16384 263 us; 2999 x 1408 in 24 groups, GELU 18 us (three rounds of tiles).  Slower at the
 // first of these: values kept in registers by 512 threads (305 us), CTA pairs that share the rows' maxima over distributed
 // shared memory with two CTAs an SM (421), short tiles with fewer lanes a column (205), packed products (207).
 namespace bd {
@@ -590,8 +590,8 @@ __global__ void __launch_bounds__(bd::THREADS, 1) block_dact_kernel(const BlockD
 
 // Blocks of dh along the rows, a.row_jobs of a row from a.row_first on: all of them where nothing else is
 // wanted; those of u's half (and the one that holds the border) where cols is not a multiple of 128 and
-// the tiles above do not hold whole blocks.  16 lanes a block, two rows of each in flight.  (8192 x 11024: 308 us for both
-// kernels, 196 where the blocks line up.)
+// the tiles above do not hold whole blocks.  16 lanes a block, two rows of each in flight.  (8192 x 11024: 310 us for both
+// kernels, 190 where the blocks line up.)
 template <int FMT, bool GATED, bool SILU>
 __global__ void __launch_bounds__(ba::ACT_THREADS) block_dact_rows_kernel(const BlockDactArgs a) {
     using namespace ba;
